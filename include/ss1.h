@@ -501,6 +501,220 @@ ss1_status ss1_backward(const ss1_tensor* x, const ss1_tensor* W_c,
 ss1_status ss1_backward_select_algo(const ss1_tensor* x, const ss1_tensor* W_c, int32_t c, int32_t BK,
                                     int32_t BN, int32_t* dx_algo, int32_t* dw_algo);
 
+/* ------------------------------------------------------------------------
+ * Operators around an SS1 layer: what a user who finetunes or serves
+ * projected layers (the SS1 author abstract: pre-trained models can be
+ * projected onto SS1, then finetuned) runs next to ss1_forward and
+ * ss1_backward.  Their definitions are this library's own (the pages give
+ * none); the conventions above hold for all of them.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * ss1_layernorm_forward -- DEVICE, asynchronous on `stream`.  Layer norm of
+ * every row of x:
+ *   mean[m] = (1/K) sum_k x[m][k],  var = (1/K) sum_k (x[m][k] - mean[m])^2,
+ *   rstd[m] = 1 / sqrt(var + eps),
+ *   y[m][k] = (x[m][k] - mean[m]) * rstd[m] * gamma[k] + beta[k]
+ *   x     : [M][K] F32 or BF16, any M >= 0 and 1 <= K < 2^24
+ *   gamma : [1][K] of x's dtype or F32
+ *   beta  : [1][K] of gamma's dtype, or NULL (no shift)
+ *   y     : [M][K], x's dtype, written; may be x itself
+ *   mean, rstd : DEVICE float[M], written; each may be NULL (not wanted)
+ * Arithmetic: float32 throughout, the variance from the differences to the
+ * mean; y rounded once.  A row that holds an infinity or a NaN gives NaN in
+ * that row alone.  x, gamma, beta, y 16-byte aligned; mean, rstd 4-byte.
+ * M == 0 enqueues nothing.
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE (also eps that is negative or not
+ * finite), SS1_ERR_DTYPE, SS1_ERR_ALIGN (before any HIP call), SS1_ERR_HIP.
+ */
+ss1_status ss1_layernorm_forward(const ss1_tensor* x, const ss1_tensor* gamma, const ss1_tensor* beta, float eps,
+                                 ss1_tensor* y, float* mean, float* rstd, void* stream);
+
+/*
+ * ss1_layernorm_backward_query -- HOST.  *bytes = the device workspace that
+ * ss1_layernorm_backward needs for an x of these sizes (only dtype and sizes
+ * are read): float32 partial sums of dgamma and dbeta.
+ *
+ * ss1_layernorm_backward -- DEVICE, asynchronous on `stream`.  Gradients of
+ * ss1_layernorm_forward for an upstream dy, with the mean and rstd that it
+ * wrote; xh = (x - mean) * rstd, g = dy * gamma:
+ *   dx[m][k] = rstd[m] * (g - mean_k(g) - xh * mean_k(g * xh))
+ *   dgamma[k] = sum_m dy[m][k] * xh[m][k],  dbeta[k] = sum_m dy[m][k]
+ *   dy, x : [M][K] F32 or BF16 (one dtype);  gamma : [1][K] as in the forward
+ *   mean, rstd : DEVICE float[M], read
+ *   dx : [M][K], x's dtype, written (NULL: not computed); may be dy itself
+ *   dgamma, dbeta : [1][K], gamma's dtype, written (NULL: not computed); all
+ *        zero when M == 0
+ *   workspace : DEVICE, 16-byte aligned, at least the queried bytes (only
+ *        needed when dgamma or dbeta is); contents unspecified afterwards.
+ *        Calls that share it must be ordered.
+ * Arithmetic: float32; the sums over m run in a fixed order (a fixed number
+ * of row groups, joined in order), so equal calls give equal bits.
+ * Errors: as the forward; SS1_ERR_SHAPE for a workspace that is too small.
+ */
+ss1_status ss1_layernorm_backward_query(const ss1_tensor* x, size_t* bytes);
+ss1_status ss1_layernorm_backward(const ss1_tensor* dy, const ss1_tensor* x, const ss1_tensor* gamma,
+                                  const float* mean, const float* rstd, ss1_tensor* dx, ss1_tensor* dgamma,
+                                  ss1_tensor* dbeta, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Largest rank of one adapter. */
+#define SS1_MAX_RANK 128
+
+/* A set of low-rank adapters of one projection K -> N.  Both factors are
+   stored rank-major: adapter e owns rows row[e] .. row[e+1]-1 of A and of B
+   (ranks may differ), and adds scale[e] * (x A_e^T) B_e to the projection. */
+typedef struct {
+    ss1_tensor A;          /* [R][K], DEVICE, F32 or BF16                         */
+    ss1_tensor B;          /* [R][N], DEVICE, A's dtype                           */
+    const int32_t* row;    /* DEVICE [count + 1], ascending, row[0] = 0           */
+    const float* scale;    /* DEVICE [count]                                      */
+    int32_t count;
+    int32_t max_rank;      /* at least every row[e+1] - row[e]; <= SS1_MAX_RANK   */
+} ss1_adapters;
+
+/* The requests of one batch: segment s is the tokens offset[s] ..
+   offset[s+1]-1 (it may be empty) and uses adapter[s], or none where that is
+   outside [0, count) (-1 by custom). */
+typedef struct {
+    const int32_t* offset;   /* DEVICE [count + 1], ascending from 0 to M */
+    const int32_t* adapter;  /* DEVICE [count]                            */
+    int32_t count;
+    int32_t reserved;        /* must be 0 */
+} ss1_segments;
+
+/*
+ * ss1_adapter_forward_query -- HOST.  *bytes = the device workspace that
+ * ss1_adapter_forward needs for these sizes (data is not read).
+ *
+ * ss1_adapter_forward -- DEVICE, asynchronous on `stream`.  The low-rank
+ * adapters of many requests beside their shared projection: for token m of
+ * segment s with adapter e = adapter[s],
+ *   v[m][j] = sum_k x[m][k] A[row[e] + j][k],             j < rank of e
+ *   y[m][n] = base[m][n] + scale[e] * sum_j v[m][j] B[row[e] + j][n]
+ * and y[m] = base[m] (v[m] = 0) for a token without an adapter.
+ *   x    : [M][K] of A's dtype
+ *   base : [M][N] of A's dtype, the shared projection's output (ss1_forward's
+ *          y), or NULL for zero
+ *   y    : [M][N], written; may be base itself
+ *   v    : [M][max_rank] F32, written (columns beyond a token's rank are 0),
+ *          what ss1_adapter_backward reads; may be NULL
+ *   workspace : DEVICE, 16-byte aligned, at least the queried bytes; contents
+ *          unspecified afterwards.  Calls that share it must be ordered.
+ * Arithmetic: products of the inputs accumulated in float32; v stays float32
+ * between the two products (bf16: as the sum of two bf16 values, an error of
+ * at most 2^-17 of v); y rounded once.  Equal calls give equal bits.
+ * Requirements: K and N multiples of 8 (BF16) or 4 (F32), below 2^24;
+ * M < 2^31; x, A, B, base, y, v 16-byte aligned, index and scale arrays
+ * 4-byte aligned.  M == 0 enqueues nothing; R == 0 (no adapter rows) and
+ * segments.count == 0 leave y = base.
+ * Index arrays that break the rules above leave y unspecified, but nothing
+ * outside the buffers is touched.
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE, SS1_ERR_DTYPE, SS1_ERR_ALIGN (before
+ * any HIP call), SS1_ERR_HIP.
+ */
+ss1_status ss1_adapter_forward_query(int64_t M, const ss1_adapters* adapters, size_t* bytes);
+ss1_status ss1_adapter_forward(const ss1_tensor* x, const ss1_adapters* adapters, const ss1_segments* segments,
+                               const ss1_tensor* base, ss1_tensor* y, ss1_tensor* v, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * ss1_adapter_backward_query -- HOST.  As ss1_adapter_forward_query.
+ *
+ * ss1_adapter_backward -- DEVICE, asynchronous on `stream`.  Gradients of
+ * ss1_adapter_forward for an upstream dy (e the adapter of token m):
+ *   dv[m][j] = scale[e] * sum_n dy[m][n] B[row[e] + j][n]
+ *   dx[m][k] = dx_base[m][k] + sum_j dv[m][j] A[row[e] + j][k]
+ *   dA[row[e] + j][k] = sum over e's tokens m of dv[m][j] x[m][k]
+ *   dB[row[e] + j][n] = scale[e] * sum over e's tokens m of v[m][j] dy[m][n]
+ * (the gradient of base is dy itself).
+ *   dy : [M][N];  x : [M][K];  v : [M][max_rank] F32 as the forward wrote it
+ *        (read for dB only; columns beyond a token's rank are not used)
+ *   dx_base : [M][K], the projection's own input gradient (ss1_backward's
+ *        dx), or NULL for zero
+ *   dx : [M][K], written (NULL: not computed); may be dx_base itself
+ *   dA : [R][K], dB : [R][N], A's dtype, written (NULL: not computed); zero
+ *        for adapters that no token uses
+ *   workspace : as in the forward
+ * Arithmetic, requirements and errors: as the forward; gradients are summed
+ * in float32 in a fixed order and rounded once.
+ */
+ss1_status ss1_adapter_backward_query(int64_t M, const ss1_adapters* adapters, size_t* bytes);
+ss1_status ss1_adapter_backward(const ss1_tensor* dy, const ss1_tensor* x, const ss1_tensor* v,
+                                const ss1_adapters* adapters, const ss1_segments* segments,
+                                const ss1_tensor* dx_base, ss1_tensor* dx, ss1_tensor* dA, ss1_tensor* dB,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Elements of an 8-bit optimizer state that share one float32 scale. */
+#define SS1_ADAMW_BLOCK 256
+
+/* One tensor of an AdamW step; every pointer is to device memory that the
+   caller owns. */
+typedef struct {
+    void* param;           /* numel values of param_dtype, read and written          */
+    const void* grad;      /* numel values of grad_dtype                              */
+    void* m;               /* first moment: float, or E4M3 codes                      */
+    void* v;               /* second moment: float; or E4M3 codes of its square root  */
+    float* master;         /* float32 master of a BF16 param, or NULL                 */
+    float* m_scale;        /* E4M3 states: ceil(numel / SS1_ADAMW_BLOCK) scales each; */
+    float* v_scale;        /*              NULL for float states                      */
+    int64_t numel;
+    float weight_decay;
+    int32_t param_dtype;   /* SS1_F32 or SS1_BF16 */
+    int32_t grad_dtype;    /* SS1_F32 or SS1_BF16 */
+    int32_t state_dtype;   /* SS1_F32 or SS1_FP8_E4M3 */
+} ss1_adamw_entry;
+
+typedef struct {
+    double lr, beta1, beta2, eps;
+    double grad_scale;             /* multiplies every gradient (1: none)                       */
+    const float* grad_scale_dev;   /* DEVICE float that multiplies it too (a clip coefficient
+                                      that the host has not seen), or NULL                      */
+    int64_t step;                  /* 1 for the first step                                      */
+    uint64_t seed;                 /* of the random bits of stochastic rounding                 */
+} ss1_adamw_hyper;
+
+/*
+ * ss1_adamw_plan -- HOST.  Checks `count` entries (host array) and lists the
+ * work of a step over them: *chunks = the number of work items, and, when map
+ * is not NULL, map[2*i], map[2*i+1] = item i's entry and its place there.
+ * The caller copies the entries and the map to the device once; they hold
+ * for as long as the tensors stay where they are.
+ * Errors: SS1_ERR_NULL (a required pointer of an entry with numel > 0, or
+ * scales that are missing), SS1_ERR_SHAPE (numel < 0 or >= 2^39, count
+ * >= 2^23, a negative or not finite weight_decay, a master beside an F32
+ * param), SS1_ERR_DTYPE, SS1_ERR_ALIGN (param, grad, m, v, master 16-byte,
+ * scales 4-byte aligned).
+ *
+ * ss1_adamw_step -- DEVICE, asynchronous on `stream`.  One AdamW step over
+ * every entry, one launch:
+ *   g = grad * grad_scale * grad_scale_dev
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - (lr / (1 - beta1^step)) m /
+ *       (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32 (coefficients from the doubles, rounded once).
+ *   - BF16 param with a master: p is the master; param = p rounded to nearest.
+ *   - BF16 param without one: p = param, and the result is rounded up or down
+ *     with the probability of its distance (small steps are kept on average).
+ *   - E4M3 states: m and r = sqrt(v) are code * scale of their block of
+ *     SS1_ADAMW_BLOCK elements.  The new scale is max |value| / 448 (1 for a
+ *     block of zeros) and the quotient is rounded up or down with the
+ *     probability of its distance: with beta2 = 0.999 one step moves r by
+ *     about 0.0005 of itself, and rounding to nearest (quantum 1/8 to 1/16)
+ *     would hold it for ever.  A nonzero r keeps at least the smallest code.
+ *     p takes the moments before they are rounded.
+ * Random bits: SplitMix64 (as in ss1_plan) of seed and (entry, element) pairs,
+ * so equal calls give equal bits; a caller passes another seed each step.
+ *   entries, map : DEVICE copies of ss1_adamw_plan's arrays; count, chunks as
+ *                  there (map items outside the entries are skipped)
+ * chunks == 0 enqueues nothing.
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE (step < 1, betas outside [0, 1),
+ * lr, eps or grad_scale negative or not finite), SS1_ERR_ALIGN (entries
+ * 8-byte, map and grad_scale_dev 4-byte), SS1_ERR_HIP.
+ */
+ss1_status ss1_adamw_plan(const ss1_adamw_entry* entries, int32_t count, int64_t* chunks, int32_t* map);
+ss1_status ss1_adamw_step(const ss1_adamw_entry* entries, int32_t count, const int32_t* map, int64_t chunks,
+                          const ss1_adamw_hyper* hyper, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,6 +33,14 @@ from ._lib import (  # noqa: F401
     sketch,
     version,
 )
+from ._ops import (  # noqa: F401
+    AdamWPlan,
+    AdapterSet,
+    adapter_backward,
+    adapter_forward,
+    layernorm_backward,
+    layernorm_forward,
+)
 
 
 @dataclass

@@ -32,7 +32,10 @@ EXPORTS = ("ss1_version", "ss1_status_string", "ss1_plan", "ss1_plan_index", "ss
            "ss1_forward_idx", "ss1_forward_algo", "ss1_forward_idx_algo", "ss1_select_algo", "ss1_sketch",
            "ss1_project", "ss1_mlp_forward", "ss1_quantize_fp8", "ss1_forward_fp8w",
            "ss1_backward", "ss1_backward_select_algo", "ss1_mlp_forward_static", "ss1_forward_fp8",
-           "ss1_forward_ws_query", "ss1_forward_ws")
+           "ss1_forward_ws_query", "ss1_forward_ws",
+           "ss1_layernorm_forward", "ss1_layernorm_backward_query", "ss1_layernorm_backward",
+           "ss1_adapter_forward_query", "ss1_adapter_forward", "ss1_adapter_backward_query", "ss1_adapter_backward",
+           "ss1_adamw_plan", "ss1_adamw_step")
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 
 
@@ -52,6 +55,29 @@ class Layer(ctypes.Structure):
     _fields_ = [("W_c", Tensor), ("hash", ctypes.c_void_p), ("sign", ctypes.c_void_p),
                 ("c", ctypes.c_int32), ("BK", ctypes.c_int32), ("BN", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("A", Tensor), ("B", Tensor), ("row", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("max_rank", ctypes.c_int32)]
+
+
+class Segments(ctypes.Structure):
+    _fields_ = [("offset", ctypes.c_void_p), ("adapter", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWEntry(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32)]
+
+
+class AdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double), ("grad_scale_dev", ctypes.c_void_p),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
 
 
 _LIB = None
@@ -108,6 +134,21 @@ def load():
     lib.ss1_select_algo.argtypes = [tp, tp, i32, i32, i32, ctypes.POINTER(i32)]
     lib.ss1_backward_select_algo.restype = i32
     lib.ss1_backward_select_algo.argtypes = [tp, tp, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    f32, size_p = ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+    ap, sp = ctypes.POINTER(Adapters), ctypes.POINTER(Segments)
+    lib.ss1_layernorm_forward.argtypes = [tp, tp, tp, f32, tp, vp, vp, vp]
+    lib.ss1_layernorm_backward_query.argtypes = [tp, size_p]
+    lib.ss1_layernorm_backward.argtypes = [tp, tp, tp, vp, vp, tp, tp, tp, vp, ctypes.c_size_t, vp]
+    lib.ss1_adapter_forward_query.argtypes = [i64, ap, size_p]
+    lib.ss1_adapter_forward.argtypes = [tp, ap, sp, tp, tp, tp, vp, ctypes.c_size_t, vp]
+    lib.ss1_adapter_backward_query.argtypes = [i64, ap, size_p]
+    lib.ss1_adapter_backward.argtypes = [tp, tp, tp, ap, sp, tp, tp, tp, tp, vp, ctypes.c_size_t, vp]
+    lib.ss1_adamw_plan.argtypes = [vp, i32, ctypes.POINTER(i64), vp]
+    lib.ss1_adamw_step.argtypes = [vp, i32, vp, i64, ctypes.POINTER(AdamWHyper), vp]
+    for name in ("ss1_layernorm_forward", "ss1_layernorm_backward_query", "ss1_layernorm_backward",
+                 "ss1_adapter_forward_query", "ss1_adapter_forward", "ss1_adapter_backward_query",
+                 "ss1_adapter_backward", "ss1_adamw_plan", "ss1_adamw_step"):
+        getattr(lib, name).restype = i32
     _LIB = lib
     return lib
 

@@ -1,6 +1,13 @@
-// AdamW over many tensors in one launch (ss1_adamw_step).  Each work item is
-// a run of kAdamWChunk elements of one tensor; the tensors' addresses come
-// from a table in device memory, so the number of tensors costs nothing.
+// AdamW over many tensors in one launch (ss1_adamw_step).
+//
+// Each work item is a run of kAdamWChunk elements of one tensor; the tensors'
+// addresses come from a table in device memory, so a step over hundreds of
+// small tensors is one launch.  A thread takes 8 consecutive elements at a
+// time (16-byte loads of bf16 and float, 8-byte loads of codes), so the 256
+// elements that share a scale of an 8-bit state are 32 lanes of one wave and
+// their maximum is 5 lane exchanges, with no LDS and no barrier.
+//
+// The step is one pass over the data, bound by HBM.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -11,7 +18,10 @@ namespace ss1 {
 
 namespace {
 
-static_assert(SS1_ADAMW_BLOCK == 256 && kAdamWChunk % SS1_ADAMW_BLOCK == 0, "a block of threads takes a scale block");
+constexpr int kThreads = 256;
+constexpr int kVec = 8;
+static_assert(SS1_ADAMW_BLOCK == 32 * kVec, "32 lanes hold the elements of one scale");
+static_assert(kAdamWChunk % (kThreads * kVec) == 0, "a chunk is whole passes of the block");
 
 // SplitMix64's output for state seed + (counter + 1) golden.
 __device__ __forceinline__ uint64_t random_bits(uint64_t seed, uint64_t counter) {
@@ -21,10 +31,6 @@ __device__ __forceinline__ uint64_t random_bits(uint64_t seed, uint64_t counter)
     return z ^ (z >> 31);
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t code) {
-    return __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(code), 0);
-}
-
 // |q| <= 448 (up to a rounding) as an E4M3 value, up or down with the
 // probability of its distance: adding 16 random bits below the last kept bit
 // and cutting off does that for the normal range (3 mantissa bits: 20 are
@@ -32,103 +38,253 @@ __device__ __forceinline__ float e4m3_value(uint8_t code) {
 __device__ __forceinline__ float e4m3_round(float q, uint32_t u16) {
     const float a = fabsf(q);
     const float high = __uint_as_float((__float_as_uint(a) + (u16 << 4)) & 0xFFF00000u);
-    const float low = floorf(__fadd_rn(a * 512.0f, static_cast<float>(u16) * 0x1p-16f)) * 0x1p-9f;
+    const float low = floorf(a * 512.0f + static_cast<float>(u16) * 0x1p-16f) * 0x1p-9f;
     return copysignf(a < 0x1p-6f ? low : fminf(high, 448.0f), q);
 }
 
-__device__ __forceinline__ uint8_t e4m3_code(float v) {
-    return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFF);
+// Elements [i, i + 8) of a tensor as float32; elements from `n` on are 0.
+__device__ __forceinline__ void load8(const float* p, int64_t i, int n, float (&v)[kVec]) {
+    if (n >= kVec) {
+        const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = j < n ? p[i + j] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t i, int n, float (&v)[kVec]) {
+    if (n >= kVec) {
+        const uint4 r = *reinterpret_cast<const uint4*>(p + i);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = j < n ? __uint_as_float(uint32_t(p[i + j]) << 16) : 0.0f;
+    }
+}
+__device__ __forceinline__ void load8(const uint8_t* p, int64_t i, int n, float (&v)[kVec]) {
+    uint32_t w[2] = {0, 0};
+    if (n >= kVec) {
+        const uint2 r = *reinterpret_cast<const uint2*>(p + i);
+        w[0] = r.x;
+        w[1] = r.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) w[j / 4] |= uint32_t(p[i + j]) << (8 * (j & 3));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        v[4 * h] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w[h]), 0);
+        v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w[h]), 1);
+        v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w[h]), 2);
+        v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w[h]), 3);
+    }
 }
 
-__device__ __forceinline__ float block_max(float v, float* red) {
-    for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+__device__ __forceinline__ void store8(float* p, int64_t i, int n, const float (&v)[kVec]) {
+    if (n >= kVec) {
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) p[i + j] = v[j];
+    }
+}
+// 16-bit patterns of 8 values.
+__device__ __forceinline__ void store8(uint16_t* p, int64_t i, int n, const uint32_t (&h)[kVec]) {
+    if (n >= kVec) {
+        *reinterpret_cast<uint4*>(p + i) =
+            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) p[i + j] = static_cast<uint16_t>(h[j]);
+    }
+}
+// E4M3 codes of 8 values that E4M3 holds exactly.
+__device__ __forceinline__ void store8(uint8_t* p, int64_t i, int n, const float (&v)[kVec]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
+        w[h] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], lo, true));
+    }
+    if (n >= kVec) {
+        *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) p[i + j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j & 3)));
+    }
 }
 
-__global__ __launch_bounds__(256) void adamw_kernel(const ss1_adamw_entry* __restrict__ entries, int count,
-                                                    const int32_t* __restrict__ map, AdamWCoef c) {
-    __shared__ float red[4];
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+// max over the 32 lanes that share a scale (the half wave).
+__device__ __forceinline__ float half_wave_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
+    return v;
+}
+
+// The state's codes of 8 values t >= or < 0 of this lane, and the new scale of
+// their block: scale = max |t| / 448 (1 for a block of zeros), the quotient by
+// IEEE division.  u[j] holds the random bits of element j.
+__device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t i, int n, const float (&t)[kVec],
+                                          const uint32_t (&u)[kVec], bool keep_nonzero) {
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) top = fmaxf(top, fabsf(t[j]));
+    top = half_wave_max(top);
+    const float scale = top > 0.0f ? __fdiv_rn(top, 448.0f) : 1.0f;
+    if (n > 0 && (threadIdx.x & 31) == 0) scales[i / SS1_ADAMW_BLOCK] = scale;
+    float q[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        q[j] = e4m3_round(__fdiv_rn(t[j], scale), u[j]);
+        if (keep_nonzero && t[j] > 0.0f) q[j] = fmaxf(q[j], 0x1p-9f);
+    }
+    store8(codes, i, n, q);
+}
+
+enum class Param { F32, Bf16Master, Bf16 };
+
+// One chunk of a tensor.  Products and sums are rounded one by one (no fused
+// multiply-add): an 8-bit state turns a last bit of difference into another
+// code now and then, and this keeps the codes those of the formula.
+template <Param P, typename G, bool EIGHT>
+__device__ __forceinline__ void adamw_chunk(const ss1_adamw_entry& e, int item, int64_t begin, const AdamWCoef& c,
+                                            float keep, float gs) {
+#pragma clang fp contract(off)
+    const uint64_t stream = static_cast<uint64_t>(item) << 40;
+    const int64_t end = min(begin + kAdamWChunk, e.numel);
+    for (int64_t at = begin; at < end; at += kThreads * kVec) {
+        const int64_t i = at + kVec * threadIdx.x;
+        // elements of this thread; a thread past the end keeps its place in
+        // the exchanges of the wave with zeros
+        const int n = static_cast<int>(max(int64_t(0), min(int64_t(kVec), end - i)));
+        float p[kVec], g[kVec], m[kVec], v[kVec], r[kVec];
+        load8(static_cast<const G*>(e.grad), i, n, g);
+        if constexpr (P == Param::Bf16Master)
+            load8(static_cast<const float*>(e.master), i, n, p);
+        else if constexpr (P == Param::F32)
+            load8(static_cast<const float*>(e.param), i, n, p);
+        else
+            load8(static_cast<const uint16_t*>(e.param), i, n, p);
+        if constexpr (EIGHT) {
+            load8(static_cast<const uint8_t*>(e.m), i, n, m);
+            load8(static_cast<const uint8_t*>(e.v), i, n, v);
+            const float ms = n > 0 ? e.m_scale[i / SS1_ADAMW_BLOCK] : 0.0f;
+            const float vs = n > 0 ? e.v_scale[i / SS1_ADAMW_BLOCK] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                m[j] *= ms;
+                v[j] *= vs;
+                v[j] *= v[j];
+            }
+        } else {
+            load8(static_cast<const float*>(e.m), i, n, m);
+            load8(static_cast<const float*>(e.v), i, n, v);
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            g[j] *= gs;
+            m[j] = c.beta1 * m[j] + c.one_minus_beta1 * g[j];
+            v[j] = c.beta2 * v[j] + c.one_minus_beta2 * g[j] * g[j];
+            r[j] = sqrtf(v[j]);
+            p[j] = p[j] * keep - c.step_size * m[j] / (r[j] * c.inv_sqrt_c2 + c.eps);
+        }
+        if constexpr (EIGHT) {
+            uint32_t um[kVec], uv[kVec];
+#pragma unroll
+            for (int j = 0; j < kVec; j += 2) {
+                const uint64_t z = random_bits(c.seed, stream + static_cast<uint64_t>((i + j) >> 1));
+                um[j] = static_cast<uint32_t>(z) & 0xFFFF;
+                uv[j] = static_cast<uint32_t>(z) >> 16;
+                um[j + 1] = static_cast<uint32_t>(z >> 32) & 0xFFFF;
+                uv[j + 1] = static_cast<uint32_t>(z >> 48);
+            }
+            quantize8(static_cast<uint8_t*>(e.m), e.m_scale, i, n, m, um, false);
+            quantize8(static_cast<uint8_t*>(e.v), e.v_scale, i, n, r, uv, true);
+        } else {
+            store8(static_cast<float*>(e.m), i, n, m);
+            store8(static_cast<float*>(e.v), i, n, v);
+        }
+        if constexpr (P == Param::F32) {
+            store8(static_cast<float*>(e.param), i, n, p);
+        } else {
+            uint32_t h[kVec];
+            if constexpr (P == Param::Bf16Master) {
+                store8(e.master, i, n, p);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) h[j] = bf16_bits(p[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; j += 4) {
+                    const uint64_t z =
+                        random_bits(c.seed, stream + (uint64_t(1) << 39) + static_cast<uint64_t>((i + j) >> 2));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t bits = __float_as_uint(p[j + q]);
+                        // adding to an infinity or a NaN would change what it is
+                        const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
+                        h[j + q] = finite ? (bits + (static_cast<uint32_t>(z >> (16 * q)) & 0xFFFF)) >> 16
+                                          : bf16_bits(p[j + q]);
+                    }
+                }
+            }
+            store8(static_cast<uint16_t*>(e.param), i, n, h);
+        }
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const ss1_adamw_entry* __restrict__ entries, int count,
+                                                         const int32_t* __restrict__ map, AdamWCoef c) {
     const int item = map[2 * static_cast<size_t>(blockIdx.x)];
     const int64_t part = map[2 * static_cast<size_t>(blockIdx.x) + 1];
     if (item < 0 || item >= count || part < 0) return;
     const ss1_adamw_entry e = entries[item];
     const float keep = static_cast<float>(1.0 - c.lr * static_cast<double>(e.weight_decay));
     const float gs = c.grad_scale_dev ? c.grad_scale * *c.grad_scale_dev : c.grad_scale;
-    const bool eight = e.state_dtype == SS1_FP8_E4M3;
-    const uint64_t stream = static_cast<uint64_t>(item) << 40;
-    const int64_t end = min((part + 1) * kAdamWChunk, e.numel);
-    for (int64_t at = part * kAdamWChunk; at < end; at += 256) {
-        const int64_t i = at + threadIdx.x;
-        const bool in = i < end;
-        float g = 0.0f, p = 0.0f, m = 0.0f, v = 0.0f;
-        if (in) {
-            g = e.grad_dtype == SS1_F32 ? static_cast<const float*>(e.grad)[i]
-                                        : static_cast<float>(static_cast<const __bf16*>(e.grad)[i]);
-            p = e.master ? e.master[i]
-                         : e.param_dtype == SS1_F32 ? static_cast<float*>(e.param)[i]
-                                                    : static_cast<float>(static_cast<__bf16*>(e.param)[i]);
-            if (eight) {
-                m = e4m3_value(static_cast<uint8_t*>(e.m)[i]) * e.m_scale[i / SS1_ADAMW_BLOCK];
-                const float r = e4m3_value(static_cast<uint8_t*>(e.v)[i]) * e.v_scale[i / SS1_ADAMW_BLOCK];
-                v = r * r;
-            } else {
-                m = static_cast<float*>(e.m)[i];
-                v = static_cast<float*>(e.v)[i];
-            }
-        }
-        g *= gs;
-        m = c.beta1 * m + c.one_minus_beta1 * g;
-        v = c.beta2 * v + c.one_minus_beta2 * g * g;
-        const float r = sqrtf(v);
-        p = p * keep - c.step_size * m / (r * c.inv_sqrt_c2 + c.eps);
-        if (eight) {
-            // the old scales of this block are read by every thread before
-            // the first barrier of block_max, and written after it
-            const float mt = block_max(fabsf(m), red), rt = block_max(r, red);
-            const float ms = mt > 0.0f ? __fdiv_rn(mt, 448.0f) : 1.0f, rs = rt > 0.0f ? __fdiv_rn(rt, 448.0f) : 1.0f;
-            if (threadIdx.x == 0) {
-                e.m_scale[at / SS1_ADAMW_BLOCK] = ms;
-                e.v_scale[at / SS1_ADAMW_BLOCK] = rs;
-            }
-            if (in) {
-                const uint64_t z = random_bits(c.seed, stream + static_cast<uint64_t>(i >> 1)) >> ((i & 1) * 32);
-                static_cast<uint8_t*>(e.m)[i] = e4m3_code(e4m3_round(__fdiv_rn(m, ms), z & 0xFFFF));
-                float q = e4m3_round(__fdiv_rn(r, rs), (z >> 16) & 0xFFFF);
-                if (r > 0.0f) q = fmaxf(q, 0x1p-9f);
-                static_cast<uint8_t*>(e.v)[i] = e4m3_code(q);
-            }
-        } else if (in) {
-            static_cast<float*>(e.m)[i] = m;
-            static_cast<float*>(e.v)[i] = v;
-        }
-        if (!in) continue;
-        if (e.master) {
-            e.master[i] = p;
-            static_cast<__bf16*>(e.param)[i] = static_cast<__bf16>(p);
-        } else if (e.param_dtype == SS1_F32) {
-            static_cast<float*>(e.param)[i] = p;
-        } else {
-            const uint64_t z = random_bits(c.seed, stream + (uint64_t(1) << 39) + static_cast<uint64_t>(i >> 2)) >>
-                               ((i & 3) * 16);
-            const uint32_t bits = __float_as_uint(p);
-            // adding to an infinity or a NaN would change what it is
-            const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
-            static_cast<uint16_t*>(e.param)[i] =
-                finite ? static_cast<uint16_t>((bits + static_cast<uint32_t>(z & 0xFFFF)) >> 16)
-                       : __builtin_bit_cast(uint16_t, static_cast<__bf16>(p));
-        }
-    }
+    const int64_t begin = part * kAdamWChunk;
+    // one branch a block: every format of a plan in the same launch
+    const bool gf = e.grad_dtype == SS1_F32, eight = e.state_dtype == SS1_FP8_E4M3;
+#define SS1_CHUNK(P)                                                                     \
+    do {                                                                                 \
+        if (gf && eight) adamw_chunk<P, float, true>(e, item, begin, c, keep, gs);       \
+        else if (gf) adamw_chunk<P, float, false>(e, item, begin, c, keep, gs);          \
+        else if (eight) adamw_chunk<P, uint16_t, true>(e, item, begin, c, keep, gs);     \
+        else adamw_chunk<P, uint16_t, false>(e, item, begin, c, keep, gs);               \
+    } while (0)
+    if (e.param_dtype == SS1_F32)
+        SS1_CHUNK(Param::F32);
+    else if (e.master)
+        SS1_CHUNK(Param::Bf16Master);
+    else
+        SS1_CHUNK(Param::Bf16);
+#undef SS1_CHUNK
 }
 
 }  // namespace
 
 ss1_status launch_adamw(const ss1_adamw_entry* entries, int32_t count, const int32_t* map, int64_t chunks,
                         const AdamWCoef& coef, void* stream) {
-    hipLaunchKernelGGL(adamw_kernel, dim3(static_cast<unsigned>(chunks)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), entries, count, map, coef);
+    // the grid's x extent times 256 threads stays under 2^32
+    const int64_t most = int64_t(1) << 23;
+    for (int64_t at = 0; at < chunks; at += most) {
+        const int64_t n = chunks - at < most ? chunks - at : most;
+        hipLaunchKernelGGL(adamw_kernel, dim3(static_cast<unsigned>(n)), dim3(kThreads), 0,
+                           static_cast<hipStream_t>(stream), entries, count, map + 2 * at, coef);
+    }
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 

@@ -4,6 +4,13 @@
 // (x - mean) rstd gamma + beta.  Backward, xh = (x - mean) rstd and
 // g = dy gamma: dx = rstd (g - mean(g) - xh mean(g xh)), and column sums of
 // dy xh (dgamma) and dy (dbeta).
+//
+// Both are one pass over the data, bound by HBM: a row lives in the registers
+// of T threads (NV vectors of 8 elements each) between its loads and its
+// stores.  The backward pass keeps each thread's columns of dgamma and dbeta
+// in registers too while a block walks over its rows, so the column sums cost
+// no second read of dy and x: every block writes one partial row, and a small
+// second launch adds those in order.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -14,136 +21,505 @@ namespace ss1 {
 
 namespace {
 
-__device__ __forceinline__ float load_f(const float* p) { return *p; }
-__device__ __forceinline__ float load_f(const __bf16* p) { return static_cast<float>(*p); }
-__device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_f(__bf16* p, float v) { *p = static_cast<__bf16>(v); }
+constexpr int kVec = 8;
 
-__device__ __forceinline__ float block_sum(float s, float* red) {
-    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-    __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+// 16-byte accesses at the alignment of one element: rows of an odd K start
+// anywhere, and global memory takes dword accesses of any alignment.
+typedef uint32_t u32x4_any2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Elements [0, n) of p as float32, the rest 0; n is kVec unless TAIL.
+template <bool TAIL>
+__device__ __forceinline__ void load8(const float* p, int n, float (&v)[kVec]) {
+    if (!TAIL || n >= kVec) {
+        const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = j < n ? p[j] : 0.0f;
+    }
+}
+template <bool TAIL>
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[kVec]) {
+    if (!TAIL || n >= kVec) {
+        const u32x4_any2 r = *reinterpret_cast<const u32x4_any2*>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(r[j] << 16);
+            v[2 * j + 1] = __uint_as_float(r[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = j < n ? __uint_as_float(uint32_t(p[j]) << 16) : 0.0f;
+    }
 }
 
-// One block of 256 threads per row.
-template <typename T, typename G>
-__global__ __launch_bounds__(256) void layernorm_forward_kernel(const T* __restrict__ x, const G* __restrict__ gamma,
-                                                                const G* __restrict__ beta, T* y,
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void store8(float* p, int n, const float (&v)[kVec]) {
+    if (!TAIL || n >= kVec) {
+        *reinterpret_cast<f32x4_any*>(p) = f32x4_any{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4_any*>(p + 4) = f32x4_any{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) p[j] = v[j];
+    }
+}
+template <bool TAIL>
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[kVec]) {
+    if (!TAIL || n >= kVec) {
+        u32x4_any2 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16;
+        *reinterpret_cast<u32x4_any2*>(p) = r;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < n) p[j] = static_cast<uint16_t>(bf16_bits(v[j]));
+    }
+}
+
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<uint16_t>(bf16_bits(v)); }
+
+// Sums over the T threads of a row (T a multiple of 64; a wave or several).
+// Rows of one wave need no LDS.  With several waves every thread of the block
+// calls this together; `red` holds one float pair a wave and alternates
+// between two halves from call to call, so one barrier a call is enough: a
+// half is written again only after the barrier of the call between.
+template <int T, int BLOCK>
+__device__ __forceinline__ float2 row_sums(float2 s, float2* red, int& phase) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        s.x += __shfl_xor(s.x, off);
+        s.y += __shfl_xor(s.y, off);
+    }
+    if constexpr (T == 64) return s;
+    float2* half = red + phase * (BLOCK / 64);
+    phase ^= 1;
+    if ((threadIdx.x & 63) == 0) half[threadIdx.x / 64] = s;
+    __syncthreads();
+    const int first = threadIdx.x / T * (T / 64);
+    float2 t = half[first];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) {
+        t.x += half[first + w].x;
+        t.y += half[first + w].y;
+    }
+    return t;
+}
+
+// ------------------------------------------------------------------- forward
+// Elements of this thread's vector i of a row; > 0 when it has any.
+__device__ __forceinline__ int count_of(int K, int at) { return min(kVec, K - at); }
+
+// BLOCK / T rows a block, a row in the registers of T threads.
+template <typename X, typename G, int T, int NV, int BLOCK, bool TAIL>
+__global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, const G* __restrict__ gamma,
+                                                                  const G* __restrict__ beta, X* y,
+                                                                  float* __restrict__ mean, float* __restrict__ rstd,
+                                                                  int64_t M, int K, float eps) {
+    __shared__ float2 red[2 * BLOCK / 64];
+    constexpr int ROWS = BLOCK / T;
+    const int t = threadIdx.x % T;
+    int phase = 0;
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * ROWS; m0 < M; m0 += static_cast<int64_t>(gridDim.x) * ROWS) {
+        const int64_t m = m0 + threadIdx.x / T;
+        const bool row = m < M;
+        const size_t base = static_cast<size_t>(m) * K;
+        float v[NV][kVec];
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = (i * T + t) * kVec;
+            const int n = row ? count_of(K, at) : 0;
+            if (n > 0) {
+                load8<TAIL>(x + base + at, n, v[i]);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) s += v[i][j];
+            }
+        }
+        const float mu = row_sums<T, BLOCK>(make_float2(s, 0.0f), red, phase).x / K;
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = (i * T + t) * kVec;
+            const int n = row ? count_of(K, at) : 0;
+            if (n > 0) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    v[i][j] = !TAIL || j < n ? v[i][j] - mu : 0.0f;
+                    q += v[i][j] * v[i][j];
+                }
+            }
+        }
+        const float rs = 1.0f / sqrtf(row_sums<T, BLOCK>(make_float2(q, 0.0f), red, phase).x / K + eps);
+        if (row && t == 0) {
+            if (mean) mean[m] = mu;
+            if (rstd) rstd[m] = rs;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = (i * T + t) * kVec;
+            const int n = row ? count_of(K, at) : 0;
+            if (n > 0) {
+                float w[kVec], b[kVec];
+                load8<TAIL>(gamma + at, n, w);
+                if (beta) load8<TAIL>(beta + at, n, b);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * rs * w[j] + (beta ? b[j] : 0.0f);
+                store8<TAIL>(y + base + at, n, v[i]);
+            }
+        }
+    }
+}
+
+// Rows too long for registers: one block a row, three passes over it (the
+// later ones from cache).
+constexpr int kLong = 512;
+template <typename X, typename G>
+__global__ __launch_bounds__(kLong) void layernorm_forward_long(const X* x, const G* __restrict__ gamma,
+                                                                const G* __restrict__ beta, X* y,
                                                                 float* __restrict__ mean, float* __restrict__ rstd,
-                                                                int K, float eps) {
-    __shared__ float red[4];
-    const size_t base = static_cast<size_t>(blockIdx.x) * K;
-    float s = 0.0f;
-    for (int k = threadIdx.x; k < K; k += 256) s += load_f(x + base + k);
-    const float mu = block_sum(s, red) / K;
-    float q = 0.0f;
-    for (int k = threadIdx.x; k < K; k += 256) {
-        const float d = load_f(x + base + k) - mu;
-        q += d * d;
-    }
-    const float rs = 1.0f / sqrtf(block_sum(q, red) / K + eps);
-    if (threadIdx.x == 0) {
-        if (mean) mean[blockIdx.x] = mu;
-        if (rstd) rstd[blockIdx.x] = rs;
-    }
-    for (int k = threadIdx.x; k < K; k += 256) {
-        const float b = beta ? load_f(beta + k) : 0.0f;
-        store_f(y + base + k, (load_f(x + base + k) - mu) * rs * load_f(gamma + k) + b);
+                                                                int64_t M, int K, float eps) {
+    __shared__ float2 red[2 * kLong / 64];
+    int phase = 0;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        const size_t base = static_cast<size_t>(m) * K;
+        float s = 0.0f;
+        for (int k = threadIdx.x; k < K; k += kLong) s += load1(x + base + k);
+        const float mu = row_sums<kLong, kLong>(make_float2(s, 0.0f), red, phase).x / K;
+        float q = 0.0f;
+        for (int k = threadIdx.x; k < K; k += kLong) {
+            const float d = load1(x + base + k) - mu;
+            q += d * d;
+        }
+        const float rs = 1.0f / sqrtf(row_sums<kLong, kLong>(make_float2(q, 0.0f), red, phase).x / K + eps);
+        if (threadIdx.x == 0) {
+            if (mean) mean[m] = mu;
+            if (rstd) rstd[m] = rs;
+        }
+        for (int k = threadIdx.x; k < K; k += kLong) {
+            const float b = beta ? load1(beta + k) : 0.0f;
+            store1(y + base + k, (load1(x + base + k) - mu) * rs * load1(gamma + k) + b);
+        }
     }
 }
 
-template <typename T, typename G>
-__global__ __launch_bounds__(256) void layernorm_dx_kernel(const T* dy, const T* __restrict__ x,
+// ------------------------------------------------------------------ backward
+// Block b takes rows b * ROWS + r, stepping by the grid; each thread keeps the
+// sums of dy xh and dy over its rows for its columns, the block joins its row
+// groups in LDS, group by group, and writes partial[b][0 or 1][k].
+template <typename X, typename G, int T, int NV, int BLOCK, bool TAIL>
+__global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, const X* __restrict__ x,
+                                                                   const G* __restrict__ gamma,
+                                                                   const float* __restrict__ mean,
+                                                                   const float* __restrict__ rstd, X* dx,
+                                                                   float* __restrict__ partial, int64_t M, int K) {
+    constexpr int ROWS = BLOCK / T;
+    __shared__ float2 red[2 * BLOCK / 64];
+    __shared__ float2 join[ROWS > 1 ? T * NV * kVec : 1];
+    const int t = threadIdx.x % T, group = threadIdx.x / T;
+    int phase = 0;
+    float2 sum[NV][kVec];  // (dgamma, dbeta) of this thread's columns
+    float w[NV][kVec];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int at = (i * T + t) * kVec;
+        const int n = count_of(K, at);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            sum[i][j] = make_float2(0.0f, 0.0f);
+            w[i][j] = 0.0f;
+        }
+        if (n > 0) load8<TAIL>(gamma + at, n, w[i]);
+    }
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * ROWS; m0 < M; m0 += static_cast<int64_t>(gridDim.x) * ROWS) {
+        const int64_t m = m0 + group;
+        const bool row = m < M;
+        const size_t base = static_cast<size_t>(m) * K;
+        const float mu = row ? mean[m] : 0.0f, rs = row ? rstd[m] : 0.0f;
+        float xh[NV][kVec], g[NV][kVec];
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = (i * T + t) * kVec;
+            const int n = row ? count_of(K, at) : 0;
+            if (n > 0) {
+                load8<TAIL>(x + base + at, n, xh[i]);
+                load8<TAIL>(dy + base + at, n, g[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int at = (i * T + t) * kVec;
+            const int n = row ? count_of(K, at) : 0;
+            if (n > 0) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    xh[i][j] = !TAIL || j < n ? (xh[i][j] - mu) * rs : 0.0f;
+                    sum[i][j].x += g[i][j] * xh[i][j];
+                    sum[i][j].y += g[i][j];
+                    g[i][j] *= w[i][j];
+                    s.x += g[i][j];
+                    s.y += g[i][j] * xh[i][j];
+                }
+            }
+        }
+        if (dx) {
+            s = row_sums<T, BLOCK>(s, red, phase);
+            const float m1 = s.x / K, m2 = s.y / K;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int at = (i * T + t) * kVec;
+                const int n = row ? count_of(K, at) : 0;
+                if (n > 0) {
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) g[i][j] = rs * (g[i][j] - m1 - xh[i][j] * m2);
+                    store8<TAIL>(dx + base + at, n, g[i]);
+                }
+            }
+        }
+    }
+    if (!partial) return;
+    if constexpr (ROWS > 1) {
+        // join[] is laid out [i][j][t]: consecutive threads, consecutive pairs
+        for (int r = ROWS - 1; r > 0; --r) {
+            if (group == r) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) join[(i * kVec + j) * T + t] = sum[i][j];
+            }
+            __syncthreads();
+            if (group == r - 1) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) {
+                        const float2 o = join[(i * kVec + j) * T + t];
+                        sum[i][j].x += o.x;
+                        sum[i][j].y += o.y;
+                    }
+            }
+            __syncthreads();
+        }
+        if (group != 0) return;
+    }
+    float* out = partial + static_cast<size_t>(blockIdx.x) * 2 * K;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int at = (i * T + t) * kVec;
+        const int n = count_of(K, at);
+        if (n > 0) {
+            float a[kVec], b[kVec];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                a[j] = sum[i][j].x;
+                b[j] = sum[i][j].y;
+            }
+            store8<TAIL>(out + at, n, a);
+            store8<TAIL>(out + K + at, n, b);
+        }
+    }
+}
+
+// Rows too long for registers: dx of one row a block.
+template <typename X, typename G>
+__global__ __launch_bounds__(kLong) void layernorm_dx_long(const X* dy, const X* __restrict__ x,
                                                            const G* __restrict__ gamma,
                                                            const float* __restrict__ mean,
-                                                           const float* __restrict__ rstd, T* dx, int K) {
-    __shared__ float red[4];
-    const size_t base = static_cast<size_t>(blockIdx.x) * K;
-    const float mu = mean[blockIdx.x], rs = rstd[blockIdx.x];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int k = threadIdx.x; k < K; k += 256) {
-        const float g = load_f(dy + base + k) * load_f(gamma + k);
-        s1 += g;
-        s2 += g * ((load_f(x + base + k) - mu) * rs);
-    }
-    s1 = block_sum(s1, red) / K;
-    s2 = block_sum(s2, red) / K;
-    for (int k = threadIdx.x; k < K; k += 256) {
-        const float g = load_f(dy + base + k) * load_f(gamma + k);
-        const float xh = (load_f(x + base + k) - mu) * rs;
-        store_f(dx + base + k, rs * (g - s1 - xh * s2));
+                                                           const float* __restrict__ rstd, X* dx, int64_t M, int K) {
+    __shared__ float2 red[2 * kLong / 64];
+    int phase = 0;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        const size_t base = static_cast<size_t>(m) * K;
+        const float mu = mean[m], rs = rstd[m];
+        float2 s = make_float2(0.0f, 0.0f);
+        for (int k = threadIdx.x; k < K; k += kLong) {
+            const float g = load1(dy + base + k) * load1(gamma + k);
+            s.x += g;
+            s.y += g * ((load1(x + base + k) - mu) * rs);
+        }
+        s = row_sums<kLong, kLong>(s, red, phase);
+        const float m1 = s.x / K, m2 = s.y / K;
+        for (int k = threadIdx.x; k < K; k += kLong) {
+            const float g = load1(dy + base + k) * load1(gamma + k);
+            const float xh = (load1(x + base + k) - mu) * rs;
+            store1(dx + base + k, rs * (g - m1 - xh * m2));
+        }
     }
 }
 
-// Partial column sums of one group of rows: partial[group][0][k] of dy xh,
-// partial[group][1][k] of dy.
-template <typename T>
-__global__ __launch_bounds__(256) void layernorm_columns_kernel(const T* __restrict__ dy, const T* __restrict__ x,
-                                                                const float* __restrict__ mean,
-                                                                const float* __restrict__ rstd,
-                                                                float* __restrict__ partial, int64_t M, int K) {
+// ... and their partial column sums: one thread a column, rows of one group.
+template <typename X>
+__global__ __launch_bounds__(256) void layernorm_columns_long(const X* __restrict__ dy, const X* __restrict__ x,
+                                                              const float* __restrict__ mean,
+                                                              const float* __restrict__ rstd,
+                                                              float* __restrict__ partial, int64_t M, int K) {
     const int k = blockIdx.x * 256 + threadIdx.x;
     if (k >= K) return;
     float dg = 0.0f, db = 0.0f;
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
         const size_t at = static_cast<size_t>(m) * K + k;
-        const float d = load_f(dy + at);
-        dg += d * ((load_f(x + at) - mean[m]) * rstd[m]);
+        const float d = load1(dy + at);
+        dg += d * ((load1(x + at) - mean[m]) * rstd[m]);
         db += d;
     }
-    partial[(static_cast<size_t>(blockIdx.y) * 2) * K + k] = dg;
-    partial[(static_cast<size_t>(blockIdx.y) * 2 + 1) * K + k] = db;
+    float* out = partial + static_cast<size_t>(blockIdx.y) * 2 * K;
+    out[k] = dg;
+    out[K + k] = db;
 }
 
-// The groups' sums joined in order.
+// The partial rows joined in a fixed order: a block takes 32 columns of the
+// [groups][2 K] matrix, thread (c, r) the rows r, r + 8, ...
 template <typename G>
 __global__ __launch_bounds__(256) void layernorm_join_kernel(const float* __restrict__ partial, G* __restrict__ dgamma,
                                                              G* __restrict__ dbeta, int groups, int K) {
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    if (k >= K) return;
-    float dg = 0.0f, db = 0.0f;
-    for (int p = 0; p < groups; ++p) {
-        dg += partial[(static_cast<size_t>(p) * 2) * K + k];
-        db += partial[(static_cast<size_t>(p) * 2 + 1) * K + k];
+    __shared__ float part[8][32];
+    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int64_t wide = 2 * static_cast<int64_t>(K);
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 + c;
+    float s = 0.0f;
+    if (at < wide) {
+#pragma unroll 16
+        for (int p = r; p < groups; p += 8) s += partial[p * wide + at];
     }
-    if (dgamma) store_f(dgamma + k, dg);
-    if (dbeta) store_f(dbeta + k, db);
+    part[r][c] = s;
+    __syncthreads();
+    if (r == 0 && at < wide) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][c];
+        if (at < K) {
+            if (dgamma) store1(dgamma + at, s);
+        } else if (dbeta) {
+            store1(dbeta + (at - K), s);
+        }
+    }
 }
 
-int row_groups(int64_t M) { return M < 256 ? static_cast<int>(M) : 256; }
+// ------------------------------------------------------------------ launches
+constexpr int64_t kMaxBlocks = int64_t(1) << 20;  // rows beyond that loop
 
-template <typename T, typename G>
+unsigned grid_for(int64_t rows, int64_t most) { return static_cast<unsigned>(rows < most ? rows : most); }
+
+template <typename X, typename G, int T, int NV>
+void forward_rows(const NormArgs& a, hipStream_t s) {
+    constexpr int BLOCK = T < 256 ? 256 : T;
+    const int64_t groups = (a.M + BLOCK / T - 1) / (BLOCK / T);
+    const dim3 grid(grid_for(groups, kMaxBlocks));
+    auto k = a.K % kVec ? layernorm_forward_kernel<X, G, T, NV, BLOCK, true>
+                        : layernorm_forward_kernel<X, G, T, NV, BLOCK, false>;
+    hipLaunchKernelGGL(k, grid, dim3(BLOCK), 0, s, static_cast<const X*>(a.x), static_cast<const G*>(a.gamma),
+                       static_cast<const G*>(a.beta), static_cast<X*>(a.y), a.mean, a.rstd, a.M, a.K, a.eps);
+}
+
+// Threads a row: one wave up to 1024 elements (no barrier), then 256, then
+// 1024; the smallest number of vectors that holds the row.
+template <typename X, typename G>
 void forward(const NormArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((layernorm_forward_kernel<T, G>), dim3(static_cast<unsigned>(a.M)), dim3(256), 0, s,
-                       static_cast<const T*>(a.x), static_cast<const G*>(a.gamma), static_cast<const G*>(a.beta),
-                       static_cast<T*>(a.y), a.mean, a.rstd, a.K, a.eps);
+    const int vecs = (a.K + kVec - 1) / kVec;
+    if (vecs <= 64) return forward_rows<X, G, 64, 1>(a, s);
+    if (vecs <= 128) return forward_rows<X, G, 64, 2>(a, s);
+    if (vecs <= 256) return forward_rows<X, G, 256, 1>(a, s);
+    if (vecs <= 512) return forward_rows<X, G, 256, 2>(a, s);
+    if (vecs <= 1024) return forward_rows<X, G, 256, 4>(a, s);
+    if (vecs <= 2048) return forward_rows<X, G, 1024, 2>(a, s);
+    if (vecs <= 4096) return forward_rows<X, G, 1024, 4>(a, s);
+    hipLaunchKernelGGL((layernorm_forward_long<X, G>), dim3(grid_for(a.M, kMaxBlocks)), dim3(kLong), 0, s,
+                       static_cast<const X*>(a.x), static_cast<const G*>(a.gamma), static_cast<const G*>(a.beta),
+                       static_cast<X*>(a.y), a.mean, a.rstd, a.M, a.K, a.eps);
 }
 
-template <typename T, typename G>
-void backward(const NormArgs& a, hipStream_t s) {
-    const unsigned kb = static_cast<unsigned>((a.K + 255) / 256);
-    const int groups = row_groups(a.M);
-    // the column sums first: dx may be dy itself
-    if (a.dgamma || a.dbeta) {
-        if (groups > 0)
-            hipLaunchKernelGGL((layernorm_columns_kernel<T>), dim3(kb, static_cast<unsigned>(groups)), dim3(256), 0, s,
-                               static_cast<const T*>(a.dy), static_cast<const T*>(a.x), a.mean_in, a.rstd_in,
-                               a.partial, a.M, a.K);
-        hipLaunchKernelGGL((layernorm_join_kernel<G>), dim3(kb), dim3(256), 0, s, a.partial,
-                           static_cast<G*>(a.dgamma), static_cast<G*>(a.dbeta), groups, a.K);
+// How the backward pass splits the rows.
+struct Split {
+    int T;       // threads a row, 0: too long for registers
+    int block;   // threads a block
+    int groups;  // blocks, and partial rows
+};
+
+constexpr int kGroups = 256;  // one block a compute unit
+
+Split split_of(int64_t M, int32_t K) {
+    const int vecs = (K + kVec - 1) / kVec;
+    Split p;
+    p.T = vecs <= 128 ? 64 : vecs <= 512 ? 256 : vecs <= 2048 ? 1024 : 0;
+    if (p.T == 0) {
+        p.block = kLong;
+        p.groups = static_cast<int>(M < kGroups ? M : kGroups);
+        return p;
     }
-    if (a.dx && a.M > 0)
-        hipLaunchKernelGGL((layernorm_dx_kernel<T, G>), dim3(static_cast<unsigned>(a.M)), dim3(256), 0, s,
-                           static_cast<const T*>(a.dy), static_cast<const T*>(a.x), static_cast<const G*>(a.gamma),
-                           a.mean_in, a.rstd_in, static_cast<T*>(a.dx), a.K);
+    // small row counts take small blocks, so that they still spread out
+    p.block = p.T == 1024 || M >= int64_t(kGroups) * (1024 / p.T) ? 1024 : 256;
+    const int64_t need = (M + p.block / p.T - 1) / (p.block / p.T);
+    p.groups = static_cast<int>(need < kGroups ? need : kGroups);
+    return p;
+}
+
+template <typename X, typename G, int T, int NV, int BLOCK>
+void backward_rows(const NormArgs& a, int groups, float* partial, hipStream_t s) {
+    auto k = a.K % kVec ? layernorm_backward_kernel<X, G, T, NV, BLOCK, true>
+                        : layernorm_backward_kernel<X, G, T, NV, BLOCK, false>;
+    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(groups)), dim3(BLOCK), 0, s, static_cast<const X*>(a.dy),
+                       static_cast<const X*>(a.x), static_cast<const G*>(a.gamma), a.mean_in, a.rstd_in,
+                       static_cast<X*>(a.dx), partial, a.M, a.K);
+}
+
+template <typename X, typename G>
+void backward(const NormArgs& a, hipStream_t s) {
+    const Split p = split_of(a.M, a.K);
+    const bool sums = a.dgamma || a.dbeta;
+    float* partial = sums ? a.partial : nullptr;
+    if (a.M > 0 && p.T == 0) {
+        // the column sums first: dx may be dy itself
+        if (sums)
+            hipLaunchKernelGGL((layernorm_columns_long<X>),
+                               dim3(static_cast<unsigned>((a.K + 255) / 256), static_cast<unsigned>(p.groups)),
+                               dim3(256), 0, s, static_cast<const X*>(a.dy), static_cast<const X*>(a.x), a.mean_in,
+                               a.rstd_in, partial, a.M, a.K);
+        if (a.dx)
+            hipLaunchKernelGGL((layernorm_dx_long<X, G>), dim3(grid_for(a.M, kMaxBlocks)), dim3(kLong), 0, s,
+                               static_cast<const X*>(a.dy), static_cast<const X*>(a.x),
+                               static_cast<const G*>(a.gamma), a.mean_in, a.rstd_in, static_cast<X*>(a.dx), a.M, a.K);
+    } else if (a.M > 0) {
+        const int vecs = (a.K + kVec - 1) / kVec;
+        if (p.T == 64 && vecs <= 64)
+            p.block == 256 ? backward_rows<X, G, 64, 1, 256>(a, p.groups, partial, s)
+                           : backward_rows<X, G, 64, 1, 1024>(a, p.groups, partial, s);
+        else if (p.T == 64)
+            p.block == 256 ? backward_rows<X, G, 64, 2, 256>(a, p.groups, partial, s)
+                           : backward_rows<X, G, 64, 2, 1024>(a, p.groups, partial, s);
+        else if (p.T == 256 && vecs <= 256)
+            p.block == 256 ? backward_rows<X, G, 256, 1, 256>(a, p.groups, partial, s)
+                           : backward_rows<X, G, 256, 1, 1024>(a, p.groups, partial, s);
+        else if (p.T == 256)
+            p.block == 256 ? backward_rows<X, G, 256, 2, 256>(a, p.groups, partial, s)
+                           : backward_rows<X, G, 256, 2, 1024>(a, p.groups, partial, s);
+        else if (vecs <= 1024)
+            backward_rows<X, G, 1024, 1, 1024>(a, p.groups, partial, s);
+        else
+            backward_rows<X, G, 1024, 2, 1024>(a, p.groups, partial, s);
+    }
+    if (sums)
+        hipLaunchKernelGGL((layernorm_join_kernel<G>), dim3(static_cast<unsigned>((2 * int64_t(a.K) + 31) / 32)),
+                           dim3(256), 0, s, partial, static_cast<G*>(a.dgamma), static_cast<G*>(a.dbeta), p.groups,
+                           a.K);
 }
 
 }  // namespace
 
 size_t layernorm_backward_workspace(int64_t M, int32_t K) {
-    return static_cast<size_t>(row_groups(M)) * 2 * static_cast<size_t>(K) * sizeof(float);
+    return static_cast<size_t>(split_of(M, K).groups) * 2 * static_cast<size_t>(K) * sizeof(float);
 }
 
 ss1_status launch_layernorm_forward(const NormArgs& a) {
@@ -151,9 +527,9 @@ ss1_status launch_layernorm_forward(const NormArgs& a) {
     if (a.dtype == SS1_F32)
         forward<float, float>(a, s);
     else if (a.affine_dtype == SS1_F32)
-        forward<__bf16, float>(a, s);
+        forward<uint16_t, float>(a, s);
     else
-        forward<__bf16, __bf16>(a, s);
+        forward<uint16_t, uint16_t>(a, s);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
@@ -162,9 +538,9 @@ ss1_status launch_layernorm_backward(const NormArgs& a) {
     if (a.dtype == SS1_F32)
         backward<float, float>(a, s);
     else if (a.affine_dtype == SS1_F32)
-        backward<__bf16, float>(a, s);
+        backward<uint16_t, float>(a, s);
     else
-        backward<__bf16, __bf16>(a, s);
+        backward<uint16_t, uint16_t>(a, s);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 

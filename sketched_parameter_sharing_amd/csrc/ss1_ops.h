@@ -73,7 +73,7 @@ ss1_status launch_adapter_forward(const AdapterArgs& a);
 ss1_status launch_adapter_backward(const AdapterArgs& a);
 
 // Elements of one work item of the AdamW step (a multiple of SS1_ADAMW_BLOCK).
-constexpr int64_t kAdamWChunk = 4096;
+constexpr int64_t kAdamWChunk = 2048;
 
 // The step's coefficients, rounded once from the caller's doubles.
 struct AdamWCoef {

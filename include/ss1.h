@@ -603,7 +603,7 @@ typedef struct {
  * Arithmetic: products of the inputs accumulated in float32; v stays float32
  * between the two products (bf16: as the sum of two bf16 values, an error of
  * at most 2^-17 of v); y rounded once.  Equal calls give equal bits.
- * Requirements: K and N multiples of 8 (BF16) or 4 (F32), below 2^24;
+ * Requirements: K and N multiples of 8 (BF16) or 4 (F32), below 2^22;
  * M < 2^31; x, A, B, base, y, v 16-byte aligned, index and scale arrays
  * 4-byte aligned.  M == 0 enqueues nothing; R == 0 (no adapter rows) and
  * segments.count == 0 leave y = base.

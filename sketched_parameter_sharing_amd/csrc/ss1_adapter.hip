@@ -1,33 +1,47 @@
 // Low-rank adapters of many requests beside a shared projection
-// (ss1_adapter_forward, _backward).  With both factors stored rank-major the
-// two directions are the same three products: the shrink v = x A^T (and
-// dv = dy B^T), the expand y = base + s v B (and dx = dx_base + dv A), and
-// the outer product dA = dv^T x (and dB = s v^T dy).
+// (ss1_adapter_forward, _backward).
+//
+// With both factors stored rank-major the two directions are the same three
+// products:
+//   shrink  v[m][j]  = sum_k x[m][k] A[j][k]           (and dv from dy and B)
+//   expand  y[m][n]  = base[m][n] + sum_j v[m][j] B[j][n]   (and dx from dv and A)
+//   outer   dA[j][k] = sum_m dv[m][j] x[m][k]          (and dB from v and dy)
+// All run on 16x16 matrix tiles with float32 accumulators.  bf16: 16x16x32
+// MFMAs; v stays float32 in memory and enters the second product as the sum
+// of two bf16 values (an error of 2^-17 of v), so that it costs no precision
+// beside the last rounding.  float32: 16x16x4 MFMAs (exact products).
+//
+// The tokens are cut into pieces that lie in one segment and in one tile of
+// TM tokens; a block takes a piece.  Every array is read through a buffer
+// descriptor that ends with its piece or adapter: rows past the end read as
+// zero and stores past it are dropped, so ragged lengths and ranks cost no
+// branch, and nothing of another request can enter a sum.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
 
+#include "ss1_device.h"
 #include "ss1_ops.h"
 
 namespace ss1 {
 
 namespace {
 
-__device__ __forceinline__ float load_f(const float* p) { return *p; }
-__device__ __forceinline__ float load_f(const __bf16* p) { return static_cast<float>(*p); }
-__device__ __forceinline__ void store_f(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_f(__bf16* p, float v) { *p = static_cast<__bf16>(v); }
+using dev::bf16x8;
+using dev::buf_load16;
+using dev::f32x4;
+using dev::make_rsrc;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;  // items beyond that loop
+constexpr uint32_t kOutside = 0x80000000u;        // past every descriptor (2^31 bytes at most)
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// Largest i in [0, n) with a[i] <= t, for ascending a; -1 when there is none.
-__device__ __forceinline__ int last_at_most(const int32_t* a, int n, int t) {
-    int lo = -1, hi = n;
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (a[mid] <= t) lo = mid; else hi = mid;
-    }
-    return lo;
+__device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint4 v) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.x, v.y, v.z, v.w}, r, voff, 0, 0);
 }
 
 // First row and rank of adapter e, inside [0, R) whatever the arrays hold.
@@ -37,115 +51,795 @@ __device__ __forceinline__ int rows_of(const AdapterView& ad, int e, int* first)
     return min(r1 - r0, ad.max_rank);
 }
 
-// The adapter of a token, or -1.
-__device__ __forceinline__ int adapter_of(const AdapterView& ad, int m) {
-    if (ad.E == 0) return -1;
-    const int s = last_at_most(ad.seg, ad.S + 1, m);
-    if (s < 0 || s >= ad.S) return -1;
-    const int e = ad.seg_adapter[s];
-    return e >= 0 && e < ad.E ? e : -1;
-}
+struct Piece {
+    int begin, n;     // tokens
+    int first, rank;  // adapter rows; rank 0: no adapter
+    float scale;
+};
 
-// One wave per (token, rank row): v[m][j] = x[m] . A[row + j].
-template <typename T>
-__global__ __launch_bounds__(64) void shrink_kernel(AdapterView ad, const T* __restrict__ x, const T* __restrict__ A,
-                                                    float* __restrict__ v, int K, int scaled) {
-    const int m = blockIdx.x, j = blockIdx.y;
-    const int e = adapter_of(ad, m);
-    int first = 0;
-    const int rank = e < 0 ? 0 : rows_of(ad, e, &first);
-    float s = 0.0f;
-    if (j < rank) {
-        const size_t xb = static_cast<size_t>(m) * K, ab = static_cast<size_t>(first + j) * K;
-        for (int k = threadIdx.x; k < K; k += 64) s += load_f(x + xb + k) * load_f(A + ab + k);
-        for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-        if (scaled) s *= ad.scale[e];
-    }
-    if (threadIdx.x == 0) v[static_cast<size_t>(m) * ad.max_rank + j] = s;
-}
-
-// One thread per output: y[m][n] = base[m][n] + s sum_j v[m][j] B[row + j][n].
-template <typename T>
-__global__ __launch_bounds__(256) void expand_kernel(AdapterView ad, const float* __restrict__ v,
-                                                     const T* __restrict__ B, const T* base, T* y, int N,
-                                                     int scaled) {
-    const int m = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x;
-    if (n >= N) return;
-    const int e = adapter_of(ad, m);
-    int first = 0;
-    const int rank = e < 0 ? 0 : rows_of(ad, e, &first);
-    float s = 0.0f;
-    for (int j = 0; j < rank; ++j)
-        s += v[static_cast<size_t>(m) * ad.max_rank + j] * load_f(B + static_cast<size_t>(first + j) * N + n);
-    if (scaled && e >= 0) s *= ad.scale[e];
-    const size_t at = static_cast<size_t>(m) * N + n;
-    store_f(y + at, (base ? load_f(base + at) : 0.0f) + s);
-}
-
-// One thread per output: dA[r][k] = sum over the tokens of r's adapter of
-// v[m][r - first] x[m][k].
-template <typename T>
-__global__ __launch_bounds__(256) void outer_kernel(AdapterView ad, const float* __restrict__ v,
-                                                    const T* __restrict__ x, T* __restrict__ dA, int K, int scaled) {
-    const int r = blockIdx.x, k = blockIdx.y * 256 + threadIdx.x;
-    if (k >= K) return;
-    float s = 0.0f;
-    const int e = ad.E > 0 ? last_at_most(ad.row, ad.E + 1, r) : -1;
-    if (e >= 0 && e < ad.E) {
-        int first = 0;
-        const int rank = rows_of(ad, e, &first);
-        if (r - first < rank) {
-            for (int i = 0; i < ad.S; ++i) {
-                if (ad.seg_adapter[i] != e) continue;
-                const int b = clampi(ad.seg[i], 0, ad.M), t = clampi(ad.seg[i + 1], b, ad.M);
-                for (int m = b; m < t; ++m)
-                    s += v[static_cast<size_t>(m) * ad.max_rank + (r - first)] *
-                         load_f(x + static_cast<size_t>(m) * K + k);
+// Piece p of the batch: with F(s) = s + offset[s] / TM, segment s has pieces
+// F(s) .. F(s+1) - 1, one for each tile of TM tokens that it touches (the last
+// may be empty), so no prefix sum over the segments is needed.  Every thread
+// of the block calls this; `sh` is 4 ints of LDS.
+__device__ __forceinline__ Piece find_piece(const AdapterView& ad, int TM, int p, int* sh) {
+    Piece out{0, 0, 0, 0, 0.0f};
+    int s = -1, b = 0, t = ad.M;
+    if (ad.S > 0) {
+        __syncthreads();
+        if (threadIdx.x == 0) sh[0] = -1;
+        __syncthreads();
+        for (int i = threadIdx.x; i < ad.S; i += kThreads) {
+            const int lo = clampi(ad.seg[i], 0, ad.M), hi = clampi(ad.seg[i + 1], lo, ad.M);
+            if (p >= i + lo / TM && p <= i + hi / TM) {
+                sh[0] = i;
+                sh[1] = lo;
+                sh[2] = hi;
             }
-            if (scaled) s *= ad.scale[e];
+        }
+        __syncthreads();
+        s = __builtin_amdgcn_readfirstlane(sh[0]);
+        if (s < 0) return out;
+        b = __builtin_amdgcn_readfirstlane(sh[1]);
+        t = __builtin_amdgcn_readfirstlane(sh[2]);
+    }
+    const int64_t tile = static_cast<int64_t>(p) - (s < 0 ? 0 : s);
+    out.begin = static_cast<int>(max(int64_t(b), tile * TM));
+    out.n = static_cast<int>(min(int64_t(t), (tile + 1) * TM)) - out.begin;
+    if (out.n <= 0 || out.n > TM) {  // empty, or offsets out of order
+        out.n = 0;
+        return out;
+    }
+    if (s >= 0 && ad.E > 0) {
+        const int e = ad.seg_adapter[s];
+        if (e >= 0 && e < ad.E) {
+            out.rank = rows_of(ad, e, &out.first);
+            out.scale = ad.scale[e];
         }
     }
-    store_f(dA + static_cast<size_t>(r) * K + k, s);
+    return out;
+}
+
+int64_t pieces_of(int64_t M, int64_t S, int TM) { return M / TM + (S > 0 ? S : 1); }
+
+// ------------------------------------------------------------ matrix operands
+// An operand lane holds 16 bytes of one row of a [rows][k] matrix: 8 bf16 of
+// 32 k, or 4 floats of 16 k (four 16x16x4 products, the i-th of the floats i).
+__device__ __forceinline__ f32x4 mma(const __bf16*, uint4 a, uint4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const float*, uint4 a, uint4 b, f32x4 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], c, 0, 0, 0);
+    return c;
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+
+// v as hi + lo, two bf16 values (lo 0 where hi is infinite or NaN).
+__device__ __forceinline__ void split(float v, uint32_t* hi, uint32_t* lo) {
+    *hi = bf16_bits(v);
+    const float h = __uint_as_float(*hi << 16);
+    *lo = (*hi & 0x7F80u) == 0x7F80u ? 0u : bf16_bits(v - h);
+}
+
+// Eight rows of 8 bf16 columns -> for each column its 8 rows (an operand).
+__device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t a = (&r[2 * q].x)[d], b = (&r[2 * q + 1].x)[d];
+            lo[q] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            hi[q] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        }
+        f[2 * d] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        f[2 * d + 1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+}
+
+// ---------------------------------------------------------------------- shrink
+// One block: a piece and a slice q of K; its waves split the slice, their
+// tiles are added in LDS.  A wave's operands come straight from global memory,
+// 64 bytes of 16 rows at a time.  part[q][m][max_rank].
+template <typename T, int TT, int RT>
+__device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,
+                                            int max_rank, float scale, f32x4* red) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, g = lane >> 4;
+    const uint32_t Kb = static_cast<uint32_t>(K) * sizeof(T);
+    const int units = static_cast<int>((Kb + 63) / 64);
+    const int u0 = static_cast<int>(static_cast<int64_t>(units) * (q * kWaves + wave) / (Q * kWaves));
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (q * kWaves + wave + 1) / (Q * kWaves));
+    const auto rx = make_rsrc(x + static_cast<size_t>(pc.begin) * K, static_cast<uint32_t>(pc.n) * Kb);
+    const auto ra = make_rsrc(A + static_cast<size_t>(pc.first) * K, static_cast<uint32_t>(pc.rank) * Kb);
+    f32x4 acc[TT][RT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0, 0, 0, 0};
+    const uint32_t lane_off = row * Kb + 16 * g;
+#pragma unroll 4
+    for (int u = u0; u < u1; ++u) {
+        const uint32_t at = 64u * u;
+        const uint32_t off = at + 16 * g < Kb ? lane_off + at : kOutside;
+        uint4 xf[TT], af[RT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) xf[t] = buf_load16(rx, off + t * 16 * Kb, 0);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) af[r] = buf_load16(ra, off + r * 16 * Kb, 0);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[t][r] = mma(x, xf[t], af[r], acc[t][r]);
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RT; ++r) red[(wave * RT + r) * 64 + lane] = acc[t][r];
+        __syncthreads();
+        for (int i = threadIdx.x; i < RT * 64; i += kThreads) {
+            f32x4 s = red[i];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) s += red[w * RT * 64 + i];
+            const int j = 16 * (i >> 6) + (i & 15), m = 16 * t + 4 * ((i >> 4) & 3);
+            if (j < max_rank)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (m + k < pc.n) out[static_cast<size_t>(m + k) * max_rank + j] = s[k] * scale;
+        }
+    }
+    const int rest = max_rank - 16 * RT;  // columns past the tiles are zero
+    if (rest > 0)
+        for (int i = threadIdx.x; i < pc.n * rest; i += kThreads)
+            out[static_cast<size_t>(i / rest) * max_rank + 16 * RT + i % rest] = 0.0f;
+}
+
+template <typename T, int TT, int RT>
+__global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const T* __restrict__ x,
+                                                          const T* __restrict__ A, float* __restrict__ part, int K,
+                                                          int Q, int scaled, int64_t items) {
+    __shared__ f32x4 red[kWaves * RT * 64];
+    __shared__ int sh[4];
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int q = static_cast<int>(item % Q);
+        const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q), sh);
+        if (pc.n == 0) continue;
+        float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * ad.max_rank;
+        const float scale = scaled ? pc.scale : 1.0f;
+        if (pc.rank == 0) {
+            for (int i = threadIdx.x; i < pc.n * ad.max_rank; i += kThreads) out[i] = 0.0f;
+            continue;
+        }
+        // tiles for the rank of this adapter, not for the largest
+        if (RT == 1 || pc.rank <= 16)
+            shrink_body<T, TT, 1>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+        else if (RT == 2 || pc.rank <= 32)
+            shrink_body<T, TT, RT < 2 ? RT : 2>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+        else if (RT == 4 || pc.rank <= 64)
+            shrink_body<T, TT, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+        else
+            shrink_body<T, TT, RT>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+    }
+}
+
+// ---------------------------------------------------------------------- expand
+// One block: a piece and `per` column tiles (kWaves * 16 vectors of 16 bytes
+// each).  The piece's v (its Q partial sums added) goes to LDS in the order of
+// the operands; each wave takes 16 vectors of columns, keeps them of B in
+// registers and walks over the piece's tokens.
+// Rank units: 32 (bf16: one product each of hi and lo) or 16 (float32).
+template <typename T>
+struct Unit;
+template <>
+struct Unit<__bf16> {
+    static constexpr int kRanks = 32, kLoads = 8, kCols = 8, kFrags = 2;
+};
+template <>
+struct Unit<float> {
+    static constexpr int kRanks = 16, kLoads = 4, kCols = 4, kFrags = 1;
+};
+
+// v of 16 tokens and one rank unit as operands in LDS: frag[h][lane] (hi, lo),
+// or for float32 frag[lane] with float i = rank 4 i + g.
+__device__ __forceinline__ void stage_one(const __bf16*, uint4* frag, int m, int g, const float (&v)[8]) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(v[j], &hi[j], &lo[j]);
+    frag[m + 16 * g] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+    frag[64 + m + 16 * g] =
+        make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+}
+__device__ __forceinline__ void stage_one(const float*, uint4* frag, int m, int g, const float (&v)[4]) {
+    frag[m + 16 * g] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                  __float_as_uint(v[3]));
+}
+
+// Columns of B of one rank unit: bf16, column j of this lane's eight, rows
+// 8 g + i; float32, column j of four, rows 4 i + g.
+__device__ __forceinline__ void load_columns(const __bf16*, __amdgpu_buffer_rsrc_t r, uint32_t unit, int g,
+                                             uint32_t Nb, uint32_t col, uint4 (&f)[8]) {
+    uint4 t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = buf_load16(r, col == kOutside ? kOutside : (unit * 32 + 8 * g + i) * Nb + col, 0);
+    transpose8(t, f);
+}
+__device__ __forceinline__ void load_columns(const float*, __amdgpu_buffer_rsrc_t r, uint32_t unit, int g, uint32_t Nb,
+                                             uint32_t col, uint4 (&f)[4]) {
+    uint4 t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = buf_load16(r, col == kOutside ? kOutside : (unit * 16 + 4 * i + g) * Nb + col, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = make_uint4((&t[0].x)[j], (&t[1].x)[j], (&t[2].x)[j], (&t[3].x)[j]);
+}
+
+// 16 bytes of a row of base into element i of the column accumulators, and back.
+__device__ __forceinline__ void unpack(const __bf16*, uint4 w, int i, f32x4 (&acc)[8]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        acc[2 * d][i] = __uint_as_float((&w.x)[d] << 16);
+        acc[2 * d + 1][i] = __uint_as_float((&w.x)[d] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const float*, uint4 w, int i, f32x4 (&acc)[4]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) acc[d][i] = __uint_as_float((&w.x)[d]);
+}
+__device__ __forceinline__ uint4 pack(const __bf16*, const f32x4 (&acc)[8], int i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] = bf16_bits(acc[2 * d][i]) | bf16_bits(acc[2 * d + 1][i]) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const float*, const f32x4 (&acc)[4], int i) {
+    return make_uint4(__float_as_uint(acc[0][i]), __float_as_uint(acc[1][i]), __float_as_uint(acc[2][i]),
+                      __float_as_uint(acc[3][i]));
+}
+
+template <typename T, int TT, int KU>
+__device__ __forceinline__ void expand_body(const Piece& pc, const float* part, size_t slice, int Q, int max_rank,
+                                            const T* B, const T* base, T* y, float* v_out, int N, int tile0,
+                                            int tiles, float scale, uint4* frags) {
+    using U = Unit<T>;
+    constexpr int GROUP = U::kRanks / 4;  // ranks of one operand lane
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    // v of the piece, summed over the slices of K in order
+    for (int i = threadIdx.x; i < 16 * TT * KU * 4; i += kThreads) {
+        const int m = i / (KU * 4), unit = i % (KU * 4) / 4, gi = i % 4;
+        float v[GROUP];
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+            const int r = unit * U::kRanks + (sizeof(T) == 2 ? gi * 8 + j : j * 4 + gi);
+            float s = 0.0f;
+            if (m < pc.n && r < pc.rank) {
+                const float* at = part + static_cast<size_t>(pc.begin + m) * max_rank + r;
+                for (int q = 0; q < Q; ++q) s += at[q * slice];
+                if (v_out) v_out[static_cast<size_t>(pc.begin + m) * max_rank + r] = s;
+            }
+            v[j] = s * scale;
+        }
+        stage_one(B, frags + ((m >> 4) * KU + unit) * U::kFrags * 64, m & 15, gi, v);
+    }
+    if (v_out)  // zero columns past the rank
+        for (int i = threadIdx.x; i < pc.n * (max_rank - pc.rank); i += kThreads)
+            v_out[static_cast<size_t>(pc.begin + i / (max_rank - pc.rank)) * max_rank + pc.rank +
+                  i % (max_rank - pc.rank)] = 0.0f;
+    __syncthreads();
+    const uint32_t Nb = static_cast<uint32_t>(N) * sizeof(T);
+    const auto rb = make_rsrc(B + static_cast<size_t>(pc.first) * N, static_cast<uint32_t>(pc.rank) * Nb);
+    const auto ry = make_rsrc(y + static_cast<size_t>(pc.begin) * N, static_cast<uint32_t>(pc.n) * Nb);
+    const auto rs = make_rsrc((base ? base : y) + static_cast<size_t>(pc.begin) * N,
+                              base ? static_cast<uint32_t>(pc.n) * Nb : 0u);
+    for (int tile = tile0; tile < tile0 + tiles; ++tile) {
+        uint32_t col = 16u * (static_cast<uint32_t>(tile) * kThreads / 4 + wave * 16 + c);
+        if (col >= Nb) col = kOutside;
+        uint4 f[KU][U::kCols];
+#pragma unroll
+        for (int k = 0; k < KU; ++k) load_columns(B, rb, k, g, Nb, col, f[k]);
+        // base one tile of 16 tokens ahead
+        uint4 old[2][4];
+        const auto fetch = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                old[t & 1][i] = buf_load16(rs, col == kOutside ? kOutside : (16 * t + 4 * g + i) * Nb + col, 0);
+        };
+        fetch(0);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            if (t + 1 < TT) fetch(t + 1);
+            f32x4 acc[U::kCols];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack(B, old[t & 1][i], i, acc);
+#pragma unroll
+            for (int k = 0; k < KU; ++k)
+#pragma unroll
+                for (int h = 0; h < U::kFrags; ++h) {
+                    const uint4 a = frags[((t * KU + k) * U::kFrags + h) * 64 + lane];
+#pragma unroll
+                    for (int j = 0; j < U::kCols; ++j) acc[j] = mma(B, a, f[k][j], acc[j]);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                buf_store16(ry, col == kOutside ? kOutside : (16 * t + 4 * g + i) * Nb + col, pack(B, acc, i));
+        }
+    }
+}
+
+template <typename T, int TT, int KU>
+__global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, const float* __restrict__ part, int Q,
+                                                          const T* __restrict__ B, const T* base, T* y,
+                                                          float* __restrict__ v_out, int N, int scaled, int columns,
+                                                          int per, int tiles, int64_t items) {
+    __shared__ uint4 frags[TT * KU * Unit<T>::kFrags * 64];
+    __shared__ int sh[4];
+    constexpr int TM = 16 * TT;
+    const size_t slice = static_cast<size_t>(ad.M) * ad.max_rank;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cg = static_cast<int>(item % columns);
+        const Piece pc = find_piece(ad, TM, static_cast<int>(item / columns), sh);
+        if (pc.n == 0) continue;
+        const int tile0 = cg * per, count = min(per, tiles - tile0);
+        float* vo = cg == 0 ? v_out : nullptr;
+        if (pc.rank == 0) {
+            if (vo)
+                for (int i = threadIdx.x; i < pc.n * ad.max_rank; i += kThreads)
+                    vo[static_cast<size_t>(pc.begin) * ad.max_rank + i] = 0.0f;
+            if (base == y) continue;
+            // a copy of the block's columns (zeros without a base)
+            const uint32_t Nb = static_cast<uint32_t>(N) * sizeof(T);
+            const uint32_t c0 = static_cast<uint32_t>(tile0) * kThreads / 4, c1 = min((tile0 + count) * kThreads / 4u, Nb / 16);
+            const int wide = static_cast<int>(c1 - c0);
+            const size_t at = static_cast<size_t>(pc.begin) * N;
+            for (int i = threadIdx.x; i < pc.n * wide; i += kThreads) {
+                const size_t o = static_cast<size_t>(i / wide) * (Nb / 16) + c0 + i % wide;
+                reinterpret_cast<uint4*>(y + at)[o] =
+                    base ? reinterpret_cast<const uint4*>(base + at)[o] : make_uint4(0, 0, 0, 0);
+            }
+            continue;
+        }
+        const float scale = scaled ? pc.scale : 1.0f;
+        constexpr int R = Unit<T>::kRanks;
+        if (KU == 1 || pc.rank <= R)
+            expand_body<T, TT, 1>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+        else if (KU == 2 || pc.rank <= 2 * R)
+            expand_body<T, TT, KU < 2 ? KU : 2>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+        else if (KU == 4 || pc.rank <= 4 * R)
+            expand_body<T, TT, KU < 4 ? KU : 4>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+        else
+            expand_body<T, TT, KU>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+    }
+}
+
+// Partial sums joined where no expand does it.
+__global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __restrict__ part, float* __restrict__ out,
+                                                               size_t n, int Q) {
+    for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+         i += static_cast<size_t>(gridDim.x) * kThreads) {
+        float s = part[i];
+        for (int q = 1; q < Q; ++q) s += part[q * n + i];
+        out[i] = s;
+    }
+}
+
+// ----------------------------------------------------------------------- outer
+// dA and dB in one launch.  A block: one adapter, up to 16 RT of its ranks, 16
+// vectors of columns, part z of the tokens.  It lists the adapter's tokens
+// window by window in LDS (they may lie in many segments), its waves take
+// steps of the window in turn, and their tiles are added in LDS at the end.
+struct OuterJob {
+    const float* v;
+    const void* x;
+    void* out;       // the gradient, or
+    float* partial;  // [Z][R][cols] when the tokens are split
+    int cols;
+    int scaled;
+    int64_t first_item;
+};
+
+constexpr int kWindow = 256;  // tokens listed at a time
+
+template <typename T>
+struct Step;
+template <>
+struct Step<__bf16> {
+    static constexpr int kTokens = 32, kRows = 8;
+    static __device__ __forceinline__ int token(int g, int i) { return 8 * g + i; }
+};
+template <>
+struct Step<float> {
+    static constexpr int kTokens = 16, kRows = 4;
+    static __device__ __forceinline__ int token(int g, int i) { return 4 * i + g; }
+};
+
+__device__ __forceinline__ void column_operands(const __bf16*, const uint4 (&t)[8], uint4 (&f)[8]) {
+    transpose8(t, f);
+}
+__device__ __forceinline__ void column_operands(const float*, const uint4 (&t)[4], uint4 (&f)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = make_uint4((&t[0].x)[j], (&t[1].x)[j], (&t[2].x)[j], (&t[3].x)[j]);
+}
+// v of this lane's rank over its tokens as operands; h = 0, 1: hi, lo.
+__device__ __forceinline__ void rank_operands(const __bf16*, const float (&v)[8], uint4 (&f)[2]) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(v[j], &hi[j], &lo[j]);
+    f[0] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+    f[1] = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+}
+__device__ __forceinline__ void rank_operands(const float*, const float (&v)[4], uint4 (&f)[1]) {
+    f[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+template <typename T, int RT>
+__global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, OuterJob job0, OuterJob job1, int rank_groups,
+                                                         int Z, int64_t items) {
+    using U = Unit<T>;
+    using St = Step<T>;
+    __shared__ f32x4 red[2 * RT * U::kCols * 64];
+    __shared__ int tokens[kWindow];
+    __shared__ int ends[kThreads], starts[kThreads], wave_sum[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const OuterJob& job = it >= job1.first_item ? job1 : job0;
+        int64_t item = it - job.first_item;
+        const int z = static_cast<int>(item % Z);
+        item /= Z;
+        const int tiles = (job.cols + 16 * U::kCols - 1) / (16 * U::kCols);
+        const int tile = static_cast<int>(item % tiles);
+        item /= tiles;
+        const int r0 = static_cast<int>(item % rank_groups) * 16 * RT, e = static_cast<int>(item / rank_groups);
+        int first = 0;
+        const int rank = rows_of(ad, e, &first) - r0;
+        if (rank <= 0) continue;
+        first += r0;
+        const int col = (tile * 16 + c) * U::kCols;
+        const bool inside = col < job.cols;
+        const T* x = static_cast<const T*>(job.x) + (inside ? col : 0);
+        f32x4 acc[RT][U::kCols];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < U::kCols; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
+        // the adapter's tokens, 256 segments at a time
+        for (int s0 = 0; s0 < ad.S; s0 += kThreads) {
+            const int s = s0 + threadIdx.x;
+            int b = 0, n = 0;
+            if (s < ad.S && ad.seg_adapter[s] == e) {
+                b = clampi(ad.seg[s], 0, ad.M);
+                n = clampi(ad.seg[s + 1], b, ad.M) - b;
+            }
+            int sum = n;  // inclusive prefix sum over the block
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int o = __shfl_up(sum, off);
+                if (lane >= off) sum += o;
+            }
+            __syncthreads();
+            if (lane == 63) wave_sum[wave] = sum;
+            __syncthreads();
+            int before = 0, total = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                if (w < wave) before += wave_sum[w];
+                total += wave_sum[w];
+            }
+            ends[threadIdx.x] = sum + before;
+            starts[threadIdx.x] = b - (sum + before - n);  // token = starts + place in the list
+            total = __builtin_amdgcn_readfirstlane(total);
+            for (int w0 = z * kWindow; w0 < total; w0 += Z * kWindow) {
+                const int count = min(kWindow, total - w0);
+                __syncthreads();
+                if (threadIdx.x < count) {
+                    const int at = w0 + threadIdx.x;
+                    int lo = 0, hi = kThreads - 1;  // the first segment whose end is past `at`
+                    while (lo < hi) {
+                        const int mid = (lo + hi) / 2;
+                        if (ends[mid] > at) hi = mid; else lo = mid + 1;
+                    }
+                    tokens[threadIdx.x] = starts[lo] + at;
+                }
+                __syncthreads();
+                for (int t0 = wave * St::kTokens; t0 < count; t0 += kWaves * St::kTokens) {
+                    uint4 rows[St::kRows];
+                    float v[RT][St::kRows];
+#pragma unroll
+                    for (int i = 0; i < St::kRows; ++i) {
+                        const int at = t0 + St::token(g, i);
+                        const bool real = at < count;
+                        const int tok = tokens[real ? at : 0];
+                        rows[i] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(tok) * job.cols);
+                        if (!real) rows[i] = make_uint4(0, 0, 0, 0);
+                        const float* vr = job.v + static_cast<size_t>(tok) * ad.max_rank + r0;
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const int j = 16 * r + c;
+                            const float f = vr[j < rank ? j : 0];
+                            v[r][i] = real && j < rank ? f : 0.0f;
+                        }
+                    }
+                    uint4 f[U::kCols];
+                    column_operands(x, rows, f);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        uint4 a[U::kFrags];
+                        rank_operands(x, v[r], a);
+#pragma unroll
+                        for (int h = 0; h < U::kFrags; ++h)
+#pragma unroll
+                            for (int j = 0; j < U::kCols; ++j) acc[r][j] = mma(x, a[h], f[j], acc[r][j]);
+                    }
+                }
+            }
+        }
+        // (wave 0 + wave 2) + (wave 1 + wave 3)
+        constexpr int TILE = RT * U::kCols * 64;
+#pragma unroll
+        for (int half = 2; half > 0; half >>= 1) {
+            __syncthreads();
+            if (wave >= half && wave < 2 * half) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int j = 0; j < U::kCols; ++j)
+                        red[(wave - half) * TILE + (r * U::kCols + j) * 64 + lane] = acc[r][j];
+            }
+            __syncthreads();
+            if (wave < half) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int j = 0; j < U::kCols; ++j) acc[r][j] += red[wave * TILE + (r * U::kCols + j) * 64 + lane];
+            }
+        }
+        if (wave == 0 && inside) {
+            const float scale = job.scaled ? ad.scale[e] : 1.0f;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int j = 0; j < U::kCols; ++j) acc[r][j] *= scale;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 16 * r + 4 * g + i;
+                    if (j >= rank) continue;
+                    const size_t at = static_cast<size_t>(first + j) * job.cols + col;
+                    if (job.partial) {
+                        float* o = job.partial + static_cast<size_t>(z) * ad.R * job.cols + at;
+#pragma unroll
+                        for (int q = 0; q < U::kCols; q += 4)
+                            *reinterpret_cast<float4*>(o + q) =
+                                make_float4(acc[r][q][i], acc[r][q + 1][i], acc[r][q + 2][i], acc[r][q + 3][i]);
+                    } else {
+                        *reinterpret_cast<uint4*>(static_cast<T*>(job.out) + at) = pack(x, acc[r], i);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// The token parts' sums joined in order, four columns a thread.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void join_parts_kernel(const float* __restrict__ partial, T* __restrict__ out,
+                                                              size_t n, int Z) {
+    for (size_t i = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n;
+         i += static_cast<size_t>(gridDim.x) * kThreads * 4) {
+        f32x4 s = *reinterpret_cast<const f32x4*>(partial + i);
+        for (int z = 1; z < Z; ++z) s += *reinterpret_cast<const f32x4*>(partial + z * n + i);
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<f32x4*>(out + i) = s;
+        else
+            *reinterpret_cast<uint2*>(out + i) =
+                make_uint2(bf16_bits(s[0]) | bf16_bits(s[1]) << 16, bf16_bits(s[2]) | bf16_bits(s[3]) << 16);
+    }
+}
+
+// Zero gradients for a set without adapters.
+__global__ __launch_bounds__(kThreads) void zero_kernel(uint4* out, size_t n) {
+    for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+         i += static_cast<size_t>(gridDim.x) * kThreads)
+        out[i] = make_uint4(0, 0, 0, 0);
+}
+
+// -------------------------------------------------------------------- launches
+// Blocks that fill the card (two a compute unit).
+constexpr int64_t kFill = 512;
+
+int esize(int32_t dtype) { return dtype == SS1_BF16 ? 2 : 4; }
+
+// Most slices of a shrink over `cols` inputs: at least 16 units of 64 bytes a
+// block, and no more than fill the card.
+int most_slices(int64_t M, int32_t cols, int32_t dtype) {
+    const int64_t units = (static_cast<int64_t>(cols) * esize(dtype) + 63) / 64;
+    int64_t q = units / 16;
+    const int64_t fill = kFill / ((M + 63) / 64 > 0 ? (M + 63) / 64 : 1);
+    if (q > fill) q = fill;
+    if (q > 16) q = 16;
+    return static_cast<int>(q < 1 ? 1 : q);
+}
+
+// Tokens of a tile in units of 16, by the mean length of a segment: pieces of
+// single tokens gain nothing from larger tiles.
+int tile_of(int64_t M, int64_t S) {
+    const int64_t mean = S > 0 ? M / S : M;
+    return mean <= 24 ? 1 : mean <= 64 ? 2 : 4;
+}
+
+unsigned grid_of(int64_t items) { return static_cast<unsigned>(items < kMaxBlocks ? items : kMaxBlocks); }
+
+template <typename T, int TT>
+void launch_shrink_tt(const AdapterArgs& a, const void* x, const void* A, float* part, int K, int Q, int scaled,
+                      hipStream_t s) {
+    const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * TT) * Q;
+    const int rt = (a.ad.max_rank + 15) / 16;
+    auto k = rt <= 1 ? shrink_kernel<T, TT, 1> : rt <= 2 ? shrink_kernel<T, TT, 2>
+             : rt <= 4 ? shrink_kernel<T, TT, 4> : shrink_kernel<T, TT, 8>;
+    hipLaunchKernelGGL(k, dim3(grid_of(items)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
+                       static_cast<const T*>(A), part, K, Q, scaled, items);
+}
+
+// Slices of this call, at most most_slices().
+template <typename T>
+int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int K, int scaled, bool one_slice,
+                  hipStream_t s) {
+    int tt = tile_of(a.ad.M, a.ad.S);
+    if (tt > 2) tt = 2;
+    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * tt);
+    int64_t Q = kFill / pieces;
+    const int most = most_slices(a.ad.M, K, a.dtype);
+    if (Q > most) Q = most;
+    if (Q < 1 || one_slice) Q = 1;
+    if (tt == 1)
+        launch_shrink_tt<T, 1>(a, x, A, part, K, static_cast<int>(Q), scaled, s);
+    else
+        launch_shrink_tt<T, 2>(a, x, A, part, K, static_cast<int>(Q), scaled, s);
+    return static_cast<int>(Q);
+}
+
+template <typename T, int TT>
+void launch_expand_tt(const AdapterArgs& a, const float* part, int Q, const void* B, void* y, float* v_out, int N,
+                      int scaled, hipStream_t s) {
+    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * TT);
+    const int tiles = (N + 64 * Unit<T>::kCols - 1) / (64 * Unit<T>::kCols);
+    // a block takes several column tiles (v is staged once) while the card stays full
+    int64_t per = pieces * tiles / (4 * kFill);
+    if (per < 1) per = 1;
+    if (per > tiles) per = tiles;
+    const int columns = static_cast<int>((tiles + per - 1) / per);
+    const int ku = (a.ad.max_rank + Unit<T>::kRanks - 1) / Unit<T>::kRanks;
+    auto k = ku <= 1 ? expand_kernel<T, TT, 1> : ku <= 2 ? expand_kernel<T, TT, 2>
+             : (sizeof(T) == 2 || ku <= 4) ? expand_kernel<T, TT, 4> : expand_kernel<T, TT, sizeof(T) == 2 ? 4 : 8>;
+    hipLaunchKernelGGL(k, dim3(grid_of(pieces * columns)), dim3(kThreads), 0, s, a.ad, part, Q,
+                       static_cast<const T*>(B), static_cast<const T*>(a.base), static_cast<T*>(y), v_out, N, scaled,
+                       columns, static_cast<int>(per), tiles, pieces * columns);
+}
+
+template <typename T>
+void launch_expand(const AdapterArgs& a, const float* part, int Q, const void* B, void* y, float* v_out, int N,
+                   int scaled, hipStream_t s) {
+    const int tt = tile_of(a.ad.M, a.ad.S);
+    if (tt == 1)
+        launch_expand_tt<T, 1>(a, part, Q, B, y, v_out, N, scaled, s);
+    else if (tt == 2)
+        launch_expand_tt<T, 2>(a, part, Q, B, y, v_out, N, scaled, s);
+    else
+        launch_expand_tt<T, 4>(a, part, Q, B, y, v_out, N, scaled, s);
 }
 
 template <typename T>
 void forward(const AdapterArgs& a, hipStream_t s) {
-    const unsigned M = static_cast<unsigned>(a.ad.M);
-    float* v = a.v ? a.v : static_cast<float*>(a.workspace);
-    if (a.ad.max_rank > 0)
-        hipLaunchKernelGGL((shrink_kernel<T>), dim3(M, static_cast<unsigned>(a.ad.max_rank)), dim3(64), 0, s, a.ad,
-                           static_cast<const T*>(a.x), static_cast<const T*>(a.A), v, a.K, 0);
-    hipLaunchKernelGGL((expand_kernel<T>), dim3(M, static_cast<unsigned>((a.N + 255) / 256)), dim3(256), 0, s, a.ad,
-                       v, static_cast<const T*>(a.B), static_cast<const T*>(a.base), static_cast<T*>(a.y), a.N, 1);
+    float* part = static_cast<float*>(a.workspace);
+    int Q = 1;
+    if (a.ad.max_rank > 0) {
+        // one slice writes v itself
+        const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * (tile_of(a.ad.M, a.ad.S) > 1 ? 2 : 1));
+        const bool direct = a.v && (kFill / pieces <= 1 || most_slices(a.ad.M, a.K, a.dtype) == 1);
+        if (direct) part = a.v;
+        Q = launch_shrink<T>(a, a.x, a.A, part, a.K, 0, direct, s);
+    }
+    launch_expand<T>(a, part, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.N, 1, s);
+}
+
+// How the outer products are split.
+struct OuterSplit {
+    int RT, rank_groups, Z;
+};
+
+OuterSplit outer_split(int64_t M, int32_t K, int32_t N, int32_t E, int32_t max_rank, int32_t dtype) {
+    OuterSplit o;
+    const int rt = (max_rank + 15) / 16;
+    o.RT = rt <= 1 ? 1 : rt <= 2 ? 2 : 4;
+    o.rank_groups = (rt + o.RT - 1) / o.RT;
+    const int wide = 16 * (16 / esize(dtype));
+    const int64_t tiles = (K + wide - 1) / wide + (N + wide - 1) / wide;
+    const int64_t blocks = tiles * (E > 0 ? E : 1) * (o.rank_groups > 0 ? o.rank_groups : 1);
+    int64_t z = kFill / blocks;
+    const int64_t windows = (M + kWindow - 1) / kWindow;
+    if (z > windows) z = windows;
+    if (z > 16) z = 16;
+    o.Z = static_cast<int>(z < 1 ? 1 : z);
+    return o;
+}
+
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
+template <typename T>
+void zero(void* p, size_t elements, hipStream_t s) {
+    const size_t n = elements * sizeof(T) / 16;
+    if (n > 0)
+        hipLaunchKernelGGL(zero_kernel, dim3(static_cast<unsigned>(n / kThreads < 4096 ? n / kThreads + 1 : 4096)),
+                           dim3(kThreads), 0, s, static_cast<uint4*>(p), n);
+}
+
+template <typename T>
+void launch_outer(const AdapterArgs& a, const float* dv, float* partial, hipStream_t s) {
+    const OuterSplit o = outer_split(a.ad.M, a.K, a.N, a.ad.E, a.ad.max_rank, a.dtype);
+    const size_t nA = static_cast<size_t>(a.ad.R) * a.K, nB = static_cast<size_t>(a.ad.R) * a.N;
+    if (a.ad.E == 0) {
+        if (a.dA) zero<T>(a.dA, nA, s);
+        if (a.dB) zero<T>(a.dB, nB, s);
+        return;
+    }
+    const bool parts = o.Z > 1;
+    const auto count = [&](int cols) {
+        const int wide = 16 * Unit<T>::kCols;
+        return static_cast<int64_t>((cols + wide - 1) / wide) * a.ad.E * o.rank_groups * o.Z;
+    };
+    const int64_t itemsA = a.dA ? count(a.K) : 0, itemsB = a.dB ? count(a.N) : 0;
+    const OuterJob jobA{dv, a.x, a.dA, parts ? partial : nullptr, a.K, 0, 0};
+    const OuterJob jobB{a.v, a.dy, a.dB, parts ? partial + o.Z * nA : nullptr, a.N, 1, itemsA};
+    auto k = o.RT == 1 ? outer_kernel<T, 1> : o.RT == 2 ? outer_kernel<T, 2> : outer_kernel<T, 4>;
+    hipLaunchKernelGGL(k, dim3(grid_of(itemsA + itemsB)), dim3(kThreads), 0, s, a.ad, jobA, jobB, o.rank_groups, o.Z,
+                       itemsA + itemsB);
+    if (!parts) return;
+    const auto blocks = [](size_t n) { return dim3(static_cast<unsigned>(n / 1024 < 8192 ? n / 1024 + 1 : 8192)); };
+    if (a.dA)
+        hipLaunchKernelGGL((join_parts_kernel<T>), blocks(nA), dim3(kThreads), 0, s, jobA.partial,
+                           static_cast<T*>(a.dA), nA, o.Z);
+    if (a.dB)
+        hipLaunchKernelGGL((join_parts_kernel<T>), blocks(nB), dim3(kThreads), 0, s, jobB.partial,
+                           static_cast<T*>(a.dB), nB, o.Z);
 }
 
 template <typename T>
 void backward(const AdapterArgs& a, hipStream_t s) {
-    const unsigned M = static_cast<unsigned>(a.ad.M), R = static_cast<unsigned>(a.ad.R);
-    const unsigned kb = static_cast<unsigned>((a.K + 255) / 256), nb = static_cast<unsigned>((a.N + 255) / 256);
-    float* dv = static_cast<float*>(a.workspace);
-    if ((a.dx || a.dA) && a.ad.max_rank > 0 && M > 0)
-        hipLaunchKernelGGL((shrink_kernel<T>), dim3(M, static_cast<unsigned>(a.ad.max_rank)), dim3(64), 0, s, a.ad,
-                           static_cast<const T*>(a.dy), static_cast<const T*>(a.B), dv, a.N, 1);
-    if (a.dx)
-        hipLaunchKernelGGL((expand_kernel<T>), dim3(M, kb), dim3(256), 0, s, a.ad, dv, static_cast<const T*>(a.A),
-                           static_cast<const T*>(a.base), static_cast<T*>(a.dx), a.K, 0);
-    if (a.dA)
-        hipLaunchKernelGGL((outer_kernel<T>), dim3(R, kb), dim3(256), 0, s, a.ad, dv, static_cast<const T*>(a.x),
-                           static_cast<T*>(a.dA), a.K, 0);
-    if (a.dB)
-        hipLaunchKernelGGL((outer_kernel<T>), dim3(R, nb), dim3(256), 0, s, a.ad, a.v, static_cast<const T*>(a.dy),
-                           static_cast<T*>(a.dB), a.N, 1);
+    const size_t rows = static_cast<size_t>(a.ad.M) * a.ad.max_rank;
+    const int most = most_slices(a.ad.M, a.N, a.dtype);
+    float* part = static_cast<float*>(a.workspace);
+    float* joined = most > 1 ? part + round16(most * rows * 4) / 4 : part;
+    float* partial = joined + round16(rows * 4) / 4;
+    int Q = 1;
+    if ((a.dx || a.dA) && a.ad.max_rank > 0 && a.ad.M > 0)
+        Q = launch_shrink<T>(a, a.dy, a.B, part, a.N, 1, false, s);
+    const float* dv = Q > 1 ? joined : part;
+    if (a.dx) {
+        launch_expand<T>(a, part, Q, a.A, a.dx, Q > 1 && a.dA ? joined : nullptr, a.K, 0, s);
+    } else if (a.dA && Q > 1) {
+        hipLaunchKernelGGL(join_slices_kernel, dim3(static_cast<unsigned>(rows / kThreads < 4096 ? rows / kThreads + 1 : 4096)),
+                           dim3(kThreads), 0, s, part, joined, rows, Q);
+    }
+    if (a.dA || a.dB) launch_outer<T>(a, dv, partial, s);
 }
 
 }  // namespace
 
-size_t adapter_forward_workspace(int64_t M, int32_t, int32_t, int32_t, int32_t max_rank, int32_t) {
-    return static_cast<size_t>(M) * static_cast<size_t>(max_rank) * sizeof(float);
+size_t adapter_forward_workspace(int64_t M, int32_t K, int32_t, int32_t, int32_t, int32_t max_rank, int32_t dtype) {
+    return round16(static_cast<size_t>(M) * static_cast<size_t>(max_rank) * sizeof(float) *
+                   static_cast<size_t>(most_slices(M, K, dtype)));
 }
 
-size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t R, int32_t max_rank, int32_t dtype) {
-    return adapter_forward_workspace(M, K, N, R, max_rank, dtype);
+size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, int32_t R, int32_t max_rank,
+                                  int32_t dtype) {
+    const size_t rows = static_cast<size_t>(M) * static_cast<size_t>(max_rank) * sizeof(float);
+    const int most = most_slices(M, N, dtype);
+    const int Z = outer_split(M, K, N, E, max_rank, dtype).Z;
+    size_t n = round16(rows);
+    if (most > 1) n += round16(rows * static_cast<size_t>(most));
+    if (Z > 1) n += static_cast<size_t>(Z) * static_cast<size_t>(R) * (static_cast<size_t>(K) + N) * sizeof(float);
+    return n;
 }
 
 ss1_status launch_adapter_forward(const AdapterArgs& a) {

@@ -67,8 +67,10 @@ struct AdapterArgs {
     void* stream;
 };
 
-size_t adapter_forward_workspace(int64_t M, int32_t K, int32_t N, int32_t R, int32_t max_rank, int32_t dtype);
-size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t R, int32_t max_rank, int32_t dtype);
+size_t adapter_forward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, int32_t R, int32_t max_rank,
+                                 int32_t dtype);
+size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, int32_t R, int32_t max_rank,
+                                  int32_t dtype);
 ss1_status launch_adapter_forward(const AdapterArgs& a);
 ss1_status launch_adapter_backward(const AdapterArgs& a);
 

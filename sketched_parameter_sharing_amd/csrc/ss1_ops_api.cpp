@@ -14,6 +14,8 @@ bool valid_dtype(int32_t t) { return t == SS1_F32 || t == SS1_BF16; }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxCols = int64_t(1) << 24;
+// 128 rows of an adapter or 64 of x stay within 2^31 bytes
+constexpr int64_t kMaxAdapterCols = int64_t(1) << 22;
 
 // x of a layer norm: sizes and dtype.
 ss1_status check_norm_x(const ss1_tensor* x) {
@@ -137,7 +139,7 @@ ss1_status check_adapters(const ss1_adapters* ad, bool data) {
     if (A.rows < 0 || A.rows > kMaxRows || B.rows != A.rows) return SS1_ERR_SHAPE;
     const int64_t unit = A.dtype == SS1_BF16 ? 8 : 4;
     for (const int64_t n : {A.cols, B.cols})
-        if (n < unit || n >= kMaxCols || n % unit) return SS1_ERR_SHAPE;
+        if (n < unit || n >= kMaxAdapterCols || n % unit) return SS1_ERR_SHAPE;
     if (ad->count < 0 || ad->max_rank < 0 || ad->max_rank > SS1_MAX_RANK) return SS1_ERR_SHAPE;
     if (!data) return SS1_OK;
     if (A.rows > 0 && (!A.data || !B.data)) return SS1_ERR_NULL;
@@ -185,13 +187,17 @@ void fill_adapter(const ss1_adapters* ad, const ss1_segments* s, int64_t M, void
 }
 
 size_t forward_bytes(int64_t M, const ss1_adapters* ad) {
-    return ss1::adapter_forward_workspace(M, static_cast<int32_t>(ad->A.cols), static_cast<int32_t>(ad->B.cols),
+    // as fill_adapter: no rows or no ranks count as no adapters
+    const int32_t E = ad->A.rows == 0 || ad->max_rank == 0 ? 0 : ad->count;
+    return ss1::adapter_forward_workspace(M, static_cast<int32_t>(ad->A.cols), static_cast<int32_t>(ad->B.cols), E,
                                           static_cast<int32_t>(ad->A.rows), ad->max_rank, ad->A.dtype);
 }
 
 size_t backward_bytes(int64_t M, const ss1_adapters* ad) {
-    return ss1::adapter_backward_workspace(M, static_cast<int32_t>(ad->A.cols), static_cast<int32_t>(ad->B.cols),
-                                           static_cast<int32_t>(ad->A.rows), ad->max_rank, ad->A.dtype);
+    // as fill_adapter: no rows or no ranks count as no adapters
+    const int32_t E = ad->A.rows == 0 || ad->max_rank == 0 ? 0 : ad->count;
+    return ss1::adapter_backward_workspace(M, static_cast<int32_t>(ad->A.cols), static_cast<int32_t>(ad->B.cols), E,
+                                          static_cast<int32_t>(ad->A.rows), ad->max_rank, ad->A.dtype);
 }
 
 }  // namespace

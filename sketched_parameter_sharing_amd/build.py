@@ -32,6 +32,7 @@ COMMON = [
 EXTRA = {
     "ss1_fold.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "ss1_group.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "ss1_adapter.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

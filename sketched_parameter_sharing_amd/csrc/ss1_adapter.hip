@@ -20,6 +20,8 @@
 
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "ss1_device.h"
 #include "ss1_ops.h"
 
@@ -57,44 +59,40 @@ struct Piece {
     float scale;
 };
 
+// What find_piece leaves in LDS for the block.
+struct Found {
+    int p, s, begin, end, adapter;
+};
+
 // Piece p of the batch: with F(s) = s + offset[s] / TM, segment s has pieces
 // F(s) .. F(s+1) - 1, one for each tile of TM tokens that it touches (the last
 // may be empty), so no prefix sum over the segments is needed.  Every thread
-// of the block calls this; `sh` is 4 ints of LDS.
-__device__ __forceinline__ Piece find_piece(const AdapterView& ad, int TM, int p, int* sh) {
+// of the block calls this; found->p is -1 before the first call.
+__device__ __forceinline__ Piece find_piece(const AdapterView& ad, int TM, int p, Found* found) {
     Piece out{0, 0, 0, 0, 0.0f};
-    int s = -1, b = 0, t = ad.M;
+    int s = 0, b = 0, t = ad.M, e = -1;
     if (ad.S > 0) {
-        __syncthreads();
-        if (threadIdx.x == 0) sh[0] = -1;
-        __syncthreads();
+        __syncthreads();  // the last piece's readers, or the first -1
         for (int i = threadIdx.x; i < ad.S; i += kThreads) {
-            const int lo = clampi(ad.seg[i], 0, ad.M), hi = clampi(ad.seg[i + 1], lo, ad.M);
-            if (p >= i + lo / TM && p <= i + hi / TM) {
-                sh[0] = i;
-                sh[1] = lo;
-                sh[2] = hi;
-            }
+            const int o0 = ad.seg[i], o1 = ad.seg[i + 1], a = ad.seg_adapter[i];
+            const int lo = clampi(o0, 0, ad.M), hi = clampi(o1, lo, ad.M);
+            if (p >= i + lo / TM && p <= i + hi / TM) *found = Found{p, i, lo, hi, a};
         }
         __syncthreads();
-        s = __builtin_amdgcn_readfirstlane(sh[0]);
-        if (s < 0) return out;
-        b = __builtin_amdgcn_readfirstlane(sh[1]);
-        t = __builtin_amdgcn_readfirstlane(sh[2]);
+        if (__builtin_amdgcn_readfirstlane(found->p) != p) return out;  // offsets out of order
+        s = __builtin_amdgcn_readfirstlane(found->s);
+        b = __builtin_amdgcn_readfirstlane(found->begin);
+        t = __builtin_amdgcn_readfirstlane(found->end);
+        e = __builtin_amdgcn_readfirstlane(found->adapter);
     }
-    const int64_t tile = static_cast<int64_t>(p) - (s < 0 ? 0 : s);
-    out.begin = static_cast<int>(max(int64_t(b), tile * TM));
-    out.n = static_cast<int>(min(int64_t(t), (tile + 1) * TM)) - out.begin;
-    if (out.n <= 0 || out.n > TM) {  // empty, or offsets out of order
-        out.n = 0;
-        return out;
-    }
-    if (s >= 0 && ad.E > 0) {
-        const int e = ad.seg_adapter[s];
-        if (e >= 0 && e < ad.E) {
-            out.rank = rows_of(ad, e, &out.first);
-            out.scale = ad.scale[e];
-        }
+    const int64_t tile = static_cast<int64_t>(p) - s;
+    const int64_t from = max(int64_t(b), tile * TM), to = min(int64_t(t), (tile + 1) * TM);
+    if (to <= from) return out;
+    out.begin = static_cast<int>(from);
+    out.n = static_cast<int>(to - from);
+    if (e >= 0 && e < ad.E) {
+        out.rank = rows_of(ad, e, &out.first);
+        out.scale = ad.scale[e];
     }
     return out;
 }
@@ -145,10 +143,10 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
 // ---------------------------------------------------------------------- shrink
 // One block: a piece and a slice q of K; its waves split the slice, their
 // tiles are added in LDS.  A wave's operands come straight from global memory,
-// 64 bytes of 16 rows at a time.  part[q][m][max_rank].
+// 64 bytes of 16 rows at a time.  part[q][m][stride], columns past the rank 0.
 template <typename T, int TT, int RT>
 __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,
-                                            int max_rank, float scale, f32x4* red) {
+                                            int stride, float scale, f32x4* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, g = lane >> 4;
     const uint32_t Kb = static_cast<uint32_t>(K) * sizeof(T);
     const int units = static_cast<int>((Kb + 63) / 64);
@@ -162,19 +160,26 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0, 0, 0, 0};
     const uint32_t lane_off = row * Kb + 16 * g;
-#pragma unroll 4
-    for (int u = u0; u < u1; ++u) {
-        const uint32_t at = 64u * u;
-        const uint32_t off = at + 16 * g < Kb ? lane_off + at : kOutside;
-        uint4 xf[TT], af[RT];
+    // units whose loads are in flight together (past the wave's share or the
+    // row: zeros)
+    constexpr int UN = RT == 8 ? 2 : 4;
+    for (int ub = u0; ub < u1; ub += UN) {
+        uint4 xf[UN][TT], af[UN][RT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) xf[t] = buf_load16(rx, off + t * 16 * Kb, 0);
+        for (int u = 0; u < UN; ++u) {
+            const uint32_t at = 64u * (ub + u);
+            const uint32_t off = ub + u < u1 && at + 16 * g < Kb ? lane_off + at : kOutside;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) af[r] = buf_load16(ra, off + r * 16 * Kb, 0);
+            for (int t = 0; t < TT; ++t) xf[u][t] = buf_load16(rx, off + t * 16 * Kb, 0);
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+            for (int r = 0; r < RT; ++r) af[u][r] = buf_load16(ra, off + r * 16 * Kb, 0);
+        }
 #pragma unroll
-            for (int r = 0; r < RT; ++r) acc[t][r] = mma(x, xf[t], af[r], acc[t][r]);
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[t][r] = mma(x, xf[u][t], af[u][r], acc[t][r]);
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -187,43 +192,44 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) s += red[w * RT * 64 + i];
             const int j = 16 * (i >> 6) + (i & 15), m = 16 * t + 4 * ((i >> 4) & 3);
-            if (j < max_rank)
+            if (j < stride)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (m + k < pc.n) out[static_cast<size_t>(m + k) * max_rank + j] = s[k] * scale;
+                    if (m + k < pc.n) out[static_cast<size_t>(m + k) * stride + j] = j < pc.rank ? s[k] * scale : 0.0f;
         }
     }
-    const int rest = max_rank - 16 * RT;  // columns past the tiles are zero
+    const int rest = stride - 16 * RT;  // columns past the tiles are zero
     if (rest > 0)
         for (int i = threadIdx.x; i < pc.n * rest; i += kThreads)
-            out[static_cast<size_t>(i / rest) * max_rank + 16 * RT + i % rest] = 0.0f;
+            out[static_cast<size_t>(i / rest) * stride + 16 * RT + i % rest] = 0.0f;
 }
 
 template <typename T, int TT, int RT>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const T* __restrict__ x,
-                                                          const T* __restrict__ A, float* __restrict__ part, int K,
-                                                          int Q, int scaled, int64_t items) {
+                                                          const T* __restrict__ A, float* __restrict__ part, int stride,
+                                                          int K, int Q, int scaled, int64_t items) {
     __shared__ f32x4 red[kWaves * RT * 64];
-    __shared__ int sh[4];
+    __shared__ Found found;
+    if (threadIdx.x == 0) found.p = -1;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int q = static_cast<int>(item % Q);
-        const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q), sh);
+        const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q), &found);
         if (pc.n == 0) continue;
-        float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * ad.max_rank;
+        float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
         const float scale = scaled ? pc.scale : 1.0f;
         if (pc.rank == 0) {
-            for (int i = threadIdx.x; i < pc.n * ad.max_rank; i += kThreads) out[i] = 0.0f;
+            for (int i = threadIdx.x; i < pc.n * stride; i += kThreads) out[i] = 0.0f;
             continue;
         }
         // tiles for the rank of this adapter, not for the largest
         if (RT == 1 || pc.rank <= 16)
-            shrink_body<T, TT, 1>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+            shrink_body<T, TT, 1>(pc, x, A, out, K, Q, q, stride, scale, red);
         else if (RT == 2 || pc.rank <= 32)
-            shrink_body<T, TT, RT < 2 ? RT : 2>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+            shrink_body<T, TT, RT < 2 ? RT : 2>(pc, x, A, out, K, Q, q, stride, scale, red);
         else if (RT == 4 || pc.rank <= 64)
-            shrink_body<T, TT, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+            shrink_body<T, TT, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, stride, scale, red);
         else
-            shrink_body<T, TT, RT>(pc, x, A, out, K, Q, q, ad.max_rank, scale, red);
+            shrink_body<T, TT, RT>(pc, x, A, out, K, Q, q, stride, scale, red);
     }
 }
 
@@ -244,8 +250,8 @@ struct Unit<float> {
     static constexpr int kRanks = 16, kLoads = 4, kCols = 4, kFrags = 1;
 };
 
-// v of 16 tokens and one rank unit as operands in LDS: frag[h][lane] (hi, lo),
-// or for float32 frag[lane] with float i = rank 4 i + g.
+// v of 16 tokens and one rank unit as operands in LDS: frag[h][lane], h = hi,
+// lo (bf16) or only one (float32); lane m + 16 g holds the g-th group of ranks.
 __device__ __forceinline__ void stage_one(const __bf16*, uint4* frag, int m, int g, const float (&v)[8]) {
     uint32_t hi[8], lo[8];
 #pragma unroll
@@ -259,20 +265,12 @@ __device__ __forceinline__ void stage_one(const float*, uint4* frag, int m, int 
                                   __float_as_uint(v[3]));
 }
 
-// Columns of B of one rank unit: bf16, column j of this lane's eight, rows
-// 8 g + i; float32, column j of four, rows 4 i + g.
-__device__ __forceinline__ void load_columns(const __bf16*, __amdgpu_buffer_rsrc_t r, uint32_t unit, int g,
-                                             uint32_t Nb, uint32_t col, uint4 (&f)[8]) {
-    uint4 t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = buf_load16(r, col == kOutside ? kOutside : (unit * 32 + 8 * g + i) * Nb + col, 0);
+// Rows (of B: ranks; of x: tokens) of this lane's 16 bytes of columns -> one
+// operand a column.
+__device__ __forceinline__ void column_operands(const __bf16*, const uint4 (&t)[8], uint4 (&f)[8]) {
     transpose8(t, f);
 }
-__device__ __forceinline__ void load_columns(const float*, __amdgpu_buffer_rsrc_t r, uint32_t unit, int g, uint32_t Nb,
-                                             uint32_t col, uint4 (&f)[4]) {
-    uint4 t[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = buf_load16(r, col == kOutside ? kOutside : (unit * 16 + 4 * i + g) * Nb + col, 0);
+__device__ __forceinline__ void column_operands(const float*, const uint4 (&t)[4], uint4 (&f)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = make_uint4((&t[0].x)[j], (&t[1].x)[j], (&t[2].x)[j], (&t[3].x)[j]);
 }
@@ -301,59 +299,99 @@ __device__ __forceinline__ uint4 pack(const float*, const f32x4 (&acc)[4], int i
 }
 
 template <typename T, int TT, int KU>
-__device__ __forceinline__ void expand_body(const Piece& pc, const float* part, size_t slice, int Q, int max_rank,
-                                            const T* B, const T* base, T* y, float* v_out, int N, int tile0,
+__device__ __forceinline__ void expand_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
+                                            int max_rank, const T* B, const T* base, T* y, float* v_out, int N, int tile0,
                                             int tiles, float scale, uint4* frags) {
     using U = Unit<T>;
     constexpr int GROUP = U::kRanks / 4;  // ranks of one operand lane
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    // v of the piece, summed over the slices of K in order
-    for (int i = threadIdx.x; i < 16 * TT * KU * 4; i += kThreads) {
-        const int m = i / (KU * 4), unit = i % (KU * 4) / 4, gi = i % 4;
-        float v[GROUP];
-#pragma unroll
-        for (int j = 0; j < GROUP; ++j) {
-            const int r = unit * U::kRanks + (sizeof(T) == 2 ? gi * 8 + j : j * 4 + gi);
-            float s = 0.0f;
-            if (m < pc.n && r < pc.rank) {
-                const float* at = part + static_cast<size_t>(pc.begin + m) * max_rank + r;
-                for (int q = 0; q < Q; ++q) s += at[q * slice];
-                if (v_out) v_out[static_cast<size_t>(pc.begin + m) * max_rank + r] = s;
-            }
-            v[j] = s * scale;
-        }
-        stage_one(B, frags + ((m >> 4) * KU + unit) * U::kFrags * 64, m & 15, gi, v);
-    }
-    if (v_out)  // zero columns past the rank
-        for (int i = threadIdx.x; i < pc.n * (max_rank - pc.rank); i += kThreads)
-            v_out[static_cast<size_t>(pc.begin + i / (max_rank - pc.rank)) * max_rank + pc.rank +
-                  i % (max_rank - pc.rank)] = 0.0f;
-    __syncthreads();
     const uint32_t Nb = static_cast<uint32_t>(N) * sizeof(T);
     const auto rb = make_rsrc(B + static_cast<size_t>(pc.first) * N, static_cast<uint32_t>(pc.rank) * Nb);
     const auto ry = make_rsrc(y + static_cast<size_t>(pc.begin) * N, static_cast<uint32_t>(pc.n) * Nb);
     const auto rs = make_rsrc((base ? base : y) + static_cast<size_t>(pc.begin) * N,
                               base ? static_cast<uint32_t>(pc.n) * Nb : 0u);
+    const auto column = [&](int tile) {
+        const uint32_t col = 16u * (static_cast<uint32_t>(tile) * (kThreads / 4) + wave * 16 + c);
+        return col < Nb ? col : kOutside;
+    };
+    // rows of B and of base (16 tokens from 16 t on) in this lane's columns
+    uint4 rows[KU][U::kLoads], old[4];
+    // (a row's offset is under 2^31, so kOutside plus it stays outside)
+    const auto fetch_rows = [&](uint32_t col) {
+        // opaque, or the compiler keeps every row's offset in a register
+        uint32_t wide = Nb;
+        asm volatile("" : "+s"(wide));
+        uint32_t at = GROUP * g * wide + col;
+#pragma unroll
+        for (int k = 0; k < KU; ++k) {
+#pragma unroll
+            for (int i = 0; i < U::kLoads; ++i) {
+                rows[k][i] = buf_load16(rb, at, 0);
+                at += wide;
+            }
+            at += (U::kRanks - U::kLoads) * wide;
+        }
+    };
+    const auto fetch_base = [&](int t, uint32_t col, uint4 (&to)[4]) {
+        const uint32_t at = (16 * t + 4 * g) * Nb + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = buf_load16(rs, at + i * Nb, 0);
+    };
+    // in flight while v is staged
+    fetch_rows(column(tile0));
+    fetch_base(0, column(tile0), old);
+    // v of the piece, summed over the slices of K in order (columns past the
+    // rank are zero there; the stride is a multiple of 8)
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 16 * TT * KU * 4; i += kThreads) {
+        const int m = i / (KU * 4), unit = i % (KU * 4) / 4, gi = i % 4, r = unit * U::kRanks + GROUP * gi;
+        f32x4 v[GROUP / 4];
+#pragma unroll
+        for (int j = 0; j < GROUP / 4; ++j) v[j] = f32x4{0, 0, 0, 0};
+        if (m < pc.n && r < stride) {
+            const f32x4* from = reinterpret_cast<const f32x4*>(part + static_cast<size_t>(pc.begin + m) * stride + r);
+            for (int q0 = 0; q0 < Q; q0 += 4) {  // four slices' loads together
+                f32x4 w[4][GROUP / 4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < GROUP / 4; ++j) w[q][j] = from[min(q0 + q, Q - 1) * (slice / 4) + j];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < GROUP / 4; ++j)
+                        if (q0 + q < Q) v[j] += w[q][j];
+            }
+            if (v_out)
+                for (int j = 0; j < GROUP; ++j)
+                    if (r + j < max_rank) v_out[static_cast<size_t>(pc.begin + m) * max_rank + r + j] = v[j / 4][j % 4];
+        }
+        float scaled[GROUP];
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) scaled[j] = v[j / 4][j % 4] * scale;
+        stage_one(B, frags + ((m >> 4) * KU + unit) * U::kFrags * 64, m & 15, gi, scaled);
+    }
+    const int past = KU * U::kRanks;  // columns that no unit covers are zero
+    if (v_out && past < max_rank)
+        for (int i = threadIdx.x; i < pc.n * (max_rank - past); i += kThreads)
+            v_out[static_cast<size_t>(pc.begin + i / (max_rank - past)) * max_rank + past + i % (max_rank - past)] = 0.0f;
+    __syncthreads();
     for (int tile = tile0; tile < tile0 + tiles; ++tile) {
-        uint32_t col = 16u * (static_cast<uint32_t>(tile) * kThreads / 4 + wave * 16 + c);
-        if (col >= Nb) col = kOutside;
+        const uint32_t col = column(tile);
+        if (tile > tile0) {
+            fetch_rows(col);
+            fetch_base(0, col, old);
+        }
         uint4 f[KU][U::kCols];
 #pragma unroll
-        for (int k = 0; k < KU; ++k) load_columns(B, rb, k, g, Nb, col, f[k]);
-        // base one tile of 16 tokens ahead
-        uint4 old[2][4];
-        const auto fetch = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                old[t & 1][i] = buf_load16(rs, col == kOutside ? kOutside : (16 * t + 4 * g + i) * Nb + col, 0);
-        };
-        fetch(0);
-#pragma unroll
+        for (int k = 0; k < KU; ++k) column_operands(B, rows[k], f[k]);
+#pragma unroll 1
         for (int t = 0; t < TT; ++t) {
-            if (t + 1 < TT) fetch(t + 1);
+            uint4 next[4];
+            fetch_base(t + 1, col, next);  // past the piece: zeros, unused
             f32x4 acc[U::kCols];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack(B, old[t & 1][i], i, acc);
+            for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
 #pragma unroll
             for (int k = 0; k < KU; ++k)
 #pragma unroll
@@ -362,25 +400,29 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
 #pragma unroll
                     for (int j = 0; j < U::kCols; ++j) acc[j] = mma(B, a, f[k][j], acc[j]);
                 }
+            const uint32_t at = (16 * t + 4 * g) * Nb + col;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                buf_store16(ry, col == kOutside ? kOutside : (16 * t + 4 * g + i) * Nb + col, pack(B, acc, i));
+            for (int i = 0; i < 4; ++i) {
+                buf_store16(ry, at + i * Nb, pack(B, acc, i));
+                old[i] = next[i];
+            }
         }
     }
 }
 
 template <typename T, int TT, int KU>
-__global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, const float* __restrict__ part, int Q,
-                                                          const T* __restrict__ B, const T* base, T* y,
+__global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, const float* __restrict__ part,
+                                                             int stride, int Q, const T* __restrict__ B, const T* base, T* y,
                                                           float* __restrict__ v_out, int N, int scaled, int columns,
                                                           int per, int tiles, int64_t items) {
     __shared__ uint4 frags[TT * KU * Unit<T>::kFrags * 64];
-    __shared__ int sh[4];
+    __shared__ Found found;
+    if (threadIdx.x == 0) found.p = -1;
     constexpr int TM = 16 * TT;
-    const size_t slice = static_cast<size_t>(ad.M) * ad.max_rank;
+    const size_t slice = static_cast<size_t>(ad.M) * stride;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int cg = static_cast<int>(item % columns);
-        const Piece pc = find_piece(ad, TM, static_cast<int>(item / columns), sh);
+        const Piece pc = find_piece(ad, TM, static_cast<int>(item / columns), &found);
         if (pc.n == 0) continue;
         const int tile0 = cg * per, count = min(per, tiles - tile0);
         float* vo = cg == 0 ? v_out : nullptr;
@@ -404,24 +446,24 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, con
         const float scale = scaled ? pc.scale : 1.0f;
         constexpr int R = Unit<T>::kRanks;
         if (KU == 1 || pc.rank <= R)
-            expand_body<T, TT, 1>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, 1>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
         else if (KU == 2 || pc.rank <= 2 * R)
-            expand_body<T, TT, KU < 2 ? KU : 2>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
         else if (KU == 4 || pc.rank <= 4 * R)
-            expand_body<T, TT, KU < 4 ? KU : 4>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
         else
-            expand_body<T, TT, KU>(pc, part, slice, Q, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, KU>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
     }
 }
 
-// Partial sums joined where no expand does it.
+// The slices of a shrink joined in order, for the outer products.
 __global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __restrict__ part, float* __restrict__ out,
                                                                size_t n, int Q) {
-    for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<size_t>(gridDim.x) * kThreads) {
-        float s = part[i];
-        for (int q = 1; q < Q; ++q) s += part[q * n + i];
-        out[i] = s;
+    for (size_t i = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n;
+         i += static_cast<size_t>(gridDim.x) * kThreads * 4) {
+        f32x4 s = *reinterpret_cast<const f32x4*>(part + i);
+        for (int q = 1; q < Q; ++q) s += *reinterpret_cast<const f32x4*>(part + q * n + i);
+        *reinterpret_cast<f32x4*>(out + i) = s;
     }
 }
 
@@ -431,37 +473,18 @@ __global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __re
 // window by window in LDS (they may lie in many segments), its waves take
 // steps of the window in turn, and their tiles are added in LDS at the end.
 struct OuterJob {
-    const float* v;
+    const float* v;  // [M][v_stride]
     const void* x;
     void* out;       // the gradient, or
     float* partial;  // [Z][R][cols] when the tokens are split
     int cols;
+    int v_stride;
     int scaled;
     int64_t first_item;
 };
 
 constexpr int kWindow = 256;  // tokens listed at a time
 
-template <typename T>
-struct Step;
-template <>
-struct Step<__bf16> {
-    static constexpr int kTokens = 32, kRows = 8;
-    static __device__ __forceinline__ int token(int g, int i) { return 8 * g + i; }
-};
-template <>
-struct Step<float> {
-    static constexpr int kTokens = 16, kRows = 4;
-    static __device__ __forceinline__ int token(int g, int i) { return 4 * i + g; }
-};
-
-__device__ __forceinline__ void column_operands(const __bf16*, const uint4 (&t)[8], uint4 (&f)[8]) {
-    transpose8(t, f);
-}
-__device__ __forceinline__ void column_operands(const float*, const uint4 (&t)[4], uint4 (&f)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = make_uint4((&t[0].x)[j], (&t[1].x)[j], (&t[2].x)[j], (&t[3].x)[j]);
-}
 // v of this lane's rank over its tokens as operands; h = 0, 1: hi, lo.
 __device__ __forceinline__ void rank_operands(const __bf16*, const float (&v)[8], uint4 (&f)[2]) {
     uint32_t hi[8], lo[8];
@@ -474,11 +497,15 @@ __device__ __forceinline__ void rank_operands(const float*, const float (&v)[4],
     f[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
-template <typename T, int RT>
-__global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, OuterJob job0, OuterJob job1, int rank_groups,
-                                                         int Z, int64_t items) {
+// NEAR: x, dy and v are under 2^32 bytes each, so a row is a 32-bit offset of
+// one buffer descriptor, and an offset past its end reads as zero.
+template <typename T, int RT, bool NEAR>
+__global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, OuterJob job0, OuterJob job1,
+                                                            int rank_groups, int Z, int64_t items) {
     using U = Unit<T>;
-    using St = Step<T>;
+    constexpr int ROWS = U::kLoads;         // tokens of one operand lane
+    constexpr int STEP = 4 * ROWS;          // tokens of one product
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
     __shared__ f32x4 red[2 * RT * U::kCols * 64];
     __shared__ int tokens[kWindow];
     __shared__ int ends[kThreads], starts[kThreads], wave_sum[kWaves];
@@ -499,6 +526,9 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
         const int col = (tile * 16 + c) * U::kCols;
         const bool inside = col < job.cols;
         const T* x = static_cast<const T*>(job.x) + (inside ? col : 0);
+        const uint32_t row_bytes = static_cast<uint32_t>(job.cols) * sizeof(T), v_bytes = job.v_stride * 4u;
+        const auto rx = make_rsrc(job.x, static_cast<uint32_t>(ad.M) * row_bytes);
+        const auto rv = make_rsrc(job.v, static_cast<uint32_t>(ad.M) * v_bytes);
         f32x4 acc[RT][U::kCols];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -508,9 +538,10 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
         for (int s0 = 0; s0 < ad.S; s0 += kThreads) {
             const int s = s0 + threadIdx.x;
             int b = 0, n = 0;
-            if (s < ad.S && ad.seg_adapter[s] == e) {
-                b = clampi(ad.seg[s], 0, ad.M);
-                n = clampi(ad.seg[s + 1], b, ad.M) - b;
+            if (s < ad.S) {
+                const int o0 = ad.seg[s], o1 = ad.seg[s + 1], a = ad.seg_adapter[s];
+                b = clampi(o0, 0, ad.M);
+                n = a == e ? clampi(o1, b, ad.M) - b : 0;
             }
             int sum = n;  // inclusive prefix sum over the block
 #pragma unroll
@@ -533,38 +564,52 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
             for (int w0 = z * kWindow; w0 < total; w0 += Z * kWindow) {
                 const int count = min(kWindow, total - w0);
                 __syncthreads();
+                const int at = w0 + threadIdx.x;
                 if (threadIdx.x < count) {
-                    const int at = w0 + threadIdx.x;
                     int lo = 0, hi = kThreads - 1;  // the first segment whose end is past `at`
                     while (lo < hi) {
                         const int mid = (lo + hi) / 2;
                         if (ends[mid] > at) hi = mid; else lo = mid + 1;
                     }
                     tokens[threadIdx.x] = starts[lo] + at;
+                } else {
+                    tokens[threadIdx.x] = -1;
                 }
                 __syncthreads();
-                for (int t0 = wave * St::kTokens; t0 < count; t0 += kWaves * St::kTokens) {
-                    uint4 rows[St::kRows];
-                    float v[RT][St::kRows];
+                for (int t0 = wave * STEP; t0 < count; t0 += kWaves * STEP) {
+                    uint4 rows[ROWS];
+                    float v[RT][ROWS];
 #pragma unroll
-                    for (int i = 0; i < St::kRows; ++i) {
-                        const int at = t0 + St::token(g, i);
-                        const bool real = at < count;
-                        const int tok = tokens[real ? at : 0];
-                        rows[i] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(tok) * job.cols);
-                        if (!real) rows[i] = make_uint4(0, 0, 0, 0);
-                        const float* vr = job.v + static_cast<size_t>(tok) * ad.max_rank + r0;
+                    for (int i = 0; i < ROWS; ++i) {
+                        const int tok = tokens[t0 + ROWS * g + i];
+                        if constexpr (NEAR) {
+                            const uint32_t t = static_cast<uint32_t>(tok);
+                            rows[i] = buf_load16(rx, tok < 0 || !inside ? kNone : t * row_bytes + col * sizeof(T), 0);
 #pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const int j = 16 * r + c;
-                            const float f = vr[j < rank ? j : 0];
-                            v[r][i] = real && j < rank ? f : 0.0f;
+                            for (int r = 0; r < RT; ++r) {
+                                const uint32_t off = t * v_bytes + 4 * (r0 + 16 * r + c);
+                                v[r][i] = __builtin_bit_cast(
+                                    float, __builtin_amdgcn_raw_buffer_load_b32(
+                                               rv, tok < 0 || 16 * r + c >= rank ? kNone : off, 0, 0));
+                            }
+                        } else {
+                            const size_t t = tok < 0 ? 0 : tok;
+                            rows[i] = *reinterpret_cast<const uint4*>(x + t * job.cols);
+                            if (tok < 0) rows[i] = make_uint4(0, 0, 0, 0);
+                            const float* vr = job.v + t * job.v_stride + r0;
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                const int j = 16 * r + c;
+                                const float f = vr[j < rank ? j : 0];
+                                v[r][i] = tok >= 0 && j < rank ? f : 0.0f;
+                            }
                         }
                     }
                     uint4 f[U::kCols];
                     column_operands(x, rows, f);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
+                        if (16 * r >= rank) break;
                         uint4 a[U::kFrags];
                         rank_operands(x, v[r], a);
 #pragma unroll
@@ -655,9 +700,9 @@ int esize(int32_t dtype) { return dtype == SS1_BF16 ? 2 : 4; }
 int most_slices(int64_t M, int32_t cols, int32_t dtype) {
     const int64_t units = (static_cast<int64_t>(cols) * esize(dtype) + 63) / 64;
     int64_t q = units / 16;
-    const int64_t fill = kFill / ((M + 63) / 64 > 0 ? (M + 63) / 64 : 1);
+    const int64_t fill = 2 * kFill / ((M + 63) / 64 > 0 ? (M + 63) / 64 : 1);
     if (q > fill) q = fill;
-    if (q > 16) q = 16;
+    if (q > 8) q = 8;
     return static_cast<int>(q < 1 ? 1 : q);
 }
 
@@ -668,39 +713,44 @@ int tile_of(int64_t M, int64_t S) {
     return mean <= 24 ? 1 : mean <= 64 ? 2 : 4;
 }
 
+// ... of the shrink: more blocks, and fewer accumulators a wave.
+int shrink_tile_of(int64_t M, int64_t S) { return tile_of(M, S) > 1 ? 2 : 1; }
+
+// Floats of one token's row of v in the workspace: 16-byte loads of 8 ranks.
+int stride_of(int32_t max_rank) { return (max_rank + 7) / 8 * 8; }
+
 unsigned grid_of(int64_t items) { return static_cast<unsigned>(items < kMaxBlocks ? items : kMaxBlocks); }
 
 template <typename T, int TT>
-void launch_shrink_tt(const AdapterArgs& a, const void* x, const void* A, float* part, int K, int Q, int scaled,
-                      hipStream_t s) {
+void launch_shrink_tt(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int Q,
+                      int scaled, hipStream_t s) {
     const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * TT) * Q;
     const int rt = (a.ad.max_rank + 15) / 16;
     auto k = rt <= 1 ? shrink_kernel<T, TT, 1> : rt <= 2 ? shrink_kernel<T, TT, 2>
              : rt <= 4 ? shrink_kernel<T, TT, 4> : shrink_kernel<T, TT, 8>;
     hipLaunchKernelGGL(k, dim3(grid_of(items)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
-                       static_cast<const T*>(A), part, K, Q, scaled, items);
+                       static_cast<const T*>(A), part, stride, K, Q, scaled, items);
 }
 
 // Slices of this call, at most most_slices().
 template <typename T>
-int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int K, int scaled, bool one_slice,
+int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int scaled,
                   hipStream_t s) {
-    int tt = tile_of(a.ad.M, a.ad.S);
-    if (tt > 2) tt = 2;
+    const int tt = shrink_tile_of(a.ad.M, a.ad.S);
     const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * tt);
-    int64_t Q = kFill / pieces;
+    int64_t Q = 2 * kFill / pieces;
     const int most = most_slices(a.ad.M, K, a.dtype);
     if (Q > most) Q = most;
-    if (Q < 1 || one_slice) Q = 1;
+    if (Q < 1) Q = 1;
     if (tt == 1)
-        launch_shrink_tt<T, 1>(a, x, A, part, K, static_cast<int>(Q), scaled, s);
+        launch_shrink_tt<T, 1>(a, x, A, part, stride, K, static_cast<int>(Q), scaled, s);
     else
-        launch_shrink_tt<T, 2>(a, x, A, part, K, static_cast<int>(Q), scaled, s);
+        launch_shrink_tt<T, 2>(a, x, A, part, stride, K, static_cast<int>(Q), scaled, s);
     return static_cast<int>(Q);
 }
 
 template <typename T, int TT>
-void launch_expand_tt(const AdapterArgs& a, const float* part, int Q, const void* B, void* y, float* v_out, int N,
+void launch_expand_tt(const AdapterArgs& a, const float* part, int stride, int Q, const void* B, void* y, float* v_out, int N,
                       int scaled, hipStream_t s) {
     const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * TT);
     const int tiles = (N + 64 * Unit<T>::kCols - 1) / (64 * Unit<T>::kCols);
@@ -712,35 +762,37 @@ void launch_expand_tt(const AdapterArgs& a, const float* part, int Q, const void
     const int ku = (a.ad.max_rank + Unit<T>::kRanks - 1) / Unit<T>::kRanks;
     auto k = ku <= 1 ? expand_kernel<T, TT, 1> : ku <= 2 ? expand_kernel<T, TT, 2>
              : (sizeof(T) == 2 || ku <= 4) ? expand_kernel<T, TT, 4> : expand_kernel<T, TT, sizeof(T) == 2 ? 4 : 8>;
-    hipLaunchKernelGGL(k, dim3(grid_of(pieces * columns)), dim3(kThreads), 0, s, a.ad, part, Q,
+    hipLaunchKernelGGL(k, dim3(grid_of(pieces * columns)), dim3(kThreads), 0, s, a.ad, part, stride, Q,
                        static_cast<const T*>(B), static_cast<const T*>(a.base), static_cast<T*>(y), v_out, N, scaled,
                        columns, static_cast<int>(per), tiles, pieces * columns);
 }
 
 template <typename T>
-void launch_expand(const AdapterArgs& a, const float* part, int Q, const void* B, void* y, float* v_out, int N,
+void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, const void* B, void* y, float* v_out, int N,
                    int scaled, hipStream_t s) {
     const int tt = tile_of(a.ad.M, a.ad.S);
     if (tt == 1)
-        launch_expand_tt<T, 1>(a, part, Q, B, y, v_out, N, scaled, s);
+        launch_expand_tt<T, 1>(a, part, stride, Q, B, y, v_out, N, scaled, s);
     else if (tt == 2)
-        launch_expand_tt<T, 2>(a, part, Q, B, y, v_out, N, scaled, s);
+        launch_expand_tt<T, 2>(a, part, stride, Q, B, y, v_out, N, scaled, s);
     else
-        launch_expand_tt<T, 4>(a, part, Q, B, y, v_out, N, scaled, s);
+        launch_expand_tt<T, 4>(a, part, stride, Q, B, y, v_out, N, scaled, s);
 }
 
 template <typename T>
 void forward(const AdapterArgs& a, hipStream_t s) {
     float* part = static_cast<float*>(a.workspace);
+    const int stride = stride_of(a.ad.max_rank);
     int Q = 1;
     if (a.ad.max_rank > 0) {
-        // one slice writes v itself
-        const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * (tile_of(a.ad.M, a.ad.S) > 1 ? 2 : 1));
-        const bool direct = a.v && (kFill / pieces <= 1 || most_slices(a.ad.M, a.K, a.dtype) == 1);
+        // a single slice with rows of v's own length writes v itself
+        const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * shrink_tile_of(a.ad.M, a.ad.S));
+        const bool direct = a.v && stride == a.ad.max_rank &&
+                            (2 * kFill / pieces <= 1 || most_slices(a.ad.M, a.K, a.dtype) == 1);
         if (direct) part = a.v;
-        Q = launch_shrink<T>(a, a.x, a.A, part, a.K, 0, direct, s);
+        Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, s);
     }
-    launch_expand<T>(a, part, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.N, 1, s);
+    launch_expand<T>(a, part, stride, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.N, 1, s);
 }
 
 // How the outer products are split.
@@ -756,15 +808,13 @@ OuterSplit outer_split(int64_t M, int32_t K, int32_t N, int32_t E, int32_t max_r
     const int wide = 16 * (16 / esize(dtype));
     const int64_t tiles = (K + wide - 1) / wide + (N + wide - 1) / wide;
     const int64_t blocks = tiles * (E > 0 ? E : 1) * (o.rank_groups > 0 ? o.rank_groups : 1);
-    int64_t z = kFill / blocks;
+    int64_t z = 2 * kFill / blocks;
     const int64_t windows = (M + kWindow - 1) / kWindow;
     if (z > windows) z = windows;
     if (z > 16) z = 16;
     o.Z = static_cast<int>(z < 1 ? 1 : z);
     return o;
 }
-
-size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 template <typename T>
 void zero(void* p, size_t elements, hipStream_t s) {
@@ -775,7 +825,7 @@ void zero(void* p, size_t elements, hipStream_t s) {
 }
 
 template <typename T>
-void launch_outer(const AdapterArgs& a, const float* dv, float* partial, hipStream_t s) {
+void launch_outer(const AdapterArgs& a, const float* dv, int dv_stride, float* partial, hipStream_t s) {
     const OuterSplit o = outer_split(a.ad.M, a.K, a.N, a.ad.E, a.ad.max_rank, a.dtype);
     const size_t nA = static_cast<size_t>(a.ad.R) * a.K, nB = static_cast<size_t>(a.ad.R) * a.N;
     if (a.ad.E == 0) {
@@ -789,9 +839,12 @@ void launch_outer(const AdapterArgs& a, const float* dv, float* partial, hipStre
         return static_cast<int64_t>((cols + wide - 1) / wide) * a.ad.E * o.rank_groups * o.Z;
     };
     const int64_t itemsA = a.dA ? count(a.K) : 0, itemsB = a.dB ? count(a.N) : 0;
-    const OuterJob jobA{dv, a.x, a.dA, parts ? partial : nullptr, a.K, 0, 0};
-    const OuterJob jobB{a.v, a.dy, a.dB, parts ? partial + o.Z * nA : nullptr, a.N, 1, itemsA};
-    auto k = o.RT == 1 ? outer_kernel<T, 1> : o.RT == 2 ? outer_kernel<T, 2> : outer_kernel<T, 4>;
+    const OuterJob jobA{dv, a.x, a.dA, parts ? partial : nullptr, a.K, dv_stride, 0, 0};
+    const OuterJob jobB{a.v, a.dy, a.dB, parts ? partial + o.Z * nA : nullptr, a.N, a.ad.max_rank, 1, itemsA};
+    const int64_t widest = std::max(std::max(a.K, a.N) * static_cast<int64_t>(sizeof(T)), dv_stride * int64_t(4));
+    const bool near = a.ad.M * widest < (int64_t(1) << 32);
+    auto k = near ? (o.RT == 1 ? outer_kernel<T, 1, true> : o.RT == 2 ? outer_kernel<T, 2, true> : outer_kernel<T, 4, true>)
+                  : (o.RT == 1 ? outer_kernel<T, 1, false> : o.RT == 2 ? outer_kernel<T, 2, false> : outer_kernel<T, 4, false>);
     hipLaunchKernelGGL(k, dim3(grid_of(itemsA + itemsB)), dim3(kThreads), 0, s, a.ad, jobA, jobB, o.rank_groups, o.Z,
                        itemsA + itemsB);
     if (!parts) return;
@@ -806,38 +859,34 @@ void launch_outer(const AdapterArgs& a, const float* dv, float* partial, hipStre
 
 template <typename T>
 void backward(const AdapterArgs& a, hipStream_t s) {
-    const size_t rows = static_cast<size_t>(a.ad.M) * a.ad.max_rank;
+    const int stride = stride_of(a.ad.max_rank);
+    const size_t rows = static_cast<size_t>(a.ad.M) * stride;
     const int most = most_slices(a.ad.M, a.N, a.dtype);
     float* part = static_cast<float*>(a.workspace);
-    float* joined = most > 1 ? part + round16(most * rows * 4) / 4 : part;
-    float* partial = joined + round16(rows * 4) / 4;
+    float* joined = most > 1 ? part + most * rows : part;
+    float* partial = joined + rows;
     int Q = 1;
     if ((a.dx || a.dA) && a.ad.max_rank > 0 && a.ad.M > 0)
-        Q = launch_shrink<T>(a, a.dy, a.B, part, a.N, 1, false, s);
-    const float* dv = Q > 1 ? joined : part;
-    if (a.dx) {
-        launch_expand<T>(a, part, Q, a.A, a.dx, Q > 1 && a.dA ? joined : nullptr, a.K, 0, s);
-    } else if (a.dA && Q > 1) {
-        hipLaunchKernelGGL(join_slices_kernel, dim3(static_cast<unsigned>(rows / kThreads < 4096 ? rows / kThreads + 1 : 4096)),
-                           dim3(kThreads), 0, s, part, joined, rows, Q);
-    }
-    if (a.dA || a.dB) launch_outer<T>(a, dv, partial, s);
+        Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, s);
+    if (a.dx) launch_expand<T>(a, part, stride, Q, a.A, a.dx, nullptr, a.K, 0, s);
+    if (a.dA && Q > 1)
+        hipLaunchKernelGGL(join_slices_kernel,
+                           dim3(static_cast<unsigned>(rows / 1024 < 4096 ? rows / 1024 + 1 : 4096)), dim3(kThreads), 0,
+                           s, part, joined, rows, Q);
+    if (a.dA || a.dB) launch_outer<T>(a, Q > 1 ? joined : part, stride, partial, s);
 }
 
 }  // namespace
 
 size_t adapter_forward_workspace(int64_t M, int32_t K, int32_t, int32_t, int32_t, int32_t max_rank, int32_t dtype) {
-    return round16(static_cast<size_t>(M) * static_cast<size_t>(max_rank) * sizeof(float) *
-                   static_cast<size_t>(most_slices(M, K, dtype)));
+    return static_cast<size_t>(M) * stride_of(max_rank) * sizeof(float) * most_slices(M, K, dtype);
 }
 
 size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, int32_t R, int32_t max_rank,
                                   int32_t dtype) {
-    const size_t rows = static_cast<size_t>(M) * static_cast<size_t>(max_rank) * sizeof(float);
-    const int most = most_slices(M, N, dtype);
-    const int Z = outer_split(M, K, N, E, max_rank, dtype).Z;
-    size_t n = round16(rows);
-    if (most > 1) n += round16(rows * static_cast<size_t>(most));
+    const size_t rows = static_cast<size_t>(M) * stride_of(max_rank) * sizeof(float);
+    const int most = most_slices(M, N, dtype), Z = outer_split(M, K, N, E, max_rank, dtype).Z;
+    size_t n = rows * (most > 1 ? most + 1 : 1);
     if (Z > 1) n += static_cast<size_t>(Z) * static_cast<size_t>(R) * (static_cast<size_t>(K) + N) * sizeof(float);
     return n;
 }

@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "ss1_device.h"
+#include "ss1_dma.h"
 #include "ss1_ops.h"
 
 namespace ss1 {
@@ -33,6 +34,7 @@ using dev::bf16x8;
 using dev::buf_load16;
 using dev::f32x4;
 using dev::make_rsrc;
+using dev::pair_lane_mask;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
@@ -113,6 +115,11 @@ __device__ __forceinline__ f32x4 mma(const float*, uint4 a, uint4 b, f32x4 c) {
     return c;
 }
 
+// Two loads of 8 rows x 128 bytes -> two operands of 16 rows x 64 bytes.
+__device__ __forceinline__ void pair_operands(uint4 a, uint4 b, uint32_t lo8, uint4& t0, uint4& t1) {
+    dev::pair_operands(a, b, lo8, t0, t1);
+}
+
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
@@ -142,16 +149,18 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
 
 // ---------------------------------------------------------------------- shrink
 // One block: a piece and a slice q of K; its waves split the slice, their
-// tiles are added in LDS.  A wave's operands come straight from global memory,
-// 64 bytes of 16 rows at a time.  part[q][m][stride], columns past the rank 0.
+// tiles are added in LDS.  A wave's operands come straight from global memory
+// in whole 128-byte lines.  part[q][m][stride], columns past the rank 0.
 template <typename T, int TT, int RT>
 __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,
                                             int stride, float scale, f32x4* red) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t Kb = static_cast<uint32_t>(K) * sizeof(T);
-    const int units = static_cast<int>((Kb + 63) / 64);
-    const int u0 = static_cast<int>(static_cast<int64_t>(units) * (q * kWaves + wave) / (Q * kWaves));
-    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (q * kWaves + wave + 1) / (Q * kWaves));
+    const int units = static_cast<int>((Kb + 127) / 128);
+    // the slice's units go to the waves in turn, so that the block reads each
+    // row in one run of memory
+    const int u0 = static_cast<int>(static_cast<int64_t>(units) * q / Q);
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (q + 1) / Q);
     const auto rx = make_rsrc(x + static_cast<size_t>(pc.begin) * K, static_cast<uint32_t>(pc.n) * Kb);
     const auto ra = make_rsrc(A + static_cast<size_t>(pc.first) * K, static_cast<uint32_t>(pc.rank) * Kb);
     f32x4 acc[TT][RT];
@@ -159,27 +168,38 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
     for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0, 0, 0, 0};
-    const uint32_t lane_off = row * Kb + 16 * g;
+    // a load covers 8 rows x 128 bytes; pair_operands makes two operands of
+    // 16 rows x 64 bytes from two loads
+    const uint32_t piece = 16u * ((lane >> 4) + 4 * ((lane >> 3) & 1)), lo8 = pair_lane_mask(lane);
+    const uint32_t lane_off = (lane & 7) * Kb + piece;
     // units whose loads are in flight together (past the wave's share or the
     // row: zeros)
-    constexpr int UN = RT == 8 ? 2 : 4;
-    for (int ub = u0; ub < u1; ub += UN) {
-        uint4 xf[UN][TT], af[UN][RT];
+    constexpr int UN = TT + RT <= 4 ? 2 : 1;
+    for (int ub = u0 + wave * UN; ub < u1; ub += UN * kWaves) {
+        uint4 xf[UN][TT][2], af[UN][RT][2];
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            const uint32_t at = 64u * (ub + u);
-            const uint32_t off = ub + u < u1 && at + 16 * g < Kb ? lane_off + at : kOutside;
+            const uint32_t at = 128u * (ub + u);
+            const uint32_t off = ub + u < u1 && at + piece < Kb ? lane_off + at : kOutside;
 #pragma unroll
-            for (int t = 0; t < TT; ++t) xf[u][t] = buf_load16(rx, off + t * 16 * Kb, 0);
+            for (int t = 0; t < 2 * TT; ++t) xf[u][t / 2][t % 2] = buf_load16(rx, off + t * 8 * Kb, 0);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) af[u][r] = buf_load16(ra, off + r * 16 * Kb, 0);
+            for (int r = 0; r < 2 * RT; ++r) af[u][r / 2][r % 2] = buf_load16(ra, off + r * 8 * Kb, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);  // or each load sinks to its first use
 #pragma unroll
-        for (int u = 0; u < UN; ++u)
+        for (int u = 0; u < UN; ++u) {
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
+            for (int t = 0; t < TT; ++t) pair_operands(xf[u][t][0], xf[u][t][1], lo8, xf[u][t][0], xf[u][t][1]);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) acc[t][r] = mma(x, xf[u][t], af[u][r], acc[t][r]);
+            for (int r = 0; r < RT; ++r) {
+                pair_operands(af[u][r][0], af[u][r][1], lo8, af[u][r][0], af[u][r][1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) acc[t][r] = mma(x, xf[u][t][h], af[u][r][h], acc[t][r]);
+            }
+        }
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -230,6 +250,114 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const 
             shrink_body<T, TT, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, stride, scale, red);
         else
             shrink_body<T, TT, RT>(pc, x, A, out, K, Q, q, stride, scale, red);
+    }
+}
+
+// The shrink of long segments: 64 tokens and a slice of K a block, in stages
+// of 128 bytes of every row of x and A.  Each stage goes from global memory
+// straight to LDS (whole lines, no registers), a ring of kStages of them deep;
+// wave w takes tokens 16 w .. 16 w + 15 of the tile and all ranks, so nothing
+// has to be added across the waves.
+constexpr int kStages = 3;
+
+// Wave-wide loads (8 rows x 128 bytes) of a stage, the same number a wave;
+// rows of A past the rank read as zero.
+constexpr int stage_loads(int RT) { return (8 + 2 * RT + kWaves - 1) / kWaves; }
+
+template <typename T, int RT>
+__device__ __forceinline__ void shrink_tile_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q,
+                                                 int q, int stride, float scale, uint8_t* ring) {
+    constexpr int L = stage_loads(RT), BYTES = L * kWaves * 1024;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t Kb = static_cast<uint32_t>(K) * sizeof(T);
+    const int units = static_cast<int>((Kb + 127) / 128);
+    const int u0 = static_cast<int>(static_cast<int64_t>(units) * q / Q);
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (q + 1) / Q);
+    const auto rx = dev::dma_rsrc(x + static_cast<size_t>(pc.begin) * K, static_cast<uint32_t>(pc.n) * Kb);
+    const auto ra = dev::dma_rsrc(A + static_cast<size_t>(pc.first) * K, static_cast<uint32_t>(pc.rank) * Kb);
+    const uint32_t lds = dev::lds_address(ring);
+    // row p of a stage holds piece i of its 128 bytes at slot i ^ key(p)
+    const auto issue = [&](int u, int buffer) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int group = i * kWaves + wave, row = 8 * group + (lane >> 3);
+            const uint32_t at = 128u * u + 16 * ((lane & 7) ^ dev::swz_key<128>(row));
+            const bool in = u < u1 && at < Kb;
+            const uint32_t to = lds + buffer * BYTES + group * 1024;
+            if (group < 8)
+                dev::lds_dma16(rx, to, in ? row * Kb + at : kOutside, 0);
+            else
+                dev::lds_dma16(ra, to, in ? (row - 64) * Kb + at : kOutside, 0);
+        }
+    };
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+    __syncthreads();  // the ring's last readers
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) issue(u0 + s, s);
+    const int m = 16 * wave + (lane & 15), g = lane >> 4;
+    int buffer = 0;
+    for (int u = u0; u < u1; ++u) {
+        // this stage has landed, and everyone is done with the one before it,
+        // whose place the next stage takes
+        dev::dma_stage_barrier<L*(kStages - 2)>();
+        issue(u + kStages - 1, buffer == 0 ? kStages - 1 : buffer - 1);
+        const uint8_t* stage = ring + buffer * BYTES;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 xf = *reinterpret_cast<const uint4*>(stage + m * 128 + 16 * ((4 * h + g) ^ dev::swz_key<128>(m)));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int row = 64 + 16 * r + (lane & 15);
+                const uint4 af =
+                    *reinterpret_cast<const uint4*>(stage + row * 128 + 16 * ((4 * h + g) ^ dev::swz_key<128>(row)));
+                acc[r] = mma(x, xf, af, acc[r]);
+            }
+        }
+        buffer = buffer + 1 == kStages ? 0 : buffer + 1;
+    }
+    dev::dma_stage_barrier<0>();  // nothing in flight into the ring
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int j = 16 * r + (lane & 15);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int t = 16 * wave + 4 * g + k;
+            if (j < stride && t < pc.n) out[static_cast<size_t>(t) * stride + j] = j < pc.rank ? acc[r][k] * scale : 0.0f;
+        }
+    }
+    const int rest = stride - 16 * RT;  // columns past the tiles are zero
+    if (rest > 0)
+        for (int i = threadIdx.x; i < pc.n * rest; i += kThreads)
+            out[static_cast<size_t>(i / rest) * stride + 16 * RT + i % rest] = 0.0f;
+}
+
+template <typename T, int RT>
+__global__ __launch_bounds__(kThreads) void shrink_tile_kernel(AdapterView ad, const T* __restrict__ x,
+                                                               const T* __restrict__ A, float* __restrict__ part,
+                                                               int stride, int K, int Q, int scaled, int64_t items) {
+    __shared__ __align__(1024) uint8_t ring[kStages * stage_loads(RT) * kWaves * 1024];
+    __shared__ Found found;
+    if (threadIdx.x == 0) found.p = -1;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int q = static_cast<int>(item % Q);
+        const Piece pc = find_piece(ad, 64, static_cast<int>(item / Q), &found);
+        if (pc.n == 0) continue;
+        float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
+        const float scale = scaled ? pc.scale : 1.0f;
+        if (pc.rank == 0) {
+            for (int i = threadIdx.x; i < pc.n * stride; i += kThreads) out[i] = 0.0f;
+            continue;
+        }
+        if (RT == 1 || pc.rank <= 16)
+            shrink_tile_body<T, 1>(pc, x, A, out, K, Q, q, stride, scale, ring);
+        else if (RT == 2 || pc.rank <= 32)
+            shrink_tile_body<T, RT < 2 ? RT : 2>(pc, x, A, out, K, Q, q, stride, scale, ring);
+        else if (RT == 4 || pc.rank <= 64)
+            shrink_tile_body<T, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, stride, scale, ring);
+        else
+            shrink_tile_body<T, RT>(pc, x, A, out, K, Q, q, stride, scale, ring);
     }
 }
 
@@ -695,12 +823,12 @@ constexpr int64_t kFill = 512;
 
 int esize(int32_t dtype) { return dtype == SS1_BF16 ? 2 : 4; }
 
-// Most slices of a shrink over `cols` inputs: at least 16 units of 64 bytes a
+// Most slices of a shrink (the workspace's) over `cols` inputs: at least 8 units of 128 bytes a
 // block, and no more than fill the card.
 int most_slices(int64_t M, int32_t cols, int32_t dtype) {
-    const int64_t units = (static_cast<int64_t>(cols) * esize(dtype) + 63) / 64;
-    int64_t q = units / 16;
-    const int64_t fill = 2 * kFill / ((M + 63) / 64 > 0 ? (M + 63) / 64 : 1);
+    const int64_t units = (static_cast<int64_t>(cols) * esize(dtype) + 127) / 128;
+    int64_t q = units / 8;
+    const int64_t fill = kFill / ((M + 63) / 64 > 0 ? (M + 63) / 64 : 1);
     if (q > fill) q = fill;
     if (q > 8) q = 8;
     return static_cast<int>(q < 1 ? 1 : q);
@@ -713,40 +841,34 @@ int tile_of(int64_t M, int64_t S) {
     return mean <= 24 ? 1 : mean <= 64 ? 2 : 4;
 }
 
-// ... of the shrink: more blocks, and fewer accumulators a wave.
-int shrink_tile_of(int64_t M, int64_t S) { return tile_of(M, S) > 1 ? 2 : 1; }
+// ... of the shrink: the two kernels have 16 and 64.
+int shrink_tile_of(int64_t M, int64_t S) { return tile_of(M, S) > 1 ? 4 : 1; }
 
 // Floats of one token's row of v in the workspace: 16-byte loads of 8 ranks.
 int stride_of(int32_t max_rank) { return (max_rank + 7) / 8 * 8; }
 
 unsigned grid_of(int64_t items) { return static_cast<unsigned>(items < kMaxBlocks ? items : kMaxBlocks); }
 
-template <typename T, int TT>
-void launch_shrink_tt(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int Q,
-                      int scaled, hipStream_t s) {
-    const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * TT) * Q;
-    const int rt = (a.ad.max_rank + 15) / 16;
-    auto k = rt <= 1 ? shrink_kernel<T, TT, 1> : rt <= 2 ? shrink_kernel<T, TT, 2>
-             : rt <= 4 ? shrink_kernel<T, TT, 4> : shrink_kernel<T, TT, 8>;
-    hipLaunchKernelGGL(k, dim3(grid_of(items)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
-                       static_cast<const T*>(A), part, stride, K, Q, scaled, items);
+// Slices of a call's shrink, at most most_slices(): enough blocks to fill the
+// card.
+int slices_of(const AdapterArgs& a, int K) {
+    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * shrink_tile_of(a.ad.M, a.ad.S));
+    const int64_t Q = kFill / pieces, most = most_slices(a.ad.M, K, a.dtype);
+    return static_cast<int>(std::max(int64_t(1), std::min(Q, most)));
 }
 
-// Slices of this call, at most most_slices().
 template <typename T>
 int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int scaled,
                   hipStream_t s) {
-    const int tt = shrink_tile_of(a.ad.M, a.ad.S);
-    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * tt);
-    int64_t Q = 2 * kFill / pieces;
-    const int most = most_slices(a.ad.M, K, a.dtype);
-    if (Q > most) Q = most;
-    if (Q < 1) Q = 1;
-    if (tt == 1)
-        launch_shrink_tt<T, 1>(a, x, A, part, stride, K, static_cast<int>(Q), scaled, s);
-    else
-        launch_shrink_tt<T, 2>(a, x, A, part, stride, K, static_cast<int>(Q), scaled, s);
-    return static_cast<int>(Q);
+    const int tt = shrink_tile_of(a.ad.M, a.ad.S), Q = slices_of(a, K), rt = (a.ad.max_rank + 15) / 16;
+    const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * tt) * Q;
+    auto k = tt == 1 ? (rt <= 1 ? shrink_kernel<T, 1, 1> : rt <= 2 ? shrink_kernel<T, 1, 2>
+                        : rt <= 4 ? shrink_kernel<T, 1, 4> : shrink_kernel<T, 1, 8>)
+                     : (rt <= 1 ? shrink_tile_kernel<T, 1> : rt <= 2 ? shrink_tile_kernel<T, 2>
+                        : rt <= 4 ? shrink_tile_kernel<T, 4> : shrink_tile_kernel<T, 8>);
+    hipLaunchKernelGGL(k, dim3(grid_of(items)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
+                       static_cast<const T*>(A), part, stride, K, Q, scaled, items);
+    return Q;
 }
 
 template <typename T, int TT>
@@ -786,10 +908,7 @@ void forward(const AdapterArgs& a, hipStream_t s) {
     int Q = 1;
     if (a.ad.max_rank > 0) {
         // a single slice with rows of v's own length writes v itself
-        const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * shrink_tile_of(a.ad.M, a.ad.S));
-        const bool direct = a.v && stride == a.ad.max_rank &&
-                            (2 * kFill / pieces <= 1 || most_slices(a.ad.M, a.K, a.dtype) == 1);
-        if (direct) part = a.v;
+        if (a.v && stride == a.ad.max_rank && slices_of(a, a.K) == 1) part = a.v;
         Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, s);
     }
     launch_expand<T>(a, part, stride, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.N, 1, s);

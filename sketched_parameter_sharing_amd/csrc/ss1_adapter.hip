@@ -45,12 +45,23 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 
 __device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint4 v) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.x, v.y, v.z, v.w}, r, voff, 0, 0);
+    // non-temporal: nothing here reads it again (prefill expand 66 -> 63 us)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.x, v.y, v.z, v.w}, r, voff, 0, 2);
+}
+
+// A value that the whole wave reads at one index: a scalar load.  The scalar
+// cache is not swept by the tensors that stream through the vector caches, so
+// the few dependent reads at the start of a block take a fraction of what they
+// do behind a queue of vector loads (prefill expand: see there).
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p, int i) {
+    typedef const __attribute__((address_space(4))) T* scalar_ptr;
+    return reinterpret_cast<scalar_ptr>(reinterpret_cast<uintptr_t>(p))[__builtin_amdgcn_readfirstlane(i)];
 }
 
 // First row and rank of adapter e, inside [0, R) whatever the arrays hold.
 __device__ __forceinline__ int rows_of(const AdapterView& ad, int e, int* first) {
-    const int r0 = clampi(ad.row[e], 0, ad.R), r1 = clampi(ad.row[e + 1], r0, ad.R);
+    const int r0 = clampi(uniform_load(ad.row, e), 0, ad.R), r1 = clampi(uniform_load(ad.row, e + 1), r0, ad.R);
     *first = r0;
     return min(r1 - r0, ad.max_rank);
 }
@@ -61,31 +72,22 @@ struct Piece {
     float scale;
 };
 
-// What find_piece leaves in LDS for the block.
-struct Found {
-    int p, s, begin, end, adapter;
-};
-
 // Piece p of the batch: with F(s) = s + offset[s] / TM, segment s has pieces
 // F(s) .. F(s+1) - 1, one for each tile of TM tokens that it touches (the last
-// may be empty), so no prefix sum over the segments is needed.  Every thread
-// of the block calls this; found->p is -1 before the first call.
-__device__ __forceinline__ Piece find_piece(const AdapterView& ad, int TM, int p, Found* found) {
+// may be empty), so no prefix sum over the segments is needed: a binary search
+// of p in F finds the segment.
+__device__ __forceinline__ Piece find_piece(const AdapterView& ad, int TM, int p) {
     Piece out{0, 0, 0, 0, 0.0f};
     int s = 0, b = 0, t = ad.M, e = -1;
     if (ad.S > 0) {
-        __syncthreads();  // the last piece's readers, or the first -1
-        for (int i = threadIdx.x; i < ad.S; i += kThreads) {
-            const int o0 = ad.seg[i], o1 = ad.seg[i + 1], a = ad.seg_adapter[i];
-            const int lo = clampi(o0, 0, ad.M), hi = clampi(o1, lo, ad.M);
-            if (p >= i + lo / TM && p <= i + hi / TM) *found = Found{p, i, lo, hi, a};
+        int hi = ad.S;
+        while (hi - s > 1) {
+            const int mid = s + (hi - s) / 2;
+            if (mid + clampi(uniform_load(ad.seg, mid), 0, ad.M) / TM <= p) s = mid; else hi = mid;
         }
-        __syncthreads();
-        if (__builtin_amdgcn_readfirstlane(found->p) != p) return out;  // offsets out of order
-        s = __builtin_amdgcn_readfirstlane(found->s);
-        b = __builtin_amdgcn_readfirstlane(found->begin);
-        t = __builtin_amdgcn_readfirstlane(found->end);
-        e = __builtin_amdgcn_readfirstlane(found->adapter);
+        e = uniform_load(ad.seg_adapter, s);
+        b = clampi(uniform_load(ad.seg, s), 0, ad.M);
+        t = clampi(uniform_load(ad.seg, s + 1), b, ad.M);
     }
     const int64_t tile = static_cast<int64_t>(p) - s;
     const int64_t from = max(int64_t(b), tile * TM), to = min(int64_t(t), (tile + 1) * TM);
@@ -94,7 +96,7 @@ __device__ __forceinline__ Piece find_piece(const AdapterView& ad, int TM, int p
     out.n = static_cast<int>(to - from);
     if (e >= 0 && e < ad.E) {
         out.rank = rows_of(ad, e, &out.first);
-        out.scale = ad.scale[e];
+        out.scale = uniform_load(ad.scale, e);
     }
     return out;
 }
@@ -145,6 +147,18 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
         f[2 * d] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         f[2 * d + 1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
+}
+
+// A lane's float32 values of v as operands: hi and lo (bf16), or themselves.
+__device__ __forceinline__ void rank_operands(const __bf16*, const float (&v)[8], uint4 (&f)[2]) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(v[j], &hi[j], &lo[j]);
+    f[0] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+    f[1] = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+}
+__device__ __forceinline__ void rank_operands(const float*, const float (&v)[4], uint4 (&f)[1]) {
+    f[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
 // ---------------------------------------------------------------------- shrink
@@ -229,11 +243,9 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const 
                                                           const T* __restrict__ A, float* __restrict__ part, int stride,
                                                           int K, int Q, int scaled, int64_t items) {
     __shared__ f32x4 red[kWaves * RT * 64];
-    __shared__ Found found;
-    if (threadIdx.x == 0) found.p = -1;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int q = static_cast<int>(item % Q);
-        const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q), &found);
+        const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
         float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
         const float scale = scaled ? pc.scale : 1.0f;
@@ -338,11 +350,9 @@ __global__ __launch_bounds__(kThreads) void shrink_tile_kernel(AdapterView ad, c
                                                                const T* __restrict__ A, float* __restrict__ part,
                                                                int stride, int K, int Q, int scaled, int64_t items) {
     __shared__ __align__(1024) uint8_t ring[kStages * stage_loads(RT) * kWaves * 1024];
-    __shared__ Found found;
-    if (threadIdx.x == 0) found.p = -1;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int q = static_cast<int>(item % Q);
-        const Piece pc = find_piece(ad, 64, static_cast<int>(item / Q), &found);
+        const Piece pc = find_piece(ad, 64, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
         float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
         const float scale = scaled ? pc.scale : 1.0f;
@@ -426,9 +436,28 @@ __device__ __forceinline__ uint4 pack(const float*, const f32x4 (&acc)[4], int i
                       __float_as_uint(acc[3][i]));
 }
 
+// Tokens without an adapter: y = base (zeros without one) in `wide` 16-byte
+// columns from c0 on, and v = 0.
+template <typename T>
+__device__ __forceinline__ void without_adapter(const Piece& pc, const T* base, T* y, float* v_out, int v_stride,
+                                                int v_cols, int N, int c0, int wide) {
+    if (v_out)
+        for (int i = threadIdx.x; i < pc.n * v_cols; i += kThreads)
+            v_out[static_cast<size_t>(pc.begin + i / v_cols) * v_stride + i % v_cols] = 0.0f;
+    if (base == y) return;
+    const int row = static_cast<int>(static_cast<uint32_t>(N) * sizeof(T) / 16);
+    wide = min(wide, row - c0);
+    const size_t at = static_cast<size_t>(pc.begin) * N;
+    for (int i = threadIdx.x; i < pc.n * wide; i += kThreads) {
+        const size_t o = static_cast<size_t>(i / wide) * row + c0 + i % wide;
+        reinterpret_cast<uint4*>(y + at)[o] =
+            base ? reinterpret_cast<const uint4*>(base + at)[o] : make_uint4(0, 0, 0, 0);
+    }
+}
+
 template <typename T, int TT, int KU>
 __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
-                                            int max_rank, const T* B, const T* base, T* y, float* v_out, int N, int tile0,
+                                            int v_stride, int v_cols, const T* B, const T* base, T* y, float* v_out, int N, int tile0,
                                             int tiles, float scale, uint4* frags) {
     using U = Unit<T>;
     constexpr int GROUP = U::kRanks / 4;  // ranks of one operand lane
@@ -442,7 +471,7 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
         const uint32_t col = 16u * (static_cast<uint32_t>(tile) * (kThreads / 4) + wave * 16 + c);
         return col < Nb ? col : kOutside;
     };
-    // rows of B and of base (16 tokens from 16 t on) in this lane's columns
+    // rows of B and of base (4 g + i of 16 tokens each) in this lane's columns
     uint4 rows[KU][U::kLoads], old[4];
     // (a row's offset is under 2^31, so kOutside plus it stays outside)
     const auto fetch_rows = [&](uint32_t col) {
@@ -461,13 +490,17 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
         }
     };
     const auto fetch_base = [&](int t, uint32_t col, uint4 (&to)[4]) {
-        const uint32_t at = (16 * t + 4 * g) * Nb + col;
+        uint32_t at = (16 * t + 4 * g) * Nb + col;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = buf_load16(rs, at + i * Nb, 0);
+        for (int i = 0; i < 4; ++i) {
+            to[i] = buf_load16(rs, at, 0);
+            at += Nb;
+        }
     };
     // in flight while v is staged
     fetch_rows(column(tile0));
     fetch_base(0, column(tile0), old);
+    __syncthreads();  // the last piece's readers of frags
     // v of the piece, summed over the slices of K in order (columns past the
     // rank are zero there; the stride is a multiple of 8)
 #pragma unroll 1
@@ -492,7 +525,8 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
             }
             if (v_out)
                 for (int j = 0; j < GROUP; ++j)
-                    if (r + j < max_rank) v_out[static_cast<size_t>(pc.begin + m) * max_rank + r + j] = v[j / 4][j % 4];
+                    if (r + j < v_cols)
+                        v_out[static_cast<size_t>(pc.begin + m) * v_stride + r + j] = v[j / 4][j % 4];
         }
         float scaled[GROUP];
 #pragma unroll
@@ -500,9 +534,9 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
         stage_one(B, frags + ((m >> 4) * KU + unit) * U::kFrags * 64, m & 15, gi, scaled);
     }
     const int past = KU * U::kRanks;  // columns that no unit covers are zero
-    if (v_out && past < max_rank)
-        for (int i = threadIdx.x; i < pc.n * (max_rank - past); i += kThreads)
-            v_out[static_cast<size_t>(pc.begin + i / (max_rank - past)) * max_rank + past + i % (max_rank - past)] = 0.0f;
+    if (v_out && past < v_cols)
+        for (int i = threadIdx.x; i < pc.n * (v_cols - past); i += kThreads)
+            v_out[static_cast<size_t>(pc.begin + i / (v_cols - past)) * v_stride + past + i % (v_cols - past)] = 0.0f;
     __syncthreads();
     for (int tile = tile0; tile < tile0 + tiles; ++tile) {
         const uint32_t col = column(tile);
@@ -512,7 +546,10 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
         }
         uint4 f[KU][U::kCols];
 #pragma unroll
-        for (int k = 0; k < KU; ++k) column_operands(B, rows[k], f[k]);
+        for (int k = 0; k < KU; ++k) {
+            column_operands(B, rows[k], f[k]);
+            __builtin_amdgcn_sched_barrier(0);  // one unit's rows at a time
+        }
 #pragma unroll 1
         for (int t = 0; t < TT; ++t) {
             uint4 next[4];
@@ -528,11 +565,12 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
 #pragma unroll
                     for (int j = 0; j < U::kCols; ++j) acc[j] = mma(B, a, f[k][j], acc[j]);
                 }
-            const uint32_t at = (16 * t + 4 * g) * Nb + col;
+            uint32_t at = (16 * t + 4 * g) * Nb + col;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                buf_store16(ry, at + i * Nb, pack(B, acc, i));
+                buf_store16(ry, at, pack(B, acc, i));
                 old[i] = next[i];
+                at += Nb;
             }
         }
     }
@@ -541,50 +579,203 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
 template <typename T, int TT, int KU>
 __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, const float* __restrict__ part,
                                                              int stride, int Q, const T* __restrict__ B, const T* base, T* y,
-                                                          float* __restrict__ v_out, int N, int scaled, int columns,
-                                                          int per, int tiles, int64_t items) {
+                                                          float* __restrict__ v_out, int v_stride, int v_cols, int N,
+                                                          int scaled, int columns, int per, int tiles, int64_t items) {
     __shared__ uint4 frags[TT * KU * Unit<T>::kFrags * 64];
-    __shared__ Found found;
-    if (threadIdx.x == 0) found.p = -1;
     constexpr int TM = 16 * TT;
     const size_t slice = static_cast<size_t>(ad.M) * stride;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int cg = static_cast<int>(item % columns);
-        const Piece pc = find_piece(ad, TM, static_cast<int>(item / columns), &found);
+        const Piece pc = find_piece(ad, TM, static_cast<int>(item / columns));
         if (pc.n == 0) continue;
         const int tile0 = cg * per, count = min(per, tiles - tile0);
         float* vo = cg == 0 ? v_out : nullptr;
         if (pc.rank == 0) {
-            if (vo)
-                for (int i = threadIdx.x; i < pc.n * ad.max_rank; i += kThreads)
-                    vo[static_cast<size_t>(pc.begin) * ad.max_rank + i] = 0.0f;
-            if (base == y) continue;
-            // a copy of the block's columns (zeros without a base)
-            const uint32_t Nb = static_cast<uint32_t>(N) * sizeof(T);
-            const uint32_t c0 = static_cast<uint32_t>(tile0) * kThreads / 4, c1 = min((tile0 + count) * kThreads / 4u, Nb / 16);
-            const int wide = static_cast<int>(c1 - c0);
-            const size_t at = static_cast<size_t>(pc.begin) * N;
-            for (int i = threadIdx.x; i < pc.n * wide; i += kThreads) {
-                const size_t o = static_cast<size_t>(i / wide) * (Nb / 16) + c0 + i % wide;
-                reinterpret_cast<uint4*>(y + at)[o] =
-                    base ? reinterpret_cast<const uint4*>(base + at)[o] : make_uint4(0, 0, 0, 0);
-            }
+            without_adapter(pc, base, y, vo, v_stride, v_cols, N, tile0 * kThreads / 4, count * kThreads / 4);
             continue;
         }
         const float scale = scaled ? pc.scale : 1.0f;
         constexpr int R = Unit<T>::kRanks;
         if (KU == 1 || pc.rank <= R)
-            expand_body<T, TT, 1>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, 1>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
         else if (KU == 2 || pc.rank <= 2 * R)
-            expand_body<T, TT, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
         else if (KU == 4 || pc.rank <= 4 * R)
-            expand_body<T, TT, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
         else
-            expand_body<T, TT, KU>(pc, part, slice, Q, stride, ad.max_rank, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, TT, KU>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
     }
 }
 
-// The slices of a shrink joined in order, for the outer products.
+// The expand of long segments.  One block: 64 tokens, wave w the tokens
+// 16 w .. 16 w + 15 with their v in registers, and `tiles` column tiles of 16
+// vectors one after the other.  A tile's operands of B are made once for the
+// four waves, in LDS, by the waves in turn (rank unit k by wave k % 4), and
+// the next tile's rows of B and base are in flight meanwhile: one barrier a
+// tile, and few enough registers for four to five blocks a compute unit.
+template <typename T, int KU>
+__device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
+                                                 const T* B, const T* base, T* y, float* v_out, int v_stride,
+                                                 int v_cols, int N, int tile0, int tiles, float scale, uint4* bt) {
+    using U = Unit<T>;
+    constexpr int GROUP = U::kRanks / 4, OWN = (KU + kWaves - 1) / kWaves, BUF = KU * U::kCols * 64;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const uint32_t Nb = static_cast<uint32_t>(N) * sizeof(T);
+    const auto rb = make_rsrc(B + static_cast<size_t>(pc.first) * N, static_cast<uint32_t>(pc.rank) * Nb);
+    const auto ry = make_rsrc(y + static_cast<size_t>(pc.begin) * N, static_cast<uint32_t>(pc.n) * Nb);
+    const auto rs = make_rsrc((base ? base : y) + static_cast<size_t>(pc.begin) * N,
+                              base ? static_cast<uint32_t>(pc.n) * Nb : 0u);
+    const auto column = [&](int tile) {  // (a row's offset is under 2^31, so kOutside plus it stays outside)
+        const uint32_t col = 16u * (static_cast<uint32_t>(tile) * 16 + c);
+        return tile < tile0 + tiles && col < Nb ? col : kOutside;
+    };
+    uint4 rows[OWN][U::kLoads], old[4];
+    const auto fetch_rows = [&](uint32_t col) {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            if (wave + o * kWaves >= KU) break;
+            uint32_t at = ((wave + o * kWaves) * U::kRanks + GROUP * g) * Nb + col;
+#pragma unroll
+            for (int i = 0; i < U::kLoads; ++i) {
+                rows[o][i] = buf_load16(rb, at, 0);
+                at += Nb;
+            }
+        }
+    };
+    const auto stage_rows = [&](uint4* to) {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            if (wave + o * kWaves >= KU) break;
+            uint4 f[U::kCols];
+            column_operands(B, rows[o], f);
+#pragma unroll
+            for (int j = 0; j < U::kCols; ++j) to[((wave + o * kWaves) * U::kCols + j) * 64 + lane] = f[j];
+        }
+    };
+    const auto fetch_base = [&](uint32_t col, uint4 (&to)[4]) {
+        uint32_t at = (16 * wave + 4 * g) * Nb + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            to[i] = buf_load16(rs, at, 0);
+            at += Nb;
+        }
+    };
+    fetch_rows(column(tile0));
+    fetch_base(column(tile0), old);
+    // v of this lane's token, summed over the slices of K in order (columns
+    // past the rank are zero there; the stride is a multiple of 8)
+    uint4 va[KU][U::kFrags];
+    const int m = 16 * wave + c;
+    f32x4 v[KU][GROUP / 4];
+#pragma unroll
+    for (int k = 0; k < KU; ++k)
+#pragma unroll
+        for (int j = 0; j < GROUP / 4; ++j) v[k][j] = f32x4{0, 0, 0, 0};
+    const f32x4* from =
+        reinterpret_cast<const f32x4*>(part + static_cast<size_t>(pc.begin + min(m, pc.n - 1)) * stride);
+    for (int q0 = 0; q0 < Q; q0 += 2) {  // two slices' loads together
+        f32x4 w[2][KU][GROUP / 4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int k = 0; k < KU; ++k)
+#pragma unroll
+                for (int j = 0; j < GROUP / 4; ++j)
+                    w[q][k][j] = from[min(q0 + q, Q - 1) * (slice / 4) +
+                                      min(k * U::kRanks + GROUP * g, stride - GROUP) / 4 + j];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int k = 0; k < KU; ++k)
+#pragma unroll
+                for (int j = 0; j < GROUP / 4; ++j)
+                    if (q0 + q < Q) v[k][j] += w[q][k][j];
+    }
+#pragma unroll
+    for (int k = 0; k < KU; ++k) {
+        const int r = k * U::kRanks + GROUP * g;
+        const bool real = m < pc.n && r < stride;
+        if (v_out && real)
+            for (int j = 0; j < GROUP; ++j)
+                if (r + j < v_cols) v_out[static_cast<size_t>(pc.begin + m) * v_stride + r + j] = v[k][j / 4][j % 4];
+        float scaled[GROUP];
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) scaled[j] = real ? v[k][j / 4][j % 4] * scale : 0.0f;
+        rank_operands(B, scaled, va[k]);
+    }
+    const int past = KU * U::kRanks;  // columns that no unit covers are zero
+    if (v_out && past < v_cols)
+        for (int i = threadIdx.x; i < pc.n * (v_cols - past); i += kThreads)
+            v_out[static_cast<size_t>(pc.begin + i / (v_cols - past)) * v_stride + past + i % (v_cols - past)] = 0.0f;
+    __syncthreads();  // the last piece's readers of bt
+    stage_rows(bt);
+    int cur = 0;
+#pragma unroll 1
+    for (int tile = tile0; tile < tile0 + tiles; ++tile) {
+        const uint32_t col = column(tile), ahead = column(tile + 1);
+        fetch_rows(ahead);
+        uint4 next[4];
+        fetch_base(ahead, next);
+        // LDS only: the loads stay in flight across the barrier
+        dev::lds_barrier();
+        f32x4 acc[U::kCols];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
+        const uint4* bc = bt + cur * BUF + lane;
+#pragma unroll
+        for (int k = 0; k < KU; ++k)
+#pragma unroll
+            for (int j = 0; j < U::kCols; ++j) {
+                const uint4 f = bc[(k * U::kCols + j) * 64];
+#pragma unroll
+                for (int h = 0; h < U::kFrags; ++h) acc[j] = mma(B, va[k][h], f, acc[j]);
+            }
+        uint32_t at = (16 * wave + 4 * g) * Nb + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            buf_store16(ry, at, pack(B, acc, i));
+            old[i] = next[i];
+            at += Nb;
+        }
+        cur ^= 1;
+        if (tile + 1 < tile0 + tiles) stage_rows(bt + cur * BUF);
+    }
+}
+
+template <typename T, int KU>
+__global__ __launch_bounds__(kThreads) void expand_tile_kernel(AdapterView ad, const float* __restrict__ part,
+                                                               int stride, int Q, const T* __restrict__ B,
+                                                               const T* base, T* y, float* __restrict__ v_out,
+                                                               int v_stride, int v_cols, int N, int scaled,
+                                                               int columns, int per, int tiles, int64_t items) {
+    __shared__ uint4 bt[2 * KU * Unit<T>::kCols * 64];
+    const size_t slice = static_cast<size_t>(ad.M) * stride;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cg = static_cast<int>(item % columns);
+        const Piece pc = find_piece(ad, 64, static_cast<int>(item / columns));
+        if (pc.n == 0) continue;
+        const int tile0 = cg * per, count = min(per, tiles - tile0);
+        float* vo = cg == 0 ? v_out : nullptr;
+        if (pc.rank == 0) {
+            without_adapter(pc, base, y, vo, v_stride, v_cols, N, tile0 * 16, count * 16);
+            continue;
+        }
+        const float scale = scaled ? pc.scale : 1.0f;
+        constexpr int R = Unit<T>::kRanks;
+        if (KU == 1 || pc.rank <= R)
+            expand_tile_body<T, 1>(pc, part, slice, Q, stride, B, base, y, vo, v_stride, v_cols, N, tile0, count, scale, bt);
+        else if (KU == 2 || pc.rank <= 2 * R)
+            expand_tile_body<T, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, B, base, y, vo, v_stride, v_cols, N, tile0, count, scale, bt);
+        else if (KU == 4 || pc.rank <= 4 * R)
+            expand_tile_body<T, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, B, base, y, vo, v_stride, v_cols, N, tile0, count, scale, bt);
+        else
+            expand_tile_body<T, KU>(pc, part, slice, Q, stride, B, base, y, vo, v_stride, v_cols, N, tile0, count, scale, bt);
+    }
+}
+
+// The slices of a shrink joined in order, where no expand does it.
 __global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __restrict__ part, float* __restrict__ out,
                                                                size_t n, int Q) {
     for (size_t i = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n;
@@ -612,18 +803,6 @@ struct OuterJob {
 };
 
 constexpr int kWindow = 256;  // tokens listed at a time
-
-// v of this lane's rank over its tokens as operands; h = 0, 1: hi, lo.
-__device__ __forceinline__ void rank_operands(const __bf16*, const float (&v)[8], uint4 (&f)[2]) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) split(v[j], &hi[j], &lo[j]);
-    f[0] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-    f[1] = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
-}
-__device__ __forceinline__ void rank_operands(const float*, const float (&v)[4], uint4 (&f)[1]) {
-    f[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
 
 // NEAR: x, dy and v are under 2^32 bytes each, so a row is a 32-bit offset of
 // one buffer descriptor, and an offset past its end reads as zero.
@@ -769,7 +948,7 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
             }
         }
         if (wave == 0 && inside) {
-            const float scale = job.scaled ? ad.scale[e] : 1.0f;
+            const float scale = job.scaled ? uniform_load(ad.scale, e) : 1.0f;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
 #pragma unroll
@@ -871,34 +1050,26 @@ int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* par
     return Q;
 }
 
-template <typename T, int TT>
-void launch_expand_tt(const AdapterArgs& a, const float* part, int stride, int Q, const void* B, void* y, float* v_out, int N,
-                      int scaled, hipStream_t s) {
-    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * TT);
-    const int tiles = (N + 64 * Unit<T>::kCols - 1) / (64 * Unit<T>::kCols);
-    // a block takes several column tiles (v is staged once) while the card stays full
-    int64_t per = pieces * tiles / (4 * kFill);
-    if (per < 1) per = 1;
-    if (per > tiles) per = tiles;
+// v_out: where the summed v goes too (v_cols columns, rows v_stride apart), or
+// null.
+template <typename T>
+void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, const void* B, void* y, float* v_out,
+                   int v_stride, int v_cols, int N, int scaled, hipStream_t s) {
+    const bool tile64 = tile_of(a.ad.M, a.ad.S) > 1;
+    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, tile64 ? 64 : 16);
+    const int wide = (tile64 ? 16 : 64) * Unit<T>::kCols, tiles = (N + wide - 1) / wide;
+    // a block takes several column tiles (v is read once) while the card stays full
+    const int64_t per = std::max(int64_t(1), std::min(int64_t(tiles), pieces * tiles / (2 * kFill)));
     const int columns = static_cast<int>((tiles + per - 1) / per);
     const int ku = (a.ad.max_rank + Unit<T>::kRanks - 1) / Unit<T>::kRanks;
-    auto k = ku <= 1 ? expand_kernel<T, TT, 1> : ku <= 2 ? expand_kernel<T, TT, 2>
-             : (sizeof(T) == 2 || ku <= 4) ? expand_kernel<T, TT, 4> : expand_kernel<T, TT, sizeof(T) == 2 ? 4 : 8>;
+    constexpr int MOST = sizeof(T) == 2 ? 4 : 8;
+    auto k = tile64 ? (ku <= 1 ? expand_tile_kernel<T, 1> : ku <= 2 ? expand_tile_kernel<T, 2>
+                       : ku <= 4 ? expand_tile_kernel<T, 4> : expand_tile_kernel<T, MOST>)
+                    : (ku <= 1 ? expand_kernel<T, 1, 1> : ku <= 2 ? expand_kernel<T, 1, 2>
+                       : ku <= 4 ? expand_kernel<T, 1, 4> : expand_kernel<T, 1, MOST>);
     hipLaunchKernelGGL(k, dim3(grid_of(pieces * columns)), dim3(kThreads), 0, s, a.ad, part, stride, Q,
-                       static_cast<const T*>(B), static_cast<const T*>(a.base), static_cast<T*>(y), v_out, N, scaled,
-                       columns, static_cast<int>(per), tiles, pieces * columns);
-}
-
-template <typename T>
-void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, const void* B, void* y, float* v_out, int N,
-                   int scaled, hipStream_t s) {
-    const int tt = tile_of(a.ad.M, a.ad.S);
-    if (tt == 1)
-        launch_expand_tt<T, 1>(a, part, stride, Q, B, y, v_out, N, scaled, s);
-    else if (tt == 2)
-        launch_expand_tt<T, 2>(a, part, stride, Q, B, y, v_out, N, scaled, s);
-    else
-        launch_expand_tt<T, 4>(a, part, stride, Q, B, y, v_out, N, scaled, s);
+                       static_cast<const T*>(B), static_cast<const T*>(a.base), static_cast<T*>(y), v_out, v_stride,
+                       v_cols, N, scaled, columns, static_cast<int>(per), tiles, pieces * columns);
 }
 
 template <typename T>
@@ -911,7 +1082,7 @@ void forward(const AdapterArgs& a, hipStream_t s) {
         if (a.v && stride == a.ad.max_rank && slices_of(a, a.K) == 1) part = a.v;
         Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, s);
     }
-    launch_expand<T>(a, part, stride, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.N, 1, s);
+    launch_expand<T>(a, part, stride, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.ad.max_rank, a.ad.max_rank, a.N, 1, s);
 }
 
 // How the outer products are split.
@@ -987,8 +1158,9 @@ void backward(const AdapterArgs& a, hipStream_t s) {
     int Q = 1;
     if ((a.dx || a.dA) && a.ad.max_rank > 0 && a.ad.M > 0)
         Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, s);
-    if (a.dx) launch_expand<T>(a, part, stride, Q, a.A, a.dx, nullptr, a.K, 0, s);
-    if (a.dA && Q > 1)
+    if (a.dx)  // leaves the sum of dv's slices for the outer products
+        launch_expand<T>(a, part, stride, Q, a.A, a.dx, Q > 1 && a.dA ? joined : nullptr, stride, stride, a.K, 0, s);
+    else if (a.dA && Q > 1)
         hipLaunchKernelGGL(join_slices_kernel,
                            dim3(static_cast<unsigned>(rows / 1024 < 4096 ? rows / 1024 + 1 : 4096)), dim3(kThreads), 0,
                            s, part, joined, rows, Q);

@@ -30,6 +30,7 @@ namespace ss1 {
 
 namespace {
 
+using dev::bf16x2;
 using dev::bf16x8;
 using dev::buf_load16;
 using dev::f32x4;
@@ -151,14 +152,46 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
 
 // A lane's float32 values of v as operands: hi and lo (bf16), or themselves.
 __device__ __forceinline__ void rank_operands(const __bf16*, const float (&v)[8], uint4 (&f)[2]) {
-    uint32_t hi[8], lo[8];
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) split(v[j], &hi[j], &lo[j]);
-    f[0] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-    f[1] = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+    for (int j = 0; j < 4; ++j) {
+        hi[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * j], v[2 * j + 1]}, bf16x2));
+        const float a = v[2 * j] - __uint_as_float(hi[j] << 16);
+        const float b = v[2 * j + 1] - __uint_as_float(hi[j] & 0xFFFF0000u);
+        lo[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+        // a value whose hi is infinite has no rest (inf - inf would make it a NaN)
+        const uint32_t full = hi[j] & 0x7F807F80u;
+        if ((full & 0x7F80u) == 0x7F80u) lo[j] &= 0xFFFF0000u;
+        if ((full >> 16) == 0x7F80u) lo[j] &= 0x0000FFFFu;
+    }
+    f[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    f[1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 __device__ __forceinline__ void rank_operands(const float*, const float (&v)[4], uint4 (&f)[1]) {
     f[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+// Rows of v of a piece copied to rows of `stride` floats: the outer products
+// gather 16 bytes at a time, which rows of any other length would let run past
+// the end of the array.
+struct Repack {
+    const float* from;  // [M][cols]; null: nothing to do
+    float* to;          // [M][stride]
+    int cols, stride;
+};
+
+__device__ __forceinline__ void repack_rows(const Repack& v, int begin, int n) {
+    for (int i = threadIdx.x; i < n * v.stride; i += kThreads) {
+        const size_t m = static_cast<size_t>(begin) + i / v.stride;
+        const int j = i % v.stride;
+        v.to[m * v.stride + j] = j < v.cols ? v.from[m * v.cols + j] : 0.0f;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void repack_kernel(Repack v, int M) {
+    for (int64_t m = static_cast<int64_t>(blockIdx.x) * 16; m < M; m += static_cast<int64_t>(gridDim.x) * 16)
+        repack_rows(v, static_cast<int>(m), static_cast<int>(min(int64_t(16), M - m)));
 }
 
 // ---------------------------------------------------------------------- shrink
@@ -241,12 +274,13 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
 template <typename T, int TT, int RT>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const T* __restrict__ x,
                                                           const T* __restrict__ A, float* __restrict__ part, int stride,
-                                                          int K, int Q, int scaled, int64_t items) {
+                                                          int K, int Q, int scaled, Repack v, int64_t items) {
     __shared__ f32x4 red[kWaves * RT * 64];
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int q = static_cast<int>(item % Q);
         const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
+        if (v.from && q == 0) repack_rows(v, pc.begin, pc.n);
         float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
         const float scale = scaled ? pc.scale : 1.0f;
         if (pc.rank == 0) {
@@ -348,12 +382,14 @@ __device__ __forceinline__ void shrink_tile_body(const Piece& pc, const T* x, co
 template <typename T, int RT>
 __global__ __launch_bounds__(kThreads) void shrink_tile_kernel(AdapterView ad, const T* __restrict__ x,
                                                                const T* __restrict__ A, float* __restrict__ part,
-                                                               int stride, int K, int Q, int scaled, int64_t items) {
+                                                               int stride, int K, int Q, int scaled, Repack v,
+                                                               int64_t items) {
     __shared__ __align__(1024) uint8_t ring[kStages * stage_loads(RT) * kWaves * 1024];
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int q = static_cast<int>(item % Q);
         const Piece pc = find_piece(ad, 64, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
+        if (v.from && q == 0) repack_rows(v, pc.begin, pc.n);
         float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
         const float scale = scaled ? pc.scale : 1.0f;
         if (pc.rank == 0) {
@@ -607,18 +643,57 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, con
     }
 }
 
+// OWN of the rows of one rank unit (from `row0` on, in this lane's columns) into
+// their places in the operands of the unit's columns, 64 operands apart in LDS.
+template <int OWN>
+__device__ __forceinline__ void stage_columns(const __bf16*, const uint4 (&rows)[OWN], uint4* unit, int row0) {
+    static_assert(OWN % 2 == 0 && OWN <= 8, "whole row pairs of one unit");
+    constexpr int P = OWN / 2;
+    typedef uint32_t part __attribute__((ext_vector_type(P), aligned(4 * P)));
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        uint32_t lo[P], hi[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const uint32_t a = (&rows[2 * q].x)[d], b = (&rows[2 * q + 1].x)[d];
+            lo[q] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            hi[q] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        }
+        uint32_t* l = reinterpret_cast<uint32_t*>(unit + 2 * d * 64) + row0 / 2;
+        uint32_t* h = reinterpret_cast<uint32_t*>(unit + (2 * d + 1) * 64) + row0 / 2;
+        *reinterpret_cast<part*>(l) = __builtin_bit_cast(part, lo);
+        *reinterpret_cast<part*>(h) = __builtin_bit_cast(part, hi);
+    }
+}
+template <int OWN>
+__device__ __forceinline__ void stage_columns(const float*, const uint4 (&rows)[OWN], uint4* unit, int row0) {
+    constexpr int P = OWN < 4 ? OWN : 4;
+    typedef uint32_t part __attribute__((ext_vector_type(P), aligned(4 * P)));
+#pragma unroll
+    for (int o = 0; o < OWN; o += P)  // OWN = 8: two units
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) w[q] = (&rows[o + q].x)[j];
+            *reinterpret_cast<part*>(reinterpret_cast<uint32_t*>(unit + (o / 4 * 4 + j) * 64) + row0) =
+                __builtin_bit_cast(part, w);
+        }
+}
+
 // The expand of long segments.  One block: 64 tokens, wave w the tokens
 // 16 w .. 16 w + 15 with their v in registers, and `tiles` column tiles of 16
 // vectors one after the other.  A tile's operands of B are made once for the
-// four waves, in LDS, by the waves in turn (rank unit k by wave k % 4), and
-// the next tile's rows of B and base are in flight meanwhile: one barrier a
-// tile, and few enough registers for four to five blocks a compute unit.
+// four waves, in LDS, a quarter of its rows by each, while the rows of B of the
+// tile after it and the base of the next are in flight: one barrier a tile,
+// and registers for four blocks a compute unit.
 template <typename T, int KU>
 __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
                                                  const T* B, const T* base, T* y, float* v_out, int v_stride,
                                                  int v_cols, int N, int tile0, int tiles, float scale, uint4* bt) {
     using U = Unit<T>;
-    constexpr int GROUP = U::kRanks / 4, OWN = (KU + kWaves - 1) / kWaves, BUF = KU * U::kCols * 64;
+    constexpr int GROUP = U::kRanks / 4, BUF = KU * U::kCols * 64;
+    constexpr int OWN = KU * U::kLoads / kWaves;  // rows of B that this wave stages
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     const uint32_t Nb = static_cast<uint32_t>(N) * sizeof(T);
@@ -630,28 +705,18 @@ __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* p
         const uint32_t col = 16u * (static_cast<uint32_t>(tile) * 16 + c);
         return tile < tile0 + tiles && col < Nb ? col : kOutside;
     };
-    uint4 rows[OWN][U::kLoads], old[4];
+    uint4 rows[OWN], old[4];
     const auto fetch_rows = [&](uint32_t col) {
 #pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            if (wave + o * kWaves >= KU) break;
-            uint32_t at = ((wave + o * kWaves) * U::kRanks + GROUP * g) * Nb + col;
-#pragma unroll
-            for (int i = 0; i < U::kLoads; ++i) {
-                rows[o][i] = buf_load16(rb, at, 0);
-                at += Nb;
-            }
+        for (int i = 0; i < OWN; ++i) {
+            const int row = wave * OWN + i;  // of the KU * kLoads that a lane group has
+            const int rank = row / U::kLoads * U::kRanks + GROUP * g + row % U::kLoads;
+            rows[i] = buf_load16(rb, rank * Nb + col, 0);
         }
     };
     const auto stage_rows = [&](uint4* to) {
-#pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            if (wave + o * kWaves >= KU) break;
-            uint4 f[U::kCols];
-            column_operands(B, rows[o], f);
-#pragma unroll
-            for (int j = 0; j < U::kCols; ++j) to[((wave + o * kWaves) * U::kCols + j) * 64 + lane] = f[j];
-        }
+        uint4* unit = to + wave * OWN / U::kLoads * U::kCols * 64 + lane;
+        stage_columns(B, rows, unit, wave * OWN % U::kLoads);
     };
     const auto fetch_base = [&](uint32_t col, uint4 (&to)[4]) {
         uint32_t at = (16 * wave + 4 * g) * Nb + col;
@@ -711,15 +776,18 @@ __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* p
             v_out[static_cast<size_t>(pc.begin + i / (v_cols - past)) * v_stride + past + i % (v_cols - past)] = 0.0f;
     __syncthreads();  // the last piece's readers of bt
     stage_rows(bt);
+    fetch_rows(column(tile0 + 1));
     int cur = 0;
 #pragma unroll 1
     for (int tile = tile0; tile < tile0 + tiles; ++tile) {
-        const uint32_t col = column(tile), ahead = column(tile + 1);
-        fetch_rows(ahead);
-        uint4 next[4];
-        fetch_base(ahead, next);
-        // LDS only: the loads stay in flight across the barrier
+        const uint32_t col = column(tile);
+        // this tile's operands are in LDS and the other half is free (LDS
+        // only: the loads stay in flight across the barrier)
         dev::lds_barrier();
+        stage_rows(bt + (cur ^ 1) * BUF);  // rows that had a whole tile's time to come
+        fetch_rows(column(tile + 2));
+        uint4 next[4];
+        fetch_base(column(tile + 1), next);
         f32x4 acc[U::kCols];
 #pragma unroll
         for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
@@ -740,12 +808,11 @@ __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* p
             at += Nb;
         }
         cur ^= 1;
-        if (tile + 1 < tile0 + tiles) stage_rows(bt + cur * BUF);
     }
 }
 
 template <typename T, int KU>
-__global__ __launch_bounds__(kThreads) void expand_tile_kernel(AdapterView ad, const float* __restrict__ part,
+__global__ __launch_bounds__(kThreads, KU <= 2 ? 4 : 2) void expand_tile_kernel(AdapterView ad, const float* __restrict__ part,
                                                                int stride, int Q, const T* __restrict__ B,
                                                                const T* base, T* y, float* __restrict__ v_out,
                                                                int v_stride, int v_cols, int N, int scaled,
@@ -787,10 +854,12 @@ __global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __re
 }
 
 // ----------------------------------------------------------------------- outer
-// dA and dB in one launch.  A block: one adapter, up to 16 RT of its ranks, 16
-// vectors of columns, part z of the tokens.  It lists the adapter's tokens
-// window by window in LDS (they may lie in many segments), its waves take
-// steps of the window in turn, and their tiles are added in LDS at the end.
+// dA and dB in one launch.  A block: one adapter, up to 16 RT of its ranks, 256
+// bytes of columns, part z of the tokens.  It lists the adapter's tokens window
+// by window in LDS (they may lie in many segments) and gathers their rows of x
+// and v, 32 tokens a stage, straight into a ring in LDS.  Wave w turns rank
+// tile w of a stage's v into operands, in place and one stage ahead, and takes
+// 64 bytes of the columns with all ranks: nothing is added across the waves.
 struct OuterJob {
     const float* v;  // [M][v_stride]
     const void* x;
@@ -802,27 +871,108 @@ struct OuterJob {
     int64_t first_item;
 };
 
-constexpr int kWindow = 256;  // tokens listed at a time
+constexpr int kWindow = 1024;  // tokens listed at a time, four a thread
+constexpr int kOuterStages = 4;
 
-// NEAR: x, dy and v are under 2^32 bytes each, so a row is a 32-bit offset of
-// one buffer descriptor, and an offset past its end reads as zero.
-template <typename T, int RT, bool NEAR>
+template <typename T, int RT>
+struct Outer {
+    using U = Unit<T>;
+    static constexpr int ROWS = U::kLoads;               // tokens of one operand lane
+    static constexpr int VT = RT < 2 ? 2 : RT;           // rank tiles staged (whole loads for every wave)
+    static constexpr int CT = 4 / sizeof(T);             // column tiles of a wave
+    static constexpr int XBYTES = 32 * 256, VBYTES = 32 * 64 * VT, BYTES = XBYTES + VBYTES;
+    static constexpr int LX = XBYTES / 1024 / kWaves, LV = VBYTES / 1024 / kWaves, L = LX + LV;
+
+    // LDS places: piece i (16 bytes) of row t is stored at i ^ key, so that the
+    // four lane groups of an operand read (rows ROWS apart) and consecutive
+    // rows both fall on different banks.
+    static __device__ __forceinline__ int x_key(int t) { return 4 * ((t / ROWS) & 3); }
+    static __device__ __forceinline__ int v_key(int t) { return 4 * ((t / ROWS + t) & (VT - 1)); }
+
+    // Eight (or twice four) tokens of this lane's rank as operands, in the bytes
+    // that they came from: the tile's 128 pieces hold operand h of lane l at
+    // number 64 h + l.
+    static __device__ __forceinline__ uint4* operand(uint8_t* v, int r, int h, int lane) {
+        const int q = 64 * h + lane, t = q >> 2;
+        return reinterpret_cast<uint4*>(v + t * 64 * VT + 16 * ((4 * r + (q & 3)) ^ v_key(t)));
+    }
+    static __device__ __forceinline__ float raw(const uint8_t* v, int r, int t, int c) {
+        return *reinterpret_cast<const float*>(v + t * 64 * VT + 16 * ((4 * r + (c >> 2)) ^ v_key(t)) + 4 * (c & 3));
+    }
+    static __device__ __forceinline__ uint32_t x_word(const uint8_t* x, int t, int w) {
+        return *reinterpret_cast<const uint32_t*>(x + t * 256 + 16 * ((w >> 2) ^ x_key(t)) + 4 * (w & 3));
+    }
+};
+
+// A lane's i-th of the 32 tokens of a stage: 8 in a row (bf16: one product of
+// 32), or 4 of each half (float32: two of 16).
+template <typename T>
+__device__ __forceinline__ int stage_token(int g, int i) {
+    return sizeof(T) == 2 ? 8 * g + i : 16 * (i / 4) + 4 * g + i % 4;
+}
+
+// v of this lane's rank over its eight tokens -> the two operands of the rank
+// tile: hi and lo of all of them (bf16), or the halves as they are (float32).
+__device__ __forceinline__ void stage_operands(const __bf16* t, const float (&f)[8], uint4 (&a)[2]) {
+    rank_operands(t, f, a);
+}
+__device__ __forceinline__ void stage_operands(const float*, const float (&f)[8], uint4 (&a)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        a[h] = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
+                          __float_as_uint(f[4 * h + 3]));
+}
+
+// One stage into a wave's accumulators: w holds this lane's eight tokens' 4
+// bytes of x (two bf16 columns, or one float32), a the rank operands.
+template <int RT>
+__device__ __forceinline__ void stage_products(const __bf16* t, const uint32_t (&w)[8], const uint4 (&a)[RT][2],
+                                               int rank, f32x4 (&acc)[RT][2]) {
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        lo[q] = __builtin_amdgcn_perm(w[2 * q + 1], w[2 * q], 0x05040100u);
+        hi[q] = __builtin_amdgcn_perm(w[2 * q + 1], w[2 * q], 0x07060302u);
+    }
+    const uint4 f0 = make_uint4(lo[0], lo[1], lo[2], lo[3]), f1 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        if (16 * r >= rank) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            acc[r][0] = mma(t, a[r][h], f0, acc[r][0]);
+            acc[r][1] = mma(t, a[r][h], f1, acc[r][1]);
+        }
+    }
+}
+template <int RT>
+__device__ __forceinline__ void stage_products(const float* t, const uint32_t (&w)[8], const uint4 (&a)[RT][2],
+                                               int rank, f32x4 (&acc)[RT][1]) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        if (16 * r >= rank) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            acc[r][0] = mma(t, a[r][h], make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]), acc[r][0]);
+    }
+}
+
+template <typename T, int RT>
 __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, OuterJob job0, OuterJob job1,
                                                             int rank_groups, int Z, int64_t items) {
-    using U = Unit<T>;
-    constexpr int ROWS = U::kLoads;         // tokens of one operand lane
-    constexpr int STEP = 4 * ROWS;          // tokens of one product
-    constexpr uint32_t kNone = 0xFFFFFFFFu;
-    __shared__ f32x4 red[2 * RT * U::kCols * 64];
-    __shared__ int tokens[kWindow];
-    __shared__ int ends[kThreads], starts[kThreads], wave_sum[kWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    using O = Outer<T, RT>;
+    __shared__ __align__(1024) uint8_t ring[kOuterStages * O::BYTES];
+    __shared__ int4 tokens[kWindow / 4];
+    __shared__ int ends[kThreads], starts[kThreads], wave_sum[kWaves], window_base;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int* token_at = reinterpret_cast<const int*>(tokens);
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const OuterJob& job = it >= job1.first_item ? job1 : job0;
         int64_t item = it - job.first_item;
         const int z = static_cast<int>(item % Z);
         item /= Z;
-        const int tiles = (job.cols + 16 * U::kCols - 1) / (16 * U::kCols);
+        const uint32_t row_bytes = static_cast<uint32_t>(job.cols) * sizeof(T), v_bytes = job.v_stride * 4u;
+        const int tiles = static_cast<int>((row_bytes + 255) / 256);
         const int tile = static_cast<int>(item % tiles);
         item /= tiles;
         const int r0 = static_cast<int>(item % rank_groups) * 16 * RT, e = static_cast<int>(item / rank_groups);
@@ -830,17 +980,14 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
         const int rank = rows_of(ad, e, &first) - r0;
         if (rank <= 0) continue;
         first += r0;
-        const int col = (tile * 16 + c) * U::kCols;
-        const bool inside = col < job.cols;
-        const T* x = static_cast<const T*>(job.x) + (inside ? col : 0);
-        const uint32_t row_bytes = static_cast<uint32_t>(job.cols) * sizeof(T), v_bytes = job.v_stride * 4u;
-        const auto rx = make_rsrc(job.x, static_cast<uint32_t>(ad.M) * row_bytes);
-        const auto rv = make_rsrc(job.v, static_cast<uint32_t>(ad.M) * v_bytes);
-        f32x4 acc[RT][U::kCols];
+        // tokens of a window lie within this many rows of its first, so that
+        // 32-bit offsets from there reach all of them
+        const int reach = static_cast<int>((kOutside - 32) / max(row_bytes, v_bytes));
+        f32x4 acc[RT][O::CT];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int j = 0; j < U::kCols; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < O::CT; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
         // the adapter's tokens, 256 segments at a time
         for (int s0 = 0; s0 < ad.S; s0 += kThreads) {
             const int s = s0 + threadIdx.x;
@@ -868,123 +1015,178 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
             ends[threadIdx.x] = sum + before;
             starts[threadIdx.x] = b - (sum + before - n);  // token = starts + place in the list
             total = __builtin_amdgcn_readfirstlane(total);
-            for (int w0 = z * kWindow; w0 < total; w0 += Z * kWindow) {
-                const int count = min(kWindow, total - w0);
+            // part z: a run of whole stages
+            const int64_t stages = (total + 31) / 32;
+            const int from = static_cast<int>(stages * z / Z) * 32;
+            const int to = min(total, static_cast<int>(stages * (z + 1) / Z) * 32);
+            for (int w0 = from; w0 < to;) {
                 __syncthreads();
-                const int at = w0 + threadIdx.x;
-                if (threadIdx.x < count) {
+                const int at = w0 + 4 * threadIdx.x;
+                int t[4] = {-1, -1, -1, -1};
+                if (at < to) {
                     int lo = 0, hi = kThreads - 1;  // the first segment whose end is past `at`
                     while (lo < hi) {
                         const int mid = (lo + hi) / 2;
                         if (ends[mid] > at) hi = mid; else lo = mid + 1;
                     }
-                    tokens[threadIdx.x] = starts[lo] + at;
-                } else {
-                    tokens[threadIdx.x] = -1;
-                }
-                __syncthreads();
-                for (int t0 = wave * STEP; t0 < count; t0 += kWaves * STEP) {
-                    uint4 rows[ROWS];
-                    float v[RT][ROWS];
 #pragma unroll
-                    for (int i = 0; i < ROWS; ++i) {
-                        const int tok = tokens[t0 + ROWS * g + i];
-                        if constexpr (NEAR) {
-                            const uint32_t t = static_cast<uint32_t>(tok);
-                            rows[i] = buf_load16(rx, tok < 0 || !inside ? kNone : t * row_bytes + col * sizeof(T), 0);
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                const uint32_t off = t * v_bytes + 4 * (r0 + 16 * r + c);
-                                v[r][i] = __builtin_bit_cast(
-                                    float, __builtin_amdgcn_raw_buffer_load_b32(
-                                               rv, tok < 0 || 16 * r + c >= rank ? kNone : off, 0, 0));
-                            }
-                        } else {
-                            const size_t t = tok < 0 ? 0 : tok;
-                            rows[i] = *reinterpret_cast<const uint4*>(x + t * job.cols);
-                            if (tok < 0) rows[i] = make_uint4(0, 0, 0, 0);
-                            const float* vr = job.v + t * job.v_stride + r0;
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                const int j = 16 * r + c;
-                                const float f = vr[j < rank ? j : 0];
-                                v[r][i] = tok >= 0 && j < rank ? f : 0.0f;
-                            }
+                    for (int i = 0; i < 4; ++i)
+                        if (at + i < to) {
+                            while (ends[lo] <= at + i) ++lo;  // to <= ends[kThreads - 1]
+                            t[i] = starts[lo] + at + i;
                         }
-                    }
-                    uint4 f[U::kCols];
-                    column_operands(x, rows, f);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        if (16 * r >= rank) break;
-                        uint4 a[U::kFrags];
-                        rank_operands(x, v[r], a);
-#pragma unroll
-                        for (int h = 0; h < U::kFrags; ++h)
-#pragma unroll
-                            for (int j = 0; j < U::kCols; ++j) acc[r][j] = mma(x, a[h], f[j], acc[r][j]);
-                    }
                 }
-            }
-        }
-        // (wave 0 + wave 2) + (wave 1 + wave 3)
-        constexpr int TILE = RT * U::kCols * 64;
-#pragma unroll
-        for (int half = 2; half > 0; half >>= 1) {
-            __syncthreads();
-            if (wave >= half && wave < 2 * half) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int j = 0; j < U::kCols; ++j)
-                        red[(wave - half) * TILE + (r * U::kCols + j) * 64 + lane] = acc[r][j];
-            }
-            __syncthreads();
-            if (wave < half) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int j = 0; j < U::kCols; ++j) acc[r][j] += red[wave * TILE + (r * U::kCols + j) * 64 + lane];
-            }
-        }
-        if (wave == 0 && inside) {
-            const float scale = job.scaled ? uniform_load(ad.scale, e) : 1.0f;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-#pragma unroll
-                for (int j = 0; j < U::kCols; ++j) acc[r][j] *= scale;
+                if (threadIdx.x == 0) window_base = t[0];
+                __syncthreads();
+                const int base = __builtin_amdgcn_readfirstlane(window_base);
+                int have = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = 16 * r + 4 * g + i;
-                    if (j >= rank) continue;
-                    const size_t at = static_cast<size_t>(first + j) * job.cols + col;
-                    if (job.partial) {
-                        float* o = job.partial + static_cast<size_t>(z) * ad.R * job.cols + at;
-#pragma unroll
-                        for (int q = 0; q < U::kCols; q += 4)
-                            *reinterpret_cast<float4*>(o + q) =
-                                make_float4(acc[r][q][i], acc[r][q + 1][i], acc[r][q + 2][i], acc[r][q + 3][i]);
-                    } else {
-                        *reinterpret_cast<uint4*>(static_cast<T*>(job.out) + at) = pack(x, acc[r], i);
-                    }
+                    t[i] = t[i] >= base && t[i] - base < reach ? t[i] - base : -1;
+                    have += t[i] >= 0;
                 }
+                tokens[threadIdx.x] = make_int4(t[0], t[1], t[2], t[3]);
+#pragma unroll
+                for (int off = 32; off > 0; off >>= 1) have += __shfl_xor(have, off);
+                if (lane == 0) wave_sum[wave] = have;
+                __syncthreads();
+                const int count = __builtin_amdgcn_readfirstlane(wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3]);
+                const int64_t rows_left = ad.M - base;
+                const auto rx = dev::dma_rsrc(static_cast<const T*>(job.x) + static_cast<size_t>(base) * job.cols,
+                                              static_cast<uint32_t>(min(rows_left * row_bytes, int64_t(kOutside) - 16)));
+                const auto rv = dev::dma_rsrc(job.v + static_cast<size_t>(base) * job.v_stride,
+                                              static_cast<uint32_t>(min(rows_left * v_bytes, int64_t(kOutside) - 16)));
+                const uint32_t lds = dev::lds_address(ring);
+                constexpr int PIECES = 4 * O::VT;  // of a row of v
+                const auto list = [&](int stage, int (&tok)[O::L]) {
+#pragma unroll
+                    for (int i = 0; i < O::L; ++i) {
+                        const int row = i < O::LX ? 4 * (i * kWaves + wave) + (lane >> 4)
+                                                  : 64 / PIECES * ((i - O::LX) * kWaves + wave) + lane / PIECES;
+                        const int at = 32 * stage + row;
+                        tok[i] = at < kWindow ? token_at[at] : -1;
+                    }
+                };
+                const auto issue = [&](const int (&tok)[O::L], int buffer) {
+                    const uint32_t xl = lds + buffer * O::BYTES, vl = xl + O::XBYTES;
+#pragma unroll
+                    for (int i = 0; i < O::LX; ++i) {
+                        const int group = i * kWaves + wave, row = 4 * group + (lane >> 4);
+                        const uint32_t col = 256u * tile + 16 * ((lane & 15) ^ O::x_key(row));
+                        dev::lds_dma16(rx, xl + group * 1024,
+                                       tok[i] < 0 || col >= row_bytes ? kOutside : tok[i] * row_bytes + col, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < O::LV; ++i) {
+                        const int group = i * kWaves + wave, row = 64 / PIECES * group + lane / PIECES;
+                        const uint32_t col = 4u * r0 + 16 * ((lane & (PIECES - 1)) ^ O::v_key(row));
+                        dev::lds_dma16(rv, vl + group * 1024,
+                                       tok[O::LX + i] < 0 ? kOutside : tok[O::LX + i] * v_bytes + col, 0);
+                    }
+                };
+                // raw v of this wave's rank tile, and its operands in its place
+                const auto read_v = [&](const uint8_t* v, float (&f)[8]) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = O::raw(v, wave, stage_token<T>(lane >> 4, i), lane & 15);
+                };
+                const auto write_v = [&](uint8_t* v, float (&f)[8]) {
+                    if (16 * wave + (lane & 15) >= rank)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+                    uint4 a[2];
+                    stage_operands(static_cast<const T*>(nullptr), f, a);
+                    *O::operand(v, wave, 0, lane) = a[0];
+                    *O::operand(v, wave, 1, lane) = a[1];
+                };
+                const int steps = (min(count, kWindow) + 31) / 32;
+                int tok[O::L];
+#pragma unroll
+                for (int s = 0; s < kOuterStages - 1; ++s) {
+                    list(s, tok);
+                    issue(tok, s);
+                }
+                list(kOuterStages - 1, tok);
+                dev::dma_stage_barrier<O::L*(kOuterStages - 2)>();
+                float f[8];
+                if (wave < RT) {
+                    read_v(ring + O::XBYTES, f);
+                    __builtin_amdgcn_wave_barrier();
+                    write_v(ring + O::XBYTES, f);
+                }
+                for (int st = 0; st < steps; ++st) {
+                    // the next stage has landed and this one's operands are made;
+                    // the place of the one before is free
+                    dev::dma_stage_barrier<O::L*(kOuterStages - 3)>();
+                    const uint8_t* now = ring + st % kOuterStages * O::BYTES;
+                    uint8_t* ahead = ring + (st + 1) % kOuterStages * O::BYTES + O::XBYTES;
+                    // every LDS read of the stage before the loads are issued
+                    // (which keep memory accesses on their side)
+                    uint32_t w[8];
+                    uint4 a[RT][2];
+                    if (wave < RT) read_v(ahead, f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = O::x_word(now, stage_token<T>(lane >> 4, i), 16 * wave + (lane & 15));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            a[r][h] = *O::operand(const_cast<uint8_t*>(now) + O::XBYTES, r, h, lane);
+                    int next[O::L];
+                    list(st + kOuterStages, next);
+                    issue(tok, (st + kOuterStages - 1) % kOuterStages);
+#pragma unroll
+                    for (int i = 0; i < O::L; ++i) tok[i] = next[i];
+                    if (wave < RT) write_v(ahead, f);
+                    stage_products<RT>(static_cast<const T*>(nullptr), w, a, rank, acc);
+                }
+                dev::dma_stage_barrier<0>();  // nothing in flight into the ring
+                w0 += max(count, 1);
             }
         }
+        const float scale = job.scaled ? uniform_load(ad.scale, e) : 1.0f;
+        const int c = lane & 15, g = lane >> 4;
+        const int col = (256 * tile + 64 * wave) / static_cast<int>(sizeof(T)) + O::CT * c;
+        if (col >= job.cols) continue;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 16 * r + 4 * g + i;
+                if (j >= rank) continue;
+                const size_t at = static_cast<size_t>(first + j) * job.cols + col;
+                float* o = job.partial + static_cast<size_t>(z) * ad.R * job.cols + at;
+                if constexpr (O::CT == 2) {
+                    const float a = acc[r][0][i] * scale, b = acc[r][1][i] * scale;
+                    if (job.partial)
+                        *reinterpret_cast<float2*>(o) = make_float2(a, b);
+                    else
+                        *reinterpret_cast<uint32_t*>(static_cast<T*>(job.out) + at) = bf16_bits(a) | bf16_bits(b) << 16;
+                } else {
+                    *(job.partial ? o : static_cast<float*>(job.out) + at) = acc[r][0][i] * scale;
+                }
+            }
     }
 }
 
-// The token parts' sums joined in order, four columns a thread.
+// The token parts' sums of both gradients joined in order, four columns a
+// thread.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void join_parts_kernel(const float* __restrict__ partial, T* __restrict__ out,
-                                                              size_t n, int Z) {
-    for (size_t i = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n;
-         i += static_cast<size_t>(gridDim.x) * kThreads * 4) {
-        f32x4 s = *reinterpret_cast<const f32x4*>(partial + i);
-        for (int z = 1; z < Z; ++z) s += *reinterpret_cast<const f32x4*>(partial + z * n + i);
+__global__ __launch_bounds__(kThreads) void join_parts_kernel(const float* __restrict__ partA, T* __restrict__ dA,
+                                                              size_t nA, const float* __restrict__ partB,
+                                                              T* __restrict__ dB, size_t nB, int Z) {
+    for (size_t k = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; k < nA + nB;
+         k += static_cast<size_t>(gridDim.x) * kThreads * 4) {
+        const bool second = k >= nA;
+        const size_t i = second ? k - nA : k, n = second ? nB : nA;
+        const float* part = (second ? partB : partA) + i;
+        T* out = (second ? dB : dA) + i;
+        f32x4 s = *reinterpret_cast<const f32x4*>(part);
+        for (int z = 1; z < Z; ++z) s += *reinterpret_cast<const f32x4*>(part + z * n);
         if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<f32x4*>(out + i) = s;
+            *reinterpret_cast<f32x4*>(out) = s;
         else
-            *reinterpret_cast<uint2*>(out + i) =
+            *reinterpret_cast<uint2*>(out) =
                 make_uint2(bf16_bits(s[0]) | bf16_bits(s[1]) << 16, bf16_bits(s[2]) | bf16_bits(s[3]) << 16);
     }
 }
@@ -1038,7 +1240,7 @@ int slices_of(const AdapterArgs& a, int K) {
 
 template <typename T>
 int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int scaled,
-                  hipStream_t s) {
+                  const Repack& v, hipStream_t s) {
     const int tt = shrink_tile_of(a.ad.M, a.ad.S), Q = slices_of(a, K), rt = (a.ad.max_rank + 15) / 16;
     const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * tt) * Q;
     auto k = tt == 1 ? (rt <= 1 ? shrink_kernel<T, 1, 1> : rt <= 2 ? shrink_kernel<T, 1, 2>
@@ -1046,7 +1248,7 @@ int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* par
                      : (rt <= 1 ? shrink_tile_kernel<T, 1> : rt <= 2 ? shrink_tile_kernel<T, 2>
                         : rt <= 4 ? shrink_tile_kernel<T, 4> : shrink_tile_kernel<T, 8>);
     hipLaunchKernelGGL(k, dim3(grid_of(items)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
-                       static_cast<const T*>(A), part, stride, K, Q, scaled, items);
+                       static_cast<const T*>(A), part, stride, K, Q, scaled, v, items);
     return Q;
 }
 
@@ -1058,8 +1260,11 @@ void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, c
     const bool tile64 = tile_of(a.ad.M, a.ad.S) > 1;
     const int64_t pieces = pieces_of(a.ad.M, a.ad.S, tile64 ? 64 : 16);
     const int wide = (tile64 ? 16 : 64) * Unit<T>::kCols, tiles = (N + wide - 1) / wide;
-    // a block takes several column tiles (v is read once) while the card stays full
-    const int64_t per = std::max(int64_t(1), std::min(int64_t(tiles), pieces * tiles / (2 * kFill)));
+    // a block takes several column tiles (v is read once) while the card stays
+    // full: four at least where that leaves a block a compute unit (gradients of
+    // 8192 tokens at K = 1280: 25.8 us with one, 20.7 with two)
+    const int64_t work = pieces * tiles;
+    const int64_t per = std::max(int64_t(1), std::min(int64_t(tiles), std::max(work / (2 * kFill), std::min(int64_t(4), work / (kFill / 2)))));
     const int columns = static_cast<int>((tiles + per - 1) / per);
     const int ku = (a.ad.max_rank + Unit<T>::kRanks - 1) / Unit<T>::kRanks;
     constexpr int MOST = sizeof(T) == 2 ? 4 : 8;
@@ -1080,7 +1285,7 @@ void forward(const AdapterArgs& a, hipStream_t s) {
     if (a.ad.max_rank > 0) {
         // a single slice with rows of v's own length writes v itself
         if (a.v && stride == a.ad.max_rank && slices_of(a, a.K) == 1) part = a.v;
-        Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, s);
+        Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, Repack{}, s);
     }
     launch_expand<T>(a, part, stride, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.ad.max_rank, a.ad.max_rank, a.N, 1, s);
 }
@@ -1099,8 +1304,8 @@ OuterSplit outer_split(int64_t M, int32_t K, int32_t N, int32_t E, int32_t max_r
     const int64_t tiles = (K + wide - 1) / wide + (N + wide - 1) / wide;
     const int64_t blocks = tiles * (E > 0 ? E : 1) * (o.rank_groups > 0 ? o.rank_groups : 1);
     int64_t z = 2 * kFill / blocks;
-    const int64_t windows = (M + kWindow - 1) / kWindow;
-    if (z > windows) z = windows;
+    const int64_t most = (M + 255) / 256;  // parts of 256 tokens at least
+    if (z > most) z = most;
     if (z > 16) z = 16;
     o.Z = static_cast<int>(z < 1 ? 1 : z);
     return o;
@@ -1115,7 +1320,8 @@ void zero(void* p, size_t elements, hipStream_t s) {
 }
 
 template <typename T>
-void launch_outer(const AdapterArgs& a, const float* dv, int dv_stride, float* partial, hipStream_t s) {
+void launch_outer(const AdapterArgs& a, const float* dv, int dv_stride, const float* v, int v_stride, float* partial,
+                  hipStream_t s) {
     const OuterSplit o = outer_split(a.ad.M, a.K, a.N, a.ad.E, a.ad.max_rank, a.dtype);
     const size_t nA = static_cast<size_t>(a.ad.R) * a.K, nB = static_cast<size_t>(a.ad.R) * a.N;
     if (a.ad.E == 0) {
@@ -1130,41 +1336,49 @@ void launch_outer(const AdapterArgs& a, const float* dv, int dv_stride, float* p
     };
     const int64_t itemsA = a.dA ? count(a.K) : 0, itemsB = a.dB ? count(a.N) : 0;
     const OuterJob jobA{dv, a.x, a.dA, parts ? partial : nullptr, a.K, dv_stride, 0, 0};
-    const OuterJob jobB{a.v, a.dy, a.dB, parts ? partial + o.Z * nA : nullptr, a.N, a.ad.max_rank, 1, itemsA};
-    const int64_t widest = std::max(std::max(a.K, a.N) * static_cast<int64_t>(sizeof(T)), dv_stride * int64_t(4));
-    const bool near = a.ad.M * widest < (int64_t(1) << 32);
-    auto k = near ? (o.RT == 1 ? outer_kernel<T, 1, true> : o.RT == 2 ? outer_kernel<T, 2, true> : outer_kernel<T, 4, true>)
-                  : (o.RT == 1 ? outer_kernel<T, 1, false> : o.RT == 2 ? outer_kernel<T, 2, false> : outer_kernel<T, 4, false>);
+    const OuterJob jobB{v, a.dy, a.dB, parts ? partial + o.Z * nA : nullptr, a.N, v_stride, 1, itemsA};
+    auto k = o.RT == 1 ? outer_kernel<T, 1> : o.RT == 2 ? outer_kernel<T, 2> : outer_kernel<T, 4>;
     hipLaunchKernelGGL(k, dim3(grid_of(itemsA + itemsB)), dim3(kThreads), 0, s, a.ad, jobA, jobB, o.rank_groups, o.Z,
                        itemsA + itemsB);
     if (!parts) return;
-    const auto blocks = [](size_t n) { return dim3(static_cast<unsigned>(n / 1024 < 8192 ? n / 1024 + 1 : 8192)); };
-    if (a.dA)
-        hipLaunchKernelGGL((join_parts_kernel<T>), blocks(nA), dim3(kThreads), 0, s, jobA.partial,
-                           static_cast<T*>(a.dA), nA, o.Z);
-    if (a.dB)
-        hipLaunchKernelGGL((join_parts_kernel<T>), blocks(nB), dim3(kThreads), 0, s, jobB.partial,
-                           static_cast<T*>(a.dB), nB, o.Z);
+    const size_t a4 = a.dA ? nA : 0, b4 = a.dB ? nB : 0, blocks = (a4 + b4) / 1024 + 1;
+    hipLaunchKernelGGL((join_parts_kernel<T>), dim3(static_cast<unsigned>(std::min(blocks, size_t(8192)))),
+                       dim3(kThreads), 0, s, jobA.partial, static_cast<T*>(a.dA), a4, jobB.partial,
+                       static_cast<T*>(a.dB), b4, o.Z);
 }
+
+// Whether v's rows are whole 16-byte pieces.
+bool v_in_pieces(int32_t max_rank) { return max_rank % 4 == 0; }
 
 template <typename T>
 void backward(const AdapterArgs& a, hipStream_t s) {
     const int stride = stride_of(a.ad.max_rank);
     const size_t rows = static_cast<size_t>(a.ad.M) * stride;
     const int most = most_slices(a.ad.M, a.N, a.dtype);
+    // workspace: the slices of dv, their sum, v in rows of the stride, the
+    // parts of the gradients
     float* part = static_cast<float*>(a.workspace);
     float* joined = most > 1 ? part + most * rows : part;
-    float* partial = joined + rows;
+    float* packed = joined + rows;
+    float* partial = v_in_pieces(a.ad.max_rank) ? packed : packed + rows;
+    const bool repack = a.dB && !v_in_pieces(a.ad.max_rank);
+    const Repack v{repack ? a.v : nullptr, packed, a.ad.max_rank, stride};
     int Q = 1;
-    if ((a.dx || a.dA) && a.ad.max_rank > 0 && a.ad.M > 0)
-        Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, s);
+    const bool any = a.ad.max_rank > 0 && a.ad.M > 0;
+    if ((a.dx || a.dA) && any)
+        Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, v, s);
+    else if (repack && any)
+        hipLaunchKernelGGL(repack_kernel, dim3(grid_of((static_cast<int64_t>(a.ad.M) + 15) / 16)), dim3(kThreads), 0, s,
+                           v, a.ad.M);
     if (a.dx)  // leaves the sum of dv's slices for the outer products
         launch_expand<T>(a, part, stride, Q, a.A, a.dx, Q > 1 && a.dA ? joined : nullptr, stride, stride, a.K, 0, s);
     else if (a.dA && Q > 1)
         hipLaunchKernelGGL(join_slices_kernel,
                            dim3(static_cast<unsigned>(rows / 1024 < 4096 ? rows / 1024 + 1 : 4096)), dim3(kThreads), 0,
                            s, part, joined, rows, Q);
-    if (a.dA || a.dB) launch_outer<T>(a, Q > 1 ? joined : part, stride, partial, s);
+    if (a.dA || a.dB)
+        launch_outer<T>(a, Q > 1 ? joined : part, stride, repack ? packed : a.v, repack ? stride : a.ad.max_rank,
+                        partial, s);
 }
 
 }  // namespace
@@ -1177,7 +1391,7 @@ size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, in
                                   int32_t dtype) {
     const size_t rows = static_cast<size_t>(M) * stride_of(max_rank) * sizeof(float);
     const int most = most_slices(M, N, dtype), Z = outer_split(M, K, N, E, max_rank, dtype).Z;
-    size_t n = rows * (most > 1 ? most + 1 : 1);
+    size_t n = rows * ((most > 1 ? most + 1 : 1) + (v_in_pieces(max_rank) ? 0 : 1));
     if (Z > 1) n += static_cast<size_t>(Z) * static_cast<size_t>(R) * (static_cast<size_t>(K) + N) * sizeof(float);
     return n;
 }

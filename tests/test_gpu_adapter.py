@@ -140,6 +140,8 @@ BATCHES = [
     ([(40, 0), (40, 7), (40, -5)], [4, 4]),            # adapters outside the set: none
     ([(20, 0), (21, 1)], [0, 12]),                     # an adapter of rank 0
     ([(257, 0)], [128]),
+    ([(33, 0), (2, 1), (70, 0)], [50, 7]),             # rows of v that are no whole number of 16 bytes
+    ([(1, 0), (40, 1), (2, 0)], [2, 47]),
 ]
 SIZES = [(8, 8), (64, 40), (256, 256), (72, 1288), (1280, 520), (4096, 264)]
 

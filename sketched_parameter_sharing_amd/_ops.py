@@ -14,18 +14,75 @@ from dataclasses import dataclass
 import numpy as np
 
 from . import _lib
-from ._lib import (BF16, F32, FP8_E4M3, OK, AdamWEntry, AdamWHyper, Adapters, Segments, Tensor, _check,
-                   _check_device, _check_vec, _desc, _stream, load)
+from ._lib import BF16, F32, FP8_E4M3, AdamWEntry, AdamWHyper, Adapters, Segments, Tensor, _check, _check_vec, load
 
 MAX_RANK = 128       # SS1_MAX_RANK
 ADAMW_BLOCK = 256    # SS1_ADAMW_BLOCK
 
+# Set by _setup at the first call (importing the package does not import torch).
+_torch = None
+_codes = {}
+_raw_stream = None
+
+
+def _setup():
+    global _torch, _raw_stream
+    import torch
+    _codes.update({torch.float32: F32, torch.bfloat16: BF16})
+    # the handle of a device's current stream, without a Stream object around it
+    # (3 us of a small call); current_stream is the public way to the same handle
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _matrix(t) -> Tensor:
+    """The C ABI's view of a 2-D, contiguous GPU tensor."""
+    if not t.is_cuda:
+        raise ValueError("device entry points take GPU tensors")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("matrices must be 2-D and contiguous")
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (bfloat16 or float32)")
+    rows, cols = t.shape
+    return Tensor(t.data_ptr(), code, 0, rows, cols)
+
 
 def _row(t) -> Tensor:
     """A vector as the [1][K] tensor of the C ABI."""
-    if t.dim() != 1:
-        raise ValueError("gamma, beta and their gradients must be 1-D")
-    return _desc(t.view(1, -1))
+    if not t.is_cuda:
+        raise ValueError("device entry points take GPU tensors")
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("gamma, beta and their gradients must be 1-D and contiguous")
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (bfloat16 or float32)")
+    return Tensor(t.data_ptr(), code, 0, 1, t.shape[0])
+
+
+def _vec(t, dtype, numel: int, what: str) -> int:
+    """The address of a device array that the C ABI reads by pointer alone."""
+    if not t.is_cuda:
+        raise ValueError("device entry points take GPU tensors")
+    _check_vec(t, dtype, numel, what)
+    return t.data_ptr()
+
+
+def _check_device(*ts):
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("device entry points take GPU tensors")
+
+
+def _ref(desc, t):
+    return None if t is None else byref(desc(t))
+
+
+def _handle(stream, t):
+    """The given stream's handle, or that of the current stream of t's device."""
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 # ---------------------------------------------------------------- layer norm
@@ -34,25 +91,19 @@ def layernorm_forward(x, gamma, beta=None, eps: float = 1e-5, y=None, mean=None,
     (y, mean, rstd).  ``x`` is [M][K] bf16 or float32, ``gamma`` and ``beta``
     (may be None) are [K] of x's dtype or float32; mean and rstd, float32 [M],
     are what :func:`layernorm_backward` takes."""
-    import torch
-    _check_device(x, gamma)
-    M = x.shape[0]
+    torch = _torch or _setup()
+    tx, M = _matrix(x), x.shape[0]
     if y is None:
         y = torch.empty_like(x)
     if mean is None:
         mean = torch.empty((M,), dtype=torch.float32, device=x.device)
     if rstd is None:
-        rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _check_device(y, mean, rstd)
-    _check_vec(mean, torch.float32, M, "mean")
-    _check_vec(rstd, torch.float32, M, "rstd")
-    b = None
-    if beta is not None:
-        _check_device(beta)
-        b = byref(_row(beta))
-    st = load().ss1_layernorm_forward(byref(_desc(x)), byref(_row(gamma)), b, eps, byref(_desc(y)),
-                                      mean.data_ptr(), rstd.data_ptr(), _stream(stream))
-    _check(st, "ss1_layernorm_forward")
+        rstd = torch.empty_like(mean)
+    st = load().ss1_layernorm_forward(byref(tx), byref(_row(gamma)), _ref(_row, beta), eps, byref(_matrix(y)),
+                                      _vec(mean, torch.float32, M, "mean"), _vec(rstd, torch.float32, M, "rstd"),
+                                      _handle(stream, x))
+    if st:
+        _check(st, "ss1_layernorm_forward")
     return y, mean, rstd
 
 
@@ -60,31 +111,29 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dx=True, dgamma=True, dbeta=Tru
     """Gradients of layer norm (ss1_layernorm_backward): returns (dx, dgamma,
     dbeta); pass None for one that is not wanted, True to allocate it.  mean
     and rstd are what the forward returned."""
-    import torch
-    _check_device(dy, x, gamma, mean, rstd)
-    M = x.shape[0]
-    _check_vec(mean, torch.float32, M, "mean")
-    _check_vec(rstd, torch.float32, M, "rstd")
+    torch = _torch or _setup()
+    tx, M = _matrix(x), x.shape[0]
+    tg = _row(gamma)
     if dx is True:
         dx = torch.empty_like(x)
     if dgamma is True:
         dgamma = torch.empty_like(gamma)
     if dbeta is True:
         dbeta = torch.empty_like(gamma)
-    _check_device(*(t for t in (dx, dgamma, dbeta, workspace) if t is not None))
-    lib, tx = load(), _desc(x)
+    lib = load()
     wp, wb = None, 0
     if dgamma is not None or dbeta is not None:
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib.ss1_layernorm_backward_query(byref(tx), byref(n)), "ss1_layernorm_backward_query")
             workspace = torch.empty((n.value,), dtype=torch.uint8, device=x.device)
+        _check_device(workspace)
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = lib.ss1_layernorm_backward(byref(_desc(dy)), byref(tx), byref(_row(gamma)), mean.data_ptr(),
-                                    rstd.data_ptr(), None if dx is None else byref(_desc(dx)),
-                                    None if dgamma is None else byref(_row(dgamma)),
-                                    None if dbeta is None else byref(_row(dbeta)), wp, wb, _stream(stream))
-    _check(st, "ss1_layernorm_backward")
+    st = lib.ss1_layernorm_backward(byref(_matrix(dy)), byref(tx), byref(tg), _vec(mean, torch.float32, M, "mean"),
+                                    _vec(rstd, torch.float32, M, "rstd"), _ref(_matrix, dx), _ref(_row, dgamma),
+                                    _ref(_row, dbeta), wp, wb, _handle(stream, x))
+    if st:
+        _check(st, "ss1_layernorm_backward")
     return dx, dgamma, dbeta
 
 
@@ -105,7 +154,7 @@ class AdapterSet:
     @classmethod
     def make(cls, A, B, ranks, scale):
         """``ranks`` and ``scale`` are host sequences, one value an adapter."""
-        import torch
+        torch = _torch or _setup()
         _check_device(A, B)
         ranks = tuple(int(r) for r in ranks)
         if any(r < 0 or r > MAX_RANK for r in ranks):
@@ -119,27 +168,24 @@ class AdapterSet:
         return cls(A, B, row, sc, max(ranks, default=0), ranks)
 
     def _struct(self) -> Adapters:
-        return Adapters(_desc(self.A), _desc(self.B), self.row.data_ptr(), self.scale.data_ptr(), len(self.ranks),
+        return Adapters(_matrix(self.A), _matrix(self.B), self.row.data_ptr(), self.scale.data_ptr(), len(self.ranks),
                         self.max_rank)
 
 
 def _segments(seg, seg_adapter) -> Segments:
-    import torch
-    _check_device(seg, seg_adapter)
-    S = seg_adapter.numel()
-    _check_vec(seg, torch.int32, S + 1, "seg")
-    _check_vec(seg_adapter, torch.int32, S, "seg_adapter")
-    return Segments(seg.data_ptr(), seg_adapter.data_ptr(), S, 0)
+    S, i32 = seg_adapter.numel(), _torch.int32
+    return Segments(_vec(seg, i32, S + 1, "seg"), _vec(seg_adapter, i32, S, "seg_adapter"), S, 0)
 
 
 def _workspace(workspace, query, M: int, ad: Adapters, device, where: str):
-    import torch
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _check(query(M, byref(ad), byref(n)), where)
-        workspace = torch.empty((n.value,), dtype=torch.uint8, device=device)
+        st = query(M, byref(ad), byref(n))
+        if st:
+            _check(st, where)
+        workspace = _torch.empty((n.value,), dtype=_torch.uint8, device=device)
     _check_device(workspace)
-    return workspace, workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None, v=None, save_v: bool = False,
@@ -151,21 +197,19 @@ def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None
     none) are device tensors; ``base`` is the projection's output, or None for
     zero, and ``y`` may be base itself.  v = x A_e^T, float32 [M][max_rank], is
     what :func:`adapter_backward` takes: None unless given or ``save_v``."""
-    import torch
-    _check_device(x)
-    M, N = x.shape[0], adapters.B.shape[1]
+    torch = _torch or _setup()
+    tx, ad, lib = _matrix(x), adapters._struct(), load()
+    M = x.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        y = torch.empty((M, adapters.B.shape[1]), dtype=x.dtype, device=x.device)
     if v is None and save_v:
         v = torch.empty((M, adapters.max_rank), dtype=torch.float32, device=x.device)
-    _check_device(*(t for t in (y, base, v) if t is not None))
-    lib, ad = load(), adapters._struct()
     workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_forward_query, M, ad, x.device,
                                    "ss1_adapter_forward_query")
-    st = lib.ss1_adapter_forward(byref(_desc(x)), byref(ad), byref(_segments(seg, seg_adapter)),
-                                 None if base is None else byref(_desc(base)), byref(_desc(y)),
-                                 None if v is None else byref(_desc(v)), wp, wb, _stream(stream))
-    _check(st, "ss1_adapter_forward")
+    st = lib.ss1_adapter_forward(byref(tx), byref(ad), byref(_segments(seg, seg_adapter)), _ref(_matrix, base),
+                                 byref(_matrix(y)), _ref(_matrix, v), wp, wb, _handle(stream, x))
+    if st:
+        _check(st, "ss1_adapter_forward")
     return y, v
 
 
@@ -176,8 +220,8 @@ def adapter_backward(dy, x, v, adapters: AdapterSet, seg, seg_adapter, dx_base=N
     ``v`` is what the forward returned with ``save_v`` (needed for dB only);
     ``dx_base`` is the projection's own input gradient (ss1.backward's dx), to
     which the adapters' is added, and dx may be dx_base itself."""
-    import torch
-    _check_device(dy, x)
+    torch = _torch or _setup()
+    tx, ad, lib = _matrix(x), adapters._struct(), load()
     M = x.shape[0]
     if dx is True:
         dx = torch.empty_like(x)
@@ -185,26 +229,22 @@ def adapter_backward(dy, x, v, adapters: AdapterSet, seg, seg_adapter, dx_base=N
         dA = torch.empty_like(adapters.A)
     if dB is True:
         dB = torch.empty_like(adapters.B)
-    _check_device(*(t for t in (v, dx_base, dx, dA, dB) if t is not None))
-    lib, ad = load(), adapters._struct()
     workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_backward_query, M, ad, x.device,
                                    "ss1_adapter_backward_query")
-    opt = lambda t: None if t is None else byref(_desc(t))  # noqa: E731
-    st = lib.ss1_adapter_backward(byref(_desc(dy)), byref(_desc(x)), opt(v), byref(ad),
-                                  byref(_segments(seg, seg_adapter)), opt(dx_base), opt(dx), opt(dA), opt(dB), wp, wb,
-                                  _stream(stream))
-    _check(st, "ss1_adapter_backward")
+    st = lib.ss1_adapter_backward(byref(_matrix(dy)), byref(tx), _ref(_matrix, v), byref(ad),
+                                  byref(_segments(seg, seg_adapter)), _ref(_matrix, dx_base), _ref(_matrix, dx),
+                                  _ref(_matrix, dA), _ref(_matrix, dB), wp, wb, _handle(stream, x))
+    if st:
+        _check(st, "ss1_adapter_backward")
     return dx, dA, dB
 
 
 # --------------------------------------------------------------------- AdamW
 def _float_code(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+    return code
 
 
 @dataclass
@@ -234,7 +274,7 @@ class AdamWPlan:
         bfloat16, contiguous); ``m`` and ``v`` the states (zeros of kind
         ``state``, "f32" or "fp8", when None); ``masters`` float32 copies of
         bf16 params, or None; ``weight_decay`` one value or one a tensor."""
-        import torch
+        torch = _torch or _setup()
         params, grads = list(params), list(grads)
         n = len(params)
         if state not in ("f32", "fp8"):
@@ -303,11 +343,9 @@ class AdamWPlan:
         rounding of 8-bit states and of bf16 params without masters."""
         scale, dev = grad_scale, None
         if not isinstance(grad_scale, (int, float)):
-            import torch
-            _check_device(grad_scale)
-            _check_vec(grad_scale, torch.float32, 1, "grad_scale")
-            scale, dev = 1.0, grad_scale.data_ptr()
+            scale, dev = 1.0, _vec(grad_scale, _torch.float32, 1, "grad_scale")
         h = AdamWHyper(lr, beta1, beta2, eps, scale, dev, step, int(seed) & (2**64 - 1))
         st = load().ss1_adamw_step(self.entries.data_ptr(), self.count, self.map.data_ptr(), self.chunks, byref(h),
-                                   _stream(stream))
-        _check(st, "ss1_adamw_step")
+                                   _handle(stream, self.entries))
+        if st:
+            _check(st, "ss1_adamw_step")

@@ -696,8 +696,8 @@ typedef struct {
  *   - BF16 param without one: p = param, and the result is rounded up or down
  *     with the probability of its distance (small steps are kept on average).
  *   - E4M3 states: m and r = sqrt(v) are code * scale of their block of
- *     SS1_ADAMW_BLOCK elements.  The new scale is max |value| / 448 (1 for a
- *     block of zeros) and the quotient is rounded up or down with the
+ *     SS1_ADAMW_BLOCK elements.  The new scale is max |value| * (1/448) (1 for
+ *     a block of zeros) and the quotient is rounded up or down with the
  *     probability of its distance: with beta2 = 0.999 one step moves r by
  *     about 0.0005 of itself, and rounding to nearest (quantum 1/8 to 1/16)
  *     would hold it for ever.  A nonzero r keeps at least the smallest code.

@@ -136,16 +136,16 @@ __device__ __forceinline__ float half_wave_max(float v) {
     return v;
 }
 
-// The state's codes of 8 values t >= or < 0 of this lane, and the new scale of
-// their block: scale = max |t| / 448 (1 for a block of zeros), the quotient by
-// IEEE division.  u[j] holds the random bits of element j.
+// The state's codes of 8 values of this lane, and the new scale of their block:
+// max |t| times 1/448 as a float (1 for a block of zeros), the quotients by IEEE
+// division.  u[j] holds the random bits of element j.
 __device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t i, int n, const float (&t)[kVec],
                                           const uint32_t (&u)[kVec], bool keep_nonzero) {
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) top = fmaxf(top, fabsf(t[j]));
     top = half_wave_max(top);
-    const float scale = top > 0.0f ? __fdiv_rn(top, 448.0f) : 1.0f;
+    const float scale = top > 0.0f ? top * (1.0f / 448.0f) : 1.0f;
     if (n > 0 && (threadIdx.x & 31) == 0) scales[i / SS1_ADAMW_BLOCK] = scale;
     float q[kVec];
 #pragma unroll

@@ -194,6 +194,74 @@ __global__ __launch_bounds__(kThreads) void repack_kernel(Repack v, int M) {
         repack_rows(v, static_cast<int>(m), static_cast<int>(min(int64_t(16), M - m)));
 }
 
+// The outer products' work list.  Requests share the adapters unevenly, so the
+// tokens of each adapter are cut into parts of P: part i of adapter e is entry
+// {e, i P, end, slot}, where parts of an adapter that has several go to slots of
+// a partial buffer (slot -1: straight to the gradient).  multi[0].x counts the
+// adapters with several parts, multi[1 + i] = {e, parts, first slot}.
+struct OuterPlan {
+    int4* table;  // [most]; null: every adapter is one part (M <= P)
+    int4* multi;  // [E + 1]
+    int P, most, slots;
+};
+
+__device__ __forceinline__ int4 block_scan(int4 v, int4* sums, int4* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int x = __shfl_up(v.x, off), y = __shfl_up(v.y, off), z = __shfl_up(v.z, off);
+        if (lane >= off) v = make_int4(v.x + x, v.y + y, v.z + z, 0);
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = v;
+    __syncthreads();
+    *total = make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const int4 o = sums[w];
+        if (w < wave) v = make_int4(v.x + o.x, v.y + o.y, v.z + o.z, 0);
+        *total = make_int4(total->x + o.x, total->y + o.y, total->z + o.z, 0);
+    }
+    return v;
+}
+
+// Written by one block (an extra one of the shrink's launch); `lds` holds
+// 1024 + 64 bytes.
+__device__ void plan_outer(const AdapterView& ad, const OuterPlan& plan, int* lds) {
+    int4* sums = reinterpret_cast<int4*>(lds + kThreads);
+    int4 done = make_int4(0, 0, 0, 0);  // entries, slots, adapters with several parts
+    for (int e0 = 0; e0 < ad.E; e0 += kThreads) {
+        __syncthreads();
+        lds[threadIdx.x] = 0;
+        __syncthreads();
+        for (int s = threadIdx.x; s < ad.S; s += kThreads) {
+            const int e = ad.seg_adapter[s] - e0, b = clampi(ad.seg[s], 0, ad.M), n = clampi(ad.seg[s + 1], b, ad.M) - b;
+            if (e >= 0 && e < kThreads && e0 + e < ad.E && n > 0) atomicAdd(lds + e, n);
+        }
+        __syncthreads();
+        const int e = e0 + threadIdx.x, tokens = lds[threadIdx.x];
+        int parts = e < ad.E ? max(1, (tokens + plan.P - 1) / plan.P) : 0;
+        if (parts > plan.slots) parts = 1;  // (offsets out of order)
+        int4 total;
+        const int4 in = make_int4(parts, parts > 1 ? parts : 0, parts > 1, 0), end = block_scan(in, sums, &total);
+        const int q = done.x + end.x - in.x, slot = done.y + end.y - in.y, c = done.z + end.z - in.z;
+        const bool several = parts > 1 && slot + parts <= plan.slots;
+        for (int i = 0; i < parts; ++i)
+            if (q + i < plan.most)
+                plan.table[q + i] = several ? make_int4(e, i * plan.P, min(tokens, (i + 1) * plan.P), slot + i)
+                                            : make_int4(i == 0 ? e : -1, 0, tokens, -1);
+        if (parts > 1) plan.multi[1 + c] = several ? make_int4(e, parts, slot, 0) : make_int4(e, 0, 0, 0);
+        done = make_int4(done.x + total.x, done.y + total.y, done.z + total.z, 0);
+    }
+    for (int q = done.x + threadIdx.x; q < plan.most; q += kThreads) plan.table[q] = make_int4(-1, 0, 0, -1);
+    if (threadIdx.x == 0) plan.multi[0] = make_int4(done.z, 0, 0, 0);
+}
+
+__global__ __launch_bounds__(kThreads) void plan_outer_kernel(AdapterView ad, OuterPlan plan) {
+    __shared__ __align__(16) int lds[kThreads + 16];
+    plan_outer(ad, plan, lds);
+}
+
 // ---------------------------------------------------------------------- shrink
 // One block: a piece and a slice q of K; its waves split the slice, their
 // tiles are added in LDS.  A wave's operands come straight from global memory
@@ -274,9 +342,14 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
 template <typename T, int TT, int RT>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const T* __restrict__ x,
                                                           const T* __restrict__ A, float* __restrict__ part, int stride,
-                                                          int K, int Q, int scaled, Repack v, int64_t items) {
-    __shared__ f32x4 red[kWaves * RT * 64];
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+                                                          int K, int Q, int scaled, Repack v, OuterPlan plan, int64_t items) {
+    __shared__ f32x4 red[kWaves * RT * 64 + 64];
+    if (plan.table && blockIdx.x == gridDim.x - 1) {
+        plan_outer(ad, plan, reinterpret_cast<int*>(red));
+        return;
+    }
+    const int64_t step = gridDim.x - (plan.table != nullptr);
+    for (int64_t item = blockIdx.x; item < items; item += step) {
         const int q = static_cast<int>(item % Q);
         const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
@@ -383,9 +456,14 @@ template <typename T, int RT>
 __global__ __launch_bounds__(kThreads) void shrink_tile_kernel(AdapterView ad, const T* __restrict__ x,
                                                                const T* __restrict__ A, float* __restrict__ part,
                                                                int stride, int K, int Q, int scaled, Repack v,
-                                                               int64_t items) {
+                                                               OuterPlan plan, int64_t items) {
     __shared__ __align__(1024) uint8_t ring[kStages * stage_loads(RT) * kWaves * 1024];
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    if (plan.table && blockIdx.x == gridDim.x - 1) {
+        plan_outer(ad, plan, reinterpret_cast<int*>(ring));
+        return;
+    }
+    const int64_t step = gridDim.x - (plan.table != nullptr);
+    for (int64_t item = blockIdx.x; item < items; item += step) {
         const int q = static_cast<int>(item % Q);
         const Piece pc = find_piece(ad, 64, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
@@ -854,8 +932,8 @@ __global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __re
 }
 
 // ----------------------------------------------------------------------- outer
-// dA and dB in one launch.  A block: one adapter, up to 16 RT of its ranks, 256
-// bytes of columns, part z of the tokens.  It lists the adapter's tokens window
+// dA and dB in one launch.  A block: one part of an adapter's tokens, up to
+// 16 RT of its ranks, 256 bytes of columns.  It lists the adapter's tokens window
 // by window in LDS (they may lie in many segments) and gathers their rows of x
 // and v, 32 tokens a stage, straight into a ring in LDS.  Wave w turns rank
 // tile w of a stage's v into operands, in place and one stage ahead, and takes
@@ -864,7 +942,7 @@ struct OuterJob {
     const float* v;  // [M][v_stride]
     const void* x;
     void* out;       // the gradient, or
-    float* partial;  // [Z][R][cols] when the tokens are split
+    float* partial;  // [slots][max_rank][cols]
     int cols;
     int v_stride;
     int scaled;
@@ -959,7 +1037,7 @@ __device__ __forceinline__ void stage_products(const float* t, const uint32_t (&
 
 template <typename T, int RT>
 __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, OuterJob job0, OuterJob job1,
-                                                            int rank_groups, int Z, int64_t items) {
+                                                            int rank_groups, OuterPlan plan, int64_t items) {
     using O = Outer<T, RT>;
     __shared__ __align__(1024) uint8_t ring[kOuterStages * O::BYTES];
     __shared__ int4 tokens[kWindow / 4];
@@ -969,17 +1047,26 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const OuterJob& job = it >= job1.first_item ? job1 : job0;
         int64_t item = it - job.first_item;
-        const int z = static_cast<int>(item % Z);
-        item /= Z;
         const uint32_t row_bytes = static_cast<uint32_t>(job.cols) * sizeof(T), v_bytes = job.v_stride * 4u;
         const int tiles = static_cast<int>((row_bytes + 255) / 256);
         const int tile = static_cast<int>(item % tiles);
         item /= tiles;
-        const int r0 = static_cast<int>(item % rank_groups) * 16 * RT, e = static_cast<int>(item / rank_groups);
+        const int r0 = static_cast<int>(item % rank_groups) * 16 * RT;
+        const int q = static_cast<int>(item / rank_groups);
+        int e = q, part_from = 0, part_to = ad.M, slot = -1;
+        if (plan.table) {
+            const int* entry = reinterpret_cast<const int*>(plan.table + q);
+            e = uniform_load(entry, 0);
+            part_from = uniform_load(entry, 1);
+            part_to = uniform_load(entry, 2);
+            slot = uniform_load(entry, 3);
+        }
+        if (e < 0) continue;
         int first = 0;
         const int rank = rows_of(ad, e, &first) - r0;
         if (rank <= 0) continue;
         first += r0;
+        int listed = 0;  // tokens of the adapter in the segments so far
         // tokens of a window lie within this many rows of its first, so that
         // 32-bit offsets from there reach all of them
         const int reach = static_cast<int>((kOutside - 32) / max(row_bytes, v_bytes));
@@ -1015,10 +1102,8 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
             ends[threadIdx.x] = sum + before;
             starts[threadIdx.x] = b - (sum + before - n);  // token = starts + place in the list
             total = __builtin_amdgcn_readfirstlane(total);
-            // part z: a run of whole stages
-            const int64_t stages = (total + 31) / 32;
-            const int from = static_cast<int>(stages * z / Z) * 32;
-            const int to = min(total, static_cast<int>(stages * (z + 1) / Z) * 32);
+            const int from = max(0, part_from - listed), to = min(total, part_to - listed);
+            listed += total;
             for (int w0 = from; w0 < to;) {
                 __syncthreads();
                 const int at = w0 + 4 * threadIdx.x;
@@ -1155,34 +1240,44 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
                 const int j = 16 * r + 4 * g + i;
                 if (j >= rank) continue;
                 const size_t at = static_cast<size_t>(first + j) * job.cols + col;
-                float* o = job.partial + static_cast<size_t>(z) * ad.R * job.cols + at;
+                float* o = job.partial + (static_cast<size_t>(max(slot, 0)) * ad.max_rank + r0 + j) * job.cols + col;
                 if constexpr (O::CT == 2) {
                     const float a = acc[r][0][i] * scale, b = acc[r][1][i] * scale;
-                    if (job.partial)
+                    if (slot >= 0)
                         *reinterpret_cast<float2*>(o) = make_float2(a, b);
                     else
                         *reinterpret_cast<uint32_t*>(static_cast<T*>(job.out) + at) = bf16_bits(a) | bf16_bits(b) << 16;
                 } else {
-                    *(job.partial ? o : static_cast<float*>(job.out) + at) = acc[r][0][i] * scale;
+                    *(slot >= 0 ? o : static_cast<float*>(job.out) + at) = acc[r][0][i] * scale;
                 }
             }
     }
 }
 
-// The token parts' sums of both gradients joined in order, four columns a
-// thread.
+// The parts of the adapters that have several joined in order, both gradients,
+// four columns a thread.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void join_parts_kernel(const float* __restrict__ partA, T* __restrict__ dA,
-                                                              size_t nA, const float* __restrict__ partB,
-                                                              T* __restrict__ dB, size_t nB, int Z) {
-    for (size_t k = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; k < nA + nB;
-         k += static_cast<size_t>(gridDim.x) * kThreads * 4) {
-        const bool second = k >= nA;
-        const size_t i = second ? k - nA : k, n = second ? nB : nA;
-        const float* part = (second ? partB : partA) + i;
-        T* out = (second ? dB : dA) + i;
+__global__ __launch_bounds__(kThreads) void join_parts_kernel(AdapterView ad, OuterJob job0, OuterJob job1,
+                                                              OuterPlan plan) {
+    const int count = uniform_load(reinterpret_cast<const int*>(plan.multi), 0);
+    const int64_t colsA = job0.out ? job0.cols : 0, colsB = job1.out ? job1.cols : 0, quads = (colsA + colsB) / 4;
+    const int64_t most = static_cast<int64_t>(count) * ad.max_rank * quads;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; k < most;
+         k += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t row = k / quads;
+        const int4 m = plan.multi[1 + row / ad.max_rank];
+        const int j = static_cast<int>(row % ad.max_rank);
+        const int r0 = clampi(ad.row[m.x], 0, ad.R), r1 = clampi(ad.row[m.x + 1], r0, ad.R);
+        if (j >= r1 - r0 || m.y == 0) continue;
+        const int64_t c = k % quads * 4;
+        const bool second = c >= colsA;
+        const OuterJob& job = second ? job1 : job0;
+        const int64_t col = second ? c - colsA : c;
+        const size_t slice = static_cast<size_t>(ad.max_rank) * job.cols;
+        const float* part = job.partial + m.z * slice + static_cast<size_t>(j) * job.cols + col;
+        T* out = static_cast<T*>(job.out) + static_cast<size_t>(r0 + j) * job.cols + col;
         f32x4 s = *reinterpret_cast<const f32x4*>(part);
-        for (int z = 1; z < Z; ++z) s += *reinterpret_cast<const f32x4*>(part + z * n);
+        for (int z = 1; z < m.y; ++z) s += *reinterpret_cast<const f32x4*>(part + z * slice);
         if constexpr (sizeof(T) == 4)
             *reinterpret_cast<f32x4*>(out) = s;
         else
@@ -1240,15 +1335,15 @@ int slices_of(const AdapterArgs& a, int K) {
 
 template <typename T>
 int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int scaled,
-                  const Repack& v, hipStream_t s) {
+                  const Repack& v, const OuterPlan& plan, hipStream_t s) {
     const int tt = shrink_tile_of(a.ad.M, a.ad.S), Q = slices_of(a, K), rt = (a.ad.max_rank + 15) / 16;
     const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * tt) * Q;
     auto k = tt == 1 ? (rt <= 1 ? shrink_kernel<T, 1, 1> : rt <= 2 ? shrink_kernel<T, 1, 2>
                         : rt <= 4 ? shrink_kernel<T, 1, 4> : shrink_kernel<T, 1, 8>)
                      : (rt <= 1 ? shrink_tile_kernel<T, 1> : rt <= 2 ? shrink_tile_kernel<T, 2>
                         : rt <= 4 ? shrink_tile_kernel<T, 4> : shrink_tile_kernel<T, 8>);
-    hipLaunchKernelGGL(k, dim3(grid_of(items)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
-                       static_cast<const T*>(A), part, stride, K, Q, scaled, v, items);
+    hipLaunchKernelGGL(k, dim3(grid_of(items) + (plan.table != nullptr)), dim3(kThreads), 0, s, a.ad,
+                       static_cast<const T*>(x), static_cast<const T*>(A), part, stride, K, Q, scaled, v, plan, items);
     return Q;
 }
 
@@ -1285,31 +1380,36 @@ void forward(const AdapterArgs& a, hipStream_t s) {
     if (a.ad.max_rank > 0) {
         // a single slice with rows of v's own length writes v itself
         if (a.v && stride == a.ad.max_rank && slices_of(a, a.K) == 1) part = a.v;
-        Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, Repack{}, s);
+        Q = launch_shrink<T>(a, a.x, a.A, part, stride, a.K, 0, Repack{}, OuterPlan{}, s);
     }
     launch_expand<T>(a, part, stride, Q, a.B, a.y, part == a.v ? nullptr : a.v, a.ad.max_rank, a.ad.max_rank, a.N, 1, s);
 }
 
 // How the outer products are split.
 struct OuterSplit {
-    int RT, rank_groups, Z;
+    int RT, rank_groups;
+    int P;       // tokens of a part
+    int slots;   // partial results at most: every adapter with several parts has under 2 / P of its tokens
+    bool table;  // whether some adapter may have several
 };
 
-OuterSplit outer_split(int64_t M, int32_t K, int32_t N, int32_t E, int32_t max_rank, int32_t dtype) {
+OuterSplit outer_split(int64_t M, int32_t K, int32_t N, int32_t max_rank, int32_t dtype) {
     OuterSplit o;
     const int rt = (max_rank + 15) / 16;
     o.RT = rt <= 1 ? 1 : rt <= 2 ? 2 : 4;
-    o.rank_groups = (rt + o.RT - 1) / o.RT;
-    const int wide = 16 * (16 / esize(dtype));
+    o.rank_groups = std::max(1, (rt + o.RT - 1) / o.RT);
+    // parts enough that all tokens' would fill the card, of 256 tokens at least
+    const int wide = 256 / esize(dtype);
     const int64_t tiles = (K + wide - 1) / wide + (N + wide - 1) / wide;
-    const int64_t blocks = tiles * (E > 0 ? E : 1) * (o.rank_groups > 0 ? o.rank_groups : 1);
-    int64_t z = 2 * kFill / blocks;
-    const int64_t most = (M + 255) / 256;  // parts of 256 tokens at least
-    if (z > most) z = most;
-    if (z > 16) z = 16;
-    o.Z = static_cast<int>(z < 1 ? 1 : z);
+    const int64_t parts = std::max(int64_t(1), kFill / (tiles * o.rank_groups));
+    o.P = static_cast<int>(std::max(int64_t(256), (M / parts + 31) / 32 * 32));
+    o.table = M > o.P;
+    o.slots = o.table ? static_cast<int>(2 * M / o.P) : 0;
     return o;
 }
+
+// Entries of the work list.
+int64_t outer_entries(const OuterSplit& o, int64_t M, int32_t E) { return o.table ? E + M / o.P : E; }
 
 template <typename T>
 void zero(void* p, size_t elements, hipStream_t s) {
@@ -1320,31 +1420,26 @@ void zero(void* p, size_t elements, hipStream_t s) {
 }
 
 template <typename T>
-void launch_outer(const AdapterArgs& a, const float* dv, int dv_stride, const float* v, int v_stride, float* partial,
-                  hipStream_t s) {
-    const OuterSplit o = outer_split(a.ad.M, a.K, a.N, a.ad.E, a.ad.max_rank, a.dtype);
-    const size_t nA = static_cast<size_t>(a.ad.R) * a.K, nB = static_cast<size_t>(a.ad.R) * a.N;
+void launch_outer(const AdapterArgs& a, const OuterSplit& o, const OuterPlan& plan, const float* dv, int dv_stride,
+                  const float* v, int v_stride, float* partial, hipStream_t s) {
     if (a.ad.E == 0) {
-        if (a.dA) zero<T>(a.dA, nA, s);
-        if (a.dB) zero<T>(a.dB, nB, s);
+        if (a.dA) zero<T>(a.dA, static_cast<size_t>(a.ad.R) * a.K, s);
+        if (a.dB) zero<T>(a.dB, static_cast<size_t>(a.ad.R) * a.N, s);
         return;
     }
-    const bool parts = o.Z > 1;
     const auto count = [&](int cols) {
-        const int wide = 16 * Unit<T>::kCols;
-        return static_cast<int64_t>((cols + wide - 1) / wide) * a.ad.E * o.rank_groups * o.Z;
+        const int64_t tiles = (static_cast<int64_t>(cols) * sizeof(T) + 255) / 256;
+        return tiles * o.rank_groups * outer_entries(o, a.ad.M, a.ad.E);
     };
     const int64_t itemsA = a.dA ? count(a.K) : 0, itemsB = a.dB ? count(a.N) : 0;
-    const OuterJob jobA{dv, a.x, a.dA, parts ? partial : nullptr, a.K, dv_stride, 0, 0};
-    const OuterJob jobB{v, a.dy, a.dB, parts ? partial + o.Z * nA : nullptr, a.N, v_stride, 1, itemsA};
+    const OuterJob jobA{dv, a.x, a.dA, partial, a.K, dv_stride, 0, 0};
+    const OuterJob jobB{v, a.dy, a.dB, partial + static_cast<size_t>(o.slots) * a.ad.max_rank * a.K, a.N, v_stride, 1,
+                        itemsA};
     auto k = o.RT == 1 ? outer_kernel<T, 1> : o.RT == 2 ? outer_kernel<T, 2> : outer_kernel<T, 4>;
-    hipLaunchKernelGGL(k, dim3(grid_of(itemsA + itemsB)), dim3(kThreads), 0, s, a.ad, jobA, jobB, o.rank_groups, o.Z,
+    hipLaunchKernelGGL(k, dim3(grid_of(itemsA + itemsB)), dim3(kThreads), 0, s, a.ad, jobA, jobB, o.rank_groups, plan,
                        itemsA + itemsB);
-    if (!parts) return;
-    const size_t a4 = a.dA ? nA : 0, b4 = a.dB ? nB : 0, blocks = (a4 + b4) / 1024 + 1;
-    hipLaunchKernelGGL((join_parts_kernel<T>), dim3(static_cast<unsigned>(std::min(blocks, size_t(8192)))),
-                       dim3(kThreads), 0, s, jobA.partial, static_cast<T*>(a.dA), a4, jobB.partial,
-                       static_cast<T*>(a.dB), b4, o.Z);
+    if (o.table)
+        hipLaunchKernelGGL((join_parts_kernel<T>), dim3(2048), dim3(kThreads), 0, s, a.ad, jobA, jobB, plan);
 }
 
 // Whether v's rows are whole 16-byte pieces.
@@ -1355,21 +1450,29 @@ void backward(const AdapterArgs& a, hipStream_t s) {
     const int stride = stride_of(a.ad.max_rank);
     const size_t rows = static_cast<size_t>(a.ad.M) * stride;
     const int most = most_slices(a.ad.M, a.N, a.dtype);
-    // workspace: the slices of dv, their sum, v in rows of the stride, the
-    // parts of the gradients
-    float* part = static_cast<float*>(a.workspace);
+    const OuterSplit o = outer_split(a.ad.M, a.K, a.N, a.ad.max_rank, a.dtype);
+    const int64_t entries = o.table ? outer_entries(o, a.ad.M, a.ad.E) : 0;
+    // workspace: the work list, the slices of dv, their sum, v in rows of the
+    // stride, the parts of the gradients
+    int4* table = static_cast<int4*>(a.workspace);
+    float* part = reinterpret_cast<float*>(table + (o.table ? entries + a.ad.E + 1 : 0));
     float* joined = most > 1 ? part + most * rows : part;
     float* packed = joined + rows;
     float* partial = v_in_pieces(a.ad.max_rank) ? packed : packed + rows;
     const bool repack = a.dB && !v_in_pieces(a.ad.max_rank);
     const Repack v{repack ? a.v : nullptr, packed, a.ad.max_rank, stride};
+    const bool list = o.table && a.ad.E > 0 && (a.dA || a.dB);
+    const OuterPlan plan{list ? table : nullptr, table + entries, o.P, static_cast<int>(entries), o.slots};
     int Q = 1;
     const bool any = a.ad.max_rank > 0 && a.ad.M > 0;
-    if ((a.dx || a.dA) && any)
-        Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, v, s);
-    else if (repack && any)
-        hipLaunchKernelGGL(repack_kernel, dim3(grid_of((static_cast<int64_t>(a.ad.M) + 15) / 16)), dim3(kThreads), 0, s,
-                           v, a.ad.M);
+    if ((a.dx || a.dA) && any) {
+        Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, v, plan, s);
+    } else if (any) {
+        if (repack)
+            hipLaunchKernelGGL(repack_kernel, dim3(grid_of((static_cast<int64_t>(a.ad.M) + 15) / 16)), dim3(kThreads),
+                               0, s, v, a.ad.M);
+        if (list) hipLaunchKernelGGL(plan_outer_kernel, dim3(1), dim3(kThreads), 0, s, a.ad, plan);
+    }
     if (a.dx)  // leaves the sum of dv's slices for the outer products
         launch_expand<T>(a, part, stride, Q, a.A, a.dx, Q > 1 && a.dA ? joined : nullptr, stride, stride, a.K, 0, s);
     else if (a.dA && Q > 1)
@@ -1377,8 +1480,8 @@ void backward(const AdapterArgs& a, hipStream_t s) {
                            dim3(static_cast<unsigned>(rows / 1024 < 4096 ? rows / 1024 + 1 : 4096)), dim3(kThreads), 0,
                            s, part, joined, rows, Q);
     if (a.dA || a.dB)
-        launch_outer<T>(a, Q > 1 ? joined : part, stride, repack ? packed : a.v, repack ? stride : a.ad.max_rank,
-                        partial, s);
+        launch_outer<T>(a, o, plan, Q > 1 ? joined : part, stride, repack ? packed : a.v,
+                        repack ? stride : a.ad.max_rank, partial, s);
 }
 
 }  // namespace
@@ -1387,12 +1490,15 @@ size_t adapter_forward_workspace(int64_t M, int32_t K, int32_t, int32_t, int32_t
     return static_cast<size_t>(M) * stride_of(max_rank) * sizeof(float) * most_slices(M, K, dtype);
 }
 
-size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, int32_t R, int32_t max_rank,
+size_t adapter_backward_workspace(int64_t M, int32_t K, int32_t N, int32_t E, int32_t, int32_t max_rank,
                                   int32_t dtype) {
     const size_t rows = static_cast<size_t>(M) * stride_of(max_rank) * sizeof(float);
-    const int most = most_slices(M, N, dtype), Z = outer_split(M, K, N, E, max_rank, dtype).Z;
+    const int most = most_slices(M, N, dtype);
+    const OuterSplit o = outer_split(M, K, N, max_rank, dtype);
     size_t n = rows * ((most > 1 ? most + 1 : 1) + (v_in_pieces(max_rank) ? 0 : 1));
-    if (Z > 1) n += static_cast<size_t>(Z) * static_cast<size_t>(R) * (static_cast<size_t>(K) + N) * sizeof(float);
+    if (o.table)
+        n += static_cast<size_t>(outer_entries(o, M, E) + E + 1) * sizeof(int4) +
+             static_cast<size_t>(o.slots) * max_rank * (static_cast<size_t>(K) + N) * sizeof(float);
     return n;
 }
 

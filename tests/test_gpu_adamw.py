@@ -270,6 +270,17 @@ def test_writes_stay_inside_the_tensors():
         assert (bufs[k][inside] != 3).all()
 
 
+def test_more_than_2_to_31_elements():
+    n = 2 ** 31 + 777
+    p, grad = torch.zeros(n, device="cuda", dtype=BF), torch.zeros(n, device="cuda", dtype=BF)
+    plan = ss1.AdamWPlan.make([p], [grad], state="fp8")
+    grad[-9:] = 1.0
+    grad[5] = -1.0
+    plan.step(step=1, lr=0.5, seed=1)
+    assert p.count_nonzero() == 10 and ((p[-9:].float() + 0.5).abs() <= 2.0 ** -8).all()
+    assert abs(float(p[5]) - 0.5) <= 2.0 ** -8 and plan.m[0].view(torch.uint8).count_nonzero() == 10
+
+
 def test_empty_plan_and_graph_replays():
     ss1.AdamWPlan.make([], []).step(step=1, lr=1e-3)
     d, plan = make([3000, 17], BF, True, BF, "fp8", seed=2)

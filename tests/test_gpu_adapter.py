@@ -183,6 +183,68 @@ def test_integers_bit_for_bit(batch, K, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_many_segments_and_adapters(dtype):
+    # more segments and adapters than a block has threads, and one adapter with many times the others' tokens
+    g = torch.Generator().manual_seed(5)
+    ranks = [1 + i % 5 for i in range(300)]
+    ids = torch.randint(-1, 300, (700,), generator=g)
+    ids[torch.rand(700, generator=g) < 0.3] = 7
+    segs = [(int(n), int(e)) for n, e in zip(torch.randint(0, 5, (700,), generator=g), ids)]
+    check(Case(segs, ranks, 264, 136, dtype, seed=3))
+    c = Case(segs, ranks, 64, 40, dtype, seed=3, integers=True)
+    y, v = c.forward(base=c.base, save_v=True)
+    ry, rv, _, _ = c.forward64()
+    assert torch.equal(v.double(), rv) and torch.equal(y, ry.float().to(dtype))
+    for got, want in zip(c.backward(v, dx_base=c.dxb), c.backward64(v)[0]):
+        assert torch.equal(got, want.float().to(dtype))
+
+
+@pytest.mark.parametrize("segs,ranks", [
+    ([(2500, 0), (300, 1), (2700, 0)], [16, 24]),                     # parts of an adapter in several segments
+    ([(1, 2), (6000, 1), (31, 0), (33, 2), (1, 1)], [100, 64, 5]),
+    ([(40, i % 2) for i in range(150)], [3, 128]),
+])
+def test_uneven_sharing(segs, ranks):
+    # adapters whose tokens are cut into several parts beside adapters of one part
+    check(Case(segs, ranks, 520, 264, BF, seed=len(segs)))
+    c = Case(segs, ranks, 72, 40, BF, seed=1, integers=True)
+    _, v = c.forward(save_v=True)
+    for got, want in zip(c.backward(v), c.backward64(v, base=False)[0]):
+        assert torch.equal(got, want.float().to(BF))
+    only = c.backward(v, dx=None, dA=None)[2]                          # dB alone: no shrink runs before it
+    assert torch.equal(only, c.backward64(v)[0][2].float().to(BF))
+
+
+def test_offsets_past_32_bits():
+    # 2.4 GB of x: the tokens of one adapter lie at both ends, over 2^31 bytes apart
+    M, K, N, tail = 73001, 16384, 64, 300
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=BF)
+    A = (torch.randn((40, K), generator=g, device="cuda") / 128).to(BF)
+    B = (0.1 * torch.randn((40, N), generator=g, device="cuda")).to(BF)
+    s = ss1.AdapterSet.make(A, B, [16, 24], [1.0, 2.0])
+    seg = torch.tensor([0, 200, 500, M - tail, M], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([0, 1, -1, 0], dtype=torch.int32, device="cuda")
+    dy = torch.randn((M, N), generator=g, device="cuda", dtype=BF)
+    y, v = ss1.adapter_forward(x, s, seg, ids, save_v=True)
+    dx, dA, dB = ss1.adapter_backward(dy, x, v, s, seg, ids)
+    assert (y[500:M - tail] == 0).all() and (dx[500:M - tail] == 0).all()
+    at = torch.cat([torch.arange(200), torch.arange(M - tail, M)]).cuda()
+    xs, dys, vs = x[at].double(), dy[at].double(), v[at, :16].double()
+    A0, B0 = A[:16].double(), B[:16].double()
+    # rounding of y and dx (2^-8), and of the sums as above
+    assert ((vs - xs @ A0.t()).abs() <= n_eff(K) * U * (xs.abs() @ A0.abs().t())).all()
+    want = vs @ B0
+    assert ((y[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * (vs.abs() @ B0.abs())).all()
+    dv = dys @ B0.t()
+    want = dv @ A0
+    assert ((dx[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * (dv.abs() @ A0.abs())).all()
+    for got, l, r in ((dA[:16], dv, xs), (dB[:16], vs, dys)):
+        want = l.t() @ r
+        assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * (l.abs().t() @ r.abs())).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 def test_without_base_and_in_place(dtype):
     c = Case([(30, 0), (7, -1), (1, 1)], [16, 40], 128, 264, dtype, seed=9)
     y, v = c.forward(save_v=True)

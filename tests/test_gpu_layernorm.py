@@ -187,6 +187,20 @@ def test_constant_and_large_rows():
     assert ((y.double() - ry).abs() <= ty).all() and ((rstd.double() - rr).abs() <= tr).all()
 
 
+def test_offsets_past_32_bits():
+    # 4.6 GB of x; the last rows, against the same rows in a tensor of their own
+    M, K = 140001, 16384
+    x = torch.randn((M, K), device="cuda", dtype=torch.bfloat16)
+    gamma = torch.rand(K, device="cuda") + 0.5
+    y, mean, rstd = ss1.layernorm_forward(x, gamma)
+    dx, _, _ = ss1.layernorm_backward(x, x, gamma, mean, rstd)
+    for rows in (slice(0, 5), slice(M - 5, M)):
+        yt, mt, rt = ss1.layernorm_forward(x[rows].clone(), gamma)
+        assert torch.equal(y[rows], yt) and torch.equal(mean[rows], mt) and torch.equal(rstd[rows], rt)
+        xt = x[rows].clone()
+        assert torch.equal(dx[rows], ss1.layernorm_backward(xt, xt, gamma, mt, rt)[0])
+
+
 def test_equal_calls_give_equal_bits_and_other_streams():
     x, gamma, beta, dy = make(1500, 1000, torch.bfloat16, torch.bfloat16, seed=8)
     y, mean, rstd = ss1.layernorm_forward(x, gamma, beta)

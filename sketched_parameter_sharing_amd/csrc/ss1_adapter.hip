@@ -266,7 +266,7 @@ __global__ __launch_bounds__(kThreads) void plan_outer_kernel(AdapterView ad, Ou
 // One block: a piece and a slice q of K; its waves split the slice, their
 // tiles are added in LDS.  A wave's operands come straight from global memory
 // in whole 128-byte lines.  part[q][m][stride], columns past the rank 0.
-template <typename T, int TT, int RT>
+template <typename T, int RT>
 __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,
                                             int stride, float scale, f32x4* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -278,60 +278,52 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
     const int u1 = static_cast<int>(static_cast<int64_t>(units) * (q + 1) / Q);
     const auto rx = make_rsrc(x + static_cast<size_t>(pc.begin) * K, static_cast<uint32_t>(pc.n) * Kb);
     const auto ra = make_rsrc(A + static_cast<size_t>(pc.first) * K, static_cast<uint32_t>(pc.rank) * Kb);
-    f32x4 acc[TT][RT];
+    f32x4 acc[RT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0, 0, 0, 0};
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
     // a load covers 8 rows x 128 bytes; pair_operands makes two operands of
     // 16 rows x 64 bytes from two loads
     const uint32_t piece = 16u * ((lane >> 4) + 4 * ((lane >> 3) & 1)), lo8 = pair_lane_mask(lane);
     const uint32_t lane_off = (lane & 7) * Kb + piece;
     // units whose loads are in flight together (past the wave's share or the
     // row: zeros)
-    constexpr int UN = TT + RT <= 4 ? 2 : 1;
+    constexpr int UN = RT <= 2 ? 2 : 1;
     for (int ub = u0 + wave * UN; ub < u1; ub += UN * kWaves) {
-        uint4 xf[UN][TT][2], af[UN][RT][2];
+        uint4 xf[UN][2], af[UN][RT][2];
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             const uint32_t at = 128u * (ub + u);
             const uint32_t off = ub + u < u1 && at + piece < Kb ? lane_off + at : kOutside;
 #pragma unroll
-            for (int t = 0; t < 2 * TT; ++t) xf[u][t / 2][t % 2] = buf_load16(rx, off + t * 8 * Kb, 0);
+            for (int h = 0; h < 2; ++h) xf[u][h] = buf_load16(rx, off + h * 8 * Kb, 0);
 #pragma unroll
             for (int r = 0; r < 2 * RT; ++r) af[u][r / 2][r % 2] = buf_load16(ra, off + r * 8 * Kb, 0);
         }
         __builtin_amdgcn_sched_barrier(0);  // or each load sinks to its first use
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t) pair_operands(xf[u][t][0], xf[u][t][1], lo8, xf[u][t][0], xf[u][t][1]);
+            pair_operands(xf[u][0], xf[u][1], lo8, xf[u][0], xf[u][1]);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 pair_operands(af[u][r][0], af[u][r][1], lo8, af[u][r][0], af[u][r][1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[t][r] = mma(x, xf[u][t][h], af[u][r][h], acc[t][r]);
+                for (int h = 0; h < 2; ++h) acc[r] = mma(x, xf[u][h], af[u][r][h], acc[r]);
             }
         }
     }
+    __syncthreads();
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        __syncthreads();
+    for (int r = 0; r < RT; ++r) red[(wave * RT + r) * 64 + lane] = acc[r];
+    __syncthreads();
+    for (int i = threadIdx.x; i < RT * 64; i += kThreads) {
+        f32x4 s = red[i];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) red[(wave * RT + r) * 64 + lane] = acc[t][r];
-        __syncthreads();
-        for (int i = threadIdx.x; i < RT * 64; i += kThreads) {
-            f32x4 s = red[i];
+        for (int w = 1; w < kWaves; ++w) s += red[w * RT * 64 + i];
+        const int j = 16 * (i >> 6) + (i & 15), m = 4 * ((i >> 4) & 3);
+        if (j < stride)
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) s += red[w * RT * 64 + i];
-            const int j = 16 * (i >> 6) + (i & 15), m = 16 * t + 4 * ((i >> 4) & 3);
-            if (j < stride)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (m + k < pc.n) out[static_cast<size_t>(m + k) * stride + j] = j < pc.rank ? s[k] * scale : 0.0f;
-        }
+            for (int k = 0; k < 4; ++k)
+                if (m + k < pc.n) out[static_cast<size_t>(m + k) * stride + j] = j < pc.rank ? s[k] * scale : 0.0f;
     }
     const int rest = stride - 16 * RT;  // columns past the tiles are zero
     if (rest > 0)
@@ -339,7 +331,7 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
             out[static_cast<size_t>(i / rest) * stride + 16 * RT + i % rest] = 0.0f;
 }
 
-template <typename T, int TT, int RT>
+template <typename T, int RT>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const T* __restrict__ x,
                                                           const T* __restrict__ A, float* __restrict__ part, int stride,
                                                           int K, int Q, int scaled, Repack v, OuterPlan plan, int64_t items) {
@@ -351,7 +343,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const 
     const int64_t step = gridDim.x - (plan.table != nullptr);
     for (int64_t item = blockIdx.x; item < items; item += step) {
         const int q = static_cast<int>(item % Q);
-        const Piece pc = find_piece(ad, 16 * TT, static_cast<int>(item / Q));
+        const Piece pc = find_piece(ad, 16, static_cast<int>(item / Q));
         if (pc.n == 0) continue;
         if (v.from && q == 0) repack_rows(v, pc.begin, pc.n);
         float* out = part + (static_cast<size_t>(q) * ad.M + pc.begin) * stride;
@@ -362,13 +354,13 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterView ad, const 
         }
         // tiles for the rank of this adapter, not for the largest
         if (RT == 1 || pc.rank <= 16)
-            shrink_body<T, TT, 1>(pc, x, A, out, K, Q, q, stride, scale, red);
+            shrink_body<T, 1>(pc, x, A, out, K, Q, q, stride, scale, red);
         else if (RT == 2 || pc.rank <= 32)
-            shrink_body<T, TT, RT < 2 ? RT : 2>(pc, x, A, out, K, Q, q, stride, scale, red);
+            shrink_body<T, RT < 2 ? RT : 2>(pc, x, A, out, K, Q, q, stride, scale, red);
         else if (RT == 4 || pc.rank <= 64)
-            shrink_body<T, TT, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, stride, scale, red);
+            shrink_body<T, RT < 4 ? RT : 4>(pc, x, A, out, K, Q, q, stride, scale, red);
         else
-            shrink_body<T, TT, RT>(pc, x, A, out, K, Q, q, stride, scale, red);
+            shrink_body<T, RT>(pc, x, A, out, K, Q, q, stride, scale, red);
     }
 }
 
@@ -502,21 +494,6 @@ struct Unit<float> {
     static constexpr int kRanks = 16, kLoads = 4, kCols = 4, kFrags = 1;
 };
 
-// v of 16 tokens and one rank unit as operands in LDS: frag[h][lane], h = hi,
-// lo (bf16) or only one (float32); lane m + 16 g holds the g-th group of ranks.
-__device__ __forceinline__ void stage_one(const __bf16*, uint4* frag, int m, int g, const float (&v)[8]) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) split(v[j], &hi[j], &lo[j]);
-    frag[m + 16 * g] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-    frag[64 + m + 16 * g] =
-        make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
-}
-__device__ __forceinline__ void stage_one(const float*, uint4* frag, int m, int g, const float (&v)[4]) {
-    frag[m + 16 * g] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                  __float_as_uint(v[3]));
-}
-
 // Rows (of B: ranks; of x: tokens) of this lane's 16 bytes of columns -> one
 // operand a column.
 __device__ __forceinline__ void column_operands(const __bf16*, const uint4 (&t)[8], uint4 (&f)[8]) {
@@ -569,10 +546,10 @@ __device__ __forceinline__ void without_adapter(const Piece& pc, const T* base, 
     }
 }
 
-template <typename T, int TT, int KU>
+template <typename T, int KU>
 __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
-                                            int v_stride, int v_cols, const T* B, const T* base, T* y, float* v_out, int N, int tile0,
-                                            int tiles, float scale, uint4* frags) {
+                                            int v_stride, int v_cols, const T* B, const T* base, T* y, float* v_out,
+                                            int N, int tile0, int tiles, float scale, uint4* frags) {
     using U = Unit<T>;
     constexpr int GROUP = U::kRanks / 4;  // ranks of one operand lane
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
@@ -581,14 +558,13 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
     const auto ry = make_rsrc(y + static_cast<size_t>(pc.begin) * N, static_cast<uint32_t>(pc.n) * Nb);
     const auto rs = make_rsrc((base ? base : y) + static_cast<size_t>(pc.begin) * N,
                               base ? static_cast<uint32_t>(pc.n) * Nb : 0u);
-    const auto column = [&](int tile) {
+    const auto column = [&](int tile) {  // (a row's offset is under 2^31, so kOutside plus it stays outside)
         const uint32_t col = 16u * (static_cast<uint32_t>(tile) * (kThreads / 4) + wave * 16 + c);
-        return col < Nb ? col : kOutside;
+        return tile < tile0 + tiles && col < Nb ? col : kOutside;
     };
-    // rows of B and of base (4 g + i of 16 tokens each) in this lane's columns
+    // rows of B and of base (tokens 4 g + i) in this lane's columns
     uint4 rows[KU][U::kLoads], old[4];
-    // (a row's offset is under 2^31, so kOutside plus it stays outside)
-    const auto fetch_rows = [&](uint32_t col) {
+    const auto fetch = [&](uint32_t col) {
         // opaque, or the compiler keeps every row's offset in a register
         uint32_t wide = Nb;
         asm volatile("" : "+s"(wide));
@@ -602,23 +578,19 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
             }
             at += (U::kRanks - U::kLoads) * wide;
         }
-    };
-    const auto fetch_base = [&](int t, uint32_t col, uint4 (&to)[4]) {
-        uint32_t at = (16 * t + 4 * g) * Nb + col;
+        at = 4 * g * wide + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            to[i] = buf_load16(rs, at, 0);
-            at += Nb;
+            old[i] = buf_load16(rs, at, 0);
+            at += wide;
         }
     };
-    // in flight while v is staged
-    fetch_rows(column(tile0));
-    fetch_base(0, column(tile0), old);
-    __syncthreads();  // the last piece's readers of frags
+    fetch(column(tile0));  // in flight while v is staged
+    __syncthreads();       // the last piece's readers of frags
     // v of the piece, summed over the slices of K in order (columns past the
     // rank are zero there; the stride is a multiple of 8)
 #pragma unroll 1
-    for (int i = threadIdx.x; i < 16 * TT * KU * 4; i += kThreads) {
+    for (int i = threadIdx.x; i < 16 * KU * 4; i += kThreads) {
         const int m = i / (KU * 4), unit = i % (KU * 4) / 4, gi = i % 4, r = unit * U::kRanks + GROUP * gi;
         f32x4 v[GROUP / 4];
 #pragma unroll
@@ -645,62 +617,55 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
         float scaled[GROUP];
 #pragma unroll
         for (int j = 0; j < GROUP; ++j) scaled[j] = v[j / 4][j % 4] * scale;
-        stage_one(B, frags + ((m >> 4) * KU + unit) * U::kFrags * 64, m & 15, gi, scaled);
+        uint4 f[U::kFrags];
+        rank_operands(B, scaled, f);
+#pragma unroll
+        for (int h = 0; h < U::kFrags; ++h) frags[(unit * U::kFrags + h) * 64 + m + 16 * gi] = f[h];
     }
     const int past = KU * U::kRanks;  // columns that no unit covers are zero
     if (v_out && past < v_cols)
         for (int i = threadIdx.x; i < pc.n * (v_cols - past); i += kThreads)
             v_out[static_cast<size_t>(pc.begin + i / (v_cols - past)) * v_stride + past + i % (v_cols - past)] = 0.0f;
     __syncthreads();
+#pragma unroll 1
     for (int tile = tile0; tile < tile0 + tiles; ++tile) {
-        const uint32_t col = column(tile);
-        if (tile > tile0) {
-            fetch_rows(col);
-            fetch_base(0, col, old);
-        }
+        f32x4 acc[U::kCols];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
         uint4 f[KU][U::kCols];
 #pragma unroll
         for (int k = 0; k < KU; ++k) {
             column_operands(B, rows[k], f[k]);
             __builtin_amdgcn_sched_barrier(0);  // one unit's rows at a time
         }
-#pragma unroll 1
-        for (int t = 0; t < TT; ++t) {
-            uint4 next[4];
-            fetch_base(t + 1, col, next);  // past the piece: zeros, unused
-            f32x4 acc[U::kCols];
+        fetch(column(tile + 1));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
+        for (int k = 0; k < KU; ++k)
 #pragma unroll
-            for (int k = 0; k < KU; ++k)
+            for (int h = 0; h < U::kFrags; ++h) {
+                const uint4 a = frags[(k * U::kFrags + h) * 64 + lane];
 #pragma unroll
-                for (int h = 0; h < U::kFrags; ++h) {
-                    const uint4 a = frags[((t * KU + k) * U::kFrags + h) * 64 + lane];
-#pragma unroll
-                    for (int j = 0; j < U::kCols; ++j) acc[j] = mma(B, a, f[k][j], acc[j]);
-                }
-            uint32_t at = (16 * t + 4 * g) * Nb + col;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                buf_store16(ry, at, pack(B, acc, i));
-                old[i] = next[i];
-                at += Nb;
+                for (int j = 0; j < U::kCols; ++j) acc[j] = mma(B, a, f[k][j], acc[j]);
             }
+        uint32_t at = 4 * g * Nb + column(tile);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            buf_store16(ry, at, pack(B, acc, i));
+            at += Nb;
         }
     }
 }
 
-template <typename T, int TT, int KU>
+template <typename T, int KU>
 __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, const float* __restrict__ part,
                                                              int stride, int Q, const T* __restrict__ B, const T* base, T* y,
                                                           float* __restrict__ v_out, int v_stride, int v_cols, int N,
                                                           int scaled, int columns, int per, int tiles, int64_t items) {
-    __shared__ uint4 frags[TT * KU * Unit<T>::kFrags * 64];
-    constexpr int TM = 16 * TT;
+    __shared__ uint4 frags[KU * Unit<T>::kFrags * 64];
     const size_t slice = static_cast<size_t>(ad.M) * stride;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int cg = static_cast<int>(item % columns);
-        const Piece pc = find_piece(ad, TM, static_cast<int>(item / columns));
+        const Piece pc = find_piece(ad, 16, static_cast<int>(item / columns));
         if (pc.n == 0) continue;
         const int tile0 = cg * per, count = min(per, tiles - tile0);
         float* vo = cg == 0 ? v_out : nullptr;
@@ -711,13 +676,13 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, con
         const float scale = scaled ? pc.scale : 1.0f;
         constexpr int R = Unit<T>::kRanks;
         if (KU == 1 || pc.rank <= R)
-            expand_body<T, TT, 1>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, 1>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
         else if (KU == 2 || pc.rank <= 2 * R)
-            expand_body<T, TT, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
         else if (KU == 4 || pc.rank <= 4 * R)
-            expand_body<T, TT, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
         else
-            expand_body<T, TT, KU>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
+            expand_body<T, KU>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0, count, scale, frags);
     }
 }
 
@@ -1310,15 +1275,9 @@ int most_slices(int64_t M, int32_t cols, int32_t dtype) {
     return static_cast<int>(q < 1 ? 1 : q);
 }
 
-// Tokens of a tile in units of 16, by the mean length of a segment: pieces of
-// single tokens gain nothing from larger tiles.
-int tile_of(int64_t M, int64_t S) {
-    const int64_t mean = S > 0 ? M / S : M;
-    return mean <= 24 ? 1 : mean <= 64 ? 2 : 4;
-}
-
-// ... of the shrink: the two kernels have 16 and 64.
-int shrink_tile_of(int64_t M, int64_t S) { return tile_of(M, S) > 1 ? 4 : 1; }
+// Whether the batch takes the kernels of 64-token tiles, or those of 16: by the
+// mean length of a segment, since tiles that hold a few tokens gain nothing.
+bool long_segments(int64_t M, int64_t S) { return M > 24 * std::max(S, int64_t(1)); }
 
 // Floats of one token's row of v in the workspace: 16-byte loads of 8 ranks.
 int stride_of(int32_t max_rank) { return (max_rank + 7) / 8 * 8; }
@@ -1328,7 +1287,7 @@ unsigned grid_of(int64_t items) { return static_cast<unsigned>(items < kMaxBlock
 // Slices of a call's shrink, at most most_slices(): enough blocks to fill the
 // card.
 int slices_of(const AdapterArgs& a, int K) {
-    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, 16 * shrink_tile_of(a.ad.M, a.ad.S));
+    const int64_t pieces = pieces_of(a.ad.M, a.ad.S, long_segments(a.ad.M, a.ad.S) ? 64 : 16);
     const int64_t Q = kFill / pieces, most = most_slices(a.ad.M, K, a.dtype);
     return static_cast<int>(std::max(int64_t(1), std::min(Q, most)));
 }
@@ -1336,10 +1295,11 @@ int slices_of(const AdapterArgs& a, int K) {
 template <typename T>
 int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* part, int stride, int K, int scaled,
                   const Repack& v, const OuterPlan& plan, hipStream_t s) {
-    const int tt = shrink_tile_of(a.ad.M, a.ad.S), Q = slices_of(a, K), rt = (a.ad.max_rank + 15) / 16;
-    const int64_t items = pieces_of(a.ad.M, a.ad.S, 16 * tt) * Q;
-    auto k = tt == 1 ? (rt <= 1 ? shrink_kernel<T, 1, 1> : rt <= 2 ? shrink_kernel<T, 1, 2>
-                        : rt <= 4 ? shrink_kernel<T, 1, 4> : shrink_kernel<T, 1, 8>)
+    const bool tile64 = long_segments(a.ad.M, a.ad.S);
+    const int Q = slices_of(a, K), rt = (a.ad.max_rank + 15) / 16;
+    const int64_t items = pieces_of(a.ad.M, a.ad.S, tile64 ? 64 : 16) * Q;
+    auto k = !tile64 ? (rt <= 1 ? shrink_kernel<T, 1> : rt <= 2 ? shrink_kernel<T, 2>
+                        : rt <= 4 ? shrink_kernel<T, 4> : shrink_kernel<T, 8>)
                      : (rt <= 1 ? shrink_tile_kernel<T, 1> : rt <= 2 ? shrink_tile_kernel<T, 2>
                         : rt <= 4 ? shrink_tile_kernel<T, 4> : shrink_tile_kernel<T, 8>);
     hipLaunchKernelGGL(k, dim3(grid_of(items) + (plan.table != nullptr)), dim3(kThreads), 0, s, a.ad,
@@ -1352,7 +1312,7 @@ int launch_shrink(const AdapterArgs& a, const void* x, const void* A, float* par
 template <typename T>
 void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, const void* B, void* y, float* v_out,
                    int v_stride, int v_cols, int N, int scaled, hipStream_t s) {
-    const bool tile64 = tile_of(a.ad.M, a.ad.S) > 1;
+    const bool tile64 = long_segments(a.ad.M, a.ad.S);
     const int64_t pieces = pieces_of(a.ad.M, a.ad.S, tile64 ? 64 : 16);
     const int wide = (tile64 ? 16 : 64) * Unit<T>::kCols, tiles = (N + wide - 1) / wide;
     // a block takes several column tiles (v is read once) while the card stays
@@ -1365,8 +1325,8 @@ void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, c
     constexpr int MOST = sizeof(T) == 2 ? 4 : 8;
     auto k = tile64 ? (ku <= 1 ? expand_tile_kernel<T, 1> : ku <= 2 ? expand_tile_kernel<T, 2>
                        : ku <= 4 ? expand_tile_kernel<T, 4> : expand_tile_kernel<T, MOST>)
-                    : (ku <= 1 ? expand_kernel<T, 1, 1> : ku <= 2 ? expand_kernel<T, 1, 2>
-                       : ku <= 4 ? expand_kernel<T, 1, 4> : expand_kernel<T, 1, MOST>);
+                    : (ku <= 1 ? expand_kernel<T, 1> : ku <= 2 ? expand_kernel<T, 2>
+                       : ku <= 4 ? expand_kernel<T, 4> : expand_kernel<T, MOST>);
     hipLaunchKernelGGL(k, dim3(grid_of(pieces * columns)), dim3(kThreads), 0, s, a.ad, part, stride, Q,
                        static_cast<const T*>(B), static_cast<const T*>(a.base), static_cast<T*>(y), v_out, v_stride,
                        v_cols, N, scaled, columns, static_cast<int>(per), tiles, pieces * columns);

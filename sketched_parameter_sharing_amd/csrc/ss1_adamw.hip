@@ -129,11 +129,22 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
-// max over the 32 lanes that share a scale (the half wave).
+// The value of lane (l + N) % 16 of the 16-lane row (DPP row_ror, a VALU
+// operand modifier).
+template <int N>
+__device__ __forceinline__ float rotate(float v) {
+    return __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(v)), 0x120 + N, 0xF, 0xF, true)));
+}
+
+// max over the 32 lanes that share a scale (the half wave): rotations inside
+// the 16-lane rows, and one lane exchange between the two rows.
 __device__ __forceinline__ float half_wave_max(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-    return v;
+    v = fmaxf(v, rotate<8>(v));
+    v = fmaxf(v, rotate<4>(v));
+    v = fmaxf(v, rotate<2>(v));
+    v = fmaxf(v, rotate<1>(v));
+    return fmaxf(v, __shfl_xor(v, 16));
 }
 
 // The state's codes of 8 values of this lane, and the new scale of their block:

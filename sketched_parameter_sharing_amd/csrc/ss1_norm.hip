@@ -92,18 +92,38 @@ __device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_flo
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<uint16_t>(bf16_bits(v)); }
 
-// Sums over the T threads of a row (T a multiple of 64; a wave or several).
-// Rows of one wave need no LDS.  With several waves every thread of the block
-// calls this together; `red` holds one float pair a wave and alternates
-// between two halves from call to call, so one barrier a call is enough: a
-// half is written again only after the barrier of the call between.
-template <int T, int BLOCK>
+// The value of lane (l + N) % 16 of the 16-lane row (DPP row_ror, a VALU
+// operand modifier).
+template <int N>
+__device__ __forceinline__ float rotate(float v) {
+    return __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(v)), 0x120 + N, 0xF, 0xF, true)));
+}
+
+// Sum over the wave, the same bits in every lane (each step adds the same pairs
+// in either order): four rotations inside the 16-lane rows and four lane reads,
+// no LDS.  With LDS lane exchanges for all six steps the forward of 16384 x 768
+// bf16 took 17.1 us instead of 15.9.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += rotate<8>(v);
+    v += rotate<4>(v);
+    v += rotate<2>(v);
+    v += rotate<1>(v);
+    const int w = static_cast<int>(__float_as_uint(v));
+    const float a = __uint_as_float(__builtin_amdgcn_readlane(w, 0)), b = __uint_as_float(__builtin_amdgcn_readlane(w, 16));
+    const float c = __uint_as_float(__builtin_amdgcn_readlane(w, 32)), d = __uint_as_float(__builtin_amdgcn_readlane(w, 48));
+    return (a + b) + (c + d);
+}
+
+// Sums over the T threads of a row (T a multiple of 64; a wave or several) of
+// one or two values.  Rows of one wave need no LDS.  With several waves every
+// thread of the block calls this together; `red` holds one pair a wave and
+// alternates between two halves from call to call, so one barrier a call is
+// enough: a half is written again only after the barrier of the call between.
+template <int T, int BLOCK, bool TWO>
 __device__ __forceinline__ float2 row_sums(float2 s, float2* red, int& phase) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        s.x += __shfl_xor(s.x, off);
-        s.y += __shfl_xor(s.y, off);
-    }
+    s.x = wave_sum(s.x);
+    if (TWO) s.y = wave_sum(s.y);
     if constexpr (T == 64) return s;
     float2* half = red + phase * (BLOCK / 64);
     phase ^= 1;
@@ -114,7 +134,7 @@ __device__ __forceinline__ float2 row_sums(float2 s, float2* red, int& phase) {
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) {
         t.x += half[first + w].x;
-        t.y += half[first + w].y;
+        if (TWO) t.y += half[first + w].y;
     }
     return t;
 }
@@ -123,7 +143,10 @@ __device__ __forceinline__ float2 row_sums(float2 s, float2* red, int& phase) {
 // Elements of this thread's vector i of a row; > 0 when it has any.
 __device__ __forceinline__ int count_of(int K, int at) { return min(kVec, K - at); }
 
-// BLOCK / T rows a block, a row in the registers of T threads.
+// BLOCK / T rows at a time, a row in the registers of T threads.  With KEEP a
+// block keeps gamma and beta in registers too, over all of its rows: in float32
+// they are twice the bytes of a bf16 row (16384 x 4096 bf16: 60.7 us reading
+// them for each row, 55.9 keeping them).
 template <typename X, typename G, int T, int NV, int BLOCK, bool TAIL>
 __global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, const G* __restrict__ gamma,
                                                                   const G* __restrict__ beta, X* y,
@@ -131,8 +154,22 @@ __global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, co
                                                                   int64_t M, int K, float eps) {
     __shared__ float2 red[2 * BLOCK / 64];
     constexpr int ROWS = BLOCK / T;
+    constexpr bool KEEP = T < 1024;
     const int t = threadIdx.x % T;
     int phase = 0;
+    float w[NV][kVec], b[NV][kVec];
+    const auto affine = [&](int i) {
+        const int at = (i * T + t) * kVec, n = count_of(K, at);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) b[i][j] = 0.0f;
+        if (n > 0) {
+            load8<TAIL>(gamma + at, n, w[i]);
+            if (beta) load8<TAIL>(beta + at, n, b[i]);
+        }
+    };
+    if (KEEP)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) affine(i);
     for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * ROWS; m0 < M; m0 += static_cast<int64_t>(gridDim.x) * ROWS) {
         const int64_t m = m0 + threadIdx.x / T;
         const bool row = m < M;
@@ -149,7 +186,7 @@ __global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, co
                 for (int j = 0; j < kVec; ++j) s += v[i][j];
             }
         }
-        const float mu = row_sums<T, BLOCK>(make_float2(s, 0.0f), red, phase).x / K;
+        const float mu = row_sums<T, BLOCK, false>(make_float2(s, 0.0f), red, phase).x / K;
         float q = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -163,7 +200,7 @@ __global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, co
                 }
             }
         }
-        const float rs = 1.0f / sqrtf(row_sums<T, BLOCK>(make_float2(q, 0.0f), red, phase).x / K + eps);
+        const float rs = 1.0f / sqrtf(row_sums<T, BLOCK, false>(make_float2(q, 0.0f), red, phase).x / K + eps);
         if (row && t == 0) {
             if (mean) mean[m] = mu;
             if (rstd) rstd[m] = rs;
@@ -172,12 +209,10 @@ __global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, co
         for (int i = 0; i < NV; ++i) {
             const int at = (i * T + t) * kVec;
             const int n = row ? count_of(K, at) : 0;
+            if (!KEEP) affine(i);
             if (n > 0) {
-                float w[kVec], b[kVec];
-                load8<TAIL>(gamma + at, n, w);
-                if (beta) load8<TAIL>(beta + at, n, b);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * rs * w[j] + (beta ? b[j] : 0.0f);
+                for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * rs * w[i][j] + b[i][j];
                 store8<TAIL>(y + base + at, n, v[i]);
             }
         }
@@ -198,13 +233,13 @@ __global__ __launch_bounds__(kLong) void layernorm_forward_long(const X* x, cons
         const size_t base = static_cast<size_t>(m) * K;
         float s = 0.0f;
         for (int k = threadIdx.x; k < K; k += kLong) s += load1(x + base + k);
-        const float mu = row_sums<kLong, kLong>(make_float2(s, 0.0f), red, phase).x / K;
+        const float mu = row_sums<kLong, kLong, false>(make_float2(s, 0.0f), red, phase).x / K;
         float q = 0.0f;
         for (int k = threadIdx.x; k < K; k += kLong) {
             const float d = load1(x + base + k) - mu;
             q += d * d;
         }
-        const float rs = 1.0f / sqrtf(row_sums<kLong, kLong>(make_float2(q, 0.0f), red, phase).x / K + eps);
+        const float rs = 1.0f / sqrtf(row_sums<kLong, kLong, false>(make_float2(q, 0.0f), red, phase).x / K + eps);
         if (threadIdx.x == 0) {
             if (mean) mean[m] = mu;
             if (rstd) rstd[m] = rs;
@@ -277,7 +312,7 @@ __global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, 
             }
         }
         if (dx) {
-            s = row_sums<T, BLOCK>(s, red, phase);
+            s = row_sums<T, BLOCK, true>(s, red, phase);
             const float m1 = s.x / K, m2 = s.y / K;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -351,7 +386,7 @@ __global__ __launch_bounds__(kLong) void layernorm_dx_long(const X* dy, const X*
             s.x += g;
             s.y += g * ((load1(x + base + k) - mu) * rs);
         }
-        s = row_sums<kLong, kLong>(s, red, phase);
+        s = row_sums<kLong, kLong, true>(s, red, phase);
         const float m1 = s.x / K, m2 = s.y / K;
         for (int k = threadIdx.x; k < K; k += kLong) {
             const float g = load1(dy + base + k) * load1(gamma + k);
@@ -413,19 +448,28 @@ constexpr int64_t kMaxBlocks = int64_t(1) << 20;  // rows beyond that loop
 
 unsigned grid_for(int64_t rows, int64_t most) { return static_cast<unsigned>(rows < most ? rows : most); }
 
+// Blocks of the forward where they keep gamma and beta: enough to fill the card
+// and to even out, few enough that each has many rows.  16384 x 4096 (blocks of
+// 256): 62.5 us with 2048, 55.9 with 4096, 66.5 with one a row; 4096 x 16384
+// (blocks of 512, four vectors a thread): 70.4 with 2048, 65.4 with 1024, 61.8
+// with 512.
+constexpr int64_t keep_blocks(int block, int nv) { return nv == 4 ? 512 : int64_t(4096) * 256 / block; }
+
 template <typename X, typename G, int T, int NV>
 void forward_rows(const NormArgs& a, hipStream_t s) {
     constexpr int BLOCK = T < 256 ? 256 : T;
     const int64_t groups = (a.M + BLOCK / T - 1) / (BLOCK / T);
-    const dim3 grid(grid_for(groups, kMaxBlocks));
+    const dim3 grid(grid_for(groups, T < 1024 ? keep_blocks(BLOCK, NV) : kMaxBlocks));
     auto k = a.K % kVec ? layernorm_forward_kernel<X, G, T, NV, BLOCK, true>
                         : layernorm_forward_kernel<X, G, T, NV, BLOCK, false>;
     hipLaunchKernelGGL(k, grid, dim3(BLOCK), 0, s, static_cast<const X*>(a.x), static_cast<const G*>(a.gamma),
                        static_cast<const G*>(a.beta), static_cast<X*>(a.y), a.mean, a.rstd, a.M, a.K, a.eps);
 }
 
-// Threads a row: one wave up to 1024 elements (no barrier), then 256, then
-// 1024; the smallest number of vectors that holds the row.
+// Threads a row: one wave up to 1024 elements (no barrier; 16384 x 768: 15.9 us
+// against 25.2 with 256 threads), then 256 and 512 with up to two vectors each
+// (8192 x 8192: 59.5 us with 512 x 2, 78.1 with 256 x 4), then 512 x 4 (4096 x
+// 16384: 61.8 us, 74.9 with 1024 x 2) and 1024 x 4.
 template <typename X, typename G>
 void forward(const NormArgs& a, hipStream_t s) {
     const int vecs = (a.K + kVec - 1) / kVec;
@@ -433,8 +477,8 @@ void forward(const NormArgs& a, hipStream_t s) {
     if (vecs <= 128) return forward_rows<X, G, 64, 2>(a, s);
     if (vecs <= 256) return forward_rows<X, G, 256, 1>(a, s);
     if (vecs <= 512) return forward_rows<X, G, 256, 2>(a, s);
-    if (vecs <= 1024) return forward_rows<X, G, 256, 4>(a, s);
-    if (vecs <= 2048) return forward_rows<X, G, 1024, 2>(a, s);
+    if (vecs <= 1024) return forward_rows<X, G, 512, 2>(a, s);
+    if (vecs <= 2048) return forward_rows<X, G, 512, 4>(a, s);
     if (vecs <= 4096) return forward_rows<X, G, 1024, 4>(a, s);
     hipLaunchKernelGGL((layernorm_forward_long<X, G>), dim3(grid_for(a.M, kMaxBlocks)), dim3(kLong), 0, s,
                        static_cast<const X*>(a.x), static_cast<const G*>(a.gamma), static_cast<const G*>(a.beta),
@@ -448,7 +492,9 @@ struct Split {
     int groups;  // blocks, and partial rows
 };
 
-constexpr int kGroups = 256;  // one block a compute unit
+// One block a compute unit.  128 / 256 / 512, backward in us: 16384 x 4096: 132 /
+// 86 / 93; 16384 x 768: 32.5 / 26 / 33.5; 4096 x 8192: 82 / 53 / 54.
+constexpr int kGroups = 256;
 
 Split split_of(int64_t M, int32_t K) {
     const int vecs = (K + kVec - 1) / kVec;
@@ -459,7 +505,8 @@ Split split_of(int64_t M, int32_t K) {
         p.groups = static_cast<int>(M < kGroups ? M : kGroups);
         return p;
     }
-    // small row counts take small blocks, so that they still spread out
+    // small row counts take small blocks, so that they still spread out (512 x
+    // 768: 10.8 us against 14.8; 16384 x 768 the other way: 36 against 26)
     p.block = p.T == 1024 || M >= int64_t(kGroups) * (1024 / p.T) ? 1024 : 256;
     const int64_t need = (M + p.block / p.T - 1) / (p.block / p.T);
     p.groups = static_cast<int>(need < kGroups ? need : kGroups);

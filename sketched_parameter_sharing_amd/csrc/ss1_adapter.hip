@@ -1163,12 +1163,17 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
                     __builtin_amdgcn_wave_barrier();
                     write_v(ring + O::XBYTES, f);
                 }
-                for (int st = 0; st < steps; ++st) {
+                // ring places by constants: one turn of the ring unrolled
+                for (int turn = 0; turn < steps; turn += kOuterStages)
+#pragma unroll
+                for (int place = 0; place < kOuterStages; ++place) {
+                    const int st = turn + place;
+                    if (st >= steps) break;
                     // the next stage has landed and this one's operands are made;
                     // the place of the one before is free
                     dev::dma_stage_barrier<O::L*(kOuterStages - 3)>();
-                    const uint8_t* now = ring + st % kOuterStages * O::BYTES;
-                    uint8_t* ahead = ring + (st + 1) % kOuterStages * O::BYTES + O::XBYTES;
+                    const uint8_t* now = ring + place * O::BYTES;
+                    uint8_t* ahead = ring + (place + 1) % kOuterStages * O::BYTES + O::XBYTES;
                     // every LDS read of the stage before the loads are issued
                     // (which keep memory accesses on their side)
                     uint32_t w[8];
@@ -1184,7 +1189,7 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
                             a[r][h] = *O::operand(const_cast<uint8_t*>(now) + O::XBYTES, r, h, lane);
                     int next[O::L];
                     list(st + kOuterStages, next);
-                    issue(tok, (st + kOuterStages - 1) % kOuterStages);
+                    issue(tok, (place + kOuterStages - 1) % kOuterStages);
 #pragma unroll
                     for (int i = 0; i < O::L; ++i) tok[i] = next[i];
                     if (wave < RT) write_v(ahead, f);

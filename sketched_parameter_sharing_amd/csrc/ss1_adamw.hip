@@ -23,23 +23,26 @@ constexpr int kVec = 8;
 static_assert(SS1_ADAMW_BLOCK == 32 * kVec, "32 lanes hold the elements of one scale");
 static_assert(kAdamWChunk % (kThreads * kVec) == 0, "a chunk is whole passes of the block");
 
-// SplitMix64's output for state seed + (counter + 1) golden.
-__device__ __forceinline__ uint64_t random_bits(uint64_t seed, uint64_t counter) {
-    uint64_t z = seed + (counter + 1) * 0x9E3779B97F4A7C15ull;
+// SplitMix64: the state of a counter (the next counter's is kGolden further),
+// and the output for a state.
+constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
+__device__ __forceinline__ uint64_t random_state(uint64_t seed, uint64_t counter) {
+    return seed + (counter + 1) * kGolden;
+}
+__device__ __forceinline__ uint64_t random_bits(uint64_t z) {
     z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
     z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
     return z ^ (z >> 31);
 }
 
-// |q| <= 448 (up to a rounding) as an E4M3 value, up or down with the
+// 0 <= a <= 448 (up to a rounding) as an E4M3 value, up or down with the
 // probability of its distance: adding 16 random bits below the last kept bit
 // and cutting off does that for the normal range (3 mantissa bits: 20 are
 // dropped); below 2^-6 the quantum is 2^-9.
-__device__ __forceinline__ float e4m3_round(float q, uint32_t u16) {
-    const float a = fabsf(q);
+__device__ __forceinline__ float e4m3_round(float a, uint32_t u16) {
     const float high = __uint_as_float((__float_as_uint(a) + (u16 << 4)) & 0xFFF00000u);
     const float low = floorf(a * 512.0f + static_cast<float>(u16) * 0x1p-16f) * 0x1p-9f;
-    return copysignf(a < 0x1p-6f ? low : fminf(high, 448.0f), q);
+    return a < 0x1p-6f ? low : fminf(high, 448.0f);
 }
 
 // Elements [i, i + 8) of a tensor as float32; elements from `n` on are 0.
@@ -147,11 +150,21 @@ __device__ __forceinline__ float half_wave_max(float v) {
     return fmaxf(v, __shfl_xor(v, 16));
 }
 
+// t / scale rounded to nearest, from y = 1 / scale rounded to nearest: the
+// remainder of the first quotient is exact, and adding its share rounds as the
+// division does (Markstein 1990), while nothing leaves the normal range.
+__device__ __forceinline__ float quotient(float t, float scale, float y) {
+    const float q = t * y;
+    return fmaf(fmaf(-q, scale, t), y, q);
+}
+
 // The state's codes of 8 values of this lane, and the new scale of their block:
-// max |t| times 1/448 as a float (1 for a block of zeros), the quotients by IEEE
-// division.  u[j] holds the random bits of element j.
+// max |t| times 1/448 as a float (1 for a block of zeros), the quotients as IEEE
+// division gives them.  u[j] holds the random bits of element j.  ROOT: the
+// values are square roots, and a nonzero one keeps at least the smallest code.
+template <bool ROOT>
 __device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t i, int n, const float (&t)[kVec],
-                                          const uint32_t (&u)[kVec], bool keep_nonzero) {
+                                          const uint32_t (&u)[kVec]) {
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) top = fmaxf(top, fabsf(t[j]));
@@ -159,10 +172,22 @@ __device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t
     const float scale = top > 0.0f ? top * (1.0f / 448.0f) : 1.0f;
     if (n > 0 && (threadIdx.x & 31) == 0) scales[i / SS1_ADAMW_BLOCK] = scale;
     float q[kVec];
+    // one reciprocal for the 8 values, where their remainders cannot leave the
+    // normal range (a value under 2^-25 of the scale rounds to the same code
+    // whatever its last bit).  118M elements, in one process: 440 to 456 us with
+    // a division each, whose instructions then bound the step, 372 to 401 so
+    if (scale >= 0x1p-76f && scale <= 0x1p76f) {
+        const float y = __fdiv_rn(1.0f, scale);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) q[j] = quotient(t[j], scale, y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) q[j] = __fdiv_rn(t[j], scale);
+    }
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        q[j] = e4m3_round(__fdiv_rn(t[j], scale), u[j]);
-        if (keep_nonzero && t[j] > 0.0f) q[j] = fmaxf(q[j], 0x1p-9f);
+        q[j] = ROOT ? e4m3_round(q[j], u[j]) : copysignf(e4m3_round(fabsf(q[j]), u[j]), q[j]);
+        if (ROOT && t[j] > 0.0f) q[j] = fmaxf(q[j], 0x1p-9f);
     }
     store8(codes, i, n, q);
 }
@@ -216,16 +241,18 @@ __device__ __forceinline__ void adamw_chunk(const ss1_adamw_entry& e, int item, 
         }
         if constexpr (EIGHT) {
             uint32_t um[kVec], uv[kVec];
+            uint64_t state = random_state(c.seed, stream + static_cast<uint64_t>(i >> 1));
 #pragma unroll
             for (int j = 0; j < kVec; j += 2) {
-                const uint64_t z = random_bits(c.seed, stream + static_cast<uint64_t>((i + j) >> 1));
+                const uint64_t z = random_bits(state);
+                state += kGolden;
                 um[j] = static_cast<uint32_t>(z) & 0xFFFF;
                 uv[j] = static_cast<uint32_t>(z) >> 16;
                 um[j + 1] = static_cast<uint32_t>(z >> 32) & 0xFFFF;
                 uv[j + 1] = static_cast<uint32_t>(z >> 48);
             }
-            quantize8(static_cast<uint8_t*>(e.m), e.m_scale, i, n, m, um, false);
-            quantize8(static_cast<uint8_t*>(e.v), e.v_scale, i, n, r, uv, true);
+            quantize8<false>(static_cast<uint8_t*>(e.m), e.m_scale, i, n, m, um);
+            quantize8<true>(static_cast<uint8_t*>(e.v), e.v_scale, i, n, r, uv);
         } else {
             store8(static_cast<float*>(e.m), i, n, m);
             store8(static_cast<float*>(e.v), i, n, v);
@@ -239,10 +266,11 @@ __device__ __forceinline__ void adamw_chunk(const ss1_adamw_entry& e, int item, 
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) h[j] = bf16_bits(p[j]);
             } else {
+                uint64_t state = random_state(c.seed, stream + (uint64_t(1) << 39) + static_cast<uint64_t>(i >> 2));
 #pragma unroll
                 for (int j = 0; j < kVec; j += 4) {
-                    const uint64_t z =
-                        random_bits(c.seed, stream + (uint64_t(1) << 39) + static_cast<uint64_t>((i + j) >> 2));
+                    const uint64_t z = random_bits(state);
+                    state += kGolden;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t bits = __float_as_uint(p[j + q]);

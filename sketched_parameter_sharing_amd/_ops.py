@@ -3,7 +3,9 @@ adapters of many requests, AdamW over many tensors): argument marshalling only.
 
 Like the layer calls, every function takes GPU tensors, enqueues on the given
 or the current stream and returns without waiting; outputs and workspaces are
-allocated here when they are not given.
+allocated here when they are not given, from the memory of the stream that the
+call runs on (so that a block freed by another stream's work is not written
+before that work is done, nor a workspace reused while the call runs).
 """
 from __future__ import annotations
 
@@ -80,9 +82,16 @@ def _ref(desc, t):
     return None if t is None else byref(desc(t))
 
 
-def _handle(stream, t):
-    """The given stream's handle, or that of the current stream of t's device."""
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+def _handle(t):
+    """The handle of the current stream of t's device."""
+    return _raw_stream(t.get_device())
+
+
+def _on(stream, call, *args):
+    """The call with ``stream`` as the current one, its allocations too."""
+    torch = _torch or _setup()
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 # ---------------------------------------------------------------- layer norm
@@ -91,6 +100,8 @@ def layernorm_forward(x, gamma, beta=None, eps: float = 1e-5, y=None, mean=None,
     (y, mean, rstd).  ``x`` is [M][K] bf16 or float32, ``gamma`` and ``beta``
     (may be None) are [K] of x's dtype or float32; mean and rstd, float32 [M],
     are what :func:`layernorm_backward` takes."""
+    if stream is not None:
+        return _on(stream, layernorm_forward, x, gamma, beta, eps, y, mean, rstd)
     torch = _torch or _setup()
     tx, M = _matrix(x), x.shape[0]
     if y is None:
@@ -101,7 +112,7 @@ def layernorm_forward(x, gamma, beta=None, eps: float = 1e-5, y=None, mean=None,
         rstd = torch.empty_like(mean)
     st = load().ss1_layernorm_forward(byref(tx), byref(_row(gamma)), _ref(_row, beta), eps, byref(_matrix(y)),
                                       _vec(mean, torch.float32, M, "mean"), _vec(rstd, torch.float32, M, "rstd"),
-                                      _handle(stream, x))
+                                      _handle(x))
     if st:
         _check(st, "ss1_layernorm_forward")
     return y, mean, rstd
@@ -111,6 +122,8 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dx=True, dgamma=True, dbeta=Tru
     """Gradients of layer norm (ss1_layernorm_backward): returns (dx, dgamma,
     dbeta); pass None for one that is not wanted, True to allocate it.  mean
     and rstd are what the forward returned."""
+    if stream is not None:
+        return _on(stream, layernorm_backward, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
     torch = _torch or _setup()
     tx, M = _matrix(x), x.shape[0]
     tg = _row(gamma)
@@ -131,7 +144,7 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dx=True, dgamma=True, dbeta=Tru
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = lib.ss1_layernorm_backward(byref(_matrix(dy)), byref(tx), byref(tg), _vec(mean, torch.float32, M, "mean"),
                                     _vec(rstd, torch.float32, M, "rstd"), _ref(_matrix, dx), _ref(_row, dgamma),
-                                    _ref(_row, dbeta), wp, wb, _handle(stream, x))
+                                    _ref(_row, dbeta), wp, wb, _handle(x))
     if st:
         _check(st, "ss1_layernorm_backward")
     return dx, dgamma, dbeta
@@ -197,6 +210,8 @@ def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None
     none) are device tensors; ``base`` is the projection's output, or None for
     zero, and ``y`` may be base itself.  v = x A_e^T, float32 [M][max_rank], is
     what :func:`adapter_backward` takes: None unless given or ``save_v``."""
+    if stream is not None:
+        return _on(stream, adapter_forward, x, adapters, seg, seg_adapter, base, y, v, save_v, workspace)
     torch = _torch or _setup()
     tx, ad, lib = _matrix(x), adapters._struct(), load()
     M = x.shape[0]
@@ -207,7 +222,7 @@ def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None
     workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_forward_query, M, ad, x.device,
                                    "ss1_adapter_forward_query")
     st = lib.ss1_adapter_forward(byref(tx), byref(ad), byref(_segments(seg, seg_adapter)), _ref(_matrix, base),
-                                 byref(_matrix(y)), _ref(_matrix, v), wp, wb, _handle(stream, x))
+                                 byref(_matrix(y)), _ref(_matrix, v), wp, wb, _handle(x))
     if st:
         _check(st, "ss1_adapter_forward")
     return y, v
@@ -220,6 +235,8 @@ def adapter_backward(dy, x, v, adapters: AdapterSet, seg, seg_adapter, dx_base=N
     ``v`` is what the forward returned with ``save_v`` (needed for dB only);
     ``dx_base`` is the projection's own input gradient (ss1.backward's dx), to
     which the adapters' is added, and dx may be dx_base itself."""
+    if stream is not None:
+        return _on(stream, adapter_backward, dy, x, v, adapters, seg, seg_adapter, dx_base, dx, dA, dB, workspace)
     torch = _torch or _setup()
     tx, ad, lib = _matrix(x), adapters._struct(), load()
     M = x.shape[0]
@@ -233,7 +250,7 @@ def adapter_backward(dy, x, v, adapters: AdapterSet, seg, seg_adapter, dx_base=N
                                    "ss1_adapter_backward_query")
     st = lib.ss1_adapter_backward(byref(_matrix(dy)), byref(tx), _ref(_matrix, v), byref(ad),
                                   byref(_segments(seg, seg_adapter)), _ref(_matrix, dx_base), _ref(_matrix, dx),
-                                  _ref(_matrix, dA), _ref(_matrix, dB), wp, wb, _handle(stream, x))
+                                  _ref(_matrix, dA), _ref(_matrix, dB), wp, wb, _handle(x))
     if st:
         _check(st, "ss1_adapter_backward")
     return dx, dA, dB
@@ -346,6 +363,6 @@ class AdamWPlan:
             scale, dev = 1.0, _vec(grad_scale, _torch.float32, 1, "grad_scale")
         h = AdamWHyper(lr, beta1, beta2, eps, scale, dev, step, int(seed) & (2**64 - 1))
         st = load().ss1_adamw_step(self.entries.data_ptr(), self.count, self.map.data_ptr(), self.chunks, byref(h),
-                                   _handle(stream, self.entries))
+                                   _handle(self.entries) if stream is None else stream.cuda_stream)
         if st:
             _check(st, "ss1_adamw_step")

@@ -595,14 +595,16 @@ typedef struct {
  *   x    : [M][K] of A's dtype
  *   base : [M][N] of A's dtype, the shared projection's output (ss1_forward's
  *          y), or NULL for zero
- *   y    : [M][N], written; may be base itself
+ *   y    : [M][N], written; may be base itself, but must not overlap x
  *   v    : [M][max_rank] F32, written (columns beyond a token's rank are 0),
  *          what ss1_adapter_backward reads; may be NULL
  *   workspace : DEVICE, 16-byte aligned, at least the queried bytes; contents
  *          unspecified afterwards.  Calls that share it must be ordered.
  * Arithmetic: products of the inputs accumulated in float32; v stays float32
  * between the two products (bf16: as the sum of two bf16 values, an error of
- * at most 2^-17 of v); y rounded once.  Equal calls give equal bits.
+ * at most 2^-17 of v); y rounded once.  Equal calls give equal bits.  An
+ * infinity or a NaN in a token's x reaches that token's y alone; one in A or B
+ * may come out as either, in the tokens of its adapter alone.
  * Requirements: K and N multiples of 8 (BF16) or 4 (F32), below 2^22;
  * M < 2^31; x, A, B, base, y, v 16-byte aligned, index and scale arrays
  * 4-byte aligned.  M == 0 enqueues nothing; R == 0 (no adapter rows) and
@@ -631,7 +633,8 @@ ss1_status ss1_adapter_forward(const ss1_tensor* x, const ss1_adapters* adapters
  *        (read for dB only; columns beyond a token's rank are not used)
  *   dx_base : [M][K], the projection's own input gradient (ss1_backward's
  *        dx), or NULL for zero
- *   dx : [M][K], written (NULL: not computed); may be dx_base itself
+ *   dx : [M][K], written (NULL: not computed); may be dx_base itself, but must
+ *        not overlap dy, x or v (dA and dB are formed after it)
  *   dA : [R][K], dB : [R][N], A's dtype, written (NULL: not computed); zero
  *        for adapters that no token uses
  *   workspace : as in the forward

@@ -11,6 +11,11 @@
 // in registers too while a block walks over its rows, so the column sums cost
 // no second read of dy and x: every block writes one partial row, and a small
 // second launch adds those in order.
+//
+// 16384 x 4096 bf16: forward 55.9 us (269 MB, 4.8 TB/s), backward 79.6 + 4.9 us
+// for the join (403 MB, 5.1 TB/s in the first launch), a large copy 5.0 to 5.3.
+// 16 x 4096 forward 3.8 us and 1111 x 1283 float32 backward 10.3 + 3.9 us, both
+// below what the host takes for the calls.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -219,8 +224,9 @@ __global__ __launch_bounds__(BLOCK) void layernorm_forward_kernel(const X* x, co
     }
 }
 
-// Rows too long for registers: one block a row, three passes over it (the
-// later ones from cache).
+// Rows too long for registers (forward over 32768 elements, backward over 16384):
+// one block a row, three passes over it (the later ones from cache), single
+// elements.  A rare size, kept simple.
 constexpr int kLong = 512;
 template <typename X, typename G>
 __global__ __launch_bounds__(kLong) void layernorm_forward_long(const X* x, const G* __restrict__ gamma,
@@ -417,7 +423,8 @@ __global__ __launch_bounds__(256) void layernorm_columns_long(const X* __restric
 }
 
 // The partial rows joined in a fixed order: a block takes 32 columns of the
-// [groups][2 K] matrix, thread (c, r) the rows r, r + 8, ...
+// [groups][2 K] matrix, thread (c, r) the rows r, r + 8, ...  Bound by latency: 8
+// MB (K = 4096) in 4.9 us, most of it the launch and one chain of 32 loads.
 template <typename G>
 __global__ __launch_bounds__(256) void layernorm_join_kernel(const float* __restrict__ partial, G* __restrict__ dgamma,
                                                              G* __restrict__ dbeta, int groups, int K) {

@@ -270,7 +270,8 @@ __global__ __launch_bounds__(kThreads) void plan_outer_kernel(AdapterView ad, Ou
 // mostly from cache, in 9.5 us with launch and lookup; one token of rank 16: 3.7
 // us, the latency of its dependent reads alone), hence the slices: the more blocks
 // read a factor, the shorter each one's chain.
-template <typename T, int RT>
+// ROWS: rows of x that may be there, 8 or 16.
+template <typename T, int RT, int UN = (RT <= 2 ? 2 : 1), int ROWS = 16>
 __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,
                                             int stride, float scale, f32x4* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -289,9 +290,8 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
     // 16 rows x 64 bytes from two loads
     const uint32_t piece = 16u * ((lane >> 4) + 4 * ((lane >> 3) & 1)), lo8 = pair_lane_mask(lane);
     const uint32_t lane_off = (lane & 7) * Kb + piece;
-    // units whose loads are in flight together (past the wave's share or the
-    // row: zeros)
-    constexpr int UN = RT <= 2 ? 2 : 1;
+    // UN units' loads are in flight together (past the wave's share or the row:
+    // zeros)
     for (int ub = u0 + wave * UN; ub < u1; ub += UN * kWaves) {
         uint4 xf[UN][2], af[UN][RT][2];
 #pragma unroll
@@ -299,7 +299,8 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
             const uint32_t at = 128u * (ub + u);
             const uint32_t off = ub + u < u1 && at + piece < Kb ? lane_off + at : kOutside;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) xf[u][h] = buf_load16(rx, off + h * 8 * Kb, 0);
+            for (int h = 0; h < 2; ++h)
+                xf[u][h] = 8 * h < ROWS ? buf_load16(rx, off + h * 8 * Kb, 0) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int r = 0; r < 2 * RT; ++r) af[u][r / 2][r % 2] = buf_load16(ra, off + r * 8 * Kb, 0);
         }
@@ -498,6 +499,10 @@ __global__ __launch_bounds__(kThreads) void shrink_tile_kernel(AdapterView ad, c
 // Bound by B, base and y (64 requests, N = 14336, ranks up to 64: 55 MB of which
 // B, 51 MB, comes partly from cache, in 15.0 us).
 // Rank units: 32 (bf16: one product each of hi and lo) or 16 (float32).
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 template <typename T>
 struct Unit;
 template <>
@@ -561,10 +566,12 @@ __device__ __forceinline__ void without_adapter(const Piece& pc, const T* base, 
     }
 }
 
-template <typename T, int KU>
+// `part`: the piece's rows of v, complete when make_v() returns (called with the
+// first tile's loads in flight).
+template <typename T, int KU, typename F>
 __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
                                             int v_stride, int v_cols, const T* B, const T* base, T* y, float* v_out,
-                                            int N, int tile0, int tiles, float scale, uint4* frags) {
+                                            int N, int tile0, int tiles, float scale, uint4* frags, F make_v) {
     using U = Unit<T>;
     constexpr int GROUP = U::kRanks / 4;  // ranks of one operand lane
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
@@ -600,8 +607,9 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
             at += wide;
         }
     };
-    fetch(column(tile0));  // in flight while v is staged
-    __syncthreads();       // the last piece's readers of frags
+    fetch(column(tile0));  // in flight while v is made and staged
+    make_v();
+    __syncthreads();  // the last piece's readers of frags
     // v of the piece, summed over the slices of K in order (columns past the
     // rank are zero there; the stride is a multiple of 8)
 #pragma unroll 1
@@ -611,7 +619,7 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
 #pragma unroll
         for (int j = 0; j < GROUP / 4; ++j) v[j] = f32x4{0, 0, 0, 0};
         if (m < pc.n && r < stride) {
-            const f32x4* from = reinterpret_cast<const f32x4*>(part + static_cast<size_t>(pc.begin + m) * stride + r);
+            const f32x4* from = reinterpret_cast<const f32x4*>(part + static_cast<size_t>(m) * stride + r);
             for (int q0 = 0; q0 < Q; q0 += 4) {  // four slices' loads together
                 f32x4 w[4][GROUP / 4];
 #pragma unroll
@@ -690,19 +698,68 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, con
             continue;
         }
         const float scale = scaled ? pc.scale : 1.0f;
+        const float* rows = part + static_cast<size_t>(pc.begin) * stride;
         constexpr int R = Unit<T>::kRanks;
         if (KU == 1 || pc.rank <= R)
-            expand_body<T, 1>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
-                              count, scale, frags);
+            expand_body<T, 1>(pc, rows, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
+                              count, scale, frags, [] {});
         else if (KU == 2 || pc.rank <= 2 * R)
-            expand_body<T, KU < 2 ? KU : 2>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
-                                            count, scale, frags);
+            expand_body<T, KU < 2 ? KU : 2>(pc, rows, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
+                                            count, scale, frags, [] {});
         else if (KU == 4 || pc.rank <= 4 * R)
-            expand_body<T, KU < 4 ? KU : 4>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
-                                            count, scale, frags);
+            expand_body<T, KU < 4 ? KU : 4>(pc, rows, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
+                                            count, scale, frags, [] {});
         else
-            expand_body<T, KU>(pc, part, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
-                               count, scale, frags);
+            expand_body<T, KU>(pc, rows, slice, Q, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
+                               count, scale, frags, [] {});
+    }
+}
+
+// Shrink and expand of small batches in one launch: a block makes v of its piece
+// for itself, in LDS, and goes on to its columns, so there is one launch in place
+// of two (a call of one token is bound by the host) and no v in memory between
+// them.  Every block of a piece reads the whole of its adapter's A, at about 25
+// bytes a ns, which sets where this holds.  One token of rank 16, 4096 -> 14336: 9.6
+// us, the lookup, A, B and the stores one after the other.
+template <typename T, int KU>
+__global__ __launch_bounds__(kThreads, 2) void one_kernel(
+    AdapterView ad, const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ B, const T* base, T* y,
+    float* __restrict__ v_out, int v_stride, int v_cols, int stride, int K, int N, int scaled_v, int scaled_y, Repack v,
+    int columns, int per, int tiles, int64_t items) {
+    using U = Unit<T>;
+    constexpr int MOST = KU * U::kRanks / 16;  // rank tiles, 1 or 2
+    __shared__ f32x4 red[kWaves * MOST * 64];
+    __shared__ __align__(16) float rows[16 * 16 * MOST];
+    __shared__ uint4 frags[KU * U::kFrags * 64];
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cg = static_cast<int>(item % columns);
+        const Piece pc = find_piece(ad, 16, static_cast<int>(item / columns));
+        if (pc.n == 0) continue;
+        const int tile0 = cg * per, count = min(per, tiles - tile0);
+        float* vo = cg == 0 ? v_out : nullptr;
+        if (v.from && cg == 0) repack_rows(v, pc.begin, pc.n);
+        if (pc.rank == 0) {
+            without_adapter(pc, base, y, vo, v_stride, v_cols, N, tile0 * kThreads / 4, count * kThreads / 4);
+            continue;
+        }
+        const float vs = scaled_v ? pc.scale : 1.0f, ys = scaled_y ? pc.scale : 1.0f;
+        // MANY units of K in flight, and half the loads of x for up to 8 tokens
+        const auto run = [&](auto rt, auto ku) {
+            constexpr int RT = decltype(rt)::value, MANY = 4 / RT;
+            expand_body<T, decltype(ku)::value>(pc, rows, 0, 1, stride, v_stride, v_cols, B, base, y, vo, N, tile0,
+                                                count, ys, frags, [&] {
+                                                    if (pc.n <= 8)
+                                                        shrink_body<T, RT, MANY, 8>(pc, x, A, rows, K, 1, 0, stride, vs,
+                                                                                    red);
+                                                    else
+                                                        shrink_body<T, RT, MANY, 16>(pc, x, A, rows, K, 1, 0, stride,
+                                                                                     vs, red);
+                                                });
+        };
+        if (MOST == 1 || pc.rank <= 16)
+            run(Int<1>{}, Int<1>{});
+        else
+            run(Int<2>{}, Int<KU>{});
     }
 }
 
@@ -1305,6 +1362,10 @@ __global__ __launch_bounds__(kThreads) void zero_kernel(uint4* out, size_t n) {
 // gradients of 8192 tokens 98.8 or 103.4 (more partial sums).
 constexpr int64_t kFill = 512;
 
+// Tokens up to which the outer products take an adapter whole, without a work
+// list, and shrink and expand may be one launch.
+constexpr int64_t kWhole = 256;
+
 int esize(int32_t dtype) { return dtype == SS1_BF16 ? 2 : 4; }
 
 // Most slices of a shrink (the workspace's) over `cols` inputs: at least 8 units
@@ -1382,11 +1443,60 @@ void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, c
                        v_cols, N, scaled, columns, static_cast<int>(per), tiles, pieces * columns);
 }
 
+// How a call in one launch is split over blocks.
+struct OneSplit {
+    int64_t pieces, per;  // per: column tiles of a block
+    int tiles, columns;
+};
+
+OneSplit one_split(const AdapterArgs& a, int N) {
+    OneSplit o;
+    const int wide = kThreads / 4 * 16 / esize(a.dtype);
+    o.pieces = pieces_of(a.ad.M, a.ad.S, 16);
+    o.tiles = (N + wide - 1) / wide;
+    o.per = std::max(int64_t(1), std::min(int64_t(o.tiles), o.pieces * o.tiles / kFill));
+    o.columns = static_cast<int>((o.tiles + o.per - 1) / o.per);
+    return o;
+}
+
+// Whether shrink and expand are one launch: an adapter's A is at most 128 KB (bf16;
+// float32, whose products take four instructions, 64), which a compute unit reads
+// in 5 us, and all blocks' reads of A at most 40 MB.  The host takes 14.1 us for
+// a call of one token against 16.7.  On the device alone, one launch against two
+// in us, bf16 unless noted: 1 token of rank 8 1024 -> 4096 8.8 / 10.0, 64 tokens of
+// rank 32 1280 -> 5120 10.5 / 13.1, 256 requests of rank 16 2048 -> 2048 15.8 /
+// 20.7, at 128 KB of A 16 requests of rank 16 4096 -> 4096 11.5 / 11.2 and 8 of rank
+// 32 2048 -> 2048 11.3 / 11.1.  Beyond: 256 KB, 1 token of rank 16 8192 -> 8192 15.7
+// / 11.0; 70 MB, 64 requests of rank 16 4096 -> 4096 18.5 / 14.9; float32 at 128 KB,
+// 256 tokens of rank 16 2048 -> 2048 16.5 / 13.8.
+bool one_launch(const AdapterArgs& a, int K, int N) {
+    const int64_t factor = static_cast<int64_t>((a.ad.max_rank + 15) / 16 * 16) * K * esize(a.dtype);
+    const OneSplit o = one_split(a, N);
+    return a.ad.M <= kWhole && a.ad.max_rank <= 32 && factor <= (a.dtype == SS1_BF16 ? 128 : 64) * 1024 &&
+           factor * o.pieces * o.columns <= int64_t(40) << 20;
+}
+
+template <typename T>
+void launch_one(const AdapterArgs& a, const void* x, const void* A, const void* B, void* y, float* v_out, int v_stride,
+                int v_cols, int K, int N, int scaled_v, int scaled_y, const Repack& v, hipStream_t s) {
+    const OneSplit o = one_split(a, N);
+    constexpr int R = Unit<T>::kRanks;
+    auto k = a.ad.max_rank <= R ? one_kernel<T, 1> : one_kernel<T, 32 / R>;
+    hipLaunchKernelGGL(k, dim3(grid_of(o.pieces * o.columns)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
+                       static_cast<const T*>(A), static_cast<const T*>(B), static_cast<const T*>(a.base),
+                       static_cast<T*>(y), v_out, v_stride, v_cols, stride_of(a.ad.max_rank), K, N, scaled_v, scaled_y,
+                       v, o.columns, static_cast<int>(o.per), o.tiles, o.pieces * o.columns);
+}
+
 template <typename T>
 void forward(const AdapterArgs& a, hipStream_t s) {
     float* part = static_cast<float*>(a.workspace);
     const int stride = stride_of(a.ad.max_rank);
     int Q = 1;
+    if (a.ad.max_rank > 0 && one_launch(a, a.K, a.N)) {
+        launch_one<T>(a, a.x, a.A, a.B, a.y, a.v, a.ad.max_rank, a.ad.max_rank, a.K, a.N, 0, 1, Repack{}, s);
+        return;
+    }
     if (a.ad.max_rank > 0) {
         // a single slice with rows of v's own length writes v itself
         if (a.v && stride == a.ad.max_rank && slices_of(a, a.K) == 1) part = a.v;
@@ -1415,7 +1525,7 @@ OuterSplit outer_split(int64_t M, int32_t K, int32_t N, int32_t max_rank, int32_
     const int wide = 256 / esize(dtype);
     const int64_t tiles = (K + wide - 1) / wide + (N + wide - 1) / wide;
     const int64_t parts = std::max(int64_t(1), kFill / (tiles * o.rank_groups));
-    o.P = static_cast<int>(std::max(int64_t(256), (M / parts + 31) / 32 * 32));
+    o.P = static_cast<int>(std::max(kWhole, (M / parts + 31) / 32 * 32));
     o.table = M > o.P;
     o.slots = o.table ? static_cast<int>(2 * M / o.P) : 0;
     return o;
@@ -1478,6 +1588,12 @@ void backward(const AdapterArgs& a, hipStream_t s) {
     const OuterPlan plan{list ? table : nullptr, table + entries, o.P, static_cast<int>(entries), o.slots};
     int Q = 1;
     const bool any = a.ad.max_rank > 0 && a.ad.M > 0;
+    if (a.dx && any && !list && one_launch(a, a.N, a.K)) {
+        launch_one<T>(a, a.dy, a.B, a.A, a.dx, a.dA ? part : nullptr, stride, stride, a.N, a.K, 1, 0, v, s);
+        if (a.dA || a.dB)
+            launch_outer<T>(a, o, plan, part, stride, repack ? packed : a.v, repack ? stride : a.ad.max_rank, partial, s);
+        return;
+    }
     if ((a.dx || a.dA) && any) {
         Q = launch_shrink<T>(a, a.dy, a.B, part, stride, a.N, 1, v, plan, s);
     } else if (any) {

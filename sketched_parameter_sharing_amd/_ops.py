@@ -72,6 +72,12 @@ def _vec(t, dtype, numel: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _fresh(t, d: Tensor):
+    """A new tensor like t, whose view is d, and its own view."""
+    o = _torch.empty_like(t)
+    return o, Tensor(o.data_ptr(), d.dtype, 0, d.rows, d.cols)
+
+
 def _check_device(*ts):
     for t in ts:
         if not t.is_cuda:
@@ -80,6 +86,17 @@ def _check_device(*ts):
 
 def _ref(desc, t):
     return None if t is None else byref(desc(t))
+
+
+def _out(t, desc, like, d: Tensor):
+    """An output and the reference to its view: t itself, a new tensor like
+    ``like`` (whose view is d) for True, or neither for None."""
+    if t is None:
+        return None, None
+    if t is True:
+        t, v = _fresh(like, d)
+        return t, byref(v)
+    return t, byref(desc(t))
 
 
 def _handle(t):
@@ -103,16 +120,20 @@ def layernorm_forward(x, gamma, beta=None, eps: float = 1e-5, y=None, mean=None,
     if stream is not None:
         return _on(stream, layernorm_forward, x, gamma, beta, eps, y, mean, rstd)
     torch = _torch or _setup()
-    tx, M = _matrix(x), x.shape[0]
-    if y is None:
-        y = torch.empty_like(x)
+    tx = _matrix(x)
+    M = tx.rows
+    y, ry = _out(True if y is None else y, _matrix, x, tx)
     if mean is None:
         mean = torch.empty((M,), dtype=torch.float32, device=x.device)
+        pm = mean.data_ptr()
+    else:
+        pm = _vec(mean, torch.float32, M, "mean")
     if rstd is None:
         rstd = torch.empty_like(mean)
-    st = load().ss1_layernorm_forward(byref(tx), byref(_row(gamma)), _ref(_row, beta), eps, byref(_matrix(y)),
-                                      _vec(mean, torch.float32, M, "mean"), _vec(rstd, torch.float32, M, "rstd"),
-                                      _handle(x))
+        pr = rstd.data_ptr()
+    else:
+        pr = _vec(rstd, torch.float32, M, "rstd")
+    st = load().ss1_layernorm_forward(byref(tx), byref(_row(gamma)), _ref(_row, beta), eps, ry, pm, pr, _handle(x))
     if st:
         _check(st, "ss1_layernorm_forward")
     return y, mean, rstd
@@ -125,26 +146,24 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dx=True, dgamma=True, dbeta=Tru
     if stream is not None:
         return _on(stream, layernorm_backward, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
     torch = _torch or _setup()
-    tx, M = _matrix(x), x.shape[0]
-    tg = _row(gamma)
-    if dx is True:
-        dx = torch.empty_like(x)
-    if dgamma is True:
-        dgamma = torch.empty_like(gamma)
-    if dbeta is True:
-        dbeta = torch.empty_like(gamma)
+    tx, tg = _matrix(x), _row(gamma)
+    M = tx.rows
+    dx, rdx = _out(dx, _matrix, x, tx)
+    dgamma, rdg = _out(dgamma, _row, gamma, tg)
+    dbeta, rdb = _out(dbeta, _row, gamma, tg)
     lib = load()
     wp, wb = None, 0
     if dgamma is not None or dbeta is not None:
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib.ss1_layernorm_backward_query(byref(tx), byref(n)), "ss1_layernorm_backward_query")
-            workspace = torch.empty((n.value,), dtype=torch.uint8, device=x.device)
-        _check_device(workspace)
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            workspace, wb = torch.empty((n.value,), dtype=torch.uint8, device=x.device), n.value
+        else:
+            _check_device(workspace)
+            wb = workspace.numel() * workspace.element_size()
+        wp = workspace.data_ptr()
     st = lib.ss1_layernorm_backward(byref(_matrix(dy)), byref(tx), byref(tg), _vec(mean, torch.float32, M, "mean"),
-                                    _vec(rstd, torch.float32, M, "rstd"), _ref(_matrix, dx), _ref(_row, dgamma),
-                                    _ref(_row, dbeta), wp, wb, _handle(x))
+                                    _vec(rstd, torch.float32, M, "rstd"), rdx, rdg, rdb, wp, wb, _handle(x))
     if st:
         _check(st, "ss1_layernorm_backward")
     return dx, dgamma, dbeta
@@ -180,9 +199,21 @@ class AdapterSet:
         sc = torch.tensor([float(s) for s in scale], dtype=torch.float32).to(A.device)
         return cls(A, B, row, sc, max(ranks, default=0), ranks)
 
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_view"] = (None, None)
+
     def _struct(self) -> Adapters:
-        return Adapters(_matrix(self.A), _matrix(self.B), self.row.data_ptr(), self.scale.data_ptr(), len(self.ranks),
-                        self.max_rank)
+        """The C ABI's view of the set, made again when the factors' memory or
+        sizes or any attribute changed."""
+        A, B = self.A, self.B
+        now = (A.data_ptr(), A.shape, B.data_ptr(), B.shape)
+        seen, ad = self._view
+        if seen != now:
+            ad = Adapters(_matrix(A), _matrix(B), self.row.data_ptr(), self.scale.data_ptr(), len(self.ranks),
+                          self.max_rank)
+            self.__dict__["_view"] = (now, ad)
+        return ad
 
 
 def _segments(seg, seg_adapter) -> Segments:
@@ -190,13 +221,14 @@ def _segments(seg, seg_adapter) -> Segments:
     return Segments(_vec(seg, i32, S + 1, "seg"), _vec(seg_adapter, i32, S, "seg_adapter"), S, 0)
 
 
-def _workspace(workspace, query, M: int, ad: Adapters, device, where: str):
+def _workspace(workspace, query, M: int, ad: Adapters, x, where: str):
     if workspace is None:
         n = ctypes.c_size_t(0)
         st = query(M, byref(ad), byref(n))
         if st:
             _check(st, where)
-        workspace = _torch.empty((n.value,), dtype=_torch.uint8, device=device)
+        workspace = _torch.empty((n.value,), dtype=_torch.uint8, device=x.device)
+        return workspace, workspace.data_ptr(), n.value
     _check_device(workspace)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -214,15 +246,24 @@ def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None
         return _on(stream, adapter_forward, x, adapters, seg, seg_adapter, base, y, v, save_v, workspace)
     torch = _torch or _setup()
     tx, ad, lib = _matrix(x), adapters._struct(), load()
-    M = x.shape[0]
-    if y is None:
-        y = torch.empty((M, adapters.B.shape[1]), dtype=x.dtype, device=x.device)
+    M = tx.rows
+    rbase = None
+    if base is not None:
+        tb = _matrix(base)
+        rbase = byref(tb)
+    if y is not None:
+        ry = byref(_matrix(y))
+    elif base is not None:
+        y, ty = _fresh(base, tb)
+        ry = byref(ty)
+    else:
+        y = torch.empty((M, ad.B.cols), dtype=x.dtype, device=x.device)
+        ry = byref(Tensor(y.data_ptr(), tx.dtype, 0, M, ad.B.cols))
     if v is None and save_v:
         v = torch.empty((M, adapters.max_rank), dtype=torch.float32, device=x.device)
-    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_forward_query, M, ad, x.device,
-                                   "ss1_adapter_forward_query")
-    st = lib.ss1_adapter_forward(byref(tx), byref(ad), byref(_segments(seg, seg_adapter)), _ref(_matrix, base),
-                                 byref(_matrix(y)), _ref(_matrix, v), wp, wb, _handle(x))
+    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_forward_query, M, ad, x, "ss1_adapter_forward_query")
+    st = lib.ss1_adapter_forward(byref(tx), byref(ad), byref(_segments(seg, seg_adapter)), rbase, ry,
+                                 _ref(_matrix, v), wp, wb, _handle(x))
     if st:
         _check(st, "ss1_adapter_forward")
     return y, v
@@ -237,20 +278,16 @@ def adapter_backward(dy, x, v, adapters: AdapterSet, seg, seg_adapter, dx_base=N
     which the adapters' is added, and dx may be dx_base itself."""
     if stream is not None:
         return _on(stream, adapter_backward, dy, x, v, adapters, seg, seg_adapter, dx_base, dx, dA, dB, workspace)
-    torch = _torch or _setup()
+    _torch or _setup()
     tx, ad, lib = _matrix(x), adapters._struct(), load()
-    M = x.shape[0]
-    if dx is True:
-        dx = torch.empty_like(x)
-    if dA is True:
-        dA = torch.empty_like(adapters.A)
-    if dB is True:
-        dB = torch.empty_like(adapters.B)
-    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_backward_query, M, ad, x.device,
-                                   "ss1_adapter_backward_query")
+    M = tx.rows
+    dx, rdx = _out(dx, _matrix, x, tx)
+    dA, rdA = _out(dA, _matrix, adapters.A, ad.A)
+    dB, rdB = _out(dB, _matrix, adapters.B, ad.B)
+    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_backward_query, M, ad, x, "ss1_adapter_backward_query")
     st = lib.ss1_adapter_backward(byref(_matrix(dy)), byref(tx), _ref(_matrix, v), byref(ad),
-                                  byref(_segments(seg, seg_adapter)), _ref(_matrix, dx_base), _ref(_matrix, dx),
-                                  _ref(_matrix, dA), _ref(_matrix, dB), wp, wb, _handle(x))
+                                  byref(_segments(seg, seg_adapter)), _ref(_matrix, dx_base), rdx, rdA, rdB, wp, wb,
+                                  _handle(x))
     if st:
         _check(st, "ss1_adapter_backward")
     return dx, dA, dB
@@ -317,30 +354,42 @@ class AdamWPlan:
             if t is not None and len(t) != n:
                 raise ValueError(f"{what} must hold one for each of the {n} params")
         table = (AdamWEntry * max(n, 1))()
-        for i, p in enumerate(params):
-            _check_device(p, grads[i], m[i], v[i])
-            numel = p.numel()
-            if not p.is_contiguous():
-                raise ValueError("params must be contiguous")
-            _check_vec(grads[i], grads[i].dtype, numel, "grad")
-            code = _lib._dtype_code(m[i])
-            if code == BF16 or _lib._dtype_code(v[i]) != code or (code == FP8_E4M3) != eight:
-                raise TypeError("states must all be float32 or all E4M3 codes")
-            _check_vec(m[i], m[i].dtype, numel, "m")
-            _check_vec(v[i], v[i].dtype, numel, "v")
-            e = table[i]
-            e.param, e.grad, e.m, e.v = (t.data_ptr() or None for t in (p, grads[i], m[i], v[i]))
-            if masters is not None and masters[i] is not None:
+        rows = np.frombuffer(table, dtype=np.dtype(AdamWEntry))[:n]
+        numel = [p.numel() for p in params]
+        blocks = [-(-k // ADAMW_BLOCK) for k in numel]
+
+        def column(name, ts, what, dtype, sizes):
+            """The tensors' addresses into one field of the table."""
+            for t, k in zip(ts, sizes):
+                if not t.is_cuda or not t.is_contiguous() or t.numel() != k or (dtype is not None and t.dtype != dtype):
+                    _check_device(t)
+                    _check_vec(t, dtype or t.dtype, k, what)
+            rows[name] = [t.data_ptr() for t in ts]
+
+        if any(not p.is_contiguous() for p in params):
+            raise ValueError("params must be contiguous")
+        column("param", params, "param", None, numel)
+        column("grad", grads, "grad", None, numel)
+        kinds = {t.dtype for t in m} | {t.dtype for t in v}
+        codes = {_lib._dtype_code(t) for t in m} | {_lib._dtype_code(t) for t in v} if len(kinds) > 1 else \
+            {_lib._dtype_code(t) for t in m[:1]}
+        if len(codes) > 1 or BF16 in codes or (FP8_E4M3 in codes) != eight:
+            raise TypeError("states must all be float32 or all E4M3 codes")
+        column("m", m, "m", None, numel)
+        column("v", v, "v", None, numel)
+        if masters is not None:
+            has = [i for i, t in enumerate(masters) if t is not None]
+            for i in has:
                 _check_device(masters[i])
-                _check_vec(masters[i], torch.float32, numel, "master")
-                e.master = masters[i].data_ptr() or None
-            if eight:
-                _check_device(m_scales[i], v_scales[i])
-                _check_vec(m_scales[i], torch.float32, -(-numel // ADAMW_BLOCK), "m_scale")
-                _check_vec(v_scales[i], torch.float32, -(-numel // ADAMW_BLOCK), "v_scale")
-                e.m_scale, e.v_scale = m_scales[i].data_ptr() or None, v_scales[i].data_ptr() or None
-            e.numel, e.weight_decay = numel, decay[i]
-            e.param_dtype, e.grad_dtype, e.state_dtype = _float_code(p, "param"), _float_code(grads[i], "grad"), code
+                _check_vec(masters[i], torch.float32, numel[i], "master")
+                rows["master"][i] = masters[i].data_ptr()
+        if eight:
+            column("m_scale", m_scales, "m_scale", torch.float32, blocks)
+            column("v_scale", v_scales, "v_scale", torch.float32, blocks)
+        rows["numel"], rows["weight_decay"] = numel, decay
+        rows["param_dtype"] = [_float_code(p, "param") for p in params]
+        rows["grad_dtype"] = [_float_code(g, "grad") for g in grads]
+        rows["state_dtype"] = FP8_E4M3 if eight else F32
         lib, chunks = load(), ctypes.c_int64(0)
         _check(lib.ss1_adamw_plan(table, n, byref(chunks), None), "ss1_adamw_plan")
         host_map = np.empty((max(chunks.value, 1), 2), dtype=np.int32)

@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kThreads) void plan_outer_kernel(AdapterView ad, Ou
 // us, the latency of its dependent reads alone), hence the slices: the more blocks
 // read a factor, the shorter each one's chain.
 // ROWS: rows of x that may be there, 8 or 16.
-template <typename T, int RT, int UN = (RT <= 2 ? 2 : 1), int ROWS = 16>
+template <typename T, int RT, int UN = 1, int ROWS = 16>
 __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,
                                             int stride, float scale, f32x4* red) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -291,7 +291,7 @@ __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T
     const uint32_t piece = 16u * ((lane >> 4) + 4 * ((lane >> 3) & 1)), lo8 = pair_lane_mask(lane);
     const uint32_t lane_off = (lane & 7) * Kb + piece;
     // UN units' loads are in flight together (past the wave's share or the row:
-    // zeros)
+    // zeros); beside other blocks on the compute unit 1, 2 and 3 measure the same
     for (int ub = u0 + wave * UN; ub < u1; ub += UN * kWaves) {
         uint4 xf[UN][2], af[UN][RT][2];
 #pragma unroll

@@ -14,8 +14,8 @@
 //
 // 16384 x 4096 bf16: forward 55.9 us (269 MB, 4.8 TB/s), backward 79.6 + 4.9 us
 // for the join (403 MB, 5.1 TB/s in the first launch), a large copy 5.0 to 5.3.
-// 16 x 4096 forward 3.8 us and 1111 x 1283 float32 backward 10.3 + 3.9 us, both
-// below what the host takes for the calls.
+// 16 x 4096 forward 3.8 us and 1111 x 1283 float32 backward 11 us in one launch,
+// both below what the host takes for the calls.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -258,21 +258,15 @@ __global__ __launch_bounds__(kLong) void layernorm_forward_long(const X* x, cons
 }
 
 // ------------------------------------------------------------------ backward
-// Block b takes rows b * ROWS + r, stepping by the grid; each thread keeps the
-// sums of dy xh and dy over its rows for its columns, the block joins its row
-// groups in LDS, group by group, and writes partial[b][0 or 1][k].
-template <typename X, typename G, int T, int NV, int BLOCK, bool TAIL>
-__global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, const X* __restrict__ x,
-                                                                   const G* __restrict__ gamma,
-                                                                   const float* __restrict__ mean,
-                                                                   const float* __restrict__ rstd, X* dx,
-                                                                   float* __restrict__ partial, int64_t M, int K) {
-    constexpr int ROWS = BLOCK / T;
-    __shared__ float2 red[2 * BLOCK / 64];
-    __shared__ float2 join[ROWS > 1 ? T * NV * kVec : 1];
+// dx of the rows m0 + (thread / T), m0 from `first` on by `step`, and with SUMS
+// each thread's sums of dy xh and dy over its rows for its columns.
+template <typename X, typename G, int T, int NV, int BLOCK, bool TAIL, bool SUMS>
+__device__ __forceinline__ void backward_rows_of(const X* dy, const X* __restrict__ x, const G* __restrict__ gamma,
+                                                 const float* __restrict__ mean, const float* __restrict__ rstd, X* dx,
+                                                 int64_t M, int K, int64_t first, int64_t step, float2* red,
+                                                 float2 (&sum)[NV][kVec]) {
     const int t = threadIdx.x % T, group = threadIdx.x / T;
     int phase = 0;
-    float2 sum[NV][kVec];  // (dgamma, dbeta) of this thread's columns
     float w[NV][kVec];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -285,7 +279,7 @@ __global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, 
         }
         if (n > 0) load8<TAIL>(gamma + at, n, w[i]);
     }
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * ROWS; m0 < M; m0 += static_cast<int64_t>(gridDim.x) * ROWS) {
+    for (int64_t m0 = first; m0 < M; m0 += step) {
         const int64_t m = m0 + group;
         const bool row = m < M;
         const size_t base = static_cast<size_t>(m) * K;
@@ -309,8 +303,10 @@ __global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, 
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     xh[i][j] = !TAIL || j < n ? (xh[i][j] - mu) * rs : 0.0f;
-                    sum[i][j].x += g[i][j] * xh[i][j];
-                    sum[i][j].y += g[i][j];
+                    if (SUMS) {
+                        sum[i][j].x += g[i][j] * xh[i][j];
+                        sum[i][j].y += g[i][j];
+                    }
                     g[i][j] *= w[i][j];
                     s.x += g[i][j];
                     s.y += g[i][j] * xh[i][j];
@@ -332,6 +328,24 @@ __global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, 
             }
         }
     }
+}
+
+// Block b takes rows b * ROWS + r, stepping by the grid; the block joins its row
+// groups' column sums in LDS, group by group, and writes partial[b][0 or 1][k].
+template <typename X, typename G, int T, int NV, int BLOCK, bool TAIL>
+__global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, const X* __restrict__ x,
+                                                                   const G* __restrict__ gamma,
+                                                                   const float* __restrict__ mean,
+                                                                   const float* __restrict__ rstd, X* dx,
+                                                                   float* __restrict__ partial, int64_t M, int K) {
+    constexpr int ROWS = BLOCK / T;
+    __shared__ float2 red[2 * BLOCK / 64];
+    __shared__ float2 join[ROWS > 1 ? T * NV * kVec : 1];
+    const int t = threadIdx.x % T, group = threadIdx.x / T;
+    float2 sum[NV][kVec];  // (dgamma, dbeta) of this thread's columns
+    backward_rows_of<X, G, T, NV, BLOCK, TAIL, true>(dy, x, gamma, mean, rstd, dx, M, K,
+                                                     static_cast<int64_t>(blockIdx.x) * ROWS,
+                                                     static_cast<int64_t>(gridDim.x) * ROWS, red, sum);
     if (!partial) return;
     if constexpr (ROWS > 1) {
         // join[] is laid out [i][j][t]: consecutive threads, consecutive pairs
@@ -372,6 +386,70 @@ __global__ __launch_bounds__(BLOCK) void layernorm_backward_kernel(const X* dy, 
             store8<TAIL>(out + at, n, a);
             store8<TAIL>(out + K + at, n, b);
         }
+    }
+}
+
+// Both in one launch for small inputs, without partial rows: the first blocks take
+// a strip of kStrip vectors of columns over all rows each, the rest a group of
+// rows each.  dy and x are read twice, the second time from cache, so dx must be
+// apart from them.
+constexpr int kStrip = 2;  // 16 columns
+template <typename X, typename G, int T, int NV, bool TAIL>
+__global__ __launch_bounds__(256) void layernorm_backward_small(const X* dy, const X* __restrict__ x,
+                                                                const G* __restrict__ gamma,
+                                                                const float* __restrict__ mean,
+                                                                const float* __restrict__ rstd, X* dx,
+                                                                G* __restrict__ dgamma, G* __restrict__ dbeta, int M,
+                                                                int K, int strips) {
+    constexpr int WAVES = 4, ROWS = 256 / kStrip;
+    __shared__ float2 red[2 * WAVES];
+    __shared__ float2 join[WAVES][kStrip * kVec];
+    if (static_cast<int>(blockIdx.x) >= strips) {
+        float2 none[NV][kVec];
+        const int64_t at = static_cast<int64_t>(blockIdx.x - strips) * (256 / T);
+        backward_rows_of<X, G, T, NV, 256, TAIL, false>(dy, x, gamma, mean, rstd, dx, M, K, at, M, red, none);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, vec = lane % kStrip;
+    const int at = (static_cast<int>(blockIdx.x) * kStrip + vec) * kVec, n = count_of(K, at);
+    float2 sum[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) sum[j] = make_float2(0.0f, 0.0f);
+    if (n > 0) {
+#pragma unroll 4
+        for (int m = threadIdx.x / kStrip; m < M; m += ROWS) {
+            const size_t o = static_cast<size_t>(m) * K + at;
+            const float mu = mean[m], rs = rstd[m];
+            float a[kVec], g[kVec];
+            load8<TAIL>(x + o, n, a);
+            load8<TAIL>(dy + o, n, g);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                sum[j].x += g[j] * ((a[j] - mu) * rs);
+                sum[j].y += g[j];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+#pragma unroll
+        for (int off = kStrip; off < 64; off <<= 1) {
+            sum[j].x += __shfl_xor(sum[j].x, off);
+            sum[j].y += __shfl_xor(sum[j].y, off);
+        }
+        if (lane < kStrip) join[wave][vec * kVec + j] = sum[j];
+    }
+    __syncthreads();
+    const int k = static_cast<int>(blockIdx.x) * kStrip * kVec + threadIdx.x;
+    if (threadIdx.x < kStrip * kVec && k < K) {
+        float2 s = join[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            s.x += join[w][threadIdx.x].x;
+            s.y += join[w][threadIdx.x].y;
+        }
+        if (dgamma) store1(dgamma + k, s.x);
+        if (dbeta) store1(dbeta + k, s.y);
     }
 }
 
@@ -492,6 +570,16 @@ void forward(const NormArgs& a, hipStream_t s) {
                        static_cast<X*>(a.y), a.mean, a.rstd, a.M, a.K, a.eps);
 }
 
+// Rows and elements up to which the backward pass is one launch: a strip's block
+// reads its columns at about 25 bytes a ns, which passes the host's time for the
+// two launches there.  A call as the host makes it, one launch against two, in us,
+// bf16 / float32: 512 x 768 14.8 / 14.4 against 18.2 / 18.4, 1024 x 4096 15.6 / 18.3
+// against 18.2 / 18.0, 1280 x 1283 15.1 / 14.1 against 18.1 / 18.2, 1280 x 4096 18.3 /
+// 22.2 against 18.5 / 20.6, 2048 x 2048 17.3 / 23.6 against 18.2.  On the device
+// alone: 512 x 4096 12.5 / 14.4 against 16.3 / 16.2, 1024 x 768 10.5 / 14.6 against
+// 11.5 / 11.4, 1024 x 4096 19.2 / 21.6 against 18.3 / 19.9.
+constexpr int64_t kSmallRows = 1280, kSmallElements = int64_t(4) << 20;
+
 // How the backward pass splits the rows.
 struct Split {
     int T;       // threads a row, 0: too long for registers
@@ -529,10 +617,41 @@ void backward_rows(const NormArgs& a, int groups, float* partial, hipStream_t s)
                        static_cast<X*>(a.dx), partial, a.M, a.K);
 }
 
+template <typename X, typename G, int T, int NV>
+void backward_small(const NormArgs& a, hipStream_t s) {
+    const int strips = a.dgamma || a.dbeta ? (a.K + kStrip * kVec - 1) / (kStrip * kVec) : 0;
+    const int64_t rows = a.dx ? (a.M + 256 / T - 1) / (256 / T) : 0;
+    auto k = a.K % kVec ? layernorm_backward_small<X, G, T, NV, true> : layernorm_backward_small<X, G, T, NV, false>;
+    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(strips + rows)), dim3(256), 0, s, static_cast<const X*>(a.dy),
+                       static_cast<const X*>(a.x), static_cast<const G*>(a.gamma), a.mean_in, a.rstd_in,
+                       static_cast<X*>(a.dx), static_cast<G*>(a.dgamma), static_cast<G*>(a.dbeta),
+                       static_cast<int>(a.M), a.K, strips);
+}
+
+// Whether two [M][K] arrays share memory.
+bool overlap(const void* a, const void* b, size_t bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + bytes && q < p + bytes;
+}
+
+template <typename X>
+bool is_small(const NormArgs& a) {
+    const size_t bytes = static_cast<size_t>(a.M) * a.K * sizeof(X);
+    return a.M > 0 && a.M <= kSmallRows && a.M * a.K <= kSmallElements && a.K <= 4096 &&
+           !(a.dx && (overlap(a.dx, a.dy, bytes) || overlap(a.dx, a.x, bytes)));
+}
+
 template <typename X, typename G>
 void backward(const NormArgs& a, hipStream_t s) {
     const Split p = split_of(a.M, a.K);
     const bool sums = a.dgamma || a.dbeta;
+    if (is_small<X>(a)) {
+        const int vecs = (a.K + kVec - 1) / kVec;
+        return vecs <= 64    ? backward_small<X, G, 64, 1>(a, s)
+               : vecs <= 128 ? backward_small<X, G, 64, 2>(a, s)
+               : vecs <= 256 ? backward_small<X, G, 256, 1>(a, s)
+                             : backward_small<X, G, 256, 2>(a, s);
+    }
     float* partial = sums ? a.partial : nullptr;
     if (a.M > 0 && p.T == 0) {
         // the column sums first: dx may be dy itself

@@ -491,7 +491,7 @@ __global__ __launch_bounds__(kThreads) void shrink_tile_kernel(AdapterView ad, c
 // columns of a rank unit, 16 bytes of each of its rows turned in registers, and
 // a lane's sums are 16 bytes of four rows of y.
 //
-// expand_kernel, short segments.  One block: a piece of up to 16 tokens and `per`
+// expand_kernel, short segments.  One block: a piece of up to 16 tokens and a few
 // column tiles of kWaves * 16 vectors of 16 bytes.  The piece's v (its Q partial
 // sums added in order) goes to LDS as operands; each wave then takes 16 vectors
 // of every tile, and the rows of B and base of the next tile are in flight while
@@ -545,6 +545,12 @@ __device__ __forceinline__ uint4 pack(const __bf16*, const f32x4 (&acc)[8], int 
 __device__ __forceinline__ uint4 pack(const float*, const f32x4 (&acc)[4], int i) {
     return make_uint4(__float_as_uint(acc[0][i]), __float_as_uint(acc[1][i]), __float_as_uint(acc[2][i]),
                       __float_as_uint(acc[3][i]));
+}
+
+// First of the column tiles of block cg of `columns` (at most one a tile): shares
+// that differ by one tile at most (10 tiles in 3: 20.2 us, as 4 + 4 + 2 21.7).
+__device__ __forceinline__ int first_tile(int cg, int tiles, int columns) {
+    return static_cast<int>(static_cast<int64_t>(tiles) * cg / columns);
 }
 
 // Tokens without an adapter: y = base (zeros without one) in `wide` 16-byte
@@ -683,7 +689,7 @@ template <typename T, int KU>
 __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, const float* __restrict__ part, int stride,
                                                              int Q, const T* __restrict__ B, const T* base, T* y,
                                                              float* __restrict__ v_out, int v_stride, int v_cols,
-                                                             int N, int scaled, int columns, int per, int tiles,
+                                                             int N, int scaled, int columns, int tiles,
                                                              int64_t items) {
     __shared__ uint4 frags[KU * Unit<T>::kFrags * 64];
     const size_t slice = static_cast<size_t>(ad.M) * stride;
@@ -691,7 +697,7 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, con
         const int cg = static_cast<int>(item % columns);
         const Piece pc = find_piece(ad, 16, static_cast<int>(item / columns));
         if (pc.n == 0) continue;
-        const int tile0 = cg * per, count = min(per, tiles - tile0);
+        const int tile0 = first_tile(cg, tiles, columns), count = first_tile(cg + 1, tiles, columns) - tile0;
         float* vo = cg == 0 ? v_out : nullptr;
         if (pc.rank == 0) {
             without_adapter(pc, base, y, vo, v_stride, v_cols, N, tile0 * kThreads / 4, count * kThreads / 4);
@@ -725,7 +731,7 @@ template <typename T, int KU>
 __global__ __launch_bounds__(kThreads, 2) void one_kernel(
     AdapterView ad, const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ B, const T* base, T* y,
     float* __restrict__ v_out, int v_stride, int v_cols, int stride, int K, int N, int scaled_v, int scaled_y, Repack v,
-    int columns, int per, int tiles, int64_t items) {
+    int columns, int tiles, int64_t items) {
     using U = Unit<T>;
     constexpr int MOST = KU * U::kRanks / 16;  // rank tiles, 1 or 2
     __shared__ f32x4 red[kWaves * MOST * 64];
@@ -735,7 +741,7 @@ __global__ __launch_bounds__(kThreads, 2) void one_kernel(
         const int cg = static_cast<int>(item % columns);
         const Piece pc = find_piece(ad, 16, static_cast<int>(item / columns));
         if (pc.n == 0) continue;
-        const int tile0 = cg * per, count = min(per, tiles - tile0);
+        const int tile0 = first_tile(cg, tiles, columns), count = first_tile(cg + 1, tiles, columns) - tile0;
         float* vo = cg == 0 ? v_out : nullptr;
         if (v.from && cg == 0) repack_rows(v, pc.begin, pc.n);
         if (pc.rank == 0) {
@@ -939,7 +945,7 @@ __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* p
 template <typename T, int KU>
 __global__ __launch_bounds__(kThreads, KU <= 2 ? 4 : 2) void expand_tile_kernel(
     AdapterView ad, const float* __restrict__ part, int stride, int Q, const T* __restrict__ B, const T* base, T* y,
-    float* __restrict__ v_out, int v_stride, int v_cols, int N, int scaled, int columns, int per, int tiles,
+    float* __restrict__ v_out, int v_stride, int v_cols, int N, int scaled, int columns, int tiles,
     int64_t items) {
     __shared__ uint4 bt[2 * KU * Unit<T>::kCols * 64];
     const size_t slice = static_cast<size_t>(ad.M) * stride;
@@ -947,7 +953,7 @@ __global__ __launch_bounds__(kThreads, KU <= 2 ? 4 : 2) void expand_tile_kernel(
         const int cg = static_cast<int>(item % columns);
         const Piece pc = find_piece(ad, 64, static_cast<int>(item / columns));
         if (pc.n == 0) continue;
-        const int tile0 = cg * per, count = min(per, tiles - tile0);
+        const int tile0 = first_tile(cg, tiles, columns), count = first_tile(cg + 1, tiles, columns) - tile0;
         float* vo = cg == 0 ? v_out : nullptr;
         if (pc.rank == 0) {
             without_adapter(pc, base, y, vo, v_stride, v_cols, N, tile0 * 16, count * 16);
@@ -1440,13 +1446,13 @@ void launch_expand(const AdapterArgs& a, const float* part, int stride, int Q, c
                        : ku <= 4 ? expand_kernel<T, 4> : expand_kernel<T, MOST>);
     hipLaunchKernelGGL(k, dim3(grid_of(pieces * columns)), dim3(kThreads), 0, s, a.ad, part, stride, Q,
                        static_cast<const T*>(B), static_cast<const T*>(a.base), static_cast<T*>(y), v_out, v_stride,
-                       v_cols, N, scaled, columns, static_cast<int>(per), tiles, pieces * columns);
+                       v_cols, N, scaled, columns, tiles, pieces * columns);
 }
 
 // How a call in one launch is split over blocks.
 struct OneSplit {
-    int64_t pieces, per;  // per: column tiles of a block
-    int tiles, columns;
+    int64_t pieces;
+    int tiles, columns;  // column tiles, and the blocks that share them
 };
 
 OneSplit one_split(const AdapterArgs& a, int N) {
@@ -1454,8 +1460,8 @@ OneSplit one_split(const AdapterArgs& a, int N) {
     const int wide = kThreads / 4 * 16 / esize(a.dtype);
     o.pieces = pieces_of(a.ad.M, a.ad.S, 16);
     o.tiles = (N + wide - 1) / wide;
-    o.per = std::max(int64_t(1), std::min(int64_t(o.tiles), o.pieces * o.tiles / kFill));
-    o.columns = static_cast<int>((o.tiles + o.per - 1) / o.per);
+    const int64_t per = std::max(int64_t(1), std::min(int64_t(o.tiles), o.pieces * o.tiles / kFill));
+    o.columns = static_cast<int>((o.tiles + per - 1) / per);
     return o;
 }
 
@@ -1485,7 +1491,7 @@ void launch_one(const AdapterArgs& a, const void* x, const void* A, const void* 
     hipLaunchKernelGGL(k, dim3(grid_of(o.pieces * o.columns)), dim3(kThreads), 0, s, a.ad, static_cast<const T*>(x),
                        static_cast<const T*>(A), static_cast<const T*>(B), static_cast<const T*>(a.base),
                        static_cast<T*>(y), v_out, v_stride, v_cols, stride_of(a.ad.max_rank), K, N, scaled_v, scaled_y,
-                       v, o.columns, static_cast<int>(o.per), o.tiles, o.pieces * o.columns);
+                       v, o.columns, o.tiles, o.pieces * o.columns);
 }
 
 template <typename T>

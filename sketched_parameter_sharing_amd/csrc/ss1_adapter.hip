@@ -998,8 +998,9 @@ __global__ __launch_bounds__(kThreads) void join_slices_kernel(const float* __re
 // of x and dy in 44 us.  Bound by each block's chain (lookup, listing, first
 // gather, stages, stores): the compute units are busy for 31 us of it, in 1.5
 // rounds of blocks, the vector instructions for 13.  Blocks of 512 bytes of
-// columns, one a compute unit, took 55; parts cut evenly over all adapters' tokens
-// with several adapters a block 41 here but 5 to 18% more with many adapters.
+// columns, one a compute unit, took 55 with four waves and 47.6 with eight; parts
+// cut evenly over all adapters' tokens with several adapters a block 41 here but
+// 5 to 18% more with many adapters.
 struct OuterJob {
     const float* v;  // [M][v_stride]
     const void* x;

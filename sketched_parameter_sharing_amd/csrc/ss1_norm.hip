@@ -10,7 +10,8 @@
 // stores.  The backward pass keeps each thread's columns of dgamma and dbeta
 // in registers too while a block walks over its rows, so the column sums cost
 // no second read of dy and x: every block writes one partial row, and a small
-// second launch adds those in order.
+// second launch adds those in order.  Small inputs take one launch instead, which
+// reads dy and x twice.
 //
 // 16384 x 4096 bf16: forward 55.9 us (269 MB, 4.8 TB/s), backward 79.6 + 4.9 us
 // for the join (403 MB, 5.1 TB/s in the first launch), a large copy 5.0 to 5.3.

@@ -266,10 +266,10 @@ __global__ __launch_bounds__(kThreads) void plan_outer_kernel(AdapterView ad, Ou
 // slice, their tiles are added in LDS.  A wave's operands come straight from
 // global memory in whole 128-byte lines.  part[q][m][stride], columns past the
 // rank 0.
-// Bound by A (64 requests of ranks up to 64, K = 4096, bf16: 15 MB of factors,
-// mostly from cache, in 9.5 us with launch and lookup; one token of rank 16: 3.7
-// us, the latency of its dependent reads alone), hence the slices: the more blocks
-// read a factor, the shorter each one's chain.
+// Bound by A and the chain of dependent reads (64 requests of ranks up to 64, K =
+// 4096, bf16: 15 MB of factors, mostly from cache, in 9.4 us with launch and
+// lookup), hence the slices: the more blocks read a factor, the shorter each one's
+// chain.
 // ROWS: rows of x that may be there, 8 or 16.
 template <typename T, int RT, int UN = 1, int ROWS = 16>
 __device__ __forceinline__ void shrink_body(const Piece& pc, const T* x, const T* A, float* out, int K, int Q, int q,

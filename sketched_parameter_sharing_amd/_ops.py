@@ -203,6 +203,10 @@ class AdapterSet:
         self.__dict__[name] = value
         self.__dict__["_view"] = (None, None)
 
+    def __getstate__(self):
+        # without the view: a copy has memory of its own
+        return {**self.__dict__, "_view": (None, None)}
+
     def _struct(self) -> Adapters:
         """The C ABI's view of the set, made again when the factors' memory or
         sizes or any attribute changed."""

@@ -1,6 +1,8 @@
 """Adapters of small batches on the GPU, at the sizes where the library changes
 from one launch for both products to two: tokens, ranks, bytes of a factor and
 their total.  Definitions and tolerances as for the other batches."""
+import copy
+
 import pytest
 import torch
 
@@ -90,3 +92,17 @@ def test_infinities_and_nan_stay_with_their_request(dtype):
     rows = torch.ones(29, dtype=torch.bool, device="cuda")
     rows[16:25] = False
     assert torch.isfinite(dA[rows]).all() and torch.isfinite(dB[rows]).all()
+
+
+def test_a_used_set_is_copied_and_changed():
+    c = Case([(3, 0), (2, 1)], [8, 4], 64, 72, F, seed=44)
+    y, _ = c.forward(base=c.base)
+    twin = copy.deepcopy(c.set)
+    assert torch.equal(ss1.adapter_forward(c.x, twin, c.seg, c.ids, base=c.base)[0], y)
+    again = copy.copy(c.set)
+    assert torch.equal(ss1.adapter_forward(c.x, again, c.seg, c.ids, base=c.base)[0], y)
+    # other factors, by the attribute and by the tensor's memory
+    twin.B = torch.zeros_like(twin.B)
+    assert torch.equal(ss1.adapter_forward(c.x, twin, c.seg, c.ids, base=c.base)[0], c.base)
+    c.set.B.data = torch.zeros_like(c.set.B)
+    assert torch.equal(c.forward(base=c.base)[0], c.base)

@@ -705,6 +705,10 @@ typedef struct {
  *     about 0.0005 of itself, and rounding to nearest (quantum 1/8 to 1/16)
  *     would hold it for ever.  A nonzero r keeps at least the smallest code.
  *     p takes the moments before they are rounded.
+ *   - An infinity or a NaN stays with its element: its param and its moments
+ *     are what the formula gives.  E4M3 has a NaN and no infinity, so a moment
+ *     (m, or r) that is either is stored as NaN and does not count in the
+ *     block's maximum; the block's other elements are as without it.
  * Random bits: SplitMix64 (as in ss1_plan) of seed and (entry, element) pairs,
  * so equal calls give equal bits; a caller passes another seed each step.
  *   entries, map : DEVICE copies of ss1_adamw_plan's arrays; count, chunks as

@@ -43,7 +43,7 @@ __device__ __forceinline__ uint64_t random_bits(uint64_t z) {
 }
 
 // 0 <= a <= 448 (up to a rounding) as an E4M3 value, up or down with the
-// probability of its distance.  In the normal range (3 mantissa bits: 20 are
+// probability of its distance (448 for a NaN: quantize8 puts it back).  In the normal range (3 mantissa bits: 20 are
 // dropped) adding 16 random bits below the last kept bit and cutting off does
 // that; below 2^-6 the quantum is 2^-9.
 __device__ __forceinline__ float e4m3_normal(float a, uint32_t u16) {
@@ -148,15 +148,20 @@ __device__ __forceinline__ float rotate(float v) {
         __builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(v)), 0x120 + N, 0xF, 0xF, true)));
 }
 
+// The larger one, a NaN where either is (v_maximum3_f32, whose price is v_max3's).
+__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // max over the 32 lanes that share a scale (the half wave): rotations inside
 // the 16-lane rows, and one lane exchange between the two rows.
 __device__ __forceinline__ float half_wave_max(float v) {
-    v = fmaxf(v, rotate<8>(v));
-    v = fmaxf(v, rotate<4>(v));
-    v = fmaxf(v, rotate<2>(v));
-    v = fmaxf(v, rotate<1>(v));
-    return fmaxf(v, __shfl_xor(v, 16));
+    v = nan_max(v, rotate<8>(v));
+    v = nan_max(v, rotate<4>(v));
+    v = nan_max(v, rotate<2>(v));
+    v = nan_max(v, rotate<1>(v));
+    return nan_max(v, __shfl_xor(v, 16));
 }
+
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
 
 // t / scale rounded to nearest, from y = 1 / scale rounded to nearest: the
 // remainder of the first quotient is exact, and adding its share rounds as the
@@ -170,13 +175,22 @@ __device__ __forceinline__ float quotient(float t, float scale, float y) {
 // max |t| times 1/448 as a float (1 for a block of zeros), the quotients as IEEE
 // division gives them.  u[j] holds the random bits of element j.  ROOT: the
 // values are square roots, and a nonzero one keeps at least the smallest code.
+// E4M3 has a NaN and no infinity: a value that is either becomes its NaN and
+// stays out of the maximum, so the rest of the block keeps its scale and codes.
 template <bool ROOT>
 __device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t i, int n, const float (&t)[kVec],
                                           const uint32_t (&u)[kVec]) {
     float top = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) top = fmaxf(top, fabsf(t[j]));
+    for (int j = 0; j < kVec; ++j) top = nan_max(top, fabsf(t[j]));
     top = half_wave_max(top);
+    const bool special = !finite(top);  // the same in the 32 lanes
+    if (special) {
+        top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) top = nan_max(top, finite(t[j]) ? fabsf(t[j]) : 0.0f);
+        top = half_wave_max(top);
+    }
     const float scale = top > 0.0f ? top * (1.0f / 448.0f) : 1.0f;
     if (n > 0 && (threadIdx.x & 31) == 0) scales[i / SS1_ADAMW_BLOCK] = scale;
     float q[kVec];
@@ -208,6 +222,10 @@ __device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t
             if (a < 0x1p-6f) r[j] = e4m3_small(a, u[j]);
             if (ROOT && t[j] > 0.0f) r[j] = fmaxf(r[j], 0x1p-9f);
         }
+    if (special)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (!finite(t[j])) r[j] = NAN;
     if (!ROOT)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) r[j] = copysignf(r[j], q[j]);

@@ -309,7 +309,9 @@ def _float_code(t, what: str) -> int:
 class AdamWPlan:
     """An AdamW step over many tensors: the table of their addresses and the
     list of work items, made once on the host and copied to the GPU.  It holds
-    for as long as the tensors stay where they are (it keeps them alive).
+    for as long as the tensors stay where they are (it keeps them alive).  A
+    deep copy or a loaded plan (``torch.save``) has tensors of its own, and a
+    table of them.
 
     8-bit states are ``torch.float8_e4m3fn`` (or uint8 codes) with one float32
     scale per 256 elements; ``v`` then stands for the square root of the
@@ -324,6 +326,11 @@ class AdamWPlan:
     m_scales: list | None
     v_scales: list | None
     masters: list | None
+    weight_decay: list
+
+    def __reduce__(self):
+        # not the table: a copy's tensors lie at other addresses
+        return _plan_of, (*self.tensors, self.weight_decay)
 
     @classmethod
     def make(cls, params, grads, m=None, v=None, masters=None, m_scales=None, v_scales=None, weight_decay=0.0,
@@ -402,7 +409,7 @@ class AdamWPlan:
         entries = torch.from_numpy(np.frombuffer(table, dtype=np.uint8).copy()).to(device)
         keep = (params, grads, m, v, masters, m_scales, v_scales)
         return cls(entries, torch.from_numpy(host_map).to(device), n, chunks.value, keep, m, v, m_scales, v_scales,
-                   masters)
+                   masters, decay)
 
     def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
              grad_scale=1.0, seed: int = 0, stream=None):
@@ -419,3 +426,8 @@ class AdamWPlan:
                                    _handle(self.entries) if stream is None else stream.cuda_stream)
         if st:
             _check(st, "ss1_adamw_step")
+
+
+def _plan_of(params, grads, m, v, masters, m_scales, v_scales, weight_decay):
+    """A plan over the tensors of a copied or unpickled one (AdamWPlan.tensors)."""
+    return AdamWPlan.make(params, grads, m, v, masters, m_scales, v_scales, weight_decay)

@@ -208,14 +208,14 @@ class AdapterSet:
         return {**self.__dict__, "_view": (None, None)}
 
     def _struct(self) -> Adapters:
-        """The C ABI's view of the set, made again when the factors' memory or
-        sizes or any attribute changed."""
-        A, B = self.A, self.B
-        now = (A.data_ptr(), A.shape, B.data_ptr(), B.shape)
+        """The C ABI's view of the set, made and checked again when an attribute,
+        the memory of a tensor or the sizes, type or layout of a factor changed."""
+        A, B, row, scale = self.A, self.B, self.row, self.scale
+        now = (A.data_ptr(), A.shape, A.dtype, A.is_contiguous(), B.data_ptr(), B.shape, B.dtype, B.is_contiguous(),
+               row.data_ptr(), scale.data_ptr())
         seen, ad = self._view
         if seen != now:
-            ad = Adapters(_matrix(A), _matrix(B), self.row.data_ptr(), self.scale.data_ptr(), len(self.ranks),
-                          self.max_rank)
+            ad = Adapters(_matrix(A), _matrix(B), now[-2], now[-1], len(self.ranks), self.max_rank)
             self.__dict__["_view"] = (now, ad)
         return ad
 

@@ -1,0 +1,74 @@
+"""The C view that an adapter set keeps: a tensor of the set that was given other
+memory, another type or another layout is seen at the next call."""
+import pytest
+
+import sketched_parameter_sharing_amd as ss1
+from sketched_parameter_sharing_amd import _lib
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ss1.load()
+
+
+def used_set(dtype=F, K=64, N=72, rank=8):
+    """A set that a call has used, and a call with it."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    s = ss1.AdapterSet.make(r(2 * rank, K), r(2 * rank, N), [rank, rank], [0.5, 2.0])
+    x = r(5, K)
+    seg = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    call = lambda of=s: ss1.adapter_forward(x, of, seg, ids)[0]  # noqa: E731
+    call()
+    return s, call
+
+
+def fresh(s):
+    """A set over the same tensors that keeps no view."""
+    return ss1.AdapterSet(s.A, s.B, s.row, s.scale, s.max_rank, s.ranks)
+
+
+def test_other_memory_of_each_tensor():
+    for change in (lambda s: setattr(s.scale, "data", s.scale * 3), lambda s: setattr(s.A, "data", s.A * 2),
+                   lambda s: setattr(s.B, "data", s.B * 2),
+                   lambda s: setattr(s.row, "data", torch.tensor([0, 3, 16], dtype=torch.int32, device="cuda"))):
+        s, call = used_set()
+        y = call()
+        old = s.row.data, s.scale.data  # alive, so that the new memory is elsewhere
+        change(s)
+        assert torch.equal(call(), call(fresh(s))) and not torch.equal(call(), y)
+        del old
+
+
+def test_values_written_in_place_need_no_new_view():
+    s, call = used_set()
+    y, view = call(), s._struct()
+    s.scale.mul_(3)
+    assert s._struct() is view and torch.equal(call(), call(fresh(s))) and not torch.equal(call(), y)
+
+
+def test_a_transposed_factor_is_refused():
+    # a square A of the same memory and sizes, read the other way round
+    s, call = used_set(K=16)
+    s.A.data = s.A.t()
+    with pytest.raises(ValueError, match="contiguous"):
+        call()
+
+
+def test_another_type_in_the_same_memory_is_refused():
+    s, call = used_set(BF)
+    s.A.data = s.A.view(torch.float16)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        call()
+    s, call = used_set(BF)
+    s.A.data, s.B.data = s.A.view(F), s.B.view(F)
+    with pytest.raises(_lib.SS1Error):  # x is bf16
+        call()

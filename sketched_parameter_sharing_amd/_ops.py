@@ -215,7 +215,9 @@ class AdapterSet:
                row.data_ptr(), scale.data_ptr())
         seen, ad = self._view
         if seen != now:
-            ad = Adapters(_matrix(A), _matrix(B), now[-2], now[-1], len(self.ranks), self.max_rank)
+            count, torch = len(self.ranks), _torch or _setup()
+            ad = Adapters(_matrix(A), _matrix(B), _vec(row, torch.int32, count + 1, "row"),
+                          _vec(scale, torch.float32, count, "scale"), count, self.max_rank)
             self.__dict__["_view"] = (now, ad)
         return ad
 

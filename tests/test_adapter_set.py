@@ -72,3 +72,23 @@ def test_another_type_in_the_same_memory_is_refused():
     s.A.data, s.B.data = s.A.view(F), s.B.view(F)
     with pytest.raises(_lib.SS1Error):  # x is bf16
         call()
+
+
+def test_a_set_made_by_hand_is_checked():
+    # the dataclass is public: its index and scale arrays go to the kernels by address alone
+    s, call = used_set()
+    for change, error in ((dict(row=s.row.long()), "row must be torch.int32"), (dict(row=s.row[:2]), "row must hold 3"),
+                          (dict(row=s.row.cpu()), "GPU tensors"), (dict(scale=s.scale.double()), "scale must be"),
+                          (dict(scale=s.scale[:1]), "scale must hold 2"), (dict(scale=s.scale.cpu()), "GPU tensors"),
+                          (dict(row=s.row.repeat(2)[::2]), "row must be contiguous"),
+                          (dict(ranks=(8, 4, 4)), "row must hold 4")):
+        fields = {k: getattr(s, k) for k in ("A", "B", "row", "scale", "max_rank", "ranks")}
+        with pytest.raises(ValueError, match=error):
+            ss1.AdapterSet(**{**fields, **change})._struct()  # the view alone: nothing is launched
+    for name, value in (("row", s.row.long()), ("scale", s.scale.cpu())):
+        was = getattr(s, name)
+        setattr(s, name, value)
+        with pytest.raises(ValueError):
+            s._struct()
+        setattr(s, name, was)
+    call()

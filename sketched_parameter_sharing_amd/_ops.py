@@ -25,24 +25,34 @@ ADAMW_BLOCK = 256    # SS1_ADAMW_BLOCK
 _torch = None
 _codes = {}
 _raw_stream = None
+_current_device = None
 
 
 def _setup():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     import torch
     _codes.update({torch.float32: F32, torch.bfloat16: BF16})
     # the handle of a device's current stream, without a Stream object around it
-    # (3 us of a small call); current_stream is the public way to the same handle
+    # (3 us of a small call); current_stream is the public way to the same handle,
+    # as current_device is to the index
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
     return torch
 
 
-def _matrix(t) -> Tensor:
-    """The C ABI's view of a 2-D, contiguous GPU tensor."""
-    if not t.is_cuda:
+def _refuse_device(index: int):
+    """For a tensor on device ``index`` (-1: host memory) in a call on another."""
+    if index < 0:
         raise ValueError("device entry points take GPU tensors")
+    raise ValueError("the tensors of a call must be on one GPU")
+
+
+def _matrix(t, dev: int) -> Tensor:
+    """The C ABI's view of a 2-D, contiguous tensor on GPU ``dev``."""
+    if t.get_device() != dev:
+        _refuse_device(t.get_device())
     if t.dim() != 2 or not t.is_contiguous():
         raise ValueError("matrices must be 2-D and contiguous")
     code = _codes.get(t.dtype)
@@ -52,10 +62,10 @@ def _matrix(t) -> Tensor:
     return Tensor(t.data_ptr(), code, 0, rows, cols)
 
 
-def _row(t) -> Tensor:
+def _row(t, dev: int) -> Tensor:
     """A vector as the [1][K] tensor of the C ABI."""
-    if not t.is_cuda:
-        raise ValueError("device entry points take GPU tensors")
+    if t.get_device() != dev:
+        _refuse_device(t.get_device())
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError("gamma, beta and their gradients must be 1-D and contiguous")
     code = _codes.get(t.dtype)
@@ -64,10 +74,10 @@ def _row(t) -> Tensor:
     return Tensor(t.data_ptr(), code, 0, 1, t.shape[0])
 
 
-def _vec(t, dtype, numel: int, what: str) -> int:
+def _vec(t, dtype, numel: int, what: str, dev: int) -> int:
     """The address of a device array that the C ABI reads by pointer alone."""
-    if not t.is_cuda:
-        raise ValueError("device entry points take GPU tensors")
+    if t.get_device() != dev:
+        _refuse_device(t.get_device())
     _check_vec(t, dtype, numel, what)
     return t.data_ptr()
 
@@ -78,17 +88,11 @@ def _fresh(t, d: Tensor):
     return o, Tensor(o.data_ptr(), d.dtype, 0, d.rows, d.cols)
 
 
-def _check_device(*ts):
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("device entry points take GPU tensors")
+def _ref(desc, t, dev: int):
+    return None if t is None else byref(desc(t, dev))
 
 
-def _ref(desc, t):
-    return None if t is None else byref(desc(t))
-
-
-def _out(t, desc, like, d: Tensor):
+def _out(t, desc, like, d: Tensor, dev: int):
     """An output and the reference to its view: t itself, a new tensor like
     ``like`` (whose view is d) for True, or neither for None."""
     if t is None:
@@ -96,17 +100,30 @@ def _out(t, desc, like, d: Tensor):
     if t is True:
         t, v = _fresh(like, d)
         return t, byref(v)
-    return t, byref(desc(t))
+    return t, byref(desc(t, dev))
 
 
-def _handle(t):
-    """The handle of the current stream of t's device."""
-    return _raw_stream(t.get_device())
+def _given_workspace(workspace, dev: int):
+    """Address and bytes of a caller's workspace."""
+    if workspace.get_device() != dev:
+        _refuse_device(workspace.get_device())
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _on(stream, call, *args):
-    """The call with ``stream`` as the current one, its allocations too."""
+def _on(stream, t, call, *args):
+    """The call with the GPU of its tensor t as the current device and, when it
+    is given, ``stream`` as the current one, its allocations too."""
     torch = _torch or _setup()
+    dev = t.get_device()
+    if dev < 0:
+        _refuse_device(dev)
+    if stream is None:
+        with torch.cuda.device(dev):
+            return call(*args)
+    if stream.device_index != dev:
+        raise ValueError("the stream and the tensors of a call must be on one GPU")
     with torch.cuda.stream(stream):
         return call(*args)
 
@@ -117,23 +134,25 @@ def layernorm_forward(x, gamma, beta=None, eps: float = 1e-5, y=None, mean=None,
     (y, mean, rstd).  ``x`` is [M][K] bf16 or float32, ``gamma`` and ``beta``
     (may be None) are [K] of x's dtype or float32; mean and rstd, float32 [M],
     are what :func:`layernorm_backward` takes."""
-    if stream is not None:
-        return _on(stream, layernorm_forward, x, gamma, beta, eps, y, mean, rstd)
     torch = _torch or _setup()
-    tx = _matrix(x)
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _on(stream, x, layernorm_forward, x, gamma, beta, eps, y, mean, rstd)
+    tx = _matrix(x, dev)
     M = tx.rows
-    y, ry = _out(True if y is None else y, _matrix, x, tx)
+    y, ry = _out(True if y is None else y, _matrix, x, tx, dev)
     if mean is None:
         mean = torch.empty((M,), dtype=torch.float32, device=x.device)
         pm = mean.data_ptr()
     else:
-        pm = _vec(mean, torch.float32, M, "mean")
+        pm = _vec(mean, torch.float32, M, "mean", dev)
     if rstd is None:
         rstd = torch.empty_like(mean)
         pr = rstd.data_ptr()
     else:
-        pr = _vec(rstd, torch.float32, M, "rstd")
-    st = load().ss1_layernorm_forward(byref(tx), byref(_row(gamma)), _ref(_row, beta), eps, ry, pm, pr, _handle(x))
+        pr = _vec(rstd, torch.float32, M, "rstd", dev)
+    st = load().ss1_layernorm_forward(byref(tx), byref(_row(gamma, dev)), _ref(_row, beta, dev), eps, ry, pm, pr,
+                                      _raw_stream(dev))
     if st:
         _check(st, "ss1_layernorm_forward")
     return y, mean, rstd
@@ -143,27 +162,28 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dx=True, dgamma=True, dbeta=Tru
     """Gradients of layer norm (ss1_layernorm_backward): returns (dx, dgamma,
     dbeta); pass None for one that is not wanted, True to allocate it.  mean
     and rstd are what the forward returned."""
-    if stream is not None:
-        return _on(stream, layernorm_backward, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
     torch = _torch or _setup()
-    tx, tg = _matrix(x), _row(gamma)
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _on(stream, x, layernorm_backward, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
+    tx, tg = _matrix(x, dev), _row(gamma, dev)
     M = tx.rows
-    dx, rdx = _out(dx, _matrix, x, tx)
-    dgamma, rdg = _out(dgamma, _row, gamma, tg)
-    dbeta, rdb = _out(dbeta, _row, gamma, tg)
+    dx, rdx = _out(dx, _matrix, x, tx, dev)
+    dgamma, rdg = _out(dgamma, _row, gamma, tg, dev)
+    dbeta, rdb = _out(dbeta, _row, gamma, tg, dev)
     lib = load()
     wp, wb = None, 0
     if dgamma is not None or dbeta is not None:
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib.ss1_layernorm_backward_query(byref(tx), byref(n)), "ss1_layernorm_backward_query")
-            workspace, wb = torch.empty((n.value,), dtype=torch.uint8, device=x.device), n.value
+            workspace = torch.empty((n.value,), dtype=torch.uint8, device=x.device)
+            wp, wb = workspace.data_ptr(), n.value
         else:
-            _check_device(workspace)
-            wb = workspace.numel() * workspace.element_size()
-        wp = workspace.data_ptr()
-    st = lib.ss1_layernorm_backward(byref(_matrix(dy)), byref(tx), byref(tg), _vec(mean, torch.float32, M, "mean"),
-                                    _vec(rstd, torch.float32, M, "rstd"), rdx, rdg, rdb, wp, wb, _handle(x))
+            wp, wb = _given_workspace(workspace, dev)
+    st = lib.ss1_layernorm_backward(byref(_matrix(dy, dev)), byref(tx), byref(tg),
+                                    _vec(mean, torch.float32, M, "mean", dev),
+                                    _vec(rstd, torch.float32, M, "rstd", dev), rdx, rdg, rdb, wp, wb, _raw_stream(dev))
     if st:
         _check(st, "ss1_layernorm_backward")
     return dx, dgamma, dbeta
@@ -187,7 +207,9 @@ class AdapterSet:
     def make(cls, A, B, ranks, scale):
         """``ranks`` and ``scale`` are host sequences, one value an adapter."""
         torch = _torch or _setup()
-        _check_device(A, B)
+        dev = A.get_device()
+        if dev < 0 or B.get_device() != dev:
+            _refuse_device(min(dev, B.get_device()))
         ranks = tuple(int(r) for r in ranks)
         if any(r < 0 or r > MAX_RANK for r in ranks):
             raise ValueError(f"ranks must be 0 to {MAX_RANK}")
@@ -201,33 +223,34 @@ class AdapterSet:
 
     def __setattr__(self, name, value):
         self.__dict__[name] = value
-        self.__dict__["_view"] = (None, None)
+        self.__dict__["_view"] = (None, None, -1)
 
     def __getstate__(self):
         # without the view: a copy has memory of its own
-        return {**self.__dict__, "_view": (None, None)}
+        return {**self.__dict__, "_view": (None, None, -1)}
 
-    def _struct(self) -> Adapters:
-        """The C ABI's view of the set, made and checked again when an attribute,
-        the memory of a tensor or the sizes, type or layout of a factor changed."""
+    def _struct(self, dev: int) -> Adapters:
+        """The C ABI's view of the set for a call on GPU ``dev``, made and checked
+        again when an attribute, the memory of a tensor or the sizes, type or
+        layout of a factor changed."""
         A, B, row, scale = self.A, self.B, self.row, self.scale
         now = (A.data_ptr(), A.shape, A.dtype, A.is_contiguous(), B.data_ptr(), B.shape, B.dtype, B.is_contiguous(),
                row.data_ptr(), scale.data_ptr())
-        seen, ad = self._view
-        if seen != now:
+        seen, ad, place = self._view
+        if seen != now or place != dev:
             count, torch = len(self.ranks), _torch or _setup()
-            ad = Adapters(_matrix(A), _matrix(B), _vec(row, torch.int32, count + 1, "row"),
-                          _vec(scale, torch.float32, count, "scale"), count, self.max_rank)
-            self.__dict__["_view"] = (now, ad)
+            ad = Adapters(_matrix(A, dev), _matrix(B, dev), _vec(row, torch.int32, count + 1, "row", dev),
+                          _vec(scale, torch.float32, count, "scale", dev), count, self.max_rank)
+            self.__dict__["_view"] = (now, ad, dev)
         return ad
 
 
-def _segments(seg, seg_adapter) -> Segments:
+def _segments(seg, seg_adapter, dev: int) -> Segments:
     S, i32 = seg_adapter.numel(), _torch.int32
-    return Segments(_vec(seg, i32, S + 1, "seg"), _vec(seg_adapter, i32, S, "seg_adapter"), S, 0)
+    return Segments(_vec(seg, i32, S + 1, "seg", dev), _vec(seg_adapter, i32, S, "seg_adapter", dev), S, 0)
 
 
-def _workspace(workspace, query, M: int, ad: Adapters, x, where: str):
+def _workspace(workspace, query, M: int, ad: Adapters, x, dev: int, where: str):
     if workspace is None:
         n = ctypes.c_size_t(0)
         st = query(M, byref(ad), byref(n))
@@ -235,8 +258,7 @@ def _workspace(workspace, query, M: int, ad: Adapters, x, where: str):
             _check(st, where)
         workspace = _torch.empty((n.value,), dtype=_torch.uint8, device=x.device)
         return workspace, workspace.data_ptr(), n.value
-    _check_device(workspace)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, *_given_workspace(workspace, dev)
 
 
 def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None, v=None, save_v: bool = False,
@@ -248,17 +270,18 @@ def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None
     none) are device tensors; ``base`` is the projection's output, or None for
     zero, and ``y`` may be base itself.  v = x A_e^T, float32 [M][max_rank], is
     what :func:`adapter_backward` takes: None unless given or ``save_v``."""
-    if stream is not None:
-        return _on(stream, adapter_forward, x, adapters, seg, seg_adapter, base, y, v, save_v, workspace)
     torch = _torch or _setup()
-    tx, ad, lib = _matrix(x), adapters._struct(), load()
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _on(stream, x, adapter_forward, x, adapters, seg, seg_adapter, base, y, v, save_v, workspace)
+    tx, ad, lib = _matrix(x, dev), adapters._struct(dev), load()
     M = tx.rows
     rbase = None
     if base is not None:
-        tb = _matrix(base)
+        tb = _matrix(base, dev)
         rbase = byref(tb)
     if y is not None:
-        ry = byref(_matrix(y))
+        ry = byref(_matrix(y, dev))
     elif base is not None:
         y, ty = _fresh(base, tb)
         ry = byref(ty)
@@ -267,9 +290,10 @@ def adapter_forward(x, adapters: AdapterSet, seg, seg_adapter, base=None, y=None
         ry = byref(Tensor(y.data_ptr(), tx.dtype, 0, M, ad.B.cols))
     if v is None and save_v:
         v = torch.empty((M, adapters.max_rank), dtype=torch.float32, device=x.device)
-    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_forward_query, M, ad, x, "ss1_adapter_forward_query")
-    st = lib.ss1_adapter_forward(byref(tx), byref(ad), byref(_segments(seg, seg_adapter)), rbase, ry,
-                                 _ref(_matrix, v), wp, wb, _handle(x))
+    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_forward_query, M, ad, x, dev,
+                                   "ss1_adapter_forward_query")
+    st = lib.ss1_adapter_forward(byref(tx), byref(ad), byref(_segments(seg, seg_adapter, dev)), rbase, ry,
+                                 _ref(_matrix, v, dev), wp, wb, _raw_stream(dev))
     if st:
         _check(st, "ss1_adapter_forward")
     return y, v
@@ -282,18 +306,20 @@ def adapter_backward(dy, x, v, adapters: AdapterSet, seg, seg_adapter, dx_base=N
     ``v`` is what the forward returned with ``save_v`` (needed for dB only);
     ``dx_base`` is the projection's own input gradient (ss1.backward's dx), to
     which the adapters' is added, and dx may be dx_base itself."""
-    if stream is not None:
-        return _on(stream, adapter_backward, dy, x, v, adapters, seg, seg_adapter, dx_base, dx, dA, dB, workspace)
     _torch or _setup()
-    tx, ad, lib = _matrix(x), adapters._struct(), load()
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _on(stream, x, adapter_backward, dy, x, v, adapters, seg, seg_adapter, dx_base, dx, dA, dB, workspace)
+    tx, ad, lib = _matrix(x, dev), adapters._struct(dev), load()
     M = tx.rows
-    dx, rdx = _out(dx, _matrix, x, tx)
-    dA, rdA = _out(dA, _matrix, adapters.A, ad.A)
-    dB, rdB = _out(dB, _matrix, adapters.B, ad.B)
-    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_backward_query, M, ad, x, "ss1_adapter_backward_query")
-    st = lib.ss1_adapter_backward(byref(_matrix(dy)), byref(tx), _ref(_matrix, v), byref(ad),
-                                  byref(_segments(seg, seg_adapter)), _ref(_matrix, dx_base), rdx, rdA, rdB, wp, wb,
-                                  _handle(x))
+    dx, rdx = _out(dx, _matrix, x, tx, dev)
+    dA, rdA = _out(dA, _matrix, adapters.A, ad.A, dev)
+    dB, rdB = _out(dB, _matrix, adapters.B, ad.B, dev)
+    workspace, wp, wb = _workspace(workspace, lib.ss1_adapter_backward_query, M, ad, x, dev,
+                                   "ss1_adapter_backward_query")
+    st = lib.ss1_adapter_backward(byref(_matrix(dy, dev)), byref(tx), _ref(_matrix, v, dev), byref(ad),
+                                  byref(_segments(seg, seg_adapter, dev)), _ref(_matrix, dx_base, dev), rdx, rdA, rdB,
+                                  wp, wb, _raw_stream(dev))
     if st:
         _check(st, "ss1_adapter_backward")
     return dx, dA, dB
@@ -371,12 +397,16 @@ class AdamWPlan:
         numel = [p.numel() for p in params]
         blocks = [-(-k // ADAMW_BLOCK) for k in numel]
 
+        dev = params[0].get_device() if params else 0
+        if dev < 0:
+            _refuse_device(dev)
+
         def column(name, ts, what, dtype, sizes):
             """The tensors' addresses into one field of the table."""
             for t, k in zip(ts, sizes):
-                if not t.is_cuda or not t.is_contiguous() or t.numel() != k or (dtype is not None and t.dtype != dtype):
-                    _check_device(t)
-                    _check_vec(t, dtype or t.dtype, k, what)
+                if t.get_device() != dev or not t.is_contiguous() or t.numel() != k or (
+                        dtype is not None and t.dtype != dtype):
+                    _vec(t, dtype or t.dtype, k, what, dev)
             rows[name] = [t.data_ptr() for t in ts]
 
         if any(not p.is_contiguous() for p in params):
@@ -393,9 +423,7 @@ class AdamWPlan:
         if masters is not None:
             has = [i for i, t in enumerate(masters) if t is not None]
             for i in has:
-                _check_device(masters[i])
-                _check_vec(masters[i], torch.float32, numel[i], "master")
-                rows["master"][i] = masters[i].data_ptr()
+                rows["master"][i] = _vec(masters[i], torch.float32, numel[i], "master", dev)
         if eight:
             column("m_scale", m_scales, "m_scale", torch.float32, blocks)
             column("v_scale", v_scales, "v_scale", torch.float32, blocks)
@@ -420,12 +448,15 @@ class AdamWPlan:
         float32 GPU tensor of one element (a clip coefficient that the host
         has not seen); ``seed``, another each step, feeds the stochastic
         rounding of 8-bit states and of bf16 params without masters."""
-        scale, dev = grad_scale, None
+        dev = self.entries.get_device()
+        if stream is not None or dev < 0 or dev != _current_device():
+            return _on(stream, self.entries, self.step, step, lr, beta1, beta2, eps, grad_scale, seed)
+        scale, on_device = grad_scale, None
         if not isinstance(grad_scale, (int, float)):
-            scale, dev = 1.0, _vec(grad_scale, _torch.float32, 1, "grad_scale")
-        h = AdamWHyper(lr, beta1, beta2, eps, scale, dev, step, int(seed) & (2**64 - 1))
+            scale, on_device = 1.0, _vec(grad_scale, _torch.float32, 1, "grad_scale", dev)
+        h = AdamWHyper(lr, beta1, beta2, eps, scale, on_device, step, int(seed) & (2**64 - 1))
         st = load().ss1_adamw_step(self.entries.data_ptr(), self.count, self.map.data_ptr(), self.chunks, byref(h),
-                                   _handle(self.entries) if stream is None else stream.cuda_stream)
+                                   _raw_stream(dev))
         if st:
             _check(st, "ss1_adamw_step")
 

@@ -50,9 +50,9 @@ def test_other_memory_of_each_tensor():
 
 def test_values_written_in_place_need_no_new_view():
     s, call = used_set()
-    y, view = call(), s._struct()
+    y, view = call(), s._struct(0)
     s.scale.mul_(3)
-    assert s._struct() is view and torch.equal(call(), call(fresh(s))) and not torch.equal(call(), y)
+    assert s._struct(0) is view and torch.equal(call(), call(fresh(s))) and not torch.equal(call(), y)
 
 
 def test_a_transposed_factor_is_refused():
@@ -84,11 +84,11 @@ def test_a_set_made_by_hand_is_checked():
                           (dict(ranks=(8, 4, 4)), "row must hold 4")):
         fields = {k: getattr(s, k) for k in ("A", "B", "row", "scale", "max_rank", "ranks")}
         with pytest.raises(ValueError, match=error):
-            ss1.AdapterSet(**{**fields, **change})._struct()  # the view alone: nothing is launched
+            ss1.AdapterSet(**{**fields, **change})._struct(0)  # the view alone: nothing is launched
     for name, value in (("row", s.row.long()), ("scale", s.scale.cpu())):
         was = getattr(s, name)
         setattr(s, name, value)
         with pytest.raises(ValueError):
-            s._struct()
+            s._struct(0)
         setattr(s, name, was)
     call()

@@ -28,6 +28,7 @@
 
 #include <algorithm>
 
+#include "ss1_adapter_list.h"
 #include "ss1_device.h"
 #include "ss1_dma.h"
 #include "ss1_ops.h"
@@ -228,7 +229,7 @@ __device__ __forceinline__ int4 block_scan(int4 v, int4* sums, int4* total) {
 // 1024 + 64 bytes.
 __device__ void plan_outer(const AdapterView& ad, const OuterPlan& plan, int* lds) {
     int4* sums = reinterpret_cast<int4*>(lds + kThreads);
-    int4 done = make_int4(0, 0, 0, 0);  // entries, slots, adapters with several parts
+    PlanSums done{0, 0, 0};
     for (int e0 = 0; e0 < ad.E; e0 += kThreads) {
         __syncthreads();
         lds[threadIdx.x] = 0;
@@ -238,22 +239,22 @@ __device__ void plan_outer(const AdapterView& ad, const OuterPlan& plan, int* ld
             if (e >= 0 && e < kThreads && e0 + e < ad.E && n > 0) atomicAdd(lds + e, n);
         }
         __syncthreads();
-        const int e = e0 + threadIdx.x, tokens = lds[threadIdx.x];
-        int parts = e < ad.E ? max(1, (tokens + plan.P - 1) / plan.P) : 0;
-        if (parts > plan.slots) parts = 1;  // (offsets out of order)
+        const int e = e0 + threadIdx.x, tokens = clampi(lds[threadIdx.x], 0, ad.M);
+        const int parts = e < ad.E ? parts_of(tokens, plan.P) : 0;
         int4 total;
         const int4 in = make_int4(parts, parts > 1 ? parts : 0, parts > 1, 0), end = block_scan(in, sums, &total);
-        const int q = done.x + end.x - in.x, slot = done.y + end.y - in.y, c = done.z + end.z - in.z;
+        const int q = done.entries + end.x - in.x, slot = done.slots + end.y - in.y, c = done.several + end.z - in.z;
+        // (there is room for all of them unless the offsets are out of order)
         const bool several = parts > 1 && slot + parts <= plan.slots;
         for (int i = 0; i < parts; ++i)
             if (q + i < plan.most)
-                plan.table[q + i] = several ? make_int4(e, i * plan.P, min(tokens, (i + 1) * plan.P), slot + i)
+                plan.table[q + i] = several ? make_int4(e, i * plan.P, part_end(tokens, plan.P, i), slot + i)
                                             : make_int4(i == 0 ? e : -1, 0, tokens, -1);
         if (parts > 1) plan.multi[1 + c] = several ? make_int4(e, parts, slot, 0) : make_int4(e, 0, 0, 0);
-        done = make_int4(done.x + total.x, done.y + total.y, done.z + total.z, 0);
+        done = plan_add(done, {total.x, total.y, total.z}, plan.most, plan.slots);
     }
-    for (int q = done.x + threadIdx.x; q < plan.most; q += kThreads) plan.table[q] = make_int4(-1, 0, 0, -1);
-    if (threadIdx.x == 0) plan.multi[0] = make_int4(done.z, 0, 0, 0);
+    for (int q = done.entries + threadIdx.x; q < plan.most; q += kThreads) plan.table[q] = make_int4(-1, 0, 0, -1);
+    if (threadIdx.x == 0) plan.multi[0] = make_int4(done.several, 0, 0, 0);
 }
 
 __global__ __launch_bounds__(kThreads) void plan_outer_kernel(AdapterView ad, OuterPlan plan) {
@@ -1151,27 +1152,30 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) {
                 const int o = __shfl_up(sum, off);
-                if (lane >= off) sum += o;
+                if (lane >= off) sum = add_capped(sum, o, ad.M);
             }
+            const int up = __shfl_up(sum, 1);
             __syncthreads();
             if (lane == 63) wave_sum[wave] = sum;
             __syncthreads();
             int before = 0, total = 0;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                if (w < wave) before += wave_sum[w];
-                total += wave_sum[w];
+                if (w < wave) before = add_capped(before, wave_sum[w], ad.M);
+                total = add_capped(total, wave_sum[w], ad.M);
             }
-            ends[threadIdx.x] = sum + before;
-            starts[threadIdx.x] = b - (sum + before - n);  // token = starts + place in the list
+            const ListRun run = list_run(b, n, add_capped(before, lane > 0 ? up : 0, ad.M), ad.M);
+            ends[threadIdx.x] = run.end;
+            starts[threadIdx.x] = run.start;
             total = __builtin_amdgcn_readfirstlane(total);
             const int from = max(0, part_from - listed), to = min(total, part_to - listed);
-            listed += total;
+            listed = add_capped(listed, total, ad.M);
             for (int w0 = from; w0 < to;) {
                 __syncthreads();
-                const int at = w0 + 4 * threadIdx.x;
+                const int skip = 4 * threadIdx.x, left = to - w0 - skip;
                 int t[4] = {-1, -1, -1, -1};
-                if (at < to) {
+                if (left > 0) {
+                    const int at = w0 + skip;
                     int lo = 0, hi = kThreads - 1;  // the first segment whose end is past `at`
                     while (lo < hi) {
                         const int mid = (lo + hi) / 2;
@@ -1179,7 +1183,7 @@ __global__ __launch_bounds__(kThreads, 2) void outer_kernel(AdapterView ad, Oute
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (at + i < to) {
+                        if (i < left) {
                             while (ends[lo] <= at + i) ++lo;  // to <= ends[kThreads - 1]
                             t[i] = starts[lo] + at + i;
                         }

@@ -606,8 +606,8 @@ typedef struct {
  * infinity or a NaN in a token's x reaches that token's y alone; one in A or B
  * may come out as either, in the tokens of its adapter alone.
  * Requirements: K and N multiples of 8 (BF16) or 4 (F32), below 2^22;
- * M < 2^31; x, A, B, base, y, v 16-byte aligned, index and scale arrays
- * 4-byte aligned.  M == 0 enqueues nothing; R == 0 (no adapter rows) and
+ * M < 2^31, fewer than 2^30 segments and adapters; x, A, B, base, y, v
+ * 16-byte aligned, index and scale arrays 4-byte aligned.  M == 0 enqueues nothing; R == 0 (no adapter rows) and
  * segments.count == 0 leave y = base.
  * Index arrays that break the rules above leave y unspecified, but nothing
  * outside the buffers is touched.

@@ -16,6 +16,9 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxCols = int64_t(1) << 24;
 // 128 rows of an adapter or 64 of x stay within 2^31 bytes
 constexpr int64_t kMaxAdapterCols = int64_t(1) << 22;
+// segments plus M / 16 tiles of tokens, and adapters plus the parts of the outer
+// products, are numbered in 32 bits
+constexpr int32_t kMaxCount = int32_t(1) << 30;
 
 // x of a layer norm: sizes and dtype.
 ss1_status check_norm_x(const ss1_tensor* x) {
@@ -140,7 +143,7 @@ ss1_status check_adapters(const ss1_adapters* ad, bool data) {
     const int64_t unit = A.dtype == SS1_BF16 ? 8 : 4;
     for (const int64_t n : {A.cols, B.cols})
         if (n < unit || n >= kMaxAdapterCols || n % unit) return SS1_ERR_SHAPE;
-    if (ad->count < 0 || ad->max_rank < 0 || ad->max_rank > SS1_MAX_RANK) return SS1_ERR_SHAPE;
+    if (ad->count < 0 || ad->count >= kMaxCount || ad->max_rank < 0 || ad->max_rank > SS1_MAX_RANK) return SS1_ERR_SHAPE;
     if (!data) return SS1_OK;
     if (A.rows > 0 && (!A.data || !B.data)) return SS1_ERR_NULL;
     if (!ad->row || (ad->count > 0 && !ad->scale)) return SS1_ERR_NULL;
@@ -151,7 +154,7 @@ ss1_status check_adapters(const ss1_adapters* ad, bool data) {
 
 ss1_status check_segments(const ss1_segments* s) {
     if (!s) return SS1_ERR_NULL;
-    if (s->reserved != 0 || s->count < 0) return SS1_ERR_SHAPE;
+    if (s->reserved != 0 || s->count < 0 || s->count >= kMaxCount) return SS1_ERR_SHAPE;
     if (s->count > 0 && (!s->offset || !s->adapter)) return SS1_ERR_NULL;
     if (!aligned(s->offset, 4) || !aligned(s->adapter, 4)) return SS1_ERR_ALIGN;
     return SS1_OK;

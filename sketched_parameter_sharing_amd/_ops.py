@@ -442,19 +442,21 @@ class AdamWPlan:
                    masters, decay)
 
     def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-             grad_scale=1.0, seed: int = 0, stream=None):
+             grad_scale=1.0, seed: int | None = None, stream=None):
         """One step over every tensor, in place (ss1_adamw_step).  ``step``
         counts from 1; ``grad_scale`` multiplies the gradients: a number, or a
         float32 GPU tensor of one element (a clip coefficient that the host
-        has not seen); ``seed``, another each step, feeds the stochastic
-        rounding of 8-bit states and of bf16 params without masters."""
+        has not seen); ``seed``, another each step (``step`` itself when None),
+        feeds the stochastic rounding of 8-bit states and of bf16 params without
+        masters.  These are values of the call: a captured graph replays the
+        step, the rate and the random bits that it was captured with."""
         dev = self.entries.get_device()
         if stream is not None or dev < 0 or dev != _current_device():
             return _on(stream, self.entries, self.step, step, lr, beta1, beta2, eps, grad_scale, seed)
         scale, on_device = grad_scale, None
         if not isinstance(grad_scale, (int, float)):
             scale, on_device = 1.0, _vec(grad_scale, _torch.float32, 1, "grad_scale", dev)
-        h = AdamWHyper(lr, beta1, beta2, eps, scale, on_device, step, int(seed) & (2**64 - 1))
+        h = AdamWHyper(lr, beta1, beta2, eps, scale, on_device, step, int(step if seed is None else seed) & (2**64 - 1))
         st = load().ss1_adamw_step(self.entries.data_ptr(), self.count, self.map.data_ptr(), self.chunks, byref(h),
                                    _raw_stream(dev))
         if st:

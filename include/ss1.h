@@ -711,6 +711,8 @@ typedef struct {
  *     block's maximum; the block's other elements are as without it.
  * Random bits: SplitMix64 (as in ss1_plan) of seed and (entry, element) pairs,
  * so equal calls give equal bits; a caller passes another seed each step.
+ * hyper is read by the host during the call: a captured graph replays the step,
+ * the rate and the random bits that it was captured with.
  *   entries, map : DEVICE copies of ss1_adamw_plan's arrays; count, chunks as
  *                  there (map items outside the entries are skipped)
  * chunks == 0 enqueues nothing.

@@ -9,8 +9,10 @@
 //
 // The step is one pass over the data, bound by HBM: 118M bf16 elements with
 // float32 masters, float32 states 28 bytes an element in 665 us (4.97 TB/s, a
-// large copy's rate), 8-bit states 16 bytes in 350 to 370 us (5.3 TB/s; the vector
-// instructions, 85 an element, take about 270).  400 tensors of 1.5M elements together take
+// large copy's rate), 8-bit states 16 bytes in 350 us (5.4 TB/s; the vector
+// instructions, 85 an element, take about 270).  bf16 elements without masters:
+// 22 bytes with float32 states in 497 us (5.2 TB/s), 10 bytes with 8-bit states in
+// 295 (4.0 TB/s: the instructions of the two roundings).  400 tensors of 1.5M elements together take
 // 12 us, of which about 8 are their 39 MB and the rest one chain of reads: item,
 // entry, data.  A block passes once over a chunk: with chunks of 2048 / 4096 /
 // 8192 elements the three took 673 / 671 / 699, 459 / 469 / 471 (in the slower

@@ -53,7 +53,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 
 __device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint4 v) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    // non-temporal: nothing here reads it again (prefill expand 66 -> 63 us)
+    // non-temporal: nothing in this call reads it again (117 MB of y, the expand 66
+    // -> 63 us; smaller outputs, and what a next reader of y pays, were not measured)
     __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.x, v.y, v.z, v.w}, r, voff, 0, 2);
 }
 
@@ -726,8 +727,9 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(AdapterView ad, con
 // for itself, in LDS, and goes on to its columns, so there is one launch in place
 // of two (a call of one token is bound by the host) and no v in memory between
 // them.  Every block of a piece reads the whole of its adapter's A, at about 25
-// bytes a ns, which sets where this holds.  One token of rank 16, 4096 -> 14336: 9.6
-// us, the lookup, A, B and the stores one after the other.
+// bytes a ns, which sets where this holds: the rate of its four waves with four units
+// in flight each (blocks of more waves were not tried).  One token of rank 16, 4096 ->
+// 14336: 9.3 us, the lookup, four rounds over A, B and the stores one after the other.
 template <typename T, int KU>
 __global__ __launch_bounds__(kThreads, 2) void one_kernel(
     AdapterView ad, const T* __restrict__ x, const T* __restrict__ A, const T* __restrict__ B, const T* base, T* y,
@@ -815,10 +817,12 @@ __device__ __forceinline__ void stage_columns(const float*, const uint4 (&rows)[
 // tile after it and the base of the next are in flight: one barrier a tile,
 // and registers for four blocks a compute unit.
 // Bound by base and y: 4096 tokens, N = 14336, bf16, 235 MB and the factors in 63
-// to 65 us, 3.7 TB/s (a copy of the same rows and tiles: 44 to 46).  The rest is
-// the blocks' start (v of the piece, the first rows of B) and pieces that a
-// segment's end cuts short; deeper prefetch, 8 vectors a tile and other numbers of
-// tiles a block all measured within 5%.
+// to 65 us, 3.7 TB/s (a copy of the same rows and tiles: 44 to 46).  186 MB are read
+// where base, B and the six slices of v are 134: the 14 blocks of a piece lie on all
+// eight XCDs, and each XCD fetches the slices for itself.  Beside that the blocks'
+// start (v of the piece, the first rows of B) and pieces that a segment's end cuts
+// short; deeper prefetch, 8 vectors a tile and other numbers of tiles a block all
+// measured within 5%.
 template <typename T, int KU>
 __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* part, size_t slice, int Q, int stride,
                                                  const T* B, const T* base, T* y, float* v_out, int v_stride,
@@ -1471,8 +1475,8 @@ OneSplit one_split(const AdapterArgs& a, int N) {
 }
 
 // Whether shrink and expand are one launch: an adapter's A is at most 128 KB (bf16;
-// float32, whose products take four instructions, 64), which a compute unit reads
-// in 5 us, and all blocks' reads of A at most 40 MB.  The host takes 14.1 us for
+// float32, whose products take four instructions, 64), which a block's four waves
+// read in 5 us, and all blocks' reads of A at most 40 MB.  The host takes 14.1 us for
 // a call of one token against 16.7.  On the device alone, one launch against two
 // in us, bf16 unless noted: 1 token of rank 8 1024 -> 4096 8.8 / 10.0, 64 tokens of
 // rank 32 1280 -> 5120 10.5 / 13.1, 256 requests of rank 16 2048 -> 2048 15.8 /

@@ -15,7 +15,8 @@
 //
 // 16384 x 4096 bf16: forward 55.9 us (269 MB, 4.8 TB/s), backward 79.6 + 4.9 us
 // for the join (403 MB, 5.1 TB/s in the first launch), a large copy 5.0 to 5.3.
-// 16 x 4096 forward 3.8 us and 1111 x 1283 float32 backward 11 us in one launch,
+// float32: 107 us and, in both launches together, 162 (5.0 TB/s).
+// 16 x 4096 forward 3.7 us and 1111 x 1283 float32 backward 11.6 us in one launch,
 // both below what the host takes for the calls.
 #include <hip/hip_runtime.h>
 
@@ -571,9 +572,11 @@ void forward(const NormArgs& a, hipStream_t s) {
                        static_cast<X*>(a.y), a.mean, a.rstd, a.M, a.K, a.eps);
 }
 
-// Rows and elements up to which the backward pass is one launch: a strip's block
-// reads its columns at about 25 bytes a ns, which passes the host's time for the
-// two launches there.  A call as the host makes it, one launch against two, in us,
+// Rows and elements up to which the backward pass is one launch, by the time of a
+// call that the host makes: there a strip's block of four waves reads its columns,
+// at about 25 bytes a ns, in the host's time for the two launches.  Where the device
+// alone counts (a captured graph, a queue that runs ahead) two launches are mostly
+// ahead from 1024 rows on.  A call as the host makes it, one launch against two, in us,
 // bf16 / float32: 512 x 768 14.8 / 14.4 against 18.2 / 18.4, 1024 x 4096 15.6 / 18.3
 // against 18.2 / 18.0, 1280 x 1283 15.1 / 14.1 against 18.1 / 18.2, 1280 x 4096 18.3 /
 // 22.2 against 18.5 / 20.6, 2048 x 2048 17.3 / 23.6 against 18.2.  On the device

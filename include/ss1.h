@@ -602,13 +602,14 @@ typedef struct {
  *          unspecified afterwards.  Calls that share it must be ordered.
  * Arithmetic: products of the inputs accumulated in float32; v stays float32
  * between the two products (bf16: as the sum of two bf16 values, an error of
- * at most 2^-17 of v); y rounded once.  Equal calls give equal bits.  An
- * infinity or a NaN in a token's x reaches that token's y alone; one in A or B
+ * at most 2^-17 of v); the sum over j starts at base (bf16) or at zero, with
+ * base added to it when it is done (F32); y rounded once.  Equal calls give
+ * equal bits.  An infinity or a NaN in a token's x reaches that token's y alone; one in A or B
  * may come out as either, in the tokens of its adapter alone.
  * Requirements: K and N multiples of 8 (BF16) or 4 (F32), below 2^22;
  * M < 2^31, fewer than 2^30 segments and adapters; x, A, B, base, y, v
- * 16-byte aligned, index and scale arrays 4-byte aligned.  M == 0 enqueues nothing; R == 0 (no adapter rows) and
- * segments.count == 0 leave y = base.
+ * 16-byte aligned, index and scale arrays 4-byte aligned.  M == 0 enqueues
+ * nothing; R == 0 (no adapter rows) and segments.count == 0 leave y = base.
  * Index arrays that break the rules above leave y unspecified, but nothing
  * outside the buffers is touched.
  * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE, SS1_ERR_DTYPE, SS1_ERR_ALIGN (before

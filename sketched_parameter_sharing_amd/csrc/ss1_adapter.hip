@@ -549,6 +549,27 @@ __device__ __forceinline__ uint4 pack(const float*, const f32x4 (&acc)[4], int i
                       __float_as_uint(acc[3][i]));
 }
 
+// Where the sums of a tile start.  bf16: at base, whose share of the roundings of up
+// to 128 products is far below the last one.  float32: at zero, and base is added to
+// the finished sum; rounding every partial sum at base's size cost three of float32's
+// bits where base is large beside the adapter's share.
+__device__ __forceinline__ void start_sums(const __bf16* t, const uint4 (&old)[4], f32x4 (&acc)[8], f32x4 (&)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack(t, old[i], i, acc);
+}
+__device__ __forceinline__ void start_sums(const float* t, const uint4 (&old)[4], f32x4 (&acc)[4], f32x4 (&last)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        unpack(t, old[i], i, last);
+        acc[i] = f32x4{0, 0, 0, 0};
+    }
+}
+__device__ __forceinline__ void end_sums(const __bf16*, f32x4 (&)[8], const f32x4 (&)[8]) {}
+__device__ __forceinline__ void end_sums(const float*, f32x4 (&acc)[4], const f32x4 (&last)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += last[j];
+}
+
 // First of the column tiles of block cg of `columns` (at most one a tile): shares
 // that differ by one tile at most (10 tiles in 3: 20.2 us, as 4 + 4 + 2 21.7).
 __device__ __forceinline__ int first_tile(int cg, int tiles, int columns) {
@@ -660,9 +681,8 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
     __syncthreads();
 #pragma unroll 1
     for (int tile = tile0; tile < tile0 + tiles; ++tile) {
-        f32x4 acc[U::kCols];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
+        f32x4 acc[U::kCols], last[U::kCols];
+        start_sums(B, old, acc, last);
         uint4 f[KU][U::kCols];
 #pragma unroll
         for (int k = 0; k < KU; ++k) {
@@ -678,6 +698,7 @@ __device__ __forceinline__ void expand_body(const Piece& pc, const float* part, 
 #pragma unroll
                 for (int j = 0; j < U::kCols; ++j) acc[j] = mma(B, a, f[k][j], acc[j]);
             }
+        end_sums(B, acc, last);
         uint32_t at = 4 * g * Nb + column(tile);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -924,9 +945,8 @@ __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* p
         fetch_rows(column(tile + 2));
         uint4 next[4];
         fetch_base(column(tile + 1), next);
-        f32x4 acc[U::kCols];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack(B, old[i], i, acc);
+        f32x4 acc[U::kCols], last[U::kCols];
+        start_sums(B, old, acc, last);
         const uint4* bc = bt + cur * BUF + lane;
 #pragma unroll
         for (int k = 0; k < KU; ++k)
@@ -936,6 +956,7 @@ __device__ __forceinline__ void expand_tile_body(const Piece& pc, const float* p
 #pragma unroll
                 for (int h = 0; h < U::kFrags; ++h) acc[j] = mma(B, va[k][h], f, acc[j]);
             }
+        end_sums(B, acc, last);
         uint32_t at = (16 * wave + 4 * g) * Nb + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

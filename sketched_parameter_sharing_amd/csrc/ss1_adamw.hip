@@ -230,7 +230,7 @@ __device__ __forceinline__ void quantize8(uint8_t* codes, float* scales, int64_t
             if (!finite(t[j])) r[j] = NAN;
     if (!ROOT)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) r[j] = copysignf(r[j], q[j]);
+        for (int j = 0; j < kVec; ++j) r[j] = copysignf(r[j], t[j]);  // (the short quotient of -0 is +0)
     store8(codes, i, n, r);
 }
 

@@ -193,3 +193,19 @@ def test_random_rounding_near_the_ends_of_the_codes():
         with np.errstate(all="ignore"):
             for k, want in host_step(before, 0, fmt, 0.0, h).items():
                 assert same(host(d[k][0]), want), (seed, k)
+
+
+@pytest.mark.parametrize("beta1", [0.0, 0.5])
+def test_zeros_keep_their_sign(beta1):
+    # moments of both zeros beside others: the codes are those of the formula's quotients
+    d = make((F, False, F, "fp8"), seed=5)
+    for t in d["m"]:
+        t.view(torch.uint8)[::3] &= 128
+    plan = ss1.AdamWPlan.make(**d)
+    h = dict(lr=1e-2, beta1=beta1, beta2=0.5, eps=1e-8, grad_scale=0.0, step=3, seed=11)
+    before = {k: None if ts is None else [host(t) for t in ts] for k, ts in d.items()}
+    plan.step(**h)
+    with np.errstate(all="ignore"):
+        for i, (n, size) in enumerate(SIZES):
+            for k, want in host_step(before, i, (F, False, F, "fp8"), 0.0, h).items():
+                assert same(host(d[k][i]), want), (i, n, size, k)

@@ -682,7 +682,9 @@ typedef struct {
  * work of a step over them: *chunks = the number of work items, and, when map
  * is not NULL, map[2*i], map[2*i+1] = item i's entry and its place there.
  * The caller copies the entries and the map to the device once; they hold
- * for as long as the tensors stay where they are.
+ * for as long as the tensors stay where they are.  What the entries' steps
+ * write (params, states, masters, scales) must not overlap: they run side by
+ * side.
  * Errors: SS1_ERR_NULL (a required pointer of an entry with numel > 0, or
  * scales that are missing), SS1_ERR_SHAPE (numel < 0 or >= 2^39, count
  * >= 2^23, a negative or not finite weight_decay, a master beside an F32

@@ -333,6 +333,22 @@ def _float_code(t, what: str) -> int:
     return code
 
 
+def _check_apart(rows, numel, blocks):
+    """What a step writes lies in separate memory: it is one launch, in which two
+    entries over the same bytes (a tied parameter listed twice, one tensor as both
+    states) would race."""
+    n, k = np.array(numel, dtype=np.int64), np.array(blocks, dtype=np.int64)
+    state = np.where(rows["state_dtype"] == FP8_E4M3, 1, 4)
+    spans = [(rows["param"], n * np.where(rows["param_dtype"] == F32, 4, 2)), (rows["m"], n * state),
+             (rows["v"], n * state), (rows["master"], n * 4), (rows["m_scale"], k * 4), (rows["v_scale"], k * 4)]
+    at = np.concatenate([a for a, _ in spans])
+    end = at + np.concatenate([b for _, b in spans]).astype(np.uint64)
+    used = np.flatnonzero((at != 0) & (end > at))
+    order = used[np.argsort(at[used], kind="stable")]
+    if (end[order[:-1]] > at[order[1:]]).any():
+        raise ValueError("params, states, masters and scales must not share memory")
+
+
 @dataclass
 class AdamWPlan:
     """An AdamW step over many tensors: the table of their addresses and the
@@ -431,6 +447,7 @@ class AdamWPlan:
         rows["param_dtype"] = [_float_code(p, "param") for p in params]
         rows["grad_dtype"] = [_float_code(g, "grad") for g in grads]
         rows["state_dtype"] = FP8_E4M3 if eight else F32
+        _check_apart(rows, numel, blocks)
         lib, chunks = load(), ctypes.c_int64(0)
         _check(lib.ss1_adamw_plan(table, n, byref(chunks), None), "ss1_adamw_plan")
         host_map = np.empty((max(chunks.value, 1), 2), dtype=np.int32)

@@ -727,6 +727,214 @@ ss1_status ss1_adamw_plan(const ss1_adamw_entry* entries, int32_t count, int64_t
 ss1_status ss1_adamw_step(const ss1_adamw_entry* entries, int32_t count, const int32_t* map, int64_t chunks,
                           const ss1_adamw_hyper* hyper, void* stream);
 
+/* One gradient of ss1_gradnorm; the memory is the caller's. */
+typedef struct {
+    void* grad;            /* DEVICE, numel values of dtype (written by ss1_gradnorm_clip alone) */
+    int64_t numel;
+    int32_t dtype;         /* SS1_F32 or SS1_BF16 */
+    int32_t reserved;      /* must be 0 */
+} ss1_gradnorm_entry;
+
+/*
+ * ss1_gradnorm_plan -- HOST.  Checks `count` entries (host array) and lists the
+ * work over them as ss1_adamw_plan does: *chunks = the number of work items
+ * and, when map is not NULL, map[2*i], map[2*i+1] = item i's entry and its
+ * place there.  The caller copies both to the device once.
+ * Errors: SS1_ERR_NULL (also an entry with numel > 0 and no grad),
+ * SS1_ERR_SHAPE (numel < 0 or >= 2^39, count >= 2^23, reserved not 0),
+ * SS1_ERR_DTYPE, SS1_ERR_ALIGN (grad 16-byte aligned).
+ *
+ * ss1_gradnorm_query -- HOST.  *bytes = the device workspace of the two calls
+ * below for a plan of `chunks` items (partial sums).
+ *
+ * ss1_gradnorm -- DEVICE, asynchronous on `stream`.  The 2-norm over all the
+ * elements of all the entries and the coefficient that clips it:
+ *   norm = sqrt(sum g^2)
+ *   coef = max_norm / norm where norm > max_norm (0 where norm is infinite),
+ *          1 where it is not, NaN where norm is NaN
+ *   norm, coef : DEVICE float[1], written; each may be NULL (not wanted).
+ *                coef is what ss1_adamw_step takes as grad_scale_dev
+ * ss1_gradnorm_clip -- the same, and every gradient is multiplied by the coef
+ * that is returned, in place: g = round(g * coef), float32 product, one
+ * rounding.  Where coef is 1 nothing is written.  Entries must not overlap.
+ *   entries, map : DEVICE copies of ss1_gradnorm_plan's arrays; count, chunks
+ *                  as there (map items outside the entries are skipped)
+ *   max_norm  : >= 0; infinity does not clip
+ *   workspace : DEVICE, 16-byte aligned, at least the queried bytes; contents
+ *               unspecified afterwards.  Calls that share it must be ordered.
+ * Arithmetic: squares and sums in float64 (exact squares, so no gradient that
+ * float32 holds overflows or vanishes), in a fixed order: equal calls give
+ * equal bits.  norm and coef are rounded to float32 once (a norm beyond its
+ * range is infinite there; coef still comes from the float64 norm).
+ * chunks == 0: norm 0 and coef 1.
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE (max_norm negative or NaN, a workspace
+ * that is too small), SS1_ERR_ALIGN (entries 8-byte, map, norm and coef
+ * 4-byte), SS1_ERR_HIP.
+ */
+ss1_status ss1_gradnorm_plan(const ss1_gradnorm_entry* entries, int32_t count, int64_t* chunks, int32_t* map);
+ss1_status ss1_gradnorm_query(int64_t chunks, size_t* bytes);
+ss1_status ss1_gradnorm(const ss1_gradnorm_entry* entries, int32_t count, const int32_t* map, int64_t chunks,
+                        double max_norm, float* norm, float* coef, void* workspace, size_t workspace_bytes,
+                        void* stream);
+ss1_status ss1_gradnorm_clip(const ss1_gradnorm_entry* entries, int32_t count, const int32_t* map, int64_t chunks,
+                             double max_norm, float* norm, float* coef, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* The tokens of a batch: their rows in an embedding table. */
+typedef struct {
+    const void* id;        /* DEVICE, count integers              */
+    int64_t count;
+    int32_t bytes;         /* 4 (int32) or 8 (int64) of each one  */
+    int32_t reserved;      /* must be 0 */
+} ss1_tokens;
+
+/*
+ * ss1_embedding_forward -- DEVICE, asynchronous on `stream`.  Rows of an
+ * embedding table, scaled:
+ *   y[m][k] = scale * E[id[m]][k];  zero for an id outside [0, V) (padding)
+ *   E : [V][K] F32 or BF16, V < 2^29, 1 <= K <= 2^16
+ *   y : [M][K] F32 or BF16 (E's dtype or the other), M = tokens.count; must
+ *       not overlap E
+ * Arithmetic: the product in float32, rounded once (a scale of 1 copies).
+ * E, y 16-byte aligned, ids aligned to their size.  M == 0 enqueues nothing.
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE (also a scale that is not finite),
+ * SS1_ERR_DTYPE, SS1_ERR_ALIGN (before any HIP call), SS1_ERR_HIP.
+ *
+ * ss1_embedding_backward_query -- HOST.  *bytes = the device workspace of
+ * ss1_embedding_backward for M tokens and a table [V][K] (descriptors; data is
+ * not read).
+ *
+ * ss1_embedding_backward -- DEVICE, asynchronous on `stream`.  The table's
+ * gradient:
+ *   dE[v][k] = scale * sum over m with id[m] == v of dy[m][k]   (accumulate 0)
+ *   dE[v][k] = dE[v][k] + that sum                              (accumulate 1)
+ *   dy : [M][K] F32 or BF16, read
+ *   dE : [V][K] F32 or BF16 (dy's dtype or the other); accumulate 0: written
+ *        whole, rows without tokens as zeros; accumulate 1 (the gradient of a
+ *        table that an output layer shares): rows without tokens are not
+ *        touched.  Must not overlap dy
+ *   workspace : DEVICE, 16-byte aligned, at least the queried bytes; contents
+ *        unspecified afterwards.  Calls that share it must be ordered.
+ * Ids outside [0, V) have no gradient.  Tokens are sorted by id (stably) and
+ * summed in float32 in a fixed order that depends on the ids, M, V and K
+ * alone, scaled, added to dE in float32 and rounded once: nothing is atomic
+ * across blocks, equal calls give equal bits.
+ * Requirements: as the forward, M < 2^31, M * K and V * K under 2^40.
+ * M == 0 leaves dE zero (accumulate 0) or as it is.
+ * Errors: as the forward; SS1_ERR_SHAPE for a workspace that is too small.
+ */
+ss1_status ss1_embedding_forward(const ss1_tokens* tokens, const ss1_tensor* E, float scale, ss1_tensor* y,
+                                 void* stream);
+ss1_status ss1_embedding_backward_query(const ss1_tokens* tokens, const ss1_tensor* dE, size_t* bytes);
+ss1_status ss1_embedding_backward(const ss1_tensor* dy, const ss1_tokens* tokens, float scale, int32_t accumulate,
+                                  ss1_tensor* dE, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Elements along the reduction that share one scale of a block-scaled matrix. */
+#define SS1_FP8_BLOCK 128
+
+/*
+ * A matrix [rows][cols] in E4M3 with a power-of-two scale for each block, the
+ * form that the gfx950 matrix instructions scale by themselves:
+ *   value[r][c] = e4m3(codes[r][c]) * 2^(scale[r / block][c / 128] - 127)
+ *   codes : [rows][Cp], Cp = cols rounded up to a multiple of 128; columns from
+ *           cols on hold zeros
+ *   scale : [ceil(rows / block)][Sp] bytes (E8M0), Sp = Cp / 128 rounded up to
+ *           a multiple of 4; bytes from Cp / 128 on are 127 (never used)
+ *   block : 1 (a scale for 128 elements of a row: activations, gradients) or
+ *           128 (one for a tile of 128 x 128: weights, whose transposed codes
+ *           then are the same codes)
+ */
+typedef struct {
+    void* codes;           /* DEVICE, 16-byte aligned */
+    uint8_t* scale;        /* DEVICE, 4-byte aligned  */
+    int64_t rows;
+    int64_t cols;
+    int32_t block;         /* 1 or 128 */
+    int32_t reserved;      /* must be 0 */
+} ss1_fp8_blocks;
+
+/*
+ * ss1_quantize_fp8_blocks -- DEVICE, asynchronous on `stream`.  x [R][C] (F32
+ * or BF16) as block-scaled E4M3, along its rows (q), along its columns (qt,
+ * the transposed matrix [C][R], blocks of 128 rows of x), or both in one pass
+ * over x; either may be NULL.  For every block
+ *   scale = the smallest power of two with max |x| / scale <= 448 (1 for a
+ *           block without a nonzero finite element; at least 2^-126)
+ *   code  = the E4M3 value nearest to x / scale, ties to even (the quotient is
+ *           exact, so this is the one rounding)
+ * An infinity or a NaN becomes E4M3's NaN and does not count in the maximum:
+ * it stays with its element.
+ *   q  : rows = R, cols = C;  qt : rows = C, cols = R;  block 1 or 128 each
+ * Requirements: R, C >= 0 and < 2^31, fewer than 2^24 tiles of 128 x 128; x
+ * 16-byte aligned.
+ * R == 0 or C == 0 enqueues nothing (there are no codes).
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE, SS1_ERR_DTYPE, SS1_ERR_ALIGN (before
+ * any HIP call), SS1_ERR_HIP.
+ */
+ss1_status ss1_quantize_fp8_blocks(const ss1_tensor* x, ss1_fp8_blocks* q, ss1_fp8_blocks* qt, void* stream);
+
+/*
+ * ss1_matmul_fp8_blocks_query -- HOST.  *bytes = the device workspace of
+ * ss1_matmul_fp8_blocks for a [M][K] and b [N][K] (partial sums where the
+ * reduction is split over blocks; data is not read).
+ *
+ * ss1_matmul_fp8_blocks -- DEVICE, asynchronous on `stream`.  The product of
+ * two block-scaled matrices along their common columns:
+ *   y[m][n] = sum over blocks t of 2^(ea + eb) * sum_{k in t} a[m][k] b[n][k]
+ *   a : [M][K];  b : [N][K] (cols equal);  y : [M][N] F32 or BF16, written
+ *   workspace : DEVICE, 16-byte aligned, at least the queried bytes; contents
+ *               unspecified afterwards (NULL where none is needed).  Calls
+ *               that share it must be ordered.
+ * Arithmetic, BF16 y: v_mfma_scale_f32_16x16x128_f8f6f4, one block of 128 each;
+ * the instruction keeps 18 bits below the largest product of a block (an error
+ * of up to 2^-17 of that product for each of the others), blocks are added in
+ * float32 and y is rounded once.  F32 y: bf16 matrix instructions (every code
+ * times its scale is a bf16 value down to 2^-126), exact products, float32
+ * sums.  K == 0 gives zeros.
+ * A NaN code gives NaN in its row of y (a) or its column (b).  Equal calls give
+ * equal bits.
+ * Requirements: M, N < 2^31, fewer than 2^22 tiles of 128 x 128 in y, K < 2^23.
+ * Errors: SS1_ERR_NULL, SS1_ERR_SHAPE, SS1_ERR_DTYPE, SS1_ERR_ALIGN (before
+ * any HIP call), SS1_ERR_HIP.
+ */
+ss1_status ss1_matmul_fp8_blocks_query(const ss1_fp8_blocks* a, const ss1_fp8_blocks* b, size_t* bytes);
+ss1_status ss1_matmul_fp8_blocks(const ss1_fp8_blocks* a, const ss1_fp8_blocks* b, ss1_tensor* y, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * A dense layer in block-scaled E4M3, for the layers of a model that are not
+ * projected (the SS1 summary page, "Key results": Llama-3-8B layers are
+ * projected selectively, the others stay dense).
+ *
+ * ss1_dense_forward_fp8 -- DEVICE, asynchronous on `stream`.  y = x W^T:
+ *   x  : [M][K] F32 or BF16, quantised along its rows (blocks of 1 x 128)
+ *   w  : [N][K] block-scaled (ss1_quantize_fp8_blocks of the weight)
+ *   y  : [M][N], x's dtype, written; must not overlap x
+ *   xt : x quantised along its columns, [K][M] with block 1, written: what
+ *        ss1_dense_backward_fp8 takes.  NULL: not wanted
+ *   workspace : as ss1_matmul_fp8_blocks, by ss1_dense_forward_fp8_query
+ *
+ * ss1_dense_backward_fp8 -- DEVICE, asynchronous on `stream`.  Its gradients
+ * for an upstream dy, quantised along its rows for dx and its columns for dW:
+ *   dx = dy W,  dW = dy^T x
+ *   dy : [M][N] F32 or BF16
+ *   xt : [K][M] as the forward wrote it (read for dW only)
+ *   wt : [K][N] block-scaled: the weight quantised along its columns (read for
+ *        dx only)
+ *   dx : [M][K], dy's dtype, written (NULL: not computed)
+ *   dW : [N][K], F32 or BF16, written (NULL: not computed); zero for M == 0
+ * Each step is as the calls above define it (the same codes, the same product).
+ * Errors: as the calls above.
+ */
+ss1_status ss1_dense_forward_fp8_query(const ss1_tensor* x, const ss1_fp8_blocks* w, size_t* bytes);
+ss1_status ss1_dense_forward_fp8(const ss1_tensor* x, const ss1_fp8_blocks* w, ss1_tensor* y, ss1_fp8_blocks* xt,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+ss1_status ss1_dense_backward_fp8_query(const ss1_tensor* dy, const ss1_fp8_blocks* xt, const ss1_fp8_blocks* wt,
+                                        size_t* bytes);
+ss1_status ss1_dense_backward_fp8(const ss1_tensor* dy, const ss1_fp8_blocks* xt, const ss1_fp8_blocks* wt,
+                                  ss1_tensor* dx, ss1_tensor* dW, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

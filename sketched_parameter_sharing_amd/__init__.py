@@ -33,6 +33,16 @@ from ._lib import (  # noqa: F401
     sketch,
     version,
 )
+from ._model_ops import (  # noqa: F401
+    Fp8Blocks,
+    GradNormPlan,
+    dense_backward_fp8,
+    dense_forward_fp8,
+    embedding_backward,
+    embedding_forward,
+    matmul_fp8_blocks,
+    quantize_fp8_blocks,
+)
 from ._ops import (  # noqa: F401
     AdamWPlan,
     AdapterSet,

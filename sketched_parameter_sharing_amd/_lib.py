@@ -35,7 +35,12 @@ EXPORTS = ("ss1_version", "ss1_status_string", "ss1_plan", "ss1_plan_index", "ss
            "ss1_forward_ws_query", "ss1_forward_ws",
            "ss1_layernorm_forward", "ss1_layernorm_backward_query", "ss1_layernorm_backward",
            "ss1_adapter_forward_query", "ss1_adapter_forward", "ss1_adapter_backward_query", "ss1_adapter_backward",
-           "ss1_adamw_plan", "ss1_adamw_step")
+           "ss1_adamw_plan", "ss1_adamw_step",
+           "ss1_gradnorm_plan", "ss1_gradnorm_query", "ss1_gradnorm", "ss1_gradnorm_clip",
+           "ss1_embedding_forward", "ss1_embedding_backward_query", "ss1_embedding_backward",
+           "ss1_quantize_fp8_blocks", "ss1_matmul_fp8_blocks_query", "ss1_matmul_fp8_blocks",
+           "ss1_dense_forward_fp8_query", "ss1_dense_forward_fp8", "ss1_dense_backward_fp8_query",
+           "ss1_dense_backward_fp8")
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 
 
@@ -78,6 +83,21 @@ class AdamWHyper(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double), ("grad_scale_dev", ctypes.c_void_p),
                 ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
+
+
+class GradNormEntry(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("id", ctypes.c_void_p), ("count", ctypes.c_int64), ("bytes", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class Fp8BlocksView(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("block", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _LIB = None
@@ -149,6 +169,24 @@ def load():
                  "ss1_adapter_forward_query", "ss1_adapter_forward", "ss1_adapter_backward_query",
                  "ss1_adapter_backward", "ss1_adamw_plan", "ss1_adamw_step"):
         getattr(lib, name).restype = i32
+    f64, sz = ctypes.c_double, ctypes.c_size_t
+    kp, bp = ctypes.POINTER(Tokens), ctypes.POINTER(Fp8BlocksView)
+    for name, args in (("ss1_gradnorm_plan", [vp, i32, ctypes.POINTER(i64), vp]),
+                       ("ss1_gradnorm_query", [i64, size_p]),
+                       ("ss1_gradnorm", [vp, i32, vp, i64, f64, vp, vp, vp, sz, vp]),
+                       ("ss1_gradnorm_clip", [vp, i32, vp, i64, f64, vp, vp, vp, sz, vp]),
+                       ("ss1_embedding_forward", [kp, tp, f32, tp, vp]),
+                       ("ss1_embedding_backward_query", [kp, tp, size_p]),
+                       ("ss1_embedding_backward", [tp, kp, f32, i32, tp, vp, sz, vp]),
+                       ("ss1_quantize_fp8_blocks", [tp, bp, bp, vp]),
+                       ("ss1_matmul_fp8_blocks_query", [bp, bp, size_p]),
+                       ("ss1_matmul_fp8_blocks", [bp, bp, tp, vp, sz, vp]),
+                       ("ss1_dense_forward_fp8_query", [tp, bp, size_p]),
+                       ("ss1_dense_forward_fp8", [tp, bp, tp, bp, vp, sz, vp]),
+                       ("ss1_dense_backward_fp8_query", [tp, bp, bp, size_p]),
+                       ("ss1_dense_backward_fp8", [tp, bp, bp, tp, tp, vp, sz, vp])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = i32, args
     _LIB = lib
     return lib
 

@@ -1,0 +1,278 @@
+// The product of two block-scaled E4M3 matrices (ss1_matmul_fp8_blocks and the
+// dense layer's forward and gradients): y[m][n] = sum over blocks t of 128 of
+// 2^(ea[m][t] + eb[n][t]) * sum_{k in t} a[m][k] * b[n][k].
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 rows over 128
+// elements and takes a power-of-two scale for every row of both operands, so a
+// block of the format is one instruction and its scales cost nothing but their
+// loads.  The instruction sums over k, so any assignment of the 128 elements to
+// lanes and registers serves as long as both operands use the same one.
+//
+// That instruction lines the products of a block up at the largest and keeps 18
+// bits below it (measured: a relative error of 1e-5 to 5e-5 of a sum over 128).
+// A bf16 y does not see it beside its own rounding (4e-3); a float32 y does, and
+// is computed on the bf16 matrix cores instead, at half the rate: every code
+// times its scale is a bf16 value, so v_cvt_scalef32_pk_bf16_fp8 (one vector
+// instruction for two, full rate) widens the operands exactly as they leave LDS
+// and the sums are float32's (8e-8).
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "ss1_device.h"
+#include "ss1_dma.h"
+#include "ss1_model_ops.h"
+
+namespace ss1 {
+
+namespace {
+
+using dev::f32x4;
+using dev::i32x4;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kKS = SS1_FP8_BLOCK;  // elements (bytes) of a stage
+
+// One wave-wide load of 4 bytes per lane: lane l writes its 4 bytes at LDS
+// byte address lds + 4*l.  As dev::lds_dma16 otherwise (no register result;
+// the stage barriers order it).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_dma4(i32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+                 "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Row p of a wave's weight tile in LDS (TN = 16 * FN rows) holds column
+// neuron(p) of the output: with it the lane that holds rows 4q .. 4q+3 of every
+// 16-row block holds 4 * FN consecutive columns.
+template <int FN>
+__device__ __forceinline__ int out_column(int p) {
+    const int nb = p / 16, r = p % 16;
+    return (r / 4) * 4 * FN + nb * 4 + r % 4;
+}
+
+__device__ __forceinline__ void store4(uint16_t* p, const f32x4& v, int n, bool whole) {
+    if (whole) {
+        uint2 o;
+        o.x = dev::pack_bf16(v[0], v[1]);
+        o.y = dev::pack_bf16(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) = o;
+    } else {
+        for (int i = 0; i < n; ++i) p[i] = dev::to_bf16_bits(v[i]);
+    }
+}
+__device__ __forceinline__ void store4(float* p, const f32x4& v, int n, bool whole) {
+    if (whole) {
+        *reinterpret_cast<f32x4*>(p) = v;
+    } else {
+        for (int i = 0; i < n; ++i) p[i] = v[i];
+    }
+}
+
+// 32 codes of a row as four bf16 operands of v_mfma_f32_16x16x32_bf16, times
+// the row's scale.
+struct Wide {
+    dev::bf16x8 t[4];
+};
+__device__ __forceinline__ Wide widen(const i32x8& v, float scale) {
+    Wide o;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        uint4 w;
+        const uint32_t lo = static_cast<uint32_t>(v[2 * t]), hi = static_cast<uint32_t>(v[2 * t + 1]);
+        w.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+        w.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+        w.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+        w.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
+        o.t[t] = __builtin_bit_cast(dev::bf16x8, w);
+    }
+    return o;
+}
+
+// Block: WM x WN waves on a tile of BM rows of a and BN rows of b; NSTG LDS
+// buffers, filled by direct loads NSTG - 1 stages ahead.  Rows of 128 bytes,
+// XOR-swizzled in 16-byte pieces.  The scales of a stage come as one word a
+// row, four blocks of 128 at a time (their byte is picked by the stage).
+template <int BM, int BN, int WM, int WN, int NSTG, bool F32>
+__global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView a, BlocksView b, void* __restrict__ y,
+                                                                     int M, int N, int K, int n_mt, int n_nt) {
+    constexpr int NWV = WM * WN;
+    constexpr int TM = BM / WM, TN = BN / WN;
+    constexpr int FM = TM / 16, FN = TN / 16;
+    constexpr int AI = BM / 8 / NWV, BI = BN / 8 / NWV;
+    constexpr int SA = BM * kKS, SBB = BN * kKS, SS = (BM + BN) * 4;
+    constexpr int SB = SA + SBB + SS;
+    static_assert((BM + BN) / 64 == NWV && BM % 64 == 0, "one scale load a wave");
+    constexpr int DPW = AI + BI + 1;
+
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    constexpr int GM = 4;
+    const int tile = dev::xcd_tile(blockIdx.x, n_mt * n_nt);
+    const int strip = tile / (GM * n_nt);
+    const int gm = min(GM, n_mt - strip * GM);
+    const int rem = tile - strip * GM * n_nt;
+    const int m0 = (strip * GM + rem % gm) * BM;
+    const int n0 = (rem / gm) * BN;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int nstage = K / kKS;
+
+    const i32x4 ar = dev::dma_rsrc(a.codes + static_cast<size_t>(m0) * K,
+                                   static_cast<uint32_t>(static_cast<size_t>(min(BM, M - m0)) * K));
+    const i32x4 br = dev::dma_rsrc(b.codes + static_cast<size_t>(n0) * K,
+                                   static_cast<uint32_t>(static_cast<size_t>(min(BN, N - n0)) * K));
+    const int lr = lane >> 3;
+    const int pc = (lane & 7) ^ dev::swz_key<kKS>(wave * 8 + lr);
+    const uint32_t a_voff = static_cast<uint32_t>(lr * K + pc * 16);
+    uint32_t b_voff[BI];
+#pragma unroll
+    for (int ii = 0; ii < BI; ++ii) {
+        const int p = (wave + NWV * ii) * 8 + lr;
+        const int n = (p / TN) * TN + out_column<FN>(p % TN);
+        b_voff[ii] = static_cast<uint32_t>(n * K + pc * 16);
+    }
+    // the wave's 64 scale words: rows of a, or of b
+    const bool mine_a = wave < BM / 64;
+    const int sp = (mine_a ? wave : wave - BM / 64) * 64 + lane;
+    const BlocksView& sv = mine_a ? a : b;
+    const int s0 = mine_a ? m0 : n0;
+    const int srow = mine_a ? sp : (sp / TN) * TN + out_column<FN>(sp % TN);
+    const int64_t first = s0 >> sv.shift;
+    const int64_t rows = ((sv.rows + (int64_t(1) << sv.shift) - 1) >> sv.shift) - first;
+    const int span = ((mine_a ? BM : BN) >> sv.shift) + 1;
+    const i32x4 sr = dev::dma_rsrc(sv.scale + first * sv.scale_cols,
+                                   static_cast<uint32_t>((rows < span ? rows : span) * sv.scale_cols));
+    const uint32_t s_voff = static_cast<uint32_t>((((s0 + srow) >> sv.shift) - first) * sv.scale_cols);
+
+    const uint32_t lds0 = dev::lds_address(smem);
+    auto dma = [&](int s, int buf) {
+        const uint32_t base = lds0 + static_cast<uint32_t>(buf * SB);
+        const uint32_t k0 = static_cast<uint32_t>(s * kKS);
+#pragma unroll
+        for (int ii = 0; ii < AI; ++ii) {
+            const int row0 = (wave + NWV * ii) * 8;
+            dev::lds_dma16(ar, base + row0 * kKS, a_voff + static_cast<uint32_t>(row0 * K), k0);
+        }
+#pragma unroll
+        for (int ii = 0; ii < BI; ++ii)
+            dev::lds_dma16(br, base + SA + (wave + NWV * ii) * 8 * kKS, b_voff[ii], k0);
+        lds_dma4(sr, base + SA + SBB + wave * 256, s_voff, static_cast<uint32_t>(s & ~3));
+    };
+
+    const int fr = lane & 15, q = lane >> 4;
+    const int key = dev::swz_key<kKS>(fr);
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto step = [&](int s, int buf) {
+        if (NSTG >= 3 && nstage - 1 - s >= NSTG - 2) dev::dma_stage_barrier<(NSTG - 2) * DPW>();
+        else dev::dma_stage_barrier<0>();
+        if (s + NSTG - 1 < nstage) dma(s + NSTG - 1, (buf + NSTG - 1) % NSTG);
+        const uint8_t* S = smem + buf * SB;
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(S + SA + SBB);
+        const int byte = 8 * (s & 3);
+        auto operand = [&](const uint8_t* row) {
+            const uint4 u = *reinterpret_cast<const uint4*>(row + ((q ^ key) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(row + (((q + 4) ^ key) << 4));
+            return i32x8{static_cast<int>(u.x), static_cast<int>(u.y), static_cast<int>(u.z), static_cast<int>(u.w),
+                         static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w)};
+        };
+        if constexpr (F32) {
+            auto scale = [&](int row) { return __uint_as_float((sc[row] >> byte & 0xFFu) << 23); };
+            Wide bw[FN];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int row = wn * TN + i * 16 + fr;
+                bw[i] = widen(operand(S + SA + row * kKS), scale(BM + row));
+            }
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const int row = wm * TM + j * 16 + fr;
+                const Wide aw = widen(operand(S + row * kKS), scale(row));
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[i].t[t], aw.t[t], acc[i][j], 0, 0, 0);
+            }
+        } else {
+            i32x8 bv[FN];
+            int bs[FN];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int row = wn * TN + i * 16 + fr;
+                bv[i] = operand(S + SA + row * kKS);
+                bs[i] = static_cast<int>(sc[BM + row] >> byte);
+            }
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const int row = wm * TM + j * 16 + fr;
+                const i32x8 av = operand(S + row * kKS);
+                const int as = static_cast<int>(sc[row] >> byte);
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[i], av, acc[i][j], 0, 0, 0, bs[i],
+                                                                                 0, as);
+            }
+        }
+    };
+#pragma unroll
+    for (int p = 0; p < NSTG - 1; ++p)
+        if (p < nstage) dma(p, p);
+    for (int s1 = 0; s1 < nstage; s1 += NSTG) {
+#pragma unroll
+        for (int u = 0; u < NSTG; ++u)
+            if (s1 + u < nstage) step(s1 + u, u);
+    }
+
+    // lane holds columns nbase + 4 i .. + 3 (i < FN) of the rows m0 + .. + fr
+    const int nbase = n0 + wn * TN + q * 4 * FN;
+    const bool whole = N % 4 == 0;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int m = m0 + wm * TM + j * 16 + fr;
+        if (m >= M) continue;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int n = nbase + 4 * i;
+            if (n >= N) break;
+            const size_t at = static_cast<size_t>(m) * N + n;
+            if constexpr (F32) store4(static_cast<float*>(y) + at, acc[i][j], min(4, N - n), whole);
+            else store4(static_cast<uint16_t*>(y) + at, acc[i][j], min(4, N - n), whole);
+        }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, int NSTG, bool F32>
+ss1_status launch_tile(const MatmulBlocksArgs& p) {
+    const int64_t n_mt = (p.M + BM - 1) / BM, n_nt = (p.N + BN - 1) / BN;
+    constexpr size_t lds = static_cast<size_t>(NSTG) * (BM + BN) * (kKS + 4);
+    auto kern = &matmul_blocks_kernel<BM, BN, WM, WN, NSTG, F32>;
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            static_cast<int>(lds)) != hipSuccess)
+        return SS1_ERR_HIP;
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(n_mt * n_nt)), dim3(WM * WN * 64), lds,
+                       static_cast<hipStream_t>(p.stream), p.a, p.b, p.y, static_cast<int>(p.M),
+                       static_cast<int>(p.N), static_cast<int>(p.K), static_cast<int>(n_mt), static_cast<int>(n_nt));
+    return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
+}
+
+}  // namespace
+
+size_t matmul_blocks_workspace(int64_t, int64_t, int64_t) { return 0; }
+
+bool matmul_takes_x(int64_t, int64_t, int64_t) { return false; }
+
+ss1_status launch_matmul_blocks(const MatmulBlocksArgs& p) {
+    return p.dtype == SS1_F32 ? launch_tile<128, 128, 2, 2, 2, true>(p) : launch_tile<128, 128, 2, 2, 2, false>(p);
+}
+
+}  // namespace ss1

@@ -1,0 +1,239 @@
+// The global gradient norm over many tensors, its clip coefficient, and
+// clipping in place (ss1_gradnorm, ss1_gradnorm_clip).
+//
+// Each work item is a run of kNormChunk elements of one tensor; a block takes a
+// run of consecutive items and leaves one partial sum.  The product of two
+// float32 values is exact in float64 and the sums stay there, so gradients of
+// 1e-30 or 1e30 count like any other and the order of the sum does not show in
+// the result.  The partial sums are added by whoever needs the norm: one block
+// that writes it, or every block of the clipping pass for itself (at most
+// kNormBlocks doubles), which saves a launch between the two passes.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "ss1_model_ops.h"
+
+namespace ss1 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;
+constexpr int kPasses = static_cast<int>(kNormChunk / (kThreads * kVec));
+static_assert(kNormChunk % (kThreads * kVec) == 0, "a chunk is whole passes of the block");
+
+// Eight bf16 or float32 values as they lie in memory.
+struct RawH {
+    uint4 a;
+};
+struct RawF {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ void load_raw(const uint16_t* p, RawH& r) { r.a = *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void load_raw(const float* p, RawF& r) {
+    r.a = *reinterpret_cast<const uint4*>(p);
+    r.b = *reinterpret_cast<const uint4*>(p + 4);
+}
+__device__ __forceinline__ void widen(const RawH& r, float (&v)[kVec]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void widen(const RawF& r, float (&v)[kVec]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float(static_cast<uint32_t>(h) << 16); }
+__device__ __forceinline__ float widen(float f) { return f; }
+
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[kVec]) {
+    uint4 o;
+    o.x = bf16_bits(v[0]) | bf16_bits(v[1]) << 16;
+    o.y = bf16_bits(v[2]) | bf16_bits(v[3]) << 16;
+    o.z = bf16_bits(v[4]) | bf16_bits(v[5]) << 16;
+    o.w = bf16_bits(v[6]) | bf16_bits(v[7]) << 16;
+    *reinterpret_cast<uint4*>(p) = o;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[kVec]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<uint16_t>(bf16_bits(v)); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+// Sum of squares of this thread's elements of a chunk that starts at p and has
+// n elements left in its tensor.
+template <typename T, typename R>
+__device__ __forceinline__ double squares(const T* p, int64_t n) {
+    double s = 0.0;
+    if (n >= kNormChunk) {
+        R r[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) load_raw(p + (i * kThreads + threadIdx.x) * kVec, r[i]);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            float v[kVec];
+            widen(r[i], v);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) s = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), s);
+        }
+        return s;
+    }
+    for (int64_t i = threadIdx.x * kVec; i < n; i += kThreads * kVec) {
+        const int m = n - i < kVec ? static_cast<int>(n - i) : kVec;
+        for (int j = 0; j < m; ++j) {
+            const double v = widen(p[i + j]);
+            s = fma(v, v, s);
+        }
+    }
+    return s;
+}
+
+// The block's sum of one double a thread, in every thread.
+__device__ __forceinline__ double block_sum(double s, double* red) {
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    double t = red[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) t += red[w];
+    return t;
+}
+
+// The items of block b of `blocks`: [first, first of the next block).
+__device__ __forceinline__ int64_t first_item(int64_t chunks, int b, int blocks) {
+    return chunks * b / blocks;
+}
+
+__global__ __launch_bounds__(kThreads) void gradnorm_kernel(const ss1_gradnorm_entry* __restrict__ entries, int count,
+                                                            const int32_t* __restrict__ map, int64_t chunks,
+                                                            double* __restrict__ partial) {
+    __shared__ double red[kThreads / 64];
+    const int64_t end = first_item(chunks, blockIdx.x + 1, gridDim.x);
+    double s = 0.0;
+    for (int64_t i = first_item(chunks, blockIdx.x, gridDim.x); i < end; ++i) {
+        const int item = map[2 * i];
+        const int64_t part = map[2 * i + 1];
+        if (item < 0 || item >= count || part < 0) continue;
+        const ss1_gradnorm_entry e = entries[item];
+        const int64_t begin = part * kNormChunk;
+        if (begin >= e.numel) continue;
+        if (e.dtype == SS1_F32)
+            s += squares<float, RawF>(static_cast<const float*>(e.grad) + begin, e.numel - begin);
+        else
+            s += squares<uint16_t, RawH>(static_cast<const uint16_t*>(e.grad) + begin, e.numel - begin);
+    }
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+struct Norm {
+    float norm, coef;
+};
+
+// Norm and coefficient from the partial sums, in every thread: the same order
+// in every block that asks.
+__device__ __forceinline__ Norm finish(const double* __restrict__ partial, int parts, double max_norm, double* red) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
+    const double norm = sqrt(block_sum(s, red));
+    Norm r;
+    r.norm = static_cast<float>(norm);
+    r.coef = norm > max_norm ? static_cast<float>(max_norm / norm) : norm != norm ? r.norm : 1.0f;
+    return r;
+}
+
+__global__ __launch_bounds__(kThreads) void gradnorm_finish_kernel(const double* __restrict__ partial, int parts,
+                                                                   double max_norm, float* __restrict__ norm,
+                                                                   float* __restrict__ coef) {
+    __shared__ double red[kThreads / 64];
+    const Norm r = finish(partial, parts, max_norm, red);
+    if (threadIdx.x != 0) return;
+    if (norm) *norm = r.norm;
+    if (coef) *coef = r.coef;
+}
+
+template <typename T, typename R>
+__device__ __forceinline__ void scale_chunk(T* p, int64_t n, float coef) {
+    if (n >= kNormChunk) {
+        R r[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) load_raw(p + (i * kThreads + threadIdx.x) * kVec, r[i]);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            float v[kVec];
+            widen(r[i], v);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] *= coef;
+            store8(p + (i * kThreads + threadIdx.x) * kVec, v);
+        }
+        return;
+    }
+    for (int64_t i = threadIdx.x * kVec; i < n; i += kThreads * kVec) {
+        const int m = n - i < kVec ? static_cast<int>(n - i) : kVec;
+        for (int j = 0; j < m; ++j) store1(p + i + j, widen(p[i + j]) * coef);
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void gradclip_kernel(const ss1_gradnorm_entry* __restrict__ entries, int count,
+                                                            const int32_t* __restrict__ map, int64_t chunks,
+                                                            const double* __restrict__ partial, double max_norm,
+                                                            float* __restrict__ norm, float* __restrict__ coef) {
+    __shared__ double red[kThreads / 64];
+    const Norm r = finish(partial, gridDim.x, max_norm, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (norm) *norm = r.norm;
+        if (coef) *coef = r.coef;
+    }
+    if (r.coef == 1.0f) return;
+    const int64_t end = first_item(chunks, blockIdx.x + 1, gridDim.x);
+    for (int64_t i = first_item(chunks, blockIdx.x, gridDim.x); i < end; ++i) {
+        const int item = map[2 * i];
+        const int64_t part = map[2 * i + 1];
+        if (item < 0 || item >= count || part < 0) continue;
+        const ss1_gradnorm_entry e = entries[item];
+        const int64_t begin = part * kNormChunk;
+        if (begin >= e.numel) continue;
+        if (e.dtype == SS1_F32)
+            scale_chunk<float, RawF>(static_cast<float*>(e.grad) + begin, e.numel - begin, r.coef);
+        else
+            scale_chunk<uint16_t, RawH>(static_cast<uint16_t*>(e.grad) + begin, e.numel - begin, r.coef);
+    }
+}
+
+int blocks_of(int64_t chunks) { return static_cast<int>(chunks < kNormBlocks ? chunks : kNormBlocks); }
+
+void launch_partial(const GradNormArgs& a) {
+    if (a.chunks == 0) return;
+    hipLaunchKernelGGL(gradnorm_kernel, dim3(blocks_of(a.chunks)), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(a.stream), a.entries, a.count, a.map, a.chunks, a.partial);
+}
+
+}  // namespace
+
+ss1_status launch_gradnorm(const GradNormArgs& a) {
+    launch_partial(a);
+    hipLaunchKernelGGL(gradnorm_finish_kernel, dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(a.stream),
+                       a.partial, blocks_of(a.chunks), a.max_norm, a.norm, a.coef);
+    return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
+}
+
+ss1_status launch_gradnorm_clip(const GradNormArgs& a) {
+    if (a.chunks == 0) return launch_gradnorm(a);
+    launch_partial(a);
+    hipLaunchKernelGGL(gradclip_kernel, dim3(blocks_of(a.chunks)), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(a.stream), a.entries, a.count, a.map, a.chunks, a.partial, a.max_norm,
+                       a.norm, a.coef);
+    return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
+}
+
+}  // namespace ss1

@@ -19,6 +19,7 @@
 
 #include <stdint.h>
 
+#include "ss1_blocks.h"
 #include "ss1_device.h"
 #include "ss1_dma.h"
 #include "ss1_model_ops.h"
@@ -251,6 +252,186 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
     }
 }
 
+// ------------------------------------------------------------- few tokens
+// Up to 16 rows of a (tokens) against all of b (a weight): the weight's bytes
+// are the time, so a wave reads its operands of b straight from global memory,
+// 4 blocks of 128 of 16 rows at a time and one such unit ahead.  A block is 16
+// rows of b; its NW waves share the reduction in contiguous runs of units and
+// meet in LDS, added in order.
+//
+// With X the rows of a are x itself, quantised by every block for itself into
+// LDS (M * K elements of L2 traffic and about 10 instructions an element and
+// block, against a launch); its loads are issued before the weight's, since
+// loads return in order, and the weight's are in flight meanwhile.
+constexpr int kUnit = 4;  // blocks of 128 of a unit: the scales of one word
+
+template <typename X>
+struct RawOf {
+    uint4 v[sizeof(X) / 2];
+};
+
+template <typename X, bool F32, int NW>
+__global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksView b, const X* __restrict__ x,
+                                                           int64_t xcols, void* __restrict__ y, int M, int N, int K) {
+    constexpr bool INSIDE = !__is_same(X, void);
+    constexpr int kAhead = 4;  // passes over x whose loads are issued before the weight's
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    __shared__ f32x4 part[NW][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int fr = lane & 15, q = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const int nkb = K / kKS;
+    const int units = (nkb + kUnit - 1) / kUnit;
+    const int u0 = units * wave / NW, u1 = units * (wave + 1) / NW;
+
+    // x: 16 lanes take a block of 128 of a row
+    const int pitch = K + 64;  // four rows' 64 bytes on distinct banks
+    uint8_t* s_scale = smem + static_cast<size_t>(M) * pitch;
+    const int items = INSIDE ? M * nkb : 0;
+    constexpr int G = NW * 4;
+    float v[INSIDE ? kAhead : 1][8];
+    auto fetch = [&](int it, float (&r)[8]) {
+        if constexpr (INSIDE) {
+            const int m = it / nkb, kb = it % nkb;
+            const X* row = x + m * xcols;
+            if (xcols % 8 == 0) blocks::load8<true>(row, kb * kKS + (lane & 15) * 8, xcols, r);
+            else blocks::load8<false>(row, kb * kKS + (lane & 15) * 8, xcols, r);
+        }
+    };
+    if constexpr (INSIDE) {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+            const int it = p * G + (tid >> 4);
+            if (it < items) fetch(it, v[p]);
+        }
+    }
+
+    const __amdgpu_buffer_rsrc_t br = dev::make_rsrc(b.codes + static_cast<size_t>(n0) * K,
+                                                     static_cast<uint32_t>(static_cast<size_t>(min(16, N - n0)) * K));
+    const uint32_t b_voff = static_cast<uint32_t>(fr * K + q * 16);
+    const int n = min(n0 + fr, N - 1);
+    const uint8_t* b_scale = b.scale + (static_cast<int64_t>(n) >> b.shift) * b.scale_cols;
+    const int mr = min(fr, M - 1);  // columns of tokens past M are not stored
+    const uint8_t* a_row = INSIDE ? nullptr : a.codes + static_cast<size_t>(mr) * K + q * 16;
+    const uint8_t* a_scale = INSIDE ? nullptr : a.scale + (static_cast<int64_t>(mr) >> a.shift) * a.scale_cols;
+
+    struct Unit {
+        uint4 w[kUnit][2];
+        uint4 t[INSIDE ? 1 : kUnit][2];
+        uint32_t ws, ts;
+    };
+    auto load = [&](int u, Unit& o) {
+        o.ws = *reinterpret_cast<const uint32_t*>(b_scale + u * kUnit);
+        if constexpr (!INSIDE) o.ts = *reinterpret_cast<const uint32_t*>(a_scale + u * kUnit);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            // blocks past the last one of K: past the end of the row, and not used
+            const uint32_t k = static_cast<uint32_t>(min(u * kUnit + i, nkb - 1) * kKS);
+            o.w[i][0] = dev::buf_load16(br, b_voff, k);
+            o.w[i][1] = dev::buf_load16(br, b_voff + 64, k);
+            if constexpr (!INSIDE) {
+                o.t[i][0] = *reinterpret_cast<const uint4*>(a_row + k);
+                o.t[i][1] = *reinterpret_cast<const uint4*>(a_row + k + 64);
+            }
+        }
+    };
+    Unit cur, next;
+    if (u0 < u1) load(u0, cur);
+
+    if constexpr (INSIDE) {
+        auto put = [&](int it, const float (&r)[8]) {
+            const int m = it / nkb, kb = it % nkb;
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t f = blocks::finite_size(r[i]);
+                top = top > f ? top : f;
+            }
+            const uint32_t byte = blocks::scale_byte(blocks::max16(top));
+            const float inv = blocks::inverse_scale(byte);
+            uint2 w;
+            w.x = blocks::codes4(r[0], r[1], r[2], r[3], inv);
+            w.y = blocks::codes4(r[4], r[5], r[6], r[7], inv);
+            *reinterpret_cast<uint2*>(smem + m * pitch + kb * kKS + (lane & 15) * 8) = w;
+            if ((lane & 15) == 0) s_scale[m * nkb + kb] = static_cast<uint8_t>(byte);
+        };
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+            const int it = p * G + (tid >> 4);
+            if (it < items) put(it, v[p]);
+        }
+        for (int it = kAhead * G + (tid >> 4); it < items; it += G) {
+            fetch(it, v[0]);
+            put(it, v[0]);
+        }
+        dev::lds_barrier();
+    }
+
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto octet = [](const uint4& u, const uint4& w) {
+        return i32x8{static_cast<int>(u.x), static_cast<int>(u.y), static_cast<int>(u.z), static_cast<int>(u.w),
+                     static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w)};
+    };
+    for (int u = u0; u < u1; ++u) {
+        if (u + 1 < u1) load(u + 1, next);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            const int kb = u * kUnit + i;
+            if (kb >= nkb) break;
+            i32x8 tv;
+            uint32_t ts;
+            if constexpr (INSIDE) {
+                const uint8_t* r = smem + mr * pitch + kb * kKS + q * 16;
+                tv = octet(*reinterpret_cast<const uint4*>(r), *reinterpret_cast<const uint4*>(r + 64));
+                ts = s_scale[mr * nkb + kb];
+            } else {
+                tv = octet(cur.t[i][0], cur.t[i][1]);
+                ts = cur.ts >> (8 * i);
+            }
+            const i32x8 wv = octet(cur.w[i][0], cur.w[i][1]);
+            const uint32_t ws = cur.ws >> (8 * i);
+            if constexpr (F32) {
+                const Wide ww = widen(wv, __uint_as_float((ws & 0xFFu) << 23));
+                const Wide tw = widen(tv, __uint_as_float((ts & 0xFFu) << 23));
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.t[t], tw.t[t], acc, 0, 0, 0);
+            } else {
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, tv, acc, 0, 0, 0, static_cast<int>(ws), 0,
+                                                                       static_cast<int>(ts));
+            }
+        }
+        cur = next;
+    }
+    part[wave][lane] = acc;
+    dev::lds_barrier();
+    if (wave != 0 || fr >= M) return;
+    f32x4 sum = part[0][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += part[w][lane];
+    const int c = n0 + 4 * q;
+    if (c >= N) return;
+    const size_t at = static_cast<size_t>(fr) * N + c;
+    if constexpr (F32) store4(static_cast<float*>(y) + at, sum, min(4, N - c), N % 4 == 0);
+    else store4(static_cast<uint16_t*>(y) + at, sum, min(4, N - c), N % 4 == 0);
+}
+
+// Rows of a that the kernel above takes, and how much of x a block quantises.
+constexpr int64_t kFewRows = 16;
+constexpr int64_t kInsideRows = 4;
+constexpr int64_t kInsideBytes = 32768;
+
+template <typename X, bool F32>
+ss1_status launch_few(const MatmulBlocksArgs& p) {
+    constexpr int NW = 4;
+    const size_t lds = __is_same(X, void) ? 0 : static_cast<size_t>(up_to(p.M * (p.K + 64 + p.K / kKS), 16));
+    hipLaunchKernelGGL((few_rows_kernel<X, F32, NW>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(NW * 64), lds,
+                       static_cast<hipStream_t>(p.stream), p.a, p.b, static_cast<const X*>(p.x), p.xcols, p.y,
+                       static_cast<int>(p.M), static_cast<int>(p.N), static_cast<int>(p.K));
+    return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
+}
+
 template <int BM, int BN, int WM, int WN, int NSTG, bool F32>
 ss1_status launch_tile(const MatmulBlocksArgs& p) {
     const int64_t n_mt = (p.M + BM - 1) / BM, n_nt = (p.N + BN - 1) / BN;
@@ -269,10 +450,18 @@ ss1_status launch_tile(const MatmulBlocksArgs& p) {
 
 size_t matmul_blocks_workspace(int64_t, int64_t, int64_t) { return 0; }
 
-bool matmul_takes_x(int64_t, int64_t, int64_t) { return false; }
+bool matmul_takes_x(int64_t M, int64_t, int64_t K) {
+    return M <= kInsideRows && K > 0 && M * (K + 64 + K / kKS) <= kInsideBytes;
+}
 
 ss1_status launch_matmul_blocks(const MatmulBlocksArgs& p) {
-    return p.dtype == SS1_F32 ? launch_tile<128, 128, 2, 2, 2, true>(p) : launch_tile<128, 128, 2, 2, 2, false>(p);
+    const bool f32 = p.dtype == SS1_F32;
+    if (p.x) {
+        // y has x's dtype
+        return f32 ? launch_few<float, true>(p) : launch_few<uint16_t, false>(p);
+    }
+    if (p.M <= kFewRows && p.K > 0) return f32 ? launch_few<void, true>(p) : launch_few<void, false>(p);
+    return f32 ? launch_tile<128, 128, 2, 2, 2, true>(p) : launch_tile<128, 128, 2, 2, 2, false>(p);
 }
 
 }  // namespace ss1

@@ -36,67 +36,93 @@ constexpr int kSortRows = 512;   // rows of a sorting block at most
 constexpr int kSortKeep = 16;    // steps whose ids a lane keeps between the two passes
 constexpr int kMinBlocks = 256;  // sorting blocks at least (one a compute unit)
 constexpr int kTile = 16;        // tokens of a summing wave, up to kMaxTiles waves a column slice
-constexpr int kMaxTiles = 4096;
+constexpr int kMaxTiles = 1024;
+constexpr int kZeroVecs = 4 * kSortThreads;  // 16-byte vectors that a block of the sort's launch clears
+constexpr int64_t kZeroFirst = int64_t(32) << 20;
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr int kZeroRows = 16;    // rows of a zeroing wave
 
 // ------------------------------------------------------------ element access
-template <int VEC>
-__device__ __forceinline__ void load_row(const float* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        v[0] = *p;
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        const uint4 r = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight consecutive columns of a row, of which n > 0 are left; rows of an odd
+// width start anywhere, so the vectors are not aligned (one instruction all the
+// same, at full speed where the address is).
+constexpr int kVec = 8;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_any4 __attribute__((aligned(4)));
+
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+    u32x4 a;
+    __device__ __forceinline__ void load(const uint16_t* p, int n) {
+        if (n >= kVec) {
+            a = *reinterpret_cast<const u32x4_any2*>(p);
+        } else {
+            a = u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            for (int i = 0; i < kVec - 1; ++i)
+                if (i < n) a[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
         }
-    } else {
-        v[0] = __uint_as_float(static_cast<uint32_t>(*p) << 16);
     }
-}
+    __device__ __forceinline__ float at(int i) const {
+        return __uint_as_float(i & 1 ? a[i / 2] & 0xFFFF0000u : a[i / 2] << 16);
+    }
+};
+template <>
+struct Raw<float> {
+    u32x4 a, b;
+    __device__ __forceinline__ void load(const float* p, int n) {
+        if (n >= kVec) {
+            a = *reinterpret_cast<const u32x4_any4*>(p);
+            b = *reinterpret_cast<const u32x4_any4*>(p + 4);
+        } else {
+            a = b = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < n) a[i] = __float_as_uint(p[i]);
+                if (i + 4 < n) b[i] = __float_as_uint(p[i + 4]);
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int i) const { return __uint_as_float(i < 4 ? a[i] : b[i - 4]); }
+};
+
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
-template <int VEC>
-__device__ __forceinline__ void store_row(float* p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store_row(float* p, const float (&v)[kVec], int n) {
+    if (n >= kVec) {
+        *reinterpret_cast<u32x4_any4*>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                  __float_as_uint(v[3])};
+        *reinterpret_cast<u32x4_any4*>(p + 4) = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                                      __float_as_uint(v[6]), __float_as_uint(v[7])};
     } else {
-        *p = v[0];
+#pragma unroll
+        for (int i = 0; i < kVec - 1; ++i)
+            if (i < n) p[i] = v[i];
     }
 }
-template <int VEC>
-__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        uint4 o;
-        o.x = bf16_bits(v[0]) | bf16_bits(v[1]) << 16;
-        o.y = bf16_bits(v[2]) | bf16_bits(v[3]) << 16;
-        o.z = bf16_bits(v[4]) | bf16_bits(v[5]) << 16;
-        o.w = bf16_bits(v[6]) | bf16_bits(v[7]) << 16;
-        *reinterpret_cast<uint4*>(p) = o;
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[kVec], int n) {
+    if (n >= kVec) {
+        *reinterpret_cast<u32x4_any2*>(p) =
+            u32x4{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16,
+                  bf16_bits(v[4]) | bf16_bits(v[5]) << 16, bf16_bits(v[6]) | bf16_bits(v[7]) << 16};
     } else {
-        *p = static_cast<uint16_t>(bf16_bits(v[0]));
+#pragma unroll
+        for (int i = 0; i < kVec - 1; ++i)
+            if (i < n) p[i] = static_cast<uint16_t>(bf16_bits(v[i]));
     }
 }
 
 // -------------------------------------------------------------------- forward
-// A wave takes one token and a run of kSlices * 64 * VEC columns.
+// A wave takes one token and a run of kSlices * 64 * 8 columns.
 constexpr int kSlices = 4;
+constexpr int kSlice = 64 * kVec;
 
-template <typename I, typename TE, typename TY, int VEC>
+template <typename I, typename TE, typename TY>
 __global__ __launch_bounds__(kSumThreads) void embedding_forward_kernel(const I* __restrict__ ids, int64_t M, int64_t V,
                                                                         int K, int runs, float scale,
                                                                         const TE* __restrict__ E,
@@ -105,29 +131,23 @@ __global__ __launch_bounds__(kSumThreads) void embedding_forward_kernel(const I*
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t m = unit / runs;
     if (m >= M) return;
-    const int c0 = static_cast<int>(unit % runs) * kSlices * 64 * VEC + lane * VEC;
+    const int c0 = static_cast<int>(unit % runs) * kSlices * kSlice + lane * kVec;
     const int64_t id = static_cast<int64_t>(ids[m]);
     const bool real = id >= 0 && id < V;
-    float v[kSlices][VEC];
+    Raw<TE> r[kSlices];
 #pragma unroll
     for (int i = 0; i < kSlices; ++i) {
-        const int c = c0 + i * 64 * VEC;
-        if (real && c < K) {
-            load_row<VEC>(E + id * K + c, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i][j] = 0.0f;
-        }
+        const int c = c0 + i * kSlice;
+        if (real && c < K) r[i].load(E + id * K + c, K - c);
     }
 #pragma unroll
     for (int i = 0; i < kSlices; ++i) {
-        const int c = c0 + i * 64 * VEC;
+        const int c = c0 + i * kSlice;
         if (c >= K) break;
-        if (real) {
+        float v[kVec];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i][j] *= scale;
-        }
-        store_row<VEC>(y + m * K + c, v[i]);
+        for (int j = 0; j < kVec; ++j) v[j] = real ? r[i].at(j) * scale : 0.0f;
+        store_row(y + m * K + c, v, K - c);
     }
 }
 
@@ -161,16 +181,27 @@ __device__ __forceinline__ Own own_row(I id, int64_t V, const RowOrder& o) {
 
 // Writes start[place of row] (where the row's tokens begin in the sorted order)
 // for the block's rows, the last block also the end of the last row, and
-// order[] (the tokens by row, ascending within a row).
+// order[] (the tokens by row, ascending within a row).  Blocks from `blocks` on
+// clear the first zero_vecs 16-byte vectors of dE meanwhile.
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* __restrict__ ids, int M, int64_t V,
                                                                       RowOrder o, int32_t* __restrict__ start,
-                                                                      int32_t* __restrict__ order) {
+                                                                      int32_t* __restrict__ order,
+                                                                      u32x4* __restrict__ dE, int64_t zero_vecs) {
     __shared__ int32_t hist[kSortWaves][kSortRows];
     __shared__ int32_t sums[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (int r = tid; r < kSortWaves * kSortRows; r += kSortThreads) hist[r / kSortRows][r % kSortRows] = 0;
+    const int blocks = 1 << o.log2_blocks;
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        const int64_t at = static_cast<int64_t>(blockIdx.x - blocks) * kZeroVecs + tid;
+#pragma unroll
+        for (int i = 0; i < kZeroVecs / kSortThreads; ++i)
+            if (at + i * kSortThreads < zero_vecs) dE[at + i * kSortThreads] = u32x4{0, 0, 0, 0};
+        return;
+    }
+    for (int r = tid & 511; r < o.rows; r += 512)
+        for (int w = tid >> 9; w < kSortWaves; w += kSortThreads >> 9) hist[w][r] = 0;
     __syncthreads();
 
     // the wave's run of ids: whole steps of 64
@@ -204,9 +235,10 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
     __syncthreads();
 
     // prefix sum over the rows (thread r has row r), the waves of a row in turn
-    int mine = 0;
-    if (tid < kSortRows)
-        for (int w = 0; w < kSortWaves; ++w) mine += hist[w][tid];
+    int mine = 0, own[kSortWaves];
+    if (tid < o.rows)
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) mine += own[w] = hist[w][tid];
     int scan = mine;
     for (int off = 1; off < 64; off <<= 1) {
         const int t = __shfl_up(scan, off);
@@ -217,12 +249,13 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
     int at = base + scan - mine;
     for (int w = 0; w < wave; ++w) at += sums[w];
     if (tid < o.rows) start[static_cast<int64_t>(blockIdx.x) * o.rows + tid] = at;
-    if (blockIdx.x == gridDim.x - 1 && tid == o.rows - 1) start[static_cast<int64_t>(gridDim.x) * o.rows] = at + mine;
-    if (tid < kSortRows)
+    if (static_cast<int>(blockIdx.x) == blocks - 1 && tid == o.rows - 1)
+        start[static_cast<int64_t>(blocks) * o.rows] = at + mine;
+    if (tid < o.rows)
+#pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const int n = hist[w][tid];
             hist[w][tid] = at;
-            at += n;
+            at += own[w];
         }
     __syncthreads();
 
@@ -256,35 +289,20 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
 }
 
 // ------------------------------------------------------------------------ sum
-template <typename T, int VEC>
-__device__ __forceinline__ void write_row(T* dE, int64_t at, const float (&sum)[VEC], float scale, bool accumulate) {
-    float v[VEC];
+// dE at p from the sum of a row's tokens (n columns left).
+template <typename T>
+__device__ __forceinline__ void write_row(T* p, int n, const float (&sum)[kVec], float scale, bool accumulate) {
+    float v[kVec];
     if (accumulate) {
-        load_row<VEC>(dE + at, v);
+        Raw<T> r;
+        r.load(p, n);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] += sum[j] * scale;
+        for (int j = 0; j < kVec; ++j) v[j] = r.at(j) + sum[j] * scale;
     } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = sum[j] * scale;
+        for (int j = 0; j < kVec; ++j) v[j] = sum[j] * scale;
     }
-    store_row<VEC>(dE + at, v);
-}
-
-// A tile of the sorted order: its places [begin, end), and whether its first
-// row began before it and its last row goes on behind it.
-struct Tile {
-    int begin, end;
-    bool open_front, open_back;
-};
-template <typename I>
-__device__ __forceinline__ Tile tile_of(int64_t tile, int T, int total, const I* ids, const int32_t* order) {
-    Tile t;
-    const int64_t b = tile * T;
-    t.begin = b < total ? static_cast<int>(b) : total;
-    t.end = b + T < total ? static_cast<int>(b) + T : total;
-    t.open_front = t.begin < t.end && t.begin > 0 && ids[order[t.begin - 1]] == ids[order[t.begin]];
-    t.open_back = t.begin < t.end && t.end < total && ids[order[t.end]] == ids[order[t.end - 1]];
-    return t;
+    store_row(p, v, n);
 }
 
 struct SumArgs {
@@ -292,8 +310,9 @@ struct SumArgs {
     const int32_t* order;
     float* partial;    // [tiles][2][K]: the share of the first row, of the last row
     int64_t V;
-    int64_t tiles;
-    int64_t sum_blocks;  // blocks from here on zero rows
+    int64_t zeroed;      // rows that the sort's launch has cleared
+    int32_t tiles;
+    int32_t sum_blocks;  // blocks from here on zero rows
     int32_t T;
     int32_t K;
     int32_t slices;
@@ -302,99 +321,237 @@ struct SumArgs {
     float scale;
 };
 
-template <typename I, typename TD, typename TE, int VEC>
+__device__ __forceinline__ int tokens_of(const SumArgs& a) {
+    return a.start[(int64_t(1) << a.o.log2_blocks) * a.o.rows];
+}
+
+// The rows of the places first, first + 1, ... (lane l the l-th of 64), -1
+// outside [0, total).
+template <typename I>
+__device__ __forceinline__ int row_at(const I* ids, const int32_t* order, int place, int total) {
+    return place >= 0 && place < total ? static_cast<int>(ids[order[place]]) : -1;
+}
+
+constexpr int kBatch = 8;  // rows of dy, or shares, whose loads are in flight together
+
+template <typename I, typename TD, typename TE>
 __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __restrict__ ids, const TD* __restrict__ dy,
                                                                     TE* __restrict__ dE, SumArgs a) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = a.K;
-    if (blockIdx.x >= a.sum_blocks) {  // rows without tokens
-        const int64_t v0 = ((blockIdx.x - a.sum_blocks) * kSumWaves + wave) * kZeroRows;
+    if (static_cast<int>(blockIdx.x) >= a.sum_blocks) {  // rows without tokens
+        const int64_t v0 = a.zeroed + (static_cast<int64_t>(blockIdx.x - a.sum_blocks) * kSumWaves + wave) * kZeroRows;
         bool empty = false;
         if (lane < kZeroRows && v0 + lane < a.V) {
             const int64_t p = place_of(a.o, v0 + lane);
             empty = a.start[p] == a.start[p + 1];
         }
         uint64_t rows = __ballot(empty);
-        float zero[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) zero[j] = 0.0f;
+        const float zero[kVec] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         while (rows) {
             const int r = __builtin_ctzll(rows);
             rows &= rows - 1;
-            for (int c = lane * VEC; c < K; c += 64 * VEC) store_row<VEC>(dE + (v0 + r) * K + c, zero);
+            for (int c = lane * kVec; c < K; c += kSlice) store_row(dE + (v0 + r) * K + c, zero, K - c);
         }
         return;
     }
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kSumWaves + wave;
-    const int64_t tile = unit / a.slices;
+    const int unit = static_cast<int>(blockIdx.x) * kSumWaves + wave;
+    const int tile = unit / a.slices;
     if (tile >= a.tiles) return;
-    const int c = static_cast<int>(unit % a.slices) * 64 * VEC + lane * VEC;
-    const int total = a.start[(int64_t(1) << a.o.log2_blocks) * a.o.rows];
-    const Tile t = tile_of(tile, a.T, total, ids, a.order);
-    const bool in = c < K;
-    float sum[VEC];
+    const int c = unit % a.slices * kSlice + lane * kVec;
+    const int left = K - c;
+    const int total = tokens_of(a);
+    const int begin = min(tile * a.T, total), end = min(begin + a.T, total);
+    if (begin == end) return;
+    const int before = row_at(ids, a.order, begin - 1, total), behind = row_at(ids, a.order, end, total);
+    float sum[kVec];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
-    int64_t row = -1;
+    for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+    int row = -1;
     bool first = true;
     auto flush = [&](bool last) {
-        if (in) {
-            if (first && t.open_front)
-                store_row<VEC>(a.partial + (tile * 2) * K + c, sum);
-            else if (last && t.open_back)
-                store_row<VEC>(a.partial + (tile * 2 + 1) * K + c, sum);
+        if (left > 0) {
+            if (first && row == before)
+                store_row(a.partial + static_cast<int64_t>(tile) * 2 * K + c, sum, left);
+            else if (last && row == behind)
+                store_row(a.partial + (static_cast<int64_t>(tile) * 2 + 1) * K + c, sum, left);
             else
-                write_row<TE, VEC>(dE, row * K + c, sum, a.scale, a.accumulate);
+                write_row(dE + static_cast<int64_t>(row) * K + c, left, sum, a.scale, a.accumulate);
         }
         first = false;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
+        for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
     };
-    for (int i = t.begin; i < t.end; ++i) {
-        const int m = a.order[i];
-        const int64_t v = static_cast<int64_t>(ids[m]);
-        if (v != row) {
-            if (row >= 0) flush(false);
-            row = v;
-        }
-        if (in) {
-            float d[VEC];
-            load_row<VEC>(dy + static_cast<int64_t>(m) * K + c, d);
+    for (int i0 = begin; i0 < end; i0 += 64) {
+        const int mine = i0 + lane < end ? a.order[i0 + lane] : 0;
+        const int rows = i0 + lane < end ? static_cast<int>(ids[mine]) : -1;
+        for (int b = 0; b < 64 && i0 + b < end; b += kBatch) {
+            Raw<TD> r[kBatch];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sum[j] += d[j];
+            for (int i = 0; i < kBatch; ++i) {
+                const int m = __builtin_amdgcn_readlane(mine, b + i);
+                if (left > 0 && i0 + b + i < end) r[i].load(dy + static_cast<int64_t>(m) * K + c, left);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (i0 + b + i >= end) break;
+                const int v = __builtin_amdgcn_readlane(rows, b + i);
+                if (v != row) {
+                    if (row >= 0) flush(false);
+                    row = v;
+                }
+                if (left > 0) {
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) sum[j] += r[i].at(j);
+                }
+            }
         }
     }
-    if (row >= 0) flush(true);
+    flush(true);
 }
 
-// Rows whose tokens lie in several tiles: the wave of the tile where the row
-// begins adds the shares in order.
-template <typename I, typename TE, int VEC>
+// Rows whose tokens lie in several tiles: a block for the tile where the row
+// begins.  Its waves add a run of the shares each, in order, then the first
+// adds theirs.
+template <typename I, typename TE>
 __global__ __launch_bounds__(kSumThreads) void embedding_join_kernel(const I* __restrict__ ids, TE* __restrict__ dE,
                                                                      SumArgs a) {
+    __shared__ float part[kSumWaves - 1][kVec][64];
     const int lane = threadIdx.x & 63;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tile = unit / a.slices;
-    if (tile >= a.tiles) return;
-    const int c = static_cast<int>(unit % a.slices) * 64 * VEC + lane * VEC;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = blockIdx.x / a.slices;
     const int K = a.K;
-    const int total = a.start[(int64_t(1) << a.o.log2_blocks) * a.o.rows];
-    const Tile t = tile_of(tile, a.T, total, ids, a.order);
-    if (!t.open_back || c >= K) return;
-    const int64_t row = static_cast<int64_t>(ids[a.order[t.end - 1]]);
+    const int total = tokens_of(a);
+    const int begin = tile * a.T, end = begin + a.T;
+    if (end >= total) return;
+    const int row = row_at(ids, a.order, end, total);
+    if (row != row_at(ids, a.order, end - 1, total)) return;  // no row goes on behind the tile
     const int64_t p = place_of(a.o, row);
-    if (a.start[p] < t.begin) return;  // it began in an earlier tile
-    const int64_t last = (a.start[p + 1] - 1) / a.T;
-    float sum[VEC];
-    load_row<VEC>(a.partial + (tile * 2 + 1) * K + c, sum);
-    for (int64_t i = tile + 1; i <= last; ++i) {
-        float d[VEC];
-        load_row<VEC>(a.partial + (i * 2) * K + c, d);
+    const int from = a.start[p], to = a.start[p + 1];
+    if (from < begin) return;  // it began in an earlier tile
+    // the shares: of the tile's last row, then of the first row of the next tiles
+    const int n = (to - 1) / a.T - tile + 1;
+    const int w0 = n * wave / kSumWaves, w1 = n * (wave + 1) / kSumWaves;
+    const int c = static_cast<int>(blockIdx.x % a.slices) * kSlice + lane * kVec;
+    const int left = K - c;
+    float sum[kVec];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] += d[j];
+    for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+    for (int i0 = w0; i0 < w1; i0 += kBatch) {
+        Raw<float> r[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t t = i0 + i == 0 ? tile * 2LL + 1 : (tile + i0 + i) * 2LL;
+            if (left > 0 && i0 + i < w1) r[i].load(a.partial + t * K + c, left);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i0 + i >= w1) break;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) sum[j] += r[i].at(j);
+        }
     }
-    write_row<TE, VEC>(dE, row * K + c, sum, a.scale, a.accumulate);
+    if (wave > 0) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) part[wave - 1][j][lane] = sum[j];
+    }
+    __syncthreads();
+    if (wave > 0 || left <= 0) return;
+#pragma unroll
+    for (int w = 0; w < kSumWaves - 1; ++w)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) sum[j] += part[w][j][lane];
+    write_row(dE + static_cast<int64_t>(row) * K + c, left, sum, a.scale, a.accumulate);
+}
+
+// ---------------------------------------------------------------- few tokens
+// Up to kSortThreads tokens in one launch: a block keeps the tokens of its rows
+// in LDS, one a thread and in order, ranks each by counting the ones that come
+// before it (a smaller row, or the same row earlier), and then its waves sum
+// and write the rows, or zeros, in columns of 64 lanes.
+template <typename I, typename TD, typename TE>
+__global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __restrict__ ids,
+                                                                     const TD* __restrict__ dy, TE* __restrict__ dE,
+                                                                     int M, int64_t V, int K, RowOrder o, float scale,
+                                                                     int accumulate) {
+    __shared__ int32_t list_row[kSortThreads], list_m[kSortThreads];  // as found
+    __shared__ int32_t sorted_m[kSortThreads];
+    __shared__ int32_t begin[kSortRows + 1];
+    __shared__ int32_t sums[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row = tid < M ? own_row(ids[tid], V, o).row : -1;
+    const uint64_t found = __ballot(row >= 0);
+    if (lane == 0) sums[wave] = __popcll(found);
+    for (int r = tid; r <= o.rows; r += kSortThreads) begin[r] = 0;
+    __syncthreads();
+    int at = __popcll(found & ((uint64_t(1) << lane) - 1)), n = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) at += sums[w];
+        n += sums[w];
+    }
+    if (row >= 0) {
+        list_row[at] = row;
+        list_m[at] = tid;
+    }
+    __syncthreads();
+    if (tid < n) {
+        const int r = list_row[tid];
+        int rank = 0, last = 1;
+        for (int i = 0; i < n; ++i) {
+            const int other = list_row[i];
+            rank += other < r || (other == r && i < tid);
+            last &= !(other == r && i > tid);
+        }
+        sorted_m[rank] = list_m[tid];
+        if (last) begin[r + 1] = rank + 1;  // where the row ends
+    }
+    __syncthreads();
+    // rows without tokens end where the row before ends; a wave scans 64 at a time
+    if (wave == 0) {
+        int carry = 0;
+        for (int r0 = 1; r0 <= o.rows; r0 += 64) {
+            int e = r0 + lane <= o.rows ? begin[r0 + lane] : 0;
+            for (int off = 1; off < 64; off <<= 1) {
+                const int t = __shfl_up(e, off);
+                if (lane >= off) e = max(e, t);
+            }
+            e = max(e, carry);
+            if (r0 + lane <= o.rows) begin[r0 + lane] = e;
+            carry = __builtin_amdgcn_readlane(e, 63);
+        }
+    }
+    __syncthreads();
+    const int slices = (K + kSlice - 1) / kSlice;
+    const int units = o.rows * slices;
+    for (int u = wave; u < units; u += kSortWaves) {
+        const int r = u / slices;
+        const int64_t v = (static_cast<int64_t>(r) << o.log2_blocks) + blockIdx.x;
+        if (v >= V) break;
+        const int from = __builtin_amdgcn_readfirstlane(begin[r]), to = __builtin_amdgcn_readfirstlane(begin[r + 1]);
+        if (from == to && accumulate) continue;
+        const int c = (u - r * slices) * kSlice + lane * kVec;
+        const int left = K - c;
+        if (left <= 0) continue;
+        float sum[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+        for (int i0 = from; i0 < to; i0 += kBatch) {
+            Raw<TD> d[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (i0 + i < to) d[i].load(dy + static_cast<int64_t>(sorted_m[i0 + i]) * K + c, left);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (i0 + i >= to) break;
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) sum[j] += d[i].at(j);
+            }
+        }
+        write_row(dE + v * K + c, left, sum, scale, accumulate);
+    }
 }
 
 // -------------------------------------------------------------------- sizes
@@ -420,17 +577,15 @@ size_t start_bytes(const RowOrder& o) {
 
 template <typename I, typename TE, typename TY>
 ss1_status forward_t(const EmbeddingArgs& a) {
-    const int vec = a.K % 8 == 0 ? 8 : 1;
-    const int runs = (a.K + kSlices * 64 * vec - 1) / (kSlices * 64 * vec);
+    const int runs = (a.K + kSlices * kSlice - 1) / (kSlices * kSlice);
     // a grid's threads are numbered in 32 bits
     const int64_t most = ((int64_t(1) << 24) - 1) / runs * kSumWaves;
-    auto kern = vec == 8 ? &embedding_forward_kernel<I, TE, TY, 8> : &embedding_forward_kernel<I, TE, TY, 1>;
     for (int64_t at = 0; at < a.M; at += most) {
         const int64_t m = a.M - at < most ? a.M - at : most;
-        hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((m * runs + kSumWaves - 1) / kSumWaves)),
-                           dim3(kSumThreads), 0, static_cast<hipStream_t>(a.stream),
-                           static_cast<const I*>(a.ids) + at, m, a.V, a.K, runs, a.scale,
-                           static_cast<const TE*>(a.E), static_cast<TY*>(a.y) + at * a.K);
+        hipLaunchKernelGGL((embedding_forward_kernel<I, TE, TY>),
+                           dim3(static_cast<unsigned>((m * runs + kSumWaves - 1) / kSumWaves)), dim3(kSumThreads), 0,
+                           static_cast<hipStream_t>(a.stream), static_cast<const I*>(a.ids) + at, m, a.V, a.K, runs,
+                           a.scale, static_cast<const TE*>(a.E), static_cast<TY*>(a.y) + at * a.K);
     }
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
@@ -438,6 +593,16 @@ ss1_status forward_t(const EmbeddingArgs& a) {
 template <typename I, typename TD, typename TE>
 ss1_status backward_t(const EmbeddingArgs& a) {
     const RowOrder o = row_order(a.V);
+    const hipStream_t stream = static_cast<hipStream_t>(a.stream);
+    const I* ids = static_cast<const I*>(a.ids);
+    const TD* dy = static_cast<const TD*>(a.dy);
+    TE* dE = static_cast<TE*>(a.dE);
+    const unsigned blocks = 1u << o.log2_blocks;
+    if (a.M <= kSortThreads) {
+        hipLaunchKernelGGL((embedding_few_kernel<I, TD, TE>), dim3(blocks), dim3(kSortThreads), 0, stream, ids, dy, dE,
+                           static_cast<int>(a.M), a.V, a.K, o, a.scale, a.accumulate);
+        return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
+    }
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     SumArgs s{};
     int32_t* start = reinterpret_cast<int32_t*>(ws);
@@ -447,27 +612,30 @@ ss1_status backward_t(const EmbeddingArgs& a) {
     s.partial = reinterpret_cast<float*>(ws + start_bytes(o) + up_to(a.M * 4, 16));
     s.V = a.V;
     s.T = tile_tokens(a.M);
-    s.tiles = (a.M + s.T - 1) / s.T;
+    s.tiles = static_cast<int32_t>((a.M + s.T - 1) / s.T);
     s.K = a.K;
     s.accumulate = a.accumulate;
     s.o = o;
     s.scale = a.scale;
-    const int vec = a.K % 8 == 0 ? 8 : 1;
-    s.slices = (a.K + 64 * vec - 1) / (64 * vec);
+    s.slices = (a.K + kSlice - 1) / kSlice;
     s.sum_blocks = (s.tiles * s.slices + kSumWaves - 1) / kSumWaves;
-    const int64_t zero_blocks = a.accumulate ? 0 : (a.V + kZeroRows * kSumWaves - 1) / (kZeroRows * kSumWaves);
-    const hipStream_t stream = static_cast<hipStream_t>(a.stream);
-    const I* ids = static_cast<const I*>(a.ids);
-    TE* dE = static_cast<TE*>(a.dE);
-    hipLaunchKernelGGL((embedding_sort_kernel<I>), dim3(1u << o.log2_blocks), dim3(kSortThreads), 0, stream, ids,
-                       static_cast<int>(a.M), a.V, o, start, order);
-    auto sum = vec == 8 ? &embedding_sum_kernel<I, TD, TE, 8> : &embedding_sum_kernel<I, TD, TE, 1>;
-    if (s.sum_blocks + zero_blocks > 0)
-        hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(s.sum_blocks + zero_blocks)), dim3(kSumThreads), 0, stream,
-                           ids, static_cast<const TD*>(a.dy), dE, s);
-    auto join = vec == 8 ? &embedding_join_kernel<I, TE, 8> : &embedding_join_kernel<I, TE, 1>;
-    if (s.tiles > 1)
-        hipLaunchKernelGGL(join, dim3(static_cast<unsigned>(s.sum_blocks)), dim3(kSumThreads), 0, stream, ids, dE, s);
+    // rows that the sort's launch clears: whole 16-byte vectors, but for the
+    // rows at the table's end
+    int64_t zero_vecs = 0, zero_blocks = 0;
+    if (!a.accumulate) {
+        const int64_t row = static_cast<int64_t>(a.K) * sizeof(TE);
+        s.zeroed = kZeroFirst / row < a.V ? kZeroFirst / row / 8 * 8 : a.V / 8 * 8;
+        zero_vecs = s.zeroed * row / 16;
+        zero_blocks = (a.V - s.zeroed + kZeroRows * kSumWaves - 1) / (kZeroRows * kSumWaves);
+    }
+    hipLaunchKernelGGL((embedding_sort_kernel<I>),
+                       dim3(blocks + static_cast<unsigned>((zero_vecs + kZeroVecs - 1) / kZeroVecs)),
+                       dim3(kSortThreads), 0, stream, ids, static_cast<int>(a.M), a.V, o, start, order,
+                       reinterpret_cast<u32x4*>(dE), zero_vecs);
+    hipLaunchKernelGGL((embedding_sum_kernel<I, TD, TE>), dim3(static_cast<unsigned>(s.sum_blocks + zero_blocks)),
+                       dim3(kSumThreads), 0, stream, ids, dy, dE, s);
+    hipLaunchKernelGGL((embedding_join_kernel<I, TE>), dim3(static_cast<unsigned>(s.tiles * s.slices)),
+                       dim3(kSumThreads), 0, stream, ids, dE, s);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
@@ -492,6 +660,7 @@ ss1_status launch_embedding_forward(const EmbeddingArgs& a) {
 }
 
 size_t embedding_backward_workspace(int64_t M, int64_t V, int32_t K) {
+    if (M <= kSortThreads) return 0;
     const RowOrder o = row_order(V);
     const int64_t T = tile_tokens(M), tiles = (M + T - 1) / T;
     return start_bytes(o) + static_cast<size_t>(up_to(M * 4, 16)) + static_cast<size_t>(tiles) * 2 * K * 4;

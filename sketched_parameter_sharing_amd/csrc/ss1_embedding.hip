@@ -24,6 +24,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ss1_model_ops.h"
 
 namespace ss1 {
@@ -38,95 +40,105 @@ constexpr int kMinBlocks = 256;  // sorting blocks at least (one a compute unit)
 constexpr int kTile = 16;        // tokens of a summing wave, up to kMaxTiles waves a column slice
 constexpr int kMaxTiles = 1024;
 constexpr int kZeroVecs = 4 * kSortThreads;  // 16-byte vectors that a block of the sort's launch clears
-constexpr int64_t kZeroFirst = int64_t(32) << 20;
+constexpr int64_t kZeroFirst = int64_t(64) << 20;
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr int kZeroRows = 16;    // rows of a zeroing wave
 
 // ------------------------------------------------------------ element access
-// Eight consecutive columns of a row, of which n > 0 are left; rows of an odd
-// width start anywhere, so the vectors are not aligned (one instruction all the
-// same, at full speed where the address is).
-constexpr int kVec = 8;
+// VEC consecutive columns of a row (16 bytes of the type that is read most), of
+// which n > 0 are left; rows of an odd width start anywhere, so the vectors are
+// not aligned (one instruction all the same, at full speed where the address
+// is).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_any2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_any4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_any2 __attribute__((aligned(2)));
 
-template <typename T>
-struct Raw;
-template <>
-struct Raw<uint16_t> {
-    u32x4 a;
-    __device__ __forceinline__ void load(const uint16_t* p, int n) {
-        if (n >= kVec) {
-            a = *reinterpret_cast<const u32x4_any2*>(p);
-        } else {
-            a = u32x4{0, 0, 0, 0};
+template <typename T, int VEC>
+struct Raw {
+    static constexpr int kWords = VEC * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if (n >= VEC) {
+            if constexpr (kWords == 2) {
+                const u32x2 a = *reinterpret_cast<const u32x2_any2*>(p);
+                w[0] = a[0];
+                w[1] = a[1];
+            } else {
 #pragma unroll
-            for (int i = 0; i < kVec - 1; ++i)
-                if (i < n) a[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+                for (int i = 0; i < kWords; i += 4) {
+                    using V = typename std::conditional<sizeof(T) == 2, u32x4_any2, u32x4_any4>::type;
+                    const u32x4 a = *reinterpret_cast<const V*>(p + i * 4 / static_cast<int>(sizeof(T)));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[i + j] = a[j];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+            for (int i = 0; i < VEC - 1; ++i)
+                if (i < n) {
+                    if constexpr (sizeof(T) == 2) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+                    else w[i] = __float_as_uint(p[i]);
+                }
         }
     }
     __device__ __forceinline__ float at(int i) const {
-        return __uint_as_float(i & 1 ? a[i / 2] & 0xFFFF0000u : a[i / 2] << 16);
+        if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        else return __uint_as_float(w[i]);
     }
-};
-template <>
-struct Raw<float> {
-    u32x4 a, b;
-    __device__ __forceinline__ void load(const float* p, int n) {
-        if (n >= kVec) {
-            a = *reinterpret_cast<const u32x4_any4*>(p);
-            b = *reinterpret_cast<const u32x4_any4*>(p + 4);
-        } else {
-            a = b = u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i < n) a[i] = __float_as_uint(p[i]);
-                if (i + 4 < n) b[i] = __float_as_uint(p[i + 4]);
-            }
-        }
-    }
-    __device__ __forceinline__ float at(int i) const { return __uint_as_float(i < 4 ? a[i] : b[i - 4]); }
 };
 
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
-__device__ __forceinline__ void store_row(float* p, const float (&v)[kVec], int n) {
-    if (n >= kVec) {
-        *reinterpret_cast<u32x4_any4*>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                  __float_as_uint(v[3])};
-        *reinterpret_cast<u32x4_any4*>(p + 4) = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                                      __float_as_uint(v[6]), __float_as_uint(v[7])};
+template <int VEC>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[VEC], int n) {
+    if (n >= VEC) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4)
+            *reinterpret_cast<u32x4_any4*>(p + i) = u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                                          __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])};
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec - 1; ++i)
+        for (int i = 0; i < VEC - 1; ++i)
             if (i < n) p[i] = v[i];
     }
 }
-__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[kVec], int n) {
-    if (n >= kVec) {
-        *reinterpret_cast<u32x4_any2*>(p) =
-            u32x4{bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16,
-                  bf16_bits(v[4]) | bf16_bits(v[5]) << 16, bf16_bits(v[6]) | bf16_bits(v[7]) << 16};
+template <int VEC>
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[VEC], int n) {
+    if (n >= VEC) {
+        uint32_t w[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) w[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
+        if constexpr (VEC == 8) *reinterpret_cast<u32x4_any2*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+        else *reinterpret_cast<u32x2_any2*>(p) = u32x2{w[0], w[1]};
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec - 1; ++i)
+        for (int i = 0; i < VEC - 1; ++i)
             if (i < n) p[i] = static_cast<uint16_t>(bf16_bits(v[i]));
     }
 }
 
 // -------------------------------------------------------------------- forward
-// A wave takes one token and a run of kSlices * 64 * 8 columns.
+// A wave takes one token and a run of kSlices * 64 * VEC columns.
 constexpr int kSlices = 4;
-constexpr int kSlice = 64 * kVec;
+
+// Columns of a lane, and of a wave.
+template <typename T>
+constexpr int kVecOf = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+constexpr int kSliceOf = 64 * kVecOf<T>;
 
 template <typename I, typename TE, typename TY>
 __global__ __launch_bounds__(kSumThreads) void embedding_forward_kernel(const I* __restrict__ ids, int64_t M, int64_t V,
                                                                         int K, int runs, float scale,
                                                                         const TE* __restrict__ E,
                                                                         TY* __restrict__ y) {
+    constexpr int kVec = kVecOf<TE>, kSlice = kSliceOf<TE>;
     const int lane = threadIdx.x & 63;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t m = unit / runs;
@@ -134,7 +146,7 @@ __global__ __launch_bounds__(kSumThreads) void embedding_forward_kernel(const I*
     const int c0 = static_cast<int>(unit % runs) * kSlices * kSlice + lane * kVec;
     const int64_t id = static_cast<int64_t>(ids[m]);
     const bool real = id >= 0 && id < V;
-    Raw<TE> r[kSlices];
+    Raw<TE, kVec> r[kSlices];
 #pragma unroll
     for (int i = 0; i < kSlices; ++i) {
         const int c = c0 + i * kSlice;
@@ -147,7 +159,7 @@ __global__ __launch_bounds__(kSumThreads) void embedding_forward_kernel(const I*
         float v[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[j] = real ? r[i].at(j) * scale : 0.0f;
-        store_row(y + m * K + c, v, K - c);
+        store_row<kVec>(y + m * K + c, v, K - c);
     }
 }
 
@@ -170,12 +182,12 @@ struct Own {
 };
 template <typename I>
 __device__ __forceinline__ Own own_row(I id, int64_t V, const RowOrder& o) {
-    const int64_t v = static_cast<int64_t>(id);
-    const bool real = v >= 0 && v < V;
-    const int owner = static_cast<int>(v & ((int64_t(1) << o.log2_blocks) - 1));
+    const bool real = static_cast<uint64_t>(static_cast<int64_t>(id)) < static_cast<uint64_t>(V);
+    const uint32_t v = static_cast<uint32_t>(id);  // V < 2^29
+    const uint32_t owner = v & ((1u << o.log2_blocks) - 1);
     Own r;
-    r.row = real && owner == static_cast<int>(blockIdx.x) ? static_cast<int>(v >> o.log2_blocks) : -1;
-    r.before = real && owner < static_cast<int>(blockIdx.x);
+    r.row = real && owner == blockIdx.x ? static_cast<int>(v >> o.log2_blocks) : -1;
+    r.before = real && owner < blockIdx.x;
     return r;
 }
 
@@ -290,11 +302,11 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
 
 // ------------------------------------------------------------------------ sum
 // dE at p from the sum of a row's tokens (n columns left).
-template <typename T>
+template <typename T, int kVec>
 __device__ __forceinline__ void write_row(T* p, int n, const float (&sum)[kVec], float scale, bool accumulate) {
     float v[kVec];
     if (accumulate) {
-        Raw<T> r;
+        Raw<T, kVec> r;
         r.load(p, n);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[j] = r.at(j) + sum[j] * scale;
@@ -302,7 +314,7 @@ __device__ __forceinline__ void write_row(T* p, int n, const float (&sum)[kVec],
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[j] = sum[j] * scale;
     }
-    store_row(p, v, n);
+    store_row<kVec>(p, v, n);
 }
 
 struct SumArgs {
@@ -337,6 +349,7 @@ constexpr int kBatch = 8;  // rows of dy, or shares, whose loads are in flight t
 template <typename I, typename TD, typename TE>
 __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __restrict__ ids, const TD* __restrict__ dy,
                                                                     TE* __restrict__ dE, SumArgs a) {
+    constexpr int kVec = kVecOf<TD>, kSlice = kSliceOf<TD>;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = a.K;
@@ -348,11 +361,11 @@ __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __r
             empty = a.start[p] == a.start[p + 1];
         }
         uint64_t rows = __ballot(empty);
-        const float zero[kVec] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        const float zero[kVec] = {};
         while (rows) {
             const int r = __builtin_ctzll(rows);
             rows &= rows - 1;
-            for (int c = lane * kVec; c < K; c += kSlice) store_row(dE + (v0 + r) * K + c, zero, K - c);
+            for (int c = lane * kVec; c < K; c += kSlice) store_row<kVec>(dE + (v0 + r) * K + c, zero, K - c);
         }
         return;
     }
@@ -373,9 +386,9 @@ __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __r
     auto flush = [&](bool last) {
         if (left > 0) {
             if (first && row == before)
-                store_row(a.partial + static_cast<int64_t>(tile) * 2 * K + c, sum, left);
+                store_row<kVec>(a.partial + static_cast<int64_t>(tile) * 2 * K + c, sum, left);
             else if (last && row == behind)
-                store_row(a.partial + (static_cast<int64_t>(tile) * 2 + 1) * K + c, sum, left);
+                store_row<kVec>(a.partial + (static_cast<int64_t>(tile) * 2 + 1) * K + c, sum, left);
             else
                 write_row(dE + static_cast<int64_t>(row) * K + c, left, sum, a.scale, a.accumulate);
         }
@@ -387,7 +400,7 @@ __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __r
         const int mine = i0 + lane < end ? a.order[i0 + lane] : 0;
         const int rows = i0 + lane < end ? static_cast<int>(ids[mine]) : -1;
         for (int b = 0; b < 64 && i0 + b < end; b += kBatch) {
-            Raw<TD> r[kBatch];
+            Raw<TD, kVec> r[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int m = __builtin_amdgcn_readlane(mine, b + i);
@@ -414,9 +427,10 @@ __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __r
 // Rows whose tokens lie in several tiles: a block for the tile where the row
 // begins.  Its waves add a run of the shares each, in order, then the first
 // adds theirs.
-template <typename I, typename TE>
+template <typename I, typename TD, typename TE>
 __global__ __launch_bounds__(kSumThreads) void embedding_join_kernel(const I* __restrict__ ids, TE* __restrict__ dE,
                                                                      SumArgs a) {
+    constexpr int kVec = kVecOf<TD>, kSlice = kSliceOf<TD>;
     __shared__ float part[kSumWaves - 1][kVec][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -439,7 +453,7 @@ __global__ __launch_bounds__(kSumThreads) void embedding_join_kernel(const I* __
 #pragma unroll
     for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
     for (int i0 = w0; i0 < w1; i0 += kBatch) {
-        Raw<float> r[kBatch];
+        Raw<float, kVec> r[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int64_t t = i0 + i == 0 ? tile * 2LL + 1 : (tile + i0 + i) * 2LL;
@@ -447,9 +461,10 @@ __global__ __launch_bounds__(kSumThreads) void embedding_join_kernel(const I* __
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            if (i0 + i >= w1) break;
+            if (i0 + i < w1) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) sum[j] += r[i].at(j);
+                for (int j = 0; j < kVec; ++j) sum[j] += r[i].at(j);
+            }
         }
     }
     if (wave > 0) {
@@ -466,6 +481,8 @@ __global__ __launch_bounds__(kSumThreads) void embedding_join_kernel(const I* __
 }
 
 // ---------------------------------------------------------------- few tokens
+constexpr int kFewBatch = 16;
+
 // Up to kSortThreads tokens in one launch: a block keeps the tokens of its rows
 // in LDS, one a thread and in order, ranks each by counting the ones that come
 // before it (a smaller row, or the same row earlier), and then its waves sum
@@ -475,6 +492,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __
                                                                      const TD* __restrict__ dy, TE* __restrict__ dE,
                                                                      int M, int64_t V, int K, RowOrder o, float scale,
                                                                      int accumulate) {
+    constexpr int kVec = kVecOf<TD>, kSlice = kSliceOf<TD>;
     __shared__ int32_t list_row[kSortThreads], list_m[kSortThreads];  // as found
     __shared__ int32_t sorted_m[kSortThreads];
     __shared__ int32_t begin[kSortRows + 1];
@@ -538,16 +556,17 @@ __global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __
         float sum[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
-        for (int i0 = from; i0 < to; i0 += kBatch) {
-            Raw<TD> d[kBatch];
+        for (int i0 = from; i0 < to; i0 += kFewBatch) {
+            Raw<TD, kVec> d[kFewBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
+            for (int i = 0; i < kFewBatch; ++i)
                 if (i0 + i < to) d[i].load(dy + static_cast<int64_t>(sorted_m[i0 + i]) * K + c, left);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (i0 + i >= to) break;
+            for (int i = 0; i < kFewBatch; ++i) {
+                if (i0 + i < to) {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) sum[j] += d[i].at(j);
+                    for (int j = 0; j < kVec; ++j) sum[j] += d[i].at(j);
+                }
             }
         }
         write_row(dE + v * K + c, left, sum, scale, accumulate);
@@ -577,7 +596,8 @@ size_t start_bytes(const RowOrder& o) {
 
 template <typename I, typename TE, typename TY>
 ss1_status forward_t(const EmbeddingArgs& a) {
-    const int runs = (a.K + kSlices * kSlice - 1) / (kSlices * kSlice);
+    constexpr int kRun = kSlices * kSliceOf<TE>;
+    const int runs = (a.K + kRun - 1) / kRun;
     // a grid's threads are numbered in 32 bits
     const int64_t most = ((int64_t(1) << 24) - 1) / runs * kSumWaves;
     for (int64_t at = 0; at < a.M; at += most) {
@@ -617,7 +637,7 @@ ss1_status backward_t(const EmbeddingArgs& a) {
     s.accumulate = a.accumulate;
     s.o = o;
     s.scale = a.scale;
-    s.slices = (a.K + kSlice - 1) / kSlice;
+    s.slices = (a.K + kSliceOf<TD> - 1) / kSliceOf<TD>;
     s.sum_blocks = (s.tiles * s.slices + kSumWaves - 1) / kSumWaves;
     // rows that the sort's launch clears: whole 16-byte vectors, but for the
     // rows at the table's end
@@ -634,7 +654,7 @@ ss1_status backward_t(const EmbeddingArgs& a) {
                        reinterpret_cast<u32x4*>(dE), zero_vecs);
     hipLaunchKernelGGL((embedding_sum_kernel<I, TD, TE>), dim3(static_cast<unsigned>(s.sum_blocks + zero_blocks)),
                        dim3(kSumThreads), 0, stream, ids, dy, dE, s);
-    hipLaunchKernelGGL((embedding_join_kernel<I, TE>), dim3(static_cast<unsigned>(s.tiles * s.slices)),
+    hipLaunchKernelGGL((embedding_join_kernel<I, TD, TE>), dim3(static_cast<unsigned>(s.tiles * s.slices)),
                        dim3(kSumThreads), 0, stream, ids, dE, s);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }

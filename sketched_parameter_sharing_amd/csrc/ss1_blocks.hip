@@ -36,11 +36,68 @@ __device__ __forceinline__ void pad_scales(uint8_t* row, int64_t block, int64_t 
         for (int64_t j = blocks; j < cols; ++j) row[j] = 127;
 }
 
-template <typename T, bool VEC>
+// A thread's columns 2p and 2p + 1 of the tile in LDS, 32 rows of them: row i as
+// the bits of the two values.
+template <typename T>
+struct Pairs;
+
+template <>
+struct Pairs<uint16_t> {
+    uint32_t w[32];
+    __device__ __forceinline__ void load(const uint16_t* p, int pitch) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + i * pitch);
+    }
+    __device__ __forceinline__ uint32_t bits(int i, int h) const { return h ? w[i] & 0xFFFF0000u : w[i] << 16; }
+    __device__ __forceinline__ void tops(uint32_t (&t)[2]) const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = max_halves(m, w[i]);
+        t[0] = m << 16;
+        t[1] = m & 0xFFFF0000u;
+    }
+    // codes of rows 4j .. 4j + 3 of column h
+    __device__ __forceinline__ uint32_t codes(int j, int h, float scale) const {
+        const uint32_t sel = h ? 0x07060302u : 0x05040100u;  // the halves h of two words
+        const uint32_t lo = __builtin_amdgcn_perm(w[4 * j + 1], w[4 * j], sel);
+        const uint32_t hi = __builtin_amdgcn_perm(w[4 * j + 3], w[4 * j + 2], sel);
+        return codes2(hi, scale, codes2(lo, scale, 0, false), true);
+    }
+};
+
+template <>
+struct Pairs<float> {
+    uint32_t w[2][32];
+    __device__ __forceinline__ void load(const float* p, int pitch) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + i * pitch);
+            w[0][i] = v.x;
+            w[1][i] = v.y;
+        }
+    }
+    __device__ __forceinline__ uint32_t bits(int i, int h) const { return w[h][i]; }
+    __device__ __forceinline__ void tops(uint32_t (&t)[2]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            t[h] = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) t[h] = larger(t[h], w[h][i] & 0x7FFFFFFFu);
+        }
+    }
+    __device__ __forceinline__ uint32_t codes(int j, int h, float scale) const {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[h][4 * j + i]);
+        return codes2(v[2], v[3], scale, codes2(v[0], v[1], scale, 0, false), true);
+    }
+};
+
+template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __restrict__ x, int64_t R, int64_t C,
                                                                    uint32_t col_blocks, BlocksView q, BlocksView qt) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    T* tile = reinterpret_cast<T*>(smem);  // [128][128 + pad], only with qt
+    T* tile = reinterpret_cast<T*>(smem);  // [128][kPitch], only with qt
     constexpr int kPitch = kB + 16 / static_cast<int>(sizeof(T));
     __shared__ uint32_t s_top[4][kB];
     __shared__ uint32_t s_wave[kThreads / 64];
@@ -48,68 +105,43 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     const int64_t bc = blockIdx.x % col_blocks, br = blockIdx.x / col_blocks;
     const int64_t r0 = br * kB, c0 = bc * kB;
 
-    float v[kPasses][8];
+    Eight<T> v[kPasses];
     uint32_t top[kPasses];
+    bool special[kPasses];
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         const int64_t r = r0 + p * kRowsAPass + (tid >> 4);
-        if (r < R) {
-            load8<VEC>(x + r * C, c0 + l16 * 8, C, v[p]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-        }
+        v[p].clear();
+        if (r < R) v[p].load(x + r * C, c0 + l16 * 8, C);
     }
     uint32_t all = 0;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-        uint32_t u = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t f = finite_size(v[p][i]);
-            u = u > f ? u : f;
-        }
-        top[p] = max16(u);
-        all = all > top[p] ? all : top[p];
+        top[p] = max16(finite_top(v[p], special[p]));
+        all = larger(all, top[p]);
+        if (qt.codes) v[p].put(tile + (p * kRowsAPass + (tid >> 4)) * kPitch + l16 * 8);
     }
-    if (qt.codes) {
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            T* t = tile + (p * kRowsAPass + (tid >> 4)) * kPitch + l16 * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (sizeof(T) == 2)
-                    t[i] = static_cast<uint16_t>(__float_as_uint(v[p][i]) >> 16);
-                else
-                    t[i] = v[p][i];
-            }
-        }
-    }
-    if (q.shift || qt.shift) {  // the tile's maximum: over the wave's four rows, then the waves
-        for (int off = 16; off < 64; off <<= 1) {
-            const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), off));
-            all = all > o ? all : o;
-        }
+    const bool whole = q.shift || qt.shift;
+    if (whole) {  // the tile's maximum: over the wave's four rows, then the waves
+        for (int off = 16; off < 64; off <<= 1)
+            all = larger(all, static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), off)));
         if ((tid & 63) == 0) s_wave[tid >> 6] = all;
     }
-    __syncthreads();
-    if (q.shift || qt.shift) {
+    if (whole || qt.codes) __syncthreads();
+    if (whole) {
         all = s_wave[0];
 #pragma unroll
-        for (int w = 1; w < kThreads / 64; ++w) all = all > s_wave[w] ? all : s_wave[w];
+        for (int w = 1; w < kThreads / 64; ++w) all = larger(all, s_wave[w]);
     }
-    const int64_t blocks = q.codes ? q.code_cols / kB : 0;
     if (q.codes) {
+        const int64_t blocks = q.code_cols / kB;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
             const int64_t r = r0 + p * kRowsAPass + (tid >> 4);
             if (r >= R) continue;
             const uint32_t byte = scale_byte(q.shift ? all : top[p]);
-            const float inv = inverse_scale(byte);
-            uint2 w;
-            w.x = codes4(v[p][0], v[p][1], v[p][2], v[p][3], inv);
-            w.y = codes4(v[p][4], v[p][5], v[p][6], v[p][7], inv);
-            *reinterpret_cast<uint2*>(q.codes + r * q.code_cols + c0 + l16 * 8) = w;
+            *reinterpret_cast<uint2*>(q.codes + r * q.code_cols + c0 + l16 * 8) =
+                codes_of(v[p], scale_of(byte), special[p]);
             if (l16 == 0 && (q.shift == 0 || r == r0)) {
                 uint8_t* srow = q.scale + (r >> q.shift) * q.scale_cols;
                 srow[bc] = static_cast<uint8_t>(byte);
@@ -120,54 +152,49 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     if (!qt.codes) return;
     // columns 2 * pair and 2 * pair + 1, rows 32 * part ..
     const int pair = tid & 63, part = tid >> 6;
-    float lo[32], hi[32];
-    uint32_t tl = 0, th = 0;
+    Pairs<T> t;
+    t.load(tile + part * 32 * kPitch + 2 * pair, kPitch);
+    uint32_t tops[2];
+    t.tops(tops);
+    const bool odd = larger(tops[0], tops[1]) >= kInf;
+    if (odd) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const T* t = tile + (part * 32 + i) * kPitch + 2 * pair;
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(t);
-            lo[i] = __uint_as_float(w << 16);
-            hi[i] = __uint_as_float(w & 0xFFFF0000u);
-        } else {
-            const float2 w = *reinterpret_cast<const float2*>(t);
-            lo[i] = w.x;
-            hi[i] = w.y;
+        for (int h = 0; h < 2; ++h) {
+            tops[h] = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) tops[h] = larger(tops[h], finite_size(t.bits(i, h)));
         }
-        const uint32_t a = finite_size(lo[i]), b = finite_size(hi[i]);
-        tl = tl > a ? tl : a;
-        th = th > b ? th : b;
     }
-    s_top[part][2 * pair] = tl;
-    s_top[part][2 * pair + 1] = th;
-    __syncthreads();
-    const int64_t tblocks = qt.code_cols / kB;
+    if (!qt.shift) {
+        s_top[part][2 * pair] = tops[0];
+        s_top[part][2 * pair + 1] = tops[1];
+        __syncthreads();
+    }
+    const int64_t blocks = qt.code_cols / kB;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int col = 2 * pair + h;
         const int64_t c = c0 + col;
         if (c >= C) continue;
-        uint32_t t = all;
-        if (!qt.shift) {
-            t = s_top[0][col];
+        uint32_t m = all;
+        if (!qt.shift) m = larger(larger(s_top[0][col], s_top[1][col]), larger(s_top[2][col], s_top[3][col]));
+        const uint32_t byte = scale_byte(m);
+        const float scale = scale_of(byte);
+        uint32_t w[8];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) t = t > s_top[w][col] ? t : s_top[w][col];
+        for (int j = 0; j < 8; ++j) w[j] = t.codes(j, h, scale);
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if ((t.bits(i, h) & 0x7FFFFFFFu) >= kInf) w[i / 4] |= 0x7Fu << (8 * (i & 3));
         }
-        const uint32_t byte = scale_byte(t);
-        const float inv = inverse_scale(byte);
-        uint4 w[2];
-        uint32_t* o = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o[i] = h ? codes4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3], inv)
-                     : codes4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3], inv);
         uint4* out = reinterpret_cast<uint4*>(qt.codes + c * qt.code_cols + r0 + part * 32);
-        out[0] = w[0];
-        out[1] = w[1];
+        out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        out[1] = make_uint4(w[4], w[5], w[6], w[7]);
         if (part == 0 && (qt.shift == 0 || col == 0)) {
             uint8_t* srow = qt.scale + (c >> qt.shift) * qt.scale_cols;
             srow[br] = static_cast<uint8_t>(byte);
-            pad_scales(srow, br, tblocks, qt.scale_cols);
+            pad_scales(srow, br, blocks, qt.scale_cols);
         }
     }
 }
@@ -176,7 +203,7 @@ template <typename T>
 ss1_status launch_t(const QuantizeBlocksArgs& a) {
     const size_t pitch = kB + 16 / sizeof(T);
     const size_t lds = a.qt.codes ? kB * pitch * sizeof(T) : 0;
-    auto kern = a.C % 8 == 0 ? &quantize_blocks_kernel<T, true> : &quantize_blocks_kernel<T, false>;
+    auto kern = &quantize_blocks_kernel<T>;
     if (lds > 48 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                                hipFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(lds)) != hipSuccess)

@@ -19,6 +19,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ss1_blocks.h"
 #include "ss1_device.h"
 #include "ss1_dma.h"
@@ -265,11 +267,6 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
 // loads return in order, and the weight's are in flight meanwhile.
 constexpr int kUnit = 4;  // blocks of 128 of a unit: the scales of one word
 
-template <typename X>
-struct RawOf {
-    uint4 v[sizeof(X) / 2];
-};
-
 template <typename X, bool F32, int NW>
 __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksView b, const X* __restrict__ x,
                                                            int64_t xcols, void* __restrict__ y, int M, int N, int K) {
@@ -290,13 +287,12 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
     uint8_t* s_scale = smem + static_cast<size_t>(M) * pitch;
     const int items = INSIDE ? M * nkb : 0;
     constexpr int G = NW * 4;
-    float v[INSIDE ? kAhead : 1][8];
-    auto fetch = [&](int it, float (&r)[8]) {
+    using T = typename std::conditional<INSIDE, X, float>::type;
+    blocks::Eight<T> v[INSIDE ? kAhead : 1];
+    auto fetch = [&](int it, blocks::Eight<T>& r) {
         if constexpr (INSIDE) {
             const int m = it / nkb, kb = it % nkb;
-            const X* row = x + m * xcols;
-            if (xcols % 8 == 0) blocks::load8<true>(row, kb * kKS + (lane & 15) * 8, xcols, r);
-            else blocks::load8<false>(row, kb * kKS + (lane & 15) * 8, xcols, r);
+            r.load(x + m * xcols, kb * kKS + (lane & 15) * 8, xcols);
         }
     };
     if constexpr (INSIDE) {
@@ -340,19 +336,11 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
     if (u0 < u1) load(u0, cur);
 
     if constexpr (INSIDE) {
-        auto put = [&](int it, const float (&r)[8]) {
+        auto put = [&](int it, const blocks::Eight<T>& r) {
             const int m = it / nkb, kb = it % nkb;
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t f = blocks::finite_size(r[i]);
-                top = top > f ? top : f;
-            }
-            const uint32_t byte = blocks::scale_byte(blocks::max16(top));
-            const float inv = blocks::inverse_scale(byte);
-            uint2 w;
-            w.x = blocks::codes4(r[0], r[1], r[2], r[3], inv);
-            w.y = blocks::codes4(r[4], r[5], r[6], r[7], inv);
+            bool special;
+            const uint32_t byte = blocks::scale_byte(blocks::max16(blocks::finite_top(r, special)));
+            const uint2 w = blocks::codes_of(r, blocks::scale_of(byte), special);
             *reinterpret_cast<uint2*>(smem + m * pitch + kb * kKS + (lane & 15) * 8) = w;
             if ((lane & 15) == 0) s_scale[m * nkb + kb] = static_cast<uint8_t>(byte);
         };

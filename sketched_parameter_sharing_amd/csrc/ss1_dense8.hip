@@ -99,21 +99,27 @@ __device__ __forceinline__ Wide widen(const i32x8& v, float scale) {
 // buffers, filled by direct loads NSTG - 1 stages ahead.  Rows of 128 bytes,
 // XOR-swizzled in 16-byte pieces.  The scales of a stage come as one word a
 // row, four blocks of 128 at a time (their byte is picked by the stage).
-template <int BM, int BN, int WM, int WN, int NSTG, bool F32>
+//
+// SPLIT: the reduction is cut into `splits` runs of stages, one a block each;
+// y then is float32 [splits][M][N], added in order by join_splits_kernel.
+template <int BM, int BN, int WM, int WN, int NSTG, bool F32, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView a, BlocksView b, void* __restrict__ y,
-                                                                     int M, int N, int K, int n_mt, int n_nt) {
+                                                                     int M, int N, int K, int n_mt, int n_nt,
+                                                                     int splits) {
     constexpr int NWV = WM * WN;
     constexpr int TM = BM / WM, TN = BN / WN;
     constexpr int FM = TM / 16, FN = TN / 16;
     constexpr int AI = BM / 8 / NWV, BI = BN / 8 / NWV;
     constexpr int SA = BM * kKS, SBB = BN * kKS, SS = (BM + BN) * 4;
     constexpr int SB = SA + SBB + SS;
-    static_assert((BM + BN) / 64 == NWV && BM % 64 == 0, "one scale load a wave");
-    constexpr int DPW = AI + BI + 1;
+    constexpr int SL = (BM + BN) / 64, SI = (SL + NWV - 1) / NWV;  // loads of 64 scale words: all, of a wave
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "a load's scales belong to one operand");
+    constexpr int DPW = AI + BI + SI;
 
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     constexpr int GM = 4;
-    const int tile = dev::xcd_tile(blockIdx.x, n_mt * n_nt);
+    const int part = SPLIT ? blockIdx.x % splits : 0;
+    const int tile = dev::xcd_tile(SPLIT ? blockIdx.x / splits : blockIdx.x, n_mt * n_nt);
     const int strip = tile / (GM * n_nt);
     const int gm = min(GM, n_mt - strip * GM);
     const int rem = tile - strip * GM * n_nt;
@@ -123,7 +129,10 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int nstage = K / kKS;
+    // the block's stages: [first, last); runs start at a scale word
+    const int words = (K / kKS + 3) / 4;
+    const int first_stage = SPLIT ? words * part / splits * 4 : 0;
+    const int nstage = (SPLIT ? min(words * (part + 1) / splits * 4, K / kKS) : K / kKS) - first_stage;
 
     const i32x4 ar = dev::dma_rsrc(a.codes + static_cast<size_t>(m0) * K,
                                    static_cast<uint32_t>(static_cast<size_t>(min(BM, M - m0)) * K));
@@ -139,23 +148,31 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
         const int n = (p / TN) * TN + out_column<FN>(p % TN);
         b_voff[ii] = static_cast<uint32_t>(n * K + pc * 16);
     }
-    // the wave's 64 scale words: rows of a, or of b
-    const bool mine_a = wave < BM / 64;
-    const int sp = (mine_a ? wave : wave - BM / 64) * 64 + lane;
-    const BlocksView& sv = mine_a ? a : b;
-    const int s0 = mine_a ? m0 : n0;
-    const int srow = mine_a ? sp : (sp / TN) * TN + out_column<FN>(sp % TN);
-    const int64_t first = s0 >> sv.shift;
-    const int64_t rows = ((sv.rows + (int64_t(1) << sv.shift) - 1) >> sv.shift) - first;
-    const int span = ((mine_a ? BM : BN) >> sv.shift) + 1;
-    const i32x4 sr = dev::dma_rsrc(sv.scale + first * sv.scale_cols,
-                                   static_cast<uint32_t>((rows < span ? rows : span) * sv.scale_cols));
-    const uint32_t s_voff = static_cast<uint32_t>((((s0 + srow) >> sv.shift) - first) * sv.scale_cols);
+    // the wave's scale words, 64 a load: rows of a, or of b (the last load is
+    // made twice where the waves do not share them evenly)
+    i32x4 sr[SI];
+    uint32_t s_voff[SI], s_lds[SI];
+#pragma unroll
+    for (int ii = 0; ii < SI; ++ii) {
+        const int l = min(wave + NWV * ii, SL - 1);
+        const bool of_a = l < BM / 64;
+        const int sp = (of_a ? l : l - BM / 64) * 64 + lane;
+        const BlocksView& sv = of_a ? a : b;
+        const int s0 = of_a ? m0 : n0;
+        const int srow = of_a ? sp : (sp / TN) * TN + out_column<FN>(sp % TN);
+        const int64_t first = s0 >> sv.shift;
+        const int64_t rows = ((sv.rows + (int64_t(1) << sv.shift) - 1) >> sv.shift) - first;
+        const int span = ((of_a ? BM : BN) >> sv.shift) + 1;
+        sr[ii] = dev::dma_rsrc(sv.scale + first * sv.scale_cols,
+                               static_cast<uint32_t>((rows < span ? rows : span) * sv.scale_cols));
+        s_voff[ii] = static_cast<uint32_t>((((s0 + srow) >> sv.shift) - first) * sv.scale_cols);
+        s_lds[ii] = static_cast<uint32_t>(l * 256);
+    }
 
     const uint32_t lds0 = dev::lds_address(smem);
     auto dma = [&](int s, int buf) {
         const uint32_t base = lds0 + static_cast<uint32_t>(buf * SB);
-        const uint32_t k0 = static_cast<uint32_t>(s * kKS);
+        const uint32_t k0 = static_cast<uint32_t>((first_stage + s) * kKS);
 #pragma unroll
         for (int ii = 0; ii < AI; ++ii) {
             const int row0 = (wave + NWV * ii) * 8;
@@ -164,7 +181,9 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
 #pragma unroll
         for (int ii = 0; ii < BI; ++ii)
             dev::lds_dma16(br, base + SA + (wave + NWV * ii) * 8 * kKS, b_voff[ii], k0);
-        lds_dma4(sr, base + SA + SBB + wave * 256, s_voff, static_cast<uint32_t>(s & ~3));
+#pragma unroll
+        for (int ii = 0; ii < SI; ++ii)
+            lds_dma4(sr[ii], base + SA + SBB + s_lds[ii], s_voff[ii], static_cast<uint32_t>((first_stage + s) & ~3));
     };
 
     const int fr = lane & 15, q = lane >> 4;
@@ -215,16 +234,24 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
                 bv[i] = operand(S + SA + row * kKS);
                 bs[i] = static_cast<int>(sc[BM + row] >> byte);
             }
+            // the next 16 rows of a are read while the MFMAs of these run
+            auto rows = [&](int j) { return operand(S + (wm * TM + j * 16 + fr) * kKS); };
+            auto scales = [&](int j) { return static_cast<int>(sc[wm * TM + j * 16 + fr] >> byte); };
+            i32x8 av = rows(0);
+            int as = scales(0);
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
-                const int row = wm * TM + j * 16 + fr;
-                const i32x8 av = operand(S + row * kKS);
-                const int as = static_cast<int>(sc[row] >> byte);
+                const i32x8 an = j + 1 < FM ? rows(j + 1) : av;
+                const int sn = j + 1 < FM ? scales(j + 1) : as;
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[i], av, acc[i][j], 0, 0, 0, bs[i],
                                                                                  0, as);
+                av = an;
+                as = sn;
             }
+            __builtin_amdgcn_s_setprio(0);
         }
     };
 #pragma unroll
@@ -247,8 +274,8 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(BlocksView 
         for (int i = 0; i < FN; ++i) {
             const int n = nbase + 4 * i;
             if (n >= N) break;
-            const size_t at = static_cast<size_t>(m) * N + n;
-            if constexpr (F32) store4(static_cast<float*>(y) + at, acc[i][j], min(4, N - n), whole);
+            const size_t at = (static_cast<size_t>(part) * M + m) * N + n;
+            if constexpr (F32 || SPLIT) store4(static_cast<float*>(y) + at, acc[i][j], min(4, N - n), whole);
             else store4(static_cast<uint16_t*>(y) + at, acc[i][j], min(4, N - n), whole);
         }
     }
@@ -420,36 +447,141 @@ ss1_status launch_few(const MatmulBlocksArgs& p) {
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
-template <int BM, int BN, int WM, int WN, int NSTG, bool F32>
-ss1_status launch_tile(const MatmulBlocksArgs& p) {
+// y = the sum over the splits, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void join_splits_kernel(const float* __restrict__ part, T* __restrict__ y,
+                                                          int64_t outputs, int splits) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= outputs) return;
+    const int n = outputs - at < 4 ? static_cast<int>(outputs - at) : 4;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (outputs % 4 == 0) {
+        for (int s = 0; s < splits; ++s) sum += *reinterpret_cast<const f32x4*>(part + s * outputs + at);
+    } else {
+        for (int s = 0; s < splits; ++s)
+            for (int i = 0; i < n; ++i) sum[i] += part[s * outputs + at + i];
+    }
+    store4(y + at, sum, n, outputs % 4 == 0);
+}
+
+template <int BM, int BN, int WM, int WN, int NSTG, bool F32, bool SPLIT = false>
+ss1_status launch_tile(const MatmulBlocksArgs& p, int splits = 1) {
     const int64_t n_mt = (p.M + BM - 1) / BM, n_nt = (p.N + BN - 1) / BN;
     constexpr size_t lds = static_cast<size_t>(NSTG) * (BM + BN) * (kKS + 4);
-    auto kern = &matmul_blocks_kernel<BM, BN, WM, WN, NSTG, F32>;
+    auto kern = &matmul_blocks_kernel<BM, BN, WM, WN, NSTG, F32, SPLIT>;
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                             static_cast<int>(lds)) != hipSuccess)
         return SS1_ERR_HIP;
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(n_mt * n_nt)), dim3(WM * WN * 64), lds,
-                       static_cast<hipStream_t>(p.stream), p.a, p.b, p.y, static_cast<int>(p.M),
-                       static_cast<int>(p.N), static_cast<int>(p.K), static_cast<int>(n_mt), static_cast<int>(n_nt));
+    const hipStream_t stream = static_cast<hipStream_t>(p.stream);
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(n_mt * n_nt * splits)), dim3(WM * WN * 64), lds, stream, p.a,
+                       p.b, SPLIT ? p.workspace : p.y, static_cast<int>(p.M), static_cast<int>(p.N),
+                       static_cast<int>(p.K), static_cast<int>(n_mt), static_cast<int>(n_nt), splits);
+    if constexpr (SPLIT) {
+        const int64_t outputs = p.M * p.N;
+        using T = typename std::conditional<F32, float, uint16_t>::type;
+        hipLaunchKernelGGL(join_splits_kernel<T>, dim3(static_cast<unsigned>((outputs + 1023) / 1024)), dim3(256), 0,
+                           stream, static_cast<const float*>(p.workspace), static_cast<T*>(p.y), outputs, splits);
+    }
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
+}
+
+// ------------------------------------------------------------------- choice
+// The tiles and what a stage of 128 takes them, in us: with at most one block a
+// compute unit, and with the two that fit (one for the largest).  Measured on
+// products of 17 to 8192 rows, 640 to 14336 columns and 1280 to 14336 deep; the
+// model below picks the fastest of them or one within 6%.
+//   M, N, K (bf16)        64x64  64x128  128x128  192x256   us a product
+//   64, 14336, 4096        12.2    16.6     23.6     39.0
+//   1024, 4096, 4096       31.2    25.7     29.7     44.9
+//   5120, 1280, 8192         -       -      61.1     82.3
+//   4096, 14336, 4096        -       -       278      244
+enum Tile { kTile64, kTile64x128, kTile128, kTile192, kTiles };
+struct TileRate {
+    int bm, bn, fit;
+    double alone[2], full[2];  // bf16 y, float32 y
+};
+constexpr TileRate kRates[kTiles] = {{64, 64, 2, {0.36, 0.50}, {0.52, 0.74}},
+                                     {64, 128, 2, {0.51, 0.79}, {0.80, 1.39}},
+                                     {128, 128, 2, {0.83, 1.20}, {1.26, 1.93}},
+                                     {192, 256, 1, {1.50, 2.65}, {1.52, 2.69}}};
+constexpr int64_t kCUs = 256;
+constexpr double kLaunchUs = 3.0;       // of the launch that joins splits
+constexpr double kJoinBytesUs = 4.0e6;  // bytes a us of partial sums, written and read
+
+struct Choice {
+    Tile tile;
+    int splits;
+};
+
+double tile_us(const TileRate& r, int64_t blocks, int64_t stages, bool f32) {
+    const int64_t per = (blocks + kCUs - 1) / kCUs;
+    return static_cast<double>(stages) * (per <= 1 ? r.alone[f32] : r.full[f32] * ((per + r.fit - 1) / r.fit));
+}
+
+Choice choose(int64_t M, int64_t N, int64_t K, bool f32) {
+    const int64_t stages = K / kKS;
+    Choice best{kTile64, 1};
+    double us = 1e30;
+    for (int t = 0; t < kTiles; ++t) {
+        const TileRate& r = kRates[t];
+        const int64_t tiles = ((M + r.bm - 1) / r.bm) * ((N + r.bn - 1) / r.bn);
+        const double u = tile_us(r, tiles, stages, f32);
+        if (u < us) {
+            us = u;
+            best = {static_cast<Tile>(t), 1};
+        }
+        if (t != kTile64) continue;
+        // long reductions of few tiles: runs of at least four stages, a block each
+        for (int splits = 2; splits <= 8 && splits * 4 <= stages; splits *= 2) {
+            const double run = static_cast<double>(splits) * M * N * 8.0 / kJoinBytesUs;
+            const double v = tile_us(r, tiles * splits, (stages + splits - 1) / splits, f32) + kLaunchUs + run;
+            if (v < us) {
+                us = v;
+                best = {kTile64, splits};
+            }
+        }
+    }
+    return best;
+}
+
+// Up to 16 rows go by the weight's rows where what all blocks read of a (M * K
+// bytes each) stays below 24 MB: 16 x 4096 against 14336 rows takes 17.5 us
+// that way and 12.0 in 64 x 64 tiles, 8 x 5120 against 1280 rows 7.8 and 13.8.
+bool few_rows(int64_t M, int64_t N, int64_t K) {
+    return K > 0 && M <= kFewRows && (M <= kInsideRows || (N + 15) / 16 * M * K <= int64_t(24) << 20);
+}
+
+template <bool F32>
+ss1_status launch_choice(const MatmulBlocksArgs& p) {
+    const Choice c = choose(p.M, p.N, p.K, F32);
+    if (c.splits > 1) return launch_tile<64, 64, 2, 2, 4, F32, true>(p, c.splits);
+    switch (c.tile) {
+        case kTile64: return launch_tile<64, 64, 2, 2, 4, F32>(p);
+        case kTile64x128: return launch_tile<64, 128, 2, 2, 3, F32>(p);
+        case kTile128: return launch_tile<128, 128, 2, 2, 2, F32>(p);
+        default: return launch_tile<192, 256, 2, 4, 2, F32>(p);
+    }
 }
 
 }  // namespace
 
-size_t matmul_blocks_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t matmul_blocks_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M == 0 || N == 0 || few_rows(M, N, K)) return 0;
+    // y's type is not known here: room for either
+    const int a = choose(M, N, K, false).splits, b = choose(M, N, K, true).splits;
+    const int splits = a > b ? a : b;
+    return splits > 1 ? static_cast<size_t>(splits) * M * N * 4 : 0;
+}
 
-bool matmul_takes_x(int64_t M, int64_t, int64_t K) {
-    return M <= kInsideRows && K > 0 && M * (K + 64 + K / kKS) <= kInsideBytes;
+bool matmul_takes_x(int64_t M, int64_t N, int64_t K) {
+    return M <= kInsideRows && few_rows(M, N, K) && M * (K + 64 + K / kKS) <= kInsideBytes;
 }
 
 ss1_status launch_matmul_blocks(const MatmulBlocksArgs& p) {
     const bool f32 = p.dtype == SS1_F32;
-    if (p.x) {
-        // y has x's dtype
-        return f32 ? launch_few<float, true>(p) : launch_few<uint16_t, false>(p);
-    }
-    if (p.M <= kFewRows && p.K > 0) return f32 ? launch_few<void, true>(p) : launch_few<void, false>(p);
-    return f32 ? launch_tile<128, 128, 2, 2, 2, true>(p) : launch_tile<128, 128, 2, 2, 2, false>(p);
+    if (p.x) return f32 ? launch_few<float, true>(p) : launch_few<uint16_t, false>(p);  // y has x's dtype
+    if (few_rows(p.M, p.N, p.K)) return f32 ? launch_few<void, true>(p) : launch_few<void, false>(p);
+    return f32 ? launch_choice<true>(p) : launch_choice<false>(p);
 }
 
 }  // namespace ss1

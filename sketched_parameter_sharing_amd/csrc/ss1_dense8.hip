@@ -310,7 +310,7 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
     const int u0 = units * wave / NW, u1 = units * (wave + 1) / NW;
 
     // x: 16 lanes take a block of 128 of a row
-    const int pitch = K + 64;  // four rows' 64 bytes on distinct banks
+    const int pitch = K + 16;  // 16 rows' pieces on distinct banks
     uint8_t* s_scale = smem + static_cast<size_t>(M) * pitch;
     const int items = INSIDE ? M * nkb : 0;
     constexpr int G = NW * 4;
@@ -436,11 +436,12 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
 constexpr int64_t kFewRows = 16;
 constexpr int64_t kInsideRows = 4;
 constexpr int64_t kInsideBytes = 32768;
+constexpr int64_t kInsideAll = int64_t(20) << 20;  // elements over all blocks
 
 template <typename X, bool F32>
 ss1_status launch_few(const MatmulBlocksArgs& p) {
     constexpr int NW = 4;
-    const size_t lds = __is_same(X, void) ? 0 : static_cast<size_t>(up_to(p.M * (p.K + 64 + p.K / kKS), 16));
+    const size_t lds = __is_same(X, void) ? 0 : static_cast<size_t>(up_to(p.M * (p.K + 16 + p.K / kKS), 16));
     hipLaunchKernelGGL((few_rows_kernel<X, F32, NW>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(NW * 64), lds,
                        static_cast<hipStream_t>(p.stream), p.a, p.b, static_cast<const X*>(p.x), p.xcols, p.y,
                        static_cast<int>(p.M), static_cast<int>(p.N), static_cast<int>(p.K));
@@ -574,7 +575,7 @@ size_t matmul_blocks_workspace(int64_t M, int64_t N, int64_t K) {
 }
 
 bool matmul_takes_x(int64_t M, int64_t N, int64_t K) {
-    return M <= kInsideRows && few_rows(M, N, K) && M * (K + 64 + K / kKS) <= kInsideBytes;
+    return few_rows(M, N, K) && M * (K + 16 + K / kKS) <= kInsideBytes && (N + 15) / 16 * M * K <= kInsideAll;
 }
 
 ss1_status launch_matmul_blocks(const MatmulBlocksArgs& p) {

@@ -70,29 +70,99 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[kVec]) {
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<uint16_t>(bf16_bits(v)); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-// Sum of squares of this thread's elements of a chunk that starts at p and has
-// n elements left in its tensor.
-template <typename T, typename R>
-__device__ __forceinline__ double squares(const T* p, int64_t n) {
+// A block's work items, 64 at a time: lane l of every wave holds the l-th one's
+// address, elements left in its tensor and type, so that the chain of reads
+// (item, entry) is paid once for 64 items and not before each one's data.
+struct Items {
+    uint64_t at;
+    int64_t left;  // 0: none
+    int32_t dtype;
+
+    __device__ __forceinline__ void load(const ss1_gradnorm_entry* entries, int count, const int32_t* map, int64_t i,
+                                         int64_t end) {
+        at = 0;
+        left = 0;
+        dtype = SS1_F32;
+        if (i >= end) return;
+        const int item = map[2 * i];
+        const int64_t begin = static_cast<int64_t>(map[2 * i + 1]) * kNormChunk;
+        if (item < 0 || item >= count || begin < 0) return;
+        const ss1_gradnorm_entry e = entries[item];
+        if (begin >= e.numel) return;
+        at = reinterpret_cast<uint64_t>(e.grad) + static_cast<uint64_t>(begin) * (e.dtype == SS1_F32 ? 4 : 2);
+        left = e.numel - begin;
+        dtype = e.dtype;
+    }
+};
+struct Item {
+    uint64_t at;
+    int n;  // of the chunk: at most kNormChunk
+    bool f32;
+};
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ __forceinline__ Item item_at(const Items& t, int lane) {
+    const uint64_t left = static_cast<uint64_t>(lane_value(static_cast<uint32_t>(t.left >> 32), lane)) << 32 |
+                          lane_value(static_cast<uint32_t>(t.left), lane);
+    Item r;
+    r.at = static_cast<uint64_t>(lane_value(static_cast<uint32_t>(t.at >> 32), lane)) << 32 |
+           lane_value(static_cast<uint32_t>(t.at), lane);
+    r.n = left < static_cast<uint64_t>(kNormChunk) ? static_cast<int>(left) : static_cast<int>(kNormChunk);
+    r.f32 = lane_value(static_cast<uint32_t>(t.dtype), lane) == SS1_F32;
+    return r;
+}
+
+// A thread's share of a whole chunk as it lies in memory: kPasses vectors of
+// bf16, or twice as many of float32.
+struct Raw {
+    uint4 v[2 * kPasses];
+    __device__ __forceinline__ void load(const Item& t) {
+        if (t.n < kNormChunk) return;  // read element by element
+        const uint4* p = reinterpret_cast<const uint4*>(t.at) + threadIdx.x;
+        if (t.f32) {
+#pragma unroll
+            for (int i = 0; i < 2 * kPasses; ++i) v[i] = p[i * kThreads];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) v[i] = p[i * kThreads];
+        }
+    }
+};
+
+__device__ __forceinline__ double squared(float f, double s) {
+    const double d = f;
+    return fma(d, d, s);
+}
+__device__ __forceinline__ double squares(const Item& t, const Raw& r) {
     double s = 0.0;
-    if (n >= kNormChunk) {
-        R r[kPasses];
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) load_raw(p + (i * kThreads + threadIdx.x) * kVec, r[i]);
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            float v[kVec];
-            widen(r[i], v);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) s = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), s);
+    if (t.n < kNormChunk) {
+        if (t.f32) {
+            const float* p = reinterpret_cast<const float*>(t.at);
+            for (int i = threadIdx.x; i < t.n; i += kThreads) s = squared(p[i], s);
+        } else {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(t.at);
+            for (int i = threadIdx.x; i < t.n; i += kThreads) s = squared(widen(p[i]), s);
         }
         return s;
     }
-    for (int64_t i = threadIdx.x * kVec; i < n; i += kThreads * kVec) {
-        const int m = n - i < kVec ? static_cast<int>(n - i) : kVec;
-        for (int j = 0; j < m; ++j) {
-            const double v = widen(p[i + j]);
-            s = fma(v, v, s);
+    if (t.f32) {
+#pragma unroll
+        for (int i = 0; i < 2 * kPasses; ++i) {
+            s = squared(__uint_as_float(r.v[i].x), s);
+            s = squared(__uint_as_float(r.v[i].y), s);
+            s = squared(__uint_as_float(r.v[i].z), s);
+            s = squared(__uint_as_float(r.v[i].w), s);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s = squared(__uint_as_float(w[j] << 16), s);
+                s = squared(__uint_as_float(w[j] & 0xFFFF0000u), s);
+            }
         }
     }
     return s;
@@ -120,17 +190,25 @@ __global__ __launch_bounds__(kThreads) void gradnorm_kernel(const ss1_gradnorm_e
     __shared__ double red[kThreads / 64];
     const int64_t end = first_item(chunks, blockIdx.x + 1, gridDim.x);
     double s = 0.0;
-    for (int64_t i = first_item(chunks, blockIdx.x, gridDim.x); i < end; ++i) {
-        const int item = map[2 * i];
-        const int64_t part = map[2 * i + 1];
-        if (item < 0 || item >= count || part < 0) continue;
-        const ss1_gradnorm_entry e = entries[item];
-        const int64_t begin = part * kNormChunk;
-        if (begin >= e.numel) continue;
-        if (e.dtype == SS1_F32)
-            s += squares<float, RawF>(static_cast<const float*>(e.grad) + begin, e.numel - begin);
-        else
-            s += squares<uint16_t, RawH>(static_cast<const uint16_t*>(e.grad) + begin, e.numel - begin);
+    for (int64_t i0 = first_item(chunks, blockIdx.x, gridDim.x); i0 < end; i0 += 64) {
+        Items items;
+        items.load(entries, count, map, i0 + (threadIdx.x & 63), end);
+        const int n = end - i0 < 64 ? static_cast<int>(end - i0) : 64;
+        // the next item's data is on its way while one is summed
+        Item cur = item_at(items, 0);
+        Raw raw;
+        raw.load(cur);
+        for (int k = 0; k < n; ++k) {
+            Item next{0, 0, true};
+            Raw ahead;
+            if (k + 1 < n) {
+                next = item_at(items, k + 1);
+                ahead.load(next);
+            }
+            s += squares(cur, raw);
+            cur = next;
+            raw = ahead;
+        }
     }
     s = block_sum(s, red);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
@@ -195,8 +273,9 @@ __global__ __launch_bounds__(kThreads) void gradclip_kernel(const ss1_gradnorm_e
         if (coef) *coef = r.coef;
     }
     if (r.coef == 1.0f) return;
-    const int64_t end = first_item(chunks, blockIdx.x + 1, gridDim.x);
-    for (int64_t i = first_item(chunks, blockIdx.x, gridDim.x); i < end; ++i) {
+    // backwards: what the sum read last is still in the last-level cache
+    const int64_t begin_item = first_item(chunks, blockIdx.x, gridDim.x);
+    for (int64_t i = first_item(chunks, blockIdx.x + 1, gridDim.x) - 1; i >= begin_item; --i) {
         const int item = map[2 * i];
         const int64_t part = map[2 * i + 1];
         if (item < 0 || item >= count || part < 0) continue;

@@ -13,7 +13,7 @@ namespace ss1 {
 // ------------------------------------------------------------ gradient norm
 // Elements of one work item, and blocks (partial sums) of a call: a block takes
 // a run of consecutive items.
-constexpr int64_t kNormChunk = 4096;
+constexpr int64_t kNormChunk = 8192;
 constexpr int kNormBlocks = 2048;
 
 struct GradNormArgs {

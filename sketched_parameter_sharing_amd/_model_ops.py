@@ -345,6 +345,8 @@ def dense_backward_fp8(dy, xt: Fp8Blocks, wt: Fp8Blocks, dx=True, dW=True, dW_dt
         return _on(stream, dy, dense_backward_fp8, dy, xt, wt, dx, dW, dW_dtype, workspace)
     td, lib, n = _matrix(dy, dev), load(), ctypes.c_size_t(0)
     rx = rw = None
+    if (dx is not None and wt is None) or (dW is not None and xt is None):
+        raise ValueError("dx needs wt and dW needs xt")
     if dx is not None:
         tw = wt._struct(dev)
         rw = byref(tw)

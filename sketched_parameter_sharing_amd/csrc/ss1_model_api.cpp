@@ -450,7 +450,8 @@ extern "C" ss1_status ss1_dense_backward_fp8(const ss1_tensor* dy, const ss1_fp8
     }
     if (M > 0 && N > 0) SS1_TRY(ss1::launch_quantize_blocks(q));
     void* rest = static_cast<uint8_t*>(workspace) + at;
-    if (do_dx) SS1_TRY(ss1::launch_matmul_blocks(product(q.q, view_of(wt), dx, rest, stream)));
-    if (do_dW) SS1_TRY(ss1::launch_matmul_blocks(product(q.qt, view_of(xt), dW, rest, stream)));
-    return SS1_OK;
+    if (!do_dW) return ss1::launch_matmul_blocks(product(q.q, view_of(wt), dx, rest, stream));
+    if (!do_dx) return ss1::launch_matmul_blocks(product(q.qt, view_of(xt), dW, rest, stream));
+    return ss1::launch_matmul_pair(product(q.q, view_of(wt), dx, rest, stream),
+                                   product(q.qt, view_of(xt), dW, rest, stream));
 }

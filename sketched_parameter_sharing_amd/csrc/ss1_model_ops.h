@@ -101,5 +101,7 @@ size_t matmul_blocks_workspace(int64_t M, int64_t N, int64_t K);
 // Whether a product over x itself (not its codes) is offered at this size.
 bool matmul_takes_x(int64_t M, int64_t N, int64_t K);
 ss1_status launch_matmul_blocks(const MatmulBlocksArgs& a);
+// Two products that do not depend on each other; they may share a workspace.
+ss1_status launch_matmul_pair(const MatmulBlocksArgs& p, const MatmulBlocksArgs& q);
 
 }  // namespace ss1

@@ -7,7 +7,8 @@ in one batch of ragged sequences:
     h = LayerNorm(x);  y = SS1(h) + adapter of the sequence(h);  loss = |y - target|^2 / 2
 
 with ``layernorm_forward/backward``, ``forward``/``backward`` of the SS1 layer,
-``adapter_forward/backward`` beside it, and one ``AdamWPlan.step`` over the norm's
+``adapter_forward/backward`` beside it, the global gradient norm by
+``GradNormPlan.norm``, and one ``AdamWPlan.step``, clipped by it, over the norm's
 parameters, the compressed weight and both factors of the adapters.  Afterwards a
 decode batch of one token a request runs each request's own adapter.
 
@@ -56,6 +57,7 @@ def finetune(steps=60, K=512, N=768, c=2, tasks=3, rank=16, tokens=1536, state="
     grads = [torch.empty_like(p) for p in params]
     masters = [None, None] + [p.float() for p in params[2:]]
     opt = ss1.AdamWPlan.make(params, grads, masters=masters, weight_decay=[0.0, 0.0, 0.01, 0.0, 0.0], state=state)
+    clip = ss1.GradNormPlan.make(grads)
     dgamma, dbeta, dW, dA, dB = grads
     losses = []
     for step in range(1, steps + 1):
@@ -69,9 +71,8 @@ def finetune(steps=60, K=512, N=768, c=2, tasks=3, rank=16, tokens=1536, state="
         dh, _, _ = ss1.adapter_backward(dy, h, v, adapters, seg, task_of, dx_base=dh, dx=dh, dA=dA, dB=dB)
         ss1.layernorm_backward(dh, x, gamma, mean, rstd, dx=None, dgamma=dgamma, dbeta=dbeta)
         # clip by the global norm; the coefficient stays on the device
-        norm = torch.stack([t.float().square().sum() for t in grads]).sum().sqrt()
-        clip = (1.0 / norm.clamp(min=1.0)).reshape(1)
-        opt.step(step=step, lr=2e-3, grad_scale=clip, seed=step)
+        _, coef = clip.norm(max_norm=1.0)
+        opt.step(step=step, lr=2e-3, grad_scale=coef, seed=step)
         if report and (step == 1 or step % 10 == 0):
             report(f"step {step:4d}  loss {float(losses[-1]):.5f}")
 

@@ -57,21 +57,36 @@ __device__ __forceinline__ int out_column(int p) {
     return (r / 4) * 4 * FN + nb * 4 + r % 4;
 }
 
-__device__ __forceinline__ void store4(uint16_t* p, const f32x4& v, int n, bool whole) {
-    if (whole) {
-        uint2 o;
-        o.x = dev::pack_bf16(v[0], v[1]);
-        o.y = dev::pack_bf16(v[2], v[3]);
-        *reinterpret_cast<uint2*>(p) = o;
+// N consecutive outputs of a row that has `left` from there on; a row of an odd
+// width starts anywhere, so the vectors are not aligned.
+typedef blocks::u32x4 u32x4;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any2 __attribute__((aligned(2)));
+template <int N>
+__device__ __forceinline__ void store_run(uint16_t* p, const float (&v)[N], int left) {
+    if (left >= N) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = dev::pack_bf16(v[2 * i], v[2 * i + 1]);
+        if constexpr (N == 8) *reinterpret_cast<blocks::u32x4_any2*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+        else *reinterpret_cast<u32x2_any2*>(p) = u32x2{w[0], w[1]};
     } else {
-        for (int i = 0; i < n; ++i) p[i] = dev::to_bf16_bits(v[i]);
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i)
+            if (i < left) p[i] = dev::to_bf16_bits(v[i]);
     }
 }
-__device__ __forceinline__ void store4(float* p, const f32x4& v, int n, bool whole) {
-    if (whole) {
-        *reinterpret_cast<f32x4*>(p) = v;
+template <int N>
+__device__ __forceinline__ void store_run(float* p, const float (&v)[N], int left) {
+    if (left >= N) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<blocks::u32x4_any4*>(p + i) = u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                                                  __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])};
     } else {
-        for (int i = 0; i < n; ++i) p[i] = v[i];
+#pragma unroll
+        for (int i = 0; i < N - 1; ++i)
+            if (i < left) p[i] = v[i];
     }
 }
 
@@ -274,18 +289,21 @@ __device__ __forceinline__ void matmul_tile(const TileArgs& p, int block) {
 
     // lane holds columns nbase + 4 i .. + 3 (i < FN) of the rows m0 + .. + fr
     const int nbase = n0 + wn * TN + q * 4 * FN;
-    const bool whole = N % 4 == 0;
+    constexpr int RUN = FN % 2 == 0 ? 8 : 4;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         const int m = m0 + wm * TM + j * 16 + fr;
         if (m >= M) continue;
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const int n = nbase + 4 * i;
-            if (n >= N) break;
+        for (int h = 0; h < 4 * FN / RUN; ++h) {
+            const int n = nbase + RUN * h;
+            if (n >= N) continue;
+            float v[RUN];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) v[i] = acc[(RUN * h + i) / 4][j][i % 4];
             const size_t at = (static_cast<size_t>(part) * M + m) * N + n;
-            if constexpr (F32 || SPLIT) store4(static_cast<float*>(y) + at, acc[i][j], min(4, N - n), whole);
-            else store4(static_cast<uint16_t*>(y) + at, acc[i][j], min(4, N - n), whole);
+            if constexpr (F32 || SPLIT) store_run(static_cast<float*>(y) + at, v, N - n);
+            else store_run(static_cast<uint16_t*>(y) + at, v, N - n);
         }
     }
 }
@@ -437,8 +455,9 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
     const int c = n0 + 4 * q;
     if (c >= N) return;
     const size_t at = static_cast<size_t>(fr) * N + c;
-    if constexpr (F32) store4(static_cast<float*>(y) + at, sum, min(4, N - c), N % 4 == 0);
-    else store4(static_cast<uint16_t*>(y) + at, sum, min(4, N - c), N % 4 == 0);
+    const float out[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if constexpr (F32) store_run(static_cast<float*>(y) + at, out, N - c);
+    else store_run(static_cast<uint16_t*>(y) + at, out, N - c);
 }
 
 // Rows of a that the kernel above takes, and how much of x a block quantises.
@@ -484,7 +503,8 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const float* __restric
         for (int s = 0; s < splits; ++s)
             for (int i = 0; i < n; ++i) sum[i] += part[s * outputs + at + i];
     }
-    store4(y + at, sum, n, outputs % 4 == 0);
+    const float out[4] = {sum[0], sum[1], sum[2], sum[3]};
+    store_run(y + at, out, n);
 }
 
 template <int BM, int BN>

@@ -231,52 +231,57 @@ __device__ __forceinline__ void matmul_tile(const TileArgs& p, int block) {
             return i32x8{static_cast<int>(u.x), static_cast<int>(u.y), static_cast<int>(u.z), static_cast<int>(u.w),
                          static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w)};
         };
+        // The first rows of a are read first, then b's, so that the first MFMA
+        // waits for two reads and not for all.  From there on the next 16 rows of
+        // a are read while the MFMAs of these run; left alone, the compiler reads
+        // them behind those MFMAs and waits.
+        auto rows = [&](int j) { return operand(S + (wm * TM + j * 16 + fr) * kKS); };
+        auto word = [&](int j) { return sc[wm * TM + j * 16 + fr]; };
+        i32x8 av = rows(0), bv[FN];
+        uint32_t aw = word(0), bw[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) bw[i] = sc[BM + wn * TN + i * 16 + fr];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) bv[i] = operand(S + SA + (wn * TN + i * 16 + fr) * kKS);
+        __builtin_amdgcn_sched_barrier(0);
+        auto scale = [&](uint32_t w) { return __uint_as_float((w >> byte & 0xFFu) << 23); };
+        Wide bx[F32 ? FN : 1];
         if constexpr (F32) {
-            auto scale = [&](int row) { return __uint_as_float((sc[row] >> byte & 0xFFu) << 23); };
-            Wide bw[FN];
 #pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                const int row = wn * TN + i * 16 + fr;
-                bw[i] = widen(operand(S + SA + row * kKS), scale(BM + row));
+            for (int i = 0; i < FN; ++i) bx[i] = widen(bv[i], scale(bw[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) bw[i] >>= byte;
+        }
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            i32x8 an = av;
+            uint32_t nw = aw;
+            if (j + 1 < FM) {
+                an = rows(j + 1);
+                nw = word(j + 1);
             }
-#pragma unroll
-            for (int j = 0; j < FM; ++j) {
-                const int row = wm * TM + j * 16 + fr;
-                const Wide aw = widen(operand(S + row * kKS), scale(row));
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (F32) {
+                const Wide ax = widen(av, scale(aw));
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < FN; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[i].t[t], aw.t[t], acc[i][j], 0, 0, 0);
-            }
-        } else {
-            i32x8 bv[FN];
-            int bs[FN];
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                const int row = wn * TN + i * 16 + fr;
-                bv[i] = operand(S + SA + row * kKS);
-                bs[i] = static_cast<int>(sc[BM + row] >> byte);
-            }
-            // the next 16 rows of a are read while the MFMAs of these run
-            auto rows = [&](int j) { return operand(S + (wm * TM + j * 16 + fr) * kKS); };
-            auto scales = [&](int j) { return static_cast<int>(sc[wm * TM + j * 16 + fr] >> byte); };
-            i32x8 av = rows(0);
-            int as = scales(0);
-            __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-            for (int j = 0; j < FM; ++j) {
-                const i32x8 an = j + 1 < FM ? rows(j + 1) : av;
-                const int sn = j + 1 < FM ? scales(j + 1) : as;
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bx[i].t[t], ax.t[t], acc[i][j], 0, 0, 0);
+            } else {
+                const int as = static_cast<int>(aw >> byte);
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[i], av, acc[i][j], 0, 0, 0, bs[i],
-                                                                                 0, as);
-                av = an;
-                as = sn;
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        bv[i], av, acc[i][j], 0, 0, 0, static_cast<int>(bw[i]), 0, as);
             }
-            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            av = an;
+            aw = nw;
         }
+        __builtin_amdgcn_s_setprio(0);
     };
 #pragma unroll
     for (int p = 0; p < NSTG - 1; ++p)
@@ -541,10 +546,10 @@ ss1_status launch_tile(const MatmulBlocksArgs& p, int splits = 1) {
 // products of 17 to 8192 rows, 640 to 14336 columns and 1280 to 14336 deep; the
 // model below picks the fastest of them or one within 6%.
 //   M, N, K (bf16)        64x64  64x128  128x128  192x256   us a product
-//   64, 14336, 4096        12.2    16.6     23.6     39.0
+//   64, 14336, 4096        11.9    16.6     23.0     36.0
 //   1024, 4096, 4096       31.2    25.7     29.7     44.9
-//   5120, 1280, 8192         -       -      61.1     82.3
-//   4096, 14336, 4096        -       -       278      244
+//   2048, 4096, 4096       55.1       -     34.7     42.1
+//   4096, 14336, 4096       396       -      264      230
 enum Tile { kTile64, kTile64x128, kTile128, kTile192, kTiles };
 struct TileRate {
     int bm, bn, fit;
@@ -552,8 +557,8 @@ struct TileRate {
 };
 constexpr TileRate kRates[kTiles] = {{64, 64, 2, {0.36, 0.50}, {0.52, 0.74}},
                                      {64, 128, 2, {0.51, 0.79}, {0.80, 1.39}},
-                                     {128, 128, 2, {0.83, 1.20}, {1.26, 1.93}},
-                                     {192, 256, 1, {1.50, 2.65}, {1.52, 2.69}}};
+                                     {128, 128, 2, {0.80, 1.20}, {1.20, 1.80}},
+                                     {192, 256, 1, {1.40, 2.50}, {1.44, 2.60}}};
 constexpr int64_t kCUs = 256;
 constexpr double kLaunchUs = 3.0;       // of the launch that joins splits
 constexpr double kJoinBytesUs = 4.0e6;  // bytes a us of partial sums, written and read

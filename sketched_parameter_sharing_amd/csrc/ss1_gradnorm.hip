@@ -7,7 +7,7 @@
 // 1e-30 or 1e30 count like any other and the order of the sum does not show in
 // the result.  The partial sums are added by whoever needs the norm: one block
 // that writes it, or every block of the clipping pass for itself (at most
-// kNormBlocks doubles), which saves a launch between the two passes.
+// kNormMost doubles), which saves a launch between the two passes.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -169,13 +169,14 @@ __device__ __forceinline__ double squares(const Item& t, const Raw& r) {
 }
 
 // The block's sum of one double a thread, in every thread.
+template <int T>
 __device__ __forceinline__ double block_sum(double s, double* red) {
     for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
     __syncthreads();
     double t = red[0];
 #pragma unroll
-    for (int w = 1; w < kThreads / 64; ++w) t += red[w];
+    for (int w = 1; w < T / 64; ++w) t += red[w];
     return t;
 }
 
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void gradnorm_kernel(const ss1_gradnorm_e
             raw = ahead;
         }
     }
-    s = block_sum(s, red);
+    s = block_sum<kThreads>(s, red);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -220,21 +221,27 @@ struct Norm {
 
 // Norm and coefficient from the partial sums, in every thread: the same order
 // in every block that asks.
+template <int T>
 __device__ __forceinline__ Norm finish(const double* __restrict__ partial, int parts, double max_norm, double* red) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
-    const double norm = sqrt(block_sum(s, red));
+    constexpr int kLoads = static_cast<int>(kNormMost) / T;  // all in flight together
+    double v[kLoads], s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = threadIdx.x + i * T < parts ? partial[threadIdx.x + i * T] : 0.0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) s += v[i];
+    const double norm = sqrt(block_sum<T>(s, red));
     Norm r;
     r.norm = static_cast<float>(norm);
     r.coef = norm > max_norm ? static_cast<float>(max_norm / norm) : norm != norm ? r.norm : 1.0f;
     return r;
 }
 
-__global__ __launch_bounds__(kThreads) void gradnorm_finish_kernel(const double* __restrict__ partial, int parts,
-                                                                   double max_norm, float* __restrict__ norm,
-                                                                   float* __restrict__ coef) {
-    __shared__ double red[kThreads / 64];
-    const Norm r = finish(partial, parts, max_norm, red);
+constexpr int kFinishThreads = 1024;
+__global__ __launch_bounds__(kFinishThreads) void gradnorm_finish_kernel(const double* __restrict__ partial, int parts,
+                                                                         double max_norm, float* __restrict__ norm,
+                                                                         float* __restrict__ coef) {
+    __shared__ double red[kFinishThreads / 64];
+    const Norm r = finish<kFinishThreads>(partial, parts, max_norm, red);
     if (threadIdx.x != 0) return;
     if (norm) *norm = r.norm;
     if (coef) *coef = r.coef;
@@ -267,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void gradclip_kernel(const ss1_gradnorm_e
                                                             const double* __restrict__ partial, double max_norm,
                                                             float* __restrict__ norm, float* __restrict__ coef) {
     __shared__ double red[kThreads / 64];
-    const Norm r = finish(partial, gridDim.x, max_norm, red);
+    const Norm r = finish<kThreads>(partial, gridDim.x, max_norm, red);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         if (norm) *norm = r.norm;
         if (coef) *coef = r.coef;
@@ -289,11 +296,9 @@ __global__ __launch_bounds__(kThreads) void gradclip_kernel(const ss1_gradnorm_e
     }
 }
 
-int blocks_of(int64_t chunks) { return static_cast<int>(chunks < kNormBlocks ? chunks : kNormBlocks); }
-
 void launch_partial(const GradNormArgs& a) {
     if (a.chunks == 0) return;
-    hipLaunchKernelGGL(gradnorm_kernel, dim3(blocks_of(a.chunks)), dim3(kThreads), 0,
+    hipLaunchKernelGGL(gradnorm_kernel, dim3(gradnorm_blocks(a.chunks)), dim3(kThreads), 0,
                        static_cast<hipStream_t>(a.stream), a.entries, a.count, a.map, a.chunks, a.partial);
 }
 
@@ -301,15 +306,15 @@ void launch_partial(const GradNormArgs& a) {
 
 ss1_status launch_gradnorm(const GradNormArgs& a) {
     launch_partial(a);
-    hipLaunchKernelGGL(gradnorm_finish_kernel, dim3(1), dim3(kThreads), 0, static_cast<hipStream_t>(a.stream),
-                       a.partial, blocks_of(a.chunks), a.max_norm, a.norm, a.coef);
+    hipLaunchKernelGGL(gradnorm_finish_kernel, dim3(1), dim3(kFinishThreads), 0, static_cast<hipStream_t>(a.stream),
+                       a.partial, gradnorm_blocks(a.chunks), a.max_norm, a.norm, a.coef);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
 ss1_status launch_gradnorm_clip(const GradNormArgs& a) {
     if (a.chunks == 0) return launch_gradnorm(a);
     launch_partial(a);
-    hipLaunchKernelGGL(gradclip_kernel, dim3(blocks_of(a.chunks)), dim3(kThreads), 0,
+    hipLaunchKernelGGL(gradclip_kernel, dim3(gradnorm_blocks(a.chunks)), dim3(kThreads), 0,
                        static_cast<hipStream_t>(a.stream), a.entries, a.count, a.map, a.chunks, a.partial, a.max_norm,
                        a.norm, a.coef);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;

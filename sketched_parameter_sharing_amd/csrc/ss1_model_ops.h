@@ -11,10 +11,14 @@
 namespace ss1 {
 
 // ------------------------------------------------------------ gradient norm
-// Elements of one work item, and blocks (partial sums) of a call: a block takes
-// a run of consecutive items.
-constexpr int64_t kNormChunk = 8192;
-constexpr int kNormBlocks = 2048;
+// Elements of one work item, and blocks (partial sums) of a call: an item each
+// for up to kNormMost of them, else kNormBlocks blocks (all on the card at once)
+// with a run of consecutive items each.
+constexpr int64_t kNormChunk = 4096;
+constexpr int64_t kNormMost = 2048, kNormBlocks = 1024;
+inline int gradnorm_blocks(int64_t chunks) {
+    return static_cast<int>(chunks <= kNormMost ? chunks : kNormBlocks);
+}
 
 struct GradNormArgs {
     const ss1_gradnorm_entry* entries;
@@ -29,7 +33,7 @@ struct GradNormArgs {
 };
 
 inline size_t gradnorm_workspace(int64_t chunks) {
-    return static_cast<size_t>(chunks < kNormBlocks ? chunks : kNormBlocks) * sizeof(double);
+    return static_cast<size_t>(gradnorm_blocks(chunks)) * sizeof(double);
 }
 ss1_status launch_gradnorm(const GradNormArgs& a);
 ss1_status launch_gradnorm_clip(const GradNormArgs& a);

@@ -15,8 +15,9 @@ import sketched_parameter_sharing_amd as ss1
 
 pytestmark = pytest.mark.gpu
 HALF = 2.0 ** -24 + 1e-12
-SIZES = [[1], [7, 0, 4096, 3], [8191, 8193, 16384, 1, 2049, 40_000], [0, 0], [], [2_000_003, 5, 123_457],
-         [300 + 37 * i for i in range(700)], [20_000_000]]
+SIZES = [[1], [7, 0, 4096, 3], [4095, 4097, 16384, 1, 2049, 40_000], [0, 0], [], [2_000_003, 5, 123_457],
+         [300 + 37 * i for i in range(700)], [20_000_000],
+         [5000 + i % 3 for i in range(1024)], [4096 * 2049]]
 
 
 def make(sizes, kinds=(torch.float32, torch.bfloat16), seed=1, std=0.01):

@@ -53,14 +53,14 @@ def test_gradnorm_plan_checks(rows, status):
 
 
 def test_gradnorm_plan_lists_every_element_once():
-    sizes = [1, 0, 8192, 8193, 24576, 5]
+    sizes = [1, 0, 4096, 4097, 12288, 5]
     lib, n = _lib.load(), ctypes.c_int64(0)
     e = entries(*[(A, s, F32, 0) for s in sizes])
     assert lib.ss1_gradnorm_plan(e, len(sizes), byref(n), None) == OK
     m = np.full((n.value, 2), -7, dtype=np.int32)
     assert lib.ss1_gradnorm_plan(e, len(sizes), byref(n), m.ctypes.data) == OK
     for i, s in enumerate(sizes):
-        assert m[m[:, 0] == i, 1].tolist() == list(range(-(-s // 8192)))
+        assert m[m[:, 0] == i, 1].tolist() == list(range(-(-s // 4096)))
     assert lib.ss1_gradnorm_plan(None, 1, byref(n), None) == NULL
     assert lib.ss1_gradnorm_plan(e, 1, None, None) == NULL
     assert lib.ss1_gradnorm_plan(e, -1, byref(n), None) == SHAPE

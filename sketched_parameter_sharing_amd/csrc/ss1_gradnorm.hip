@@ -113,46 +113,53 @@ __device__ __forceinline__ Item item_at(const Items& t, int lane) {
     return r;
 }
 
-// A thread's share of a whole chunk as it lies in memory: kPasses vectors of
-// bf16, or twice as many of float32.
+// A thread's share of a chunk as it lies in memory: kPasses vectors of bf16, or
+// twice as many of float32; of a tensor's last chunk the whole vectors that are
+// there (zeros for the others) and one of the elements behind them, so that such a
+// chunk too is one trip to memory and not one for every 256 elements.
 struct Raw {
     uint4 v[2 * kPasses];
+    uint32_t tail;
     __device__ __forceinline__ void load(const Item& t) {
-        if (t.n < kNormChunk) return;  // read element by element
         const uint4* p = reinterpret_cast<const uint4*>(t.at) + threadIdx.x;
-        if (t.f32) {
+        tail = 0;
+        if (t.n == kNormChunk) {
+            if (t.f32) {
 #pragma unroll
-            for (int i = 0; i < 2 * kPasses; ++i) v[i] = p[i * kThreads];
-        } else {
+                for (int i = 0; i < 2 * kPasses; ++i) v[i] = p[i * kThreads];
+            } else {
 #pragma unroll
-            for (int i = 0; i < kPasses; ++i) v[i] = p[i * kThreads];
+                for (int i = 0; i < kPasses; ++i) v[i] = p[i * kThreads];
+            }
+            return;
+        }
+        const int per = t.f32 ? 4 : 8, whole = t.n / per, rest = t.n % per;
+#pragma unroll
+        for (int i = 0; i < 2 * kPasses; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (static_cast<int>(threadIdx.x) + i * kThreads < whole) v[i] = p[i * kThreads];
+        }
+        if (static_cast<int>(threadIdx.x) < rest) {
+            const int at = whole * per + threadIdx.x;
+            tail = t.f32 ? reinterpret_cast<const uint32_t*>(t.at)[at]
+                         : static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(t.at)[at]) << 16;
         }
     }
 };
 
-__device__ __forceinline__ double squared(float f, double s) {
-    const double d = f;
+__device__ __forceinline__ double squared(uint32_t bits, double s) {
+    const double d = __uint_as_float(bits);
     return fma(d, d, s);
 }
 __device__ __forceinline__ double squares(const Item& t, const Raw& r) {
-    double s = 0.0;
-    if (t.n < kNormChunk) {
-        if (t.f32) {
-            const float* p = reinterpret_cast<const float*>(t.at);
-            for (int i = threadIdx.x; i < t.n; i += kThreads) s = squared(p[i], s);
-        } else {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(t.at);
-            for (int i = threadIdx.x; i < t.n; i += kThreads) s = squared(widen(p[i]), s);
-        }
-        return s;
-    }
+    double s = squared(r.tail, 0.0);
     if (t.f32) {
 #pragma unroll
         for (int i = 0; i < 2 * kPasses; ++i) {
-            s = squared(__uint_as_float(r.v[i].x), s);
-            s = squared(__uint_as_float(r.v[i].y), s);
-            s = squared(__uint_as_float(r.v[i].z), s);
-            s = squared(__uint_as_float(r.v[i].w), s);
+            s = squared(r.v[i].x, s);
+            s = squared(r.v[i].y, s);
+            s = squared(r.v[i].z, s);
+            s = squared(r.v[i].w, s);
         }
     } else {
 #pragma unroll
@@ -160,8 +167,8 @@ __device__ __forceinline__ double squares(const Item& t, const Raw& r) {
             const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s = squared(__uint_as_float(w[j] << 16), s);
-                s = squared(__uint_as_float(w[j] & 0xFFFF0000u), s);
+                s = squared(w[j] << 16, s);
+                s = squared(w[j] & 0xFFFF0000u, s);
             }
         }
     }
@@ -280,9 +287,8 @@ __global__ __launch_bounds__(kThreads) void gradclip_kernel(const ss1_gradnorm_e
         if (coef) *coef = r.coef;
     }
     if (r.coef == 1.0f) return;
-    // backwards: what the sum read last is still in the last-level cache
-    const int64_t begin_item = first_item(chunks, blockIdx.x, gridDim.x);
-    for (int64_t i = first_item(chunks, blockIdx.x + 1, gridDim.x) - 1; i >= begin_item; --i) {
+    const int64_t end = first_item(chunks, blockIdx.x + 1, gridDim.x);
+    for (int64_t i = first_item(chunks, blockIdx.x, gridDim.x); i < end; ++i) {
         const int item = map[2 * i];
         const int64_t part = map[2 * i + 1];
         if (item < 0 || item >= count || part < 0) continue;

@@ -819,7 +819,7 @@ typedef struct {
  * summed in float32 in a fixed order that depends on the ids, M, V and K
  * alone, scaled, added to dE in float32 and rounded once: nothing is atomic
  * across blocks, equal calls give equal bits.
- * Requirements: as the forward, M < 2^31, M * K and V * K under 2^40.
+ * Requirements: as the forward, M < 2^30, M * K and V * K under 2^40.
  * M == 0 leaves dE zero (accumulate 0) or as it is.
  * Errors: as the forward; SS1_ERR_SHAPE for a workspace that is too small.
  */
@@ -839,7 +839,8 @@ ss1_status ss1_embedding_backward(const ss1_tensor* dy, const ss1_tokens* tokens
  *   codes : [rows][Cp], Cp = cols rounded up to a multiple of 128; columns from
  *           cols on hold zeros
  *   scale : [ceil(rows / block)][Sp] bytes (E8M0), Sp = Cp / 128 rounded up to
- *           a multiple of 4; bytes from Cp / 128 on are 127 (never used)
+ *           a multiple of 4; 1 to 254 each (2^-126 to 2^127); bytes from
+ *           Cp / 128 on are 127 (never used)
  *   block : 1 (a scale for 128 elements of a row: activations, gradients) or
  *           128 (one for a tile of 128 x 128: weights, whose transposed codes
  *           then are the same codes)

@@ -181,25 +181,173 @@ struct Own {
     bool before;
 };
 template <typename I>
-__device__ __forceinline__ Own own_row(I id, int64_t V, const RowOrder& o) {
-    const bool real = static_cast<uint64_t>(static_cast<int64_t>(id)) < static_cast<uint64_t>(V);
+__device__ __forceinline__ bool is_row(I id, int64_t V) {
+    return static_cast<uint64_t>(static_cast<int64_t>(id)) < static_cast<uint64_t>(V);
+}
+template <typename I>
+__device__ __forceinline__ Own own_row(I id, int64_t V, const RowOrder& o, uint32_t block) {
+    const bool real = is_row(id, V);
     const uint32_t v = static_cast<uint32_t>(id);  // V < 2^29
     const uint32_t owner = v & ((1u << o.log2_blocks) - 1);
     Own r;
-    r.row = real && owner == blockIdx.x ? static_cast<int>(v >> o.log2_blocks) : -1;
-    r.before = real && owner < blockIdx.x;
+    r.row = real && owner == block ? static_cast<int>(v >> o.log2_blocks) : -1;
+    r.before = real && owner < block;
     return r;
+}
+
+// Counts the wave's keys (-1: none) in LDS; the lanes that share the first one's
+// make one addition, since the additions to one address follow each other.
+__device__ __forceinline__ void count_keys(int32_t* hist, int key) {
+    const uint64_t some = __ballot(key >= 0);
+    if (some == 0) return;
+    const int lane = threadIdx.x & 63, first = __builtin_ctzll(some);
+    const uint64_t same = __ballot(key == __builtin_amdgcn_readlane(key, first));
+    if (lane == first) atomicAdd(&hist[key], static_cast<int>(__popcll(same)));
+    else if (key >= 0 && !(same >> lane & 1)) atomicAdd(&hist[key], 1);
+}
+
+// Place of each lane's key among the wave's, next[key] being the first free one:
+// the lanes of one key take consecutive places.
+__device__ __forceinline__ int take_place(int32_t* next, int key, int bits) {
+    const int lane = threadIdx.x & 63;
+    uint64_t same = __ballot(key >= 0);
+    int p = 0;
+    if (same == 0) return p;
+    for (int b = 0; b < bits; ++b) {
+        const bool bit = (key >> b) & 1;
+        const uint64_t set = __ballot(bit);
+        same &= bit ? set : ~set;
+    }
+    if (key >= 0) {
+        p = next[key] + __popcll(same & ((uint64_t(1) << lane) - 1));
+        // the key's last lane of the step, after every lane's read
+        if ((same >> lane) == 1) next[key] = p + 1;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return p;
+}
+
+// The sum over the block's threads before this one (kSortThreads of them).
+__device__ __forceinline__ int scan_before(int mine, int32_t* sums) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int scan = mine;
+    for (int off = 1; off < 64; off <<= 1) {
+        const int t = __shfl_up(scan, off);
+        if (lane >= off) scan += t;
+    }
+    if (lane == 63) sums[wave] = scan;
+    __syncthreads();
+    int at = scan - mine;
+    for (int w = 0; w < wave; ++w) at += sums[w];
+    return at;
+}
+
+// ------------------------------------------------------------- many tokens
+// With many tokens, every block's reading of all ids is the time (256 blocks x
+// 131072 ids: 91 us of the sort), so they are first handed out to the blocks
+// that own them: chunk c of the ids counts them by owner, and then puts them,
+// in order, behind those of the chunks before it.  Every chunk adds up the
+// counts for itself.
+constexpr int kOwners = 512;   // owners at most
+constexpr int kChunks = 128;   // chunks at most
+
+struct Token {
+    int32_t row;  // among the owner's
+    int32_t m;
+};
+
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void embedding_count_kernel(const I* __restrict__ ids, int M, int64_t V,
+                                                                       RowOrder o, int chunk,
+                                                                       int32_t* __restrict__ counts) {
+    __shared__ int32_t hist[kOwners];
+    const int tid = threadIdx.x, owners = 1 << o.log2_blocks;
+    for (int i = tid; i < owners; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    const int begin = blockIdx.x * chunk, end = min(begin + chunk, M);
+    for (int i = begin; i < end; i += kSortThreads) {
+        const I id = i + tid < end ? ids[i + tid] : static_cast<I>(-1);
+        count_keys(hist, is_row(id, V) ? static_cast<int>(static_cast<uint32_t>(id) & (owners - 1)) : -1);
+    }
+    __syncthreads();
+    for (int i = tid; i < owners; i += kSortThreads) counts[blockIdx.x * owners + i] = hist[i];
+}
+
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void embedding_deal_kernel(const I* __restrict__ ids, int M, int64_t V,
+                                                                      RowOrder o, int chunk, int chunks,
+                                                                      const int32_t* __restrict__ counts,
+                                                                      int32_t* __restrict__ first,
+                                                                      Token* __restrict__ tokens) {
+    __shared__ int32_t hist[kSortWaves][kOwners];
+    __shared__ int32_t total[2][kSortThreads];
+    __shared__ int32_t sums[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int owners = 1 << o.log2_blocks;
+    for (int i = tid; i < kSortWaves * owners; i += kSortThreads) hist[i >> o.log2_blocks][i & (owners - 1)] = 0;
+    // an owner's tokens, of all chunks and of those before this one: the threads
+    // of an owner take every (kSortThreads / owners)-th chunk
+    int all = 0, before = 0;
+    for (int c = tid >> o.log2_blocks; c < chunks; c += kSortThreads >> o.log2_blocks) {
+        const int n = counts[c * owners + (tid & (owners - 1))];
+        all += n;
+        before += c < static_cast<int>(blockIdx.x) ? n : 0;
+    }
+    total[0][tid] = all;
+    total[1][tid] = before;
+    __syncthreads();
+
+    const int begin = blockIdx.x * chunk, end = min(begin + chunk, M);
+    const int run = chunk / kSortWaves;  // of a wave: whole steps of 64
+    const int from = begin + wave * run;
+    auto owner_at = [&](int i) {
+        const I id = i < end ? ids[i] : static_cast<I>(-1);
+        return is_row(id, V) ? static_cast<int>(static_cast<uint32_t>(id) & (owners - 1)) : -1;
+    };
+    for (int i = 0; i < run; i += 64) count_keys(hist[wave], owner_at(from + i + lane));
+    __syncthreads();
+
+    all = before = 0;
+    if (tid < owners)
+        for (int i = tid; i < kSortThreads; i += owners) {
+            all += total[0][i];
+            before += total[1][i];
+        }
+    const int base = scan_before(all, sums);
+    if (blockIdx.x == 0 && tid < owners) first[tid] = base;
+    if (blockIdx.x == 0 && tid == owners - 1) first[owners] = base + all;
+    if (tid < owners) {
+        int at = base + before;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int n = hist[w][tid];
+            hist[w][tid] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    for (int i = 0; i < run; i += 64) {
+        const int m = from + i + lane;
+        const int owner = owner_at(m);
+        const int p = take_place(hist[wave], owner, o.log2_blocks);
+        if (owner >= 0) tokens[p] = {static_cast<int32_t>(static_cast<uint32_t>(ids[m]) >> o.log2_blocks), m};
+    }
 }
 
 // Writes start[place of row] (where the row's tokens begin in the sorted order)
 // for the block's rows, the last block also the end of the last row, and
 // order[] (the tokens by row, ascending within a row).  Blocks from `blocks` on
 // clear the first zero_vecs 16-byte vectors of dE meanwhile.
+//
+// I is the type of the ids, or Token: then the block's own tokens are dealt
+// already, from place first[block] on.
 template <typename I>
 __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* __restrict__ ids, int M, int64_t V,
-                                                                      RowOrder o, int32_t* __restrict__ start,
+                                                                      RowOrder o, const int32_t* __restrict__ first,
+                                                                      int32_t* __restrict__ start,
                                                                       int32_t* __restrict__ order,
                                                                       u32x4* __restrict__ dE, int64_t zero_vecs) {
+    constexpr bool DEALT = __is_same(I, Token);
     __shared__ int32_t hist[kSortWaves][kSortRows];
     __shared__ int32_t sums[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -214,36 +362,50 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
     }
     for (int r = tid & 511; r < o.rows; r += 512)
         for (int w = tid >> 9; w < kSortWaves; w += kSortThreads >> 9) hist[w][r] = 0;
+    const int begin = DEALT ? first[blockIdx.x] : 0, n = DEALT ? first[blockIdx.x + 1] - begin : M;
     __syncthreads();
 
-    // the wave's run of ids: whole steps of 64
-    const int steps = (M + kSortThreads - 1) / kSortThreads;
-    const int64_t first = static_cast<int64_t>(wave) * steps * 64;
-    const I none = static_cast<I>(-1);
+    // the wave's run of the tokens: whole steps of 64
+    const int steps = (n + kSortThreads - 1) / kSortThreads;
+    const int64_t run = begin + static_cast<int64_t>(wave) * steps * 64, end = begin + static_cast<int64_t>(n);
+    struct Key {
+        int row, m;
+        bool before;
+    };
+    auto fetch = [&](int s) {
+        const int64_t i = run + s * 64 + lane;
+        if constexpr (DEALT) return i < end ? ids[i] : Token{-1, 0};
+        else return i < end ? ids[i] : static_cast<I>(-1);
+    };
+    auto key_of = [&](I t, int s) {
+        if constexpr (DEALT) {
+            return Key{t.row, t.m, false};
+        } else {
+            const Own w = own_row(t, V, o, blockIdx.x);
+            return Key{w.row, static_cast<int>(run) + s * 64 + lane, w.before};
+        }
+    };
     I keep[kSortKeep];
 #pragma unroll
-    for (int s = 0; s < kSortKeep; ++s) {
-        const int64_t m = first + s * 64 + lane;
-        keep[s] = s < steps && m < M ? ids[m] : none;
-    }
+    for (int s = 0; s < kSortKeep; ++s)
+        if (s < steps) keep[s] = fetch(s);
     int before = 0;
-    auto count = [&](I id) {
-        const Own w = own_row(id, V, o);
-        if (w.row >= 0) atomicAdd(&hist[wave][w.row], 1);
-        before += __popcll(__ballot(w.before));
+    auto count = [&](I t, int s) {
+        const Key k = key_of(t, s);
+        count_keys(hist[wave], k.row);
+        if constexpr (!DEALT) before += __popcll(__ballot(k.before));
     };
 #pragma unroll
     for (int s = 0; s < kSortKeep; ++s)
-        if (s < steps) count(keep[s]);
-    for (int s = kSortKeep; s < steps; ++s) {
-        const int64_t m = first + s * 64 + lane;
-        count(m < M ? ids[m] : none);
-    }
-    if (lane == 0) sums[wave] = before;
-    __syncthreads();
-    int base = 0;
+        if (s < steps) count(keep[s], s);
+    for (int s = kSortKeep; s < steps; ++s) count(fetch(s), s);
+    int base = begin;
+    if constexpr (!DEALT) {
+        if (lane == 0) sums[wave] = before;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) base += sums[w];
+        for (int w = 0; w < kSortWaves; ++w) base += sums[w];
+    }
     __syncthreads();
 
     // prefix sum over the rows (thread r has row r), the waves of a row in turn
@@ -251,15 +413,7 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
     if (tid < o.rows)
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) mine += own[w] = hist[w][tid];
-    int scan = mine;
-    for (int off = 1; off < 64; off <<= 1) {
-        const int t = __shfl_up(scan, off);
-        if (lane >= off) scan += t;
-    }
-    if (lane == 63) sums[wave] = scan;
-    __syncthreads();
-    int at = base + scan - mine;
-    for (int w = 0; w < wave; ++w) at += sums[w];
+    int at = base + scan_before(mine, sums);
     if (tid < o.rows) start[static_cast<int64_t>(blockIdx.x) * o.rows + tid] = at;
     if (static_cast<int>(blockIdx.x) == blocks - 1 && tid == o.rows - 1)
         start[static_cast<int64_t>(blocks) * o.rows] = at + mine;
@@ -271,33 +425,16 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const I* _
         }
     __syncthreads();
 
-    // places: the lanes of one row in a step take consecutive ones
     const int bits = 32 - __builtin_clz(o.rows);
-    auto put = [&](I id, int64_t m) {
-        const int row = own_row(id, V, o).row;
-        uint64_t same = __ballot(row >= 0);
-        if (same == 0) return;
-        for (int b = 0; b < bits; ++b) {
-            const bool bit = (row >> b) & 1;
-            const uint64_t set = __ballot(bit);
-            same &= bit ? set : ~set;
-        }
-        if (row >= 0) {
-            const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-            const int p = hist[wave][row] + rank;
-            order[p] = static_cast<int32_t>(m);
-            // the row's last lane of the step, after every lane's read
-            if ((same >> lane) == 1) hist[wave][row] = p + 1;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    auto put = [&](I t, int s) {
+        const Key k = key_of(t, s);
+        const int p = take_place(hist[wave], k.row, bits);
+        if (k.row >= 0) order[p] = k.m;
     };
 #pragma unroll
     for (int s = 0; s < kSortKeep; ++s)
-        if (s < steps) put(keep[s], first + s * 64 + lane);
-    for (int s = kSortKeep; s < steps; ++s) {
-        const int64_t m = first + s * 64 + lane;
-        put(m < M ? ids[m] : none, m);
-    }
+        if (s < steps) put(keep[s], s);
+    for (int s = kSortKeep; s < steps; ++s) put(fetch(s), s);
 }
 
 // ------------------------------------------------------------------------ sum
@@ -315,6 +452,13 @@ __device__ __forceinline__ void write_row(T* p, int n, const float (&sum)[kVec],
         for (int j = 0; j < kVec; ++j) v[j] = sum[j] * scale;
     }
     store_row<kVec>(p, v, n);
+}
+
+// Zeros in columns [from, to) of a row by one wave, 16 bytes a lane side by side.
+template <typename T>
+__device__ __forceinline__ void zero_row(T* p, int from, int to, int lane) {
+    const float zero[kVecOf<T>] = {};
+    for (int c = from + lane * kVecOf<T>; c < to; c += kSliceOf<T>) store_row<kVecOf<T>>(p + c, zero, to - c);
 }
 
 struct SumArgs {
@@ -361,11 +505,10 @@ __global__ __launch_bounds__(kSumThreads) void embedding_sum_kernel(const I* __r
             empty = a.start[p] == a.start[p + 1];
         }
         uint64_t rows = __ballot(empty);
-        const float zero[kVec] = {};
         while (rows) {
             const int r = __builtin_ctzll(rows);
             rows &= rows - 1;
-            for (int c = lane * kVec; c < K; c += kSlice) store_row<kVec>(dE + (v0 + r) * K + c, zero, K - c);
+            zero_row(dE + (v0 + r) * K, 0, K, lane);
         }
         return;
     }
@@ -481,25 +624,31 @@ __global__ __launch_bounds__(kSumThreads) void embedding_join_kernel(const I* __
 }
 
 // ---------------------------------------------------------------- few tokens
+constexpr int kFewTokens = 512;
 constexpr int kFewBatch = 16;
+constexpr int kFewShared = 64;                       // more tokens: a row that the waves share
+constexpr int kFewHot = kFewTokens / kFewShared;     // such rows at most
 
-// Up to kSortThreads tokens in one launch: a block keeps the tokens of its rows
-// in LDS, one a thread and in order, ranks each by counting the ones that come
+// Up to kFewTokens tokens in one launch: a block keeps the tokens of its rows in
+// LDS, one a thread and in order, ranks each by counting the ones that come
 // before it (a smaller row, or the same row earlier), and then its waves sum
-// and write the rows, or zeros, in columns of 64 lanes.
+// and write the rows, or zeros, in columns of 64 lanes.  A row with many tokens
+// is shared by all waves of its block.
 template <typename I, typename TD, typename TE>
 __global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __restrict__ ids,
                                                                      const TD* __restrict__ dy, TE* __restrict__ dE,
                                                                      int M, int64_t V, int K, RowOrder o, float scale,
                                                                      int accumulate) {
     constexpr int kVec = kVecOf<TD>, kSlice = kSliceOf<TD>;
-    __shared__ int32_t list_row[kSortThreads], list_m[kSortThreads];  // as found
-    __shared__ int32_t sorted_m[kSortThreads];
+    __shared__ __attribute__((aligned(16))) int32_t list[kFewTokens];  // row * kFewTokens + place, as found
+    __shared__ int32_t list_m[kFewTokens], sorted_m[kFewTokens], sorted_row[kFewTokens];
     __shared__ int32_t begin[kSortRows + 1];
     __shared__ int32_t sums[kSortWaves];
+    __shared__ int32_t hot[kFewHot], hot_count;
+    __shared__ float part[kSortWaves][kVec][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row = tid < M ? own_row(ids[tid], V, o).row : -1;
+    const int row = tid < M ? own_row(ids[tid], V, o, blockIdx.x).row : -1;
     const uint64_t found = __ballot(row >= 0);
     if (lane == 0) sums[wave] = __popcll(found);
     for (int r = tid; r <= o.rows; r += kSortThreads) begin[r] = 0;
@@ -511,25 +660,30 @@ __global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __
         n += sums[w];
     }
     if (row >= 0) {
-        list_row[at] = row;
+        list[at] = row * kFewTokens + at;
         list_m[at] = tid;
     }
+    if (tid < 4 && n + tid < kFewTokens) list[n + tid] = 0x7FFFFFFF;  // the last four are read whole
     __syncthreads();
+    int rank = 0;
     if (tid < n) {
-        const int r = list_row[tid];
-        int rank = 0, last = 1;
-        for (int i = 0; i < n; ++i) {
-            const int other = list_row[i];
-            rank += other < r || (other == r && i < tid);
-            last &= !(other == r && i > tid);
+        const int mine = list[tid];
+        for (int i = 0; i < n; i += 4) {
+            const int4 k = *reinterpret_cast<const int4*>(list + i);
+            rank += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
         }
         sorted_m[rank] = list_m[tid];
-        if (last) begin[r + 1] = rank + 1;  // where the row ends
+        sorted_row[rank] = mine / kFewTokens;
+    }
+    __syncthreads();
+    if (tid < n) {  // where a row ends
+        const int r = sorted_row[tid];
+        if (tid + 1 == n || sorted_row[tid + 1] != r) begin[r + 1] = tid + 1;
     }
     __syncthreads();
     // rows without tokens end where the row before ends; a wave scans 64 at a time
     if (wave == 0) {
-        int carry = 0;
+        int carry = 0, many = 0;
         for (int r0 = 1; r0 <= o.rows; r0 += 64) {
             int e = r0 + lane <= o.rows ? begin[r0 + lane] : 0;
             for (int off = 1; off < 64; off <<= 1) {
@@ -538,29 +692,26 @@ __global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __
             }
             e = max(e, carry);
             if (r0 + lane <= o.rows) begin[r0 + lane] = e;
+            const int up = __shfl_up(e, 1);
+            const bool is_hot = r0 + lane <= o.rows && e - (lane ? up : carry) > kFewShared;
+            const uint64_t hots = __ballot(is_hot);
+            if (is_hot) hot[many + __popcll(hots & ((uint64_t(1) << lane) - 1))] = r0 + lane - 1;
+            many += __popcll(hots);
             carry = __builtin_amdgcn_readlane(e, 63);
         }
+        if (lane == 0) hot_count = many;
     }
     __syncthreads();
     const int slices = (K + kSlice - 1) / kSlice;
-    const int units = o.rows * slices;
-    for (int u = wave; u < units; u += kSortWaves) {
-        const int r = u / slices;
-        const int64_t v = (static_cast<int64_t>(r) << o.log2_blocks) + blockIdx.x;
-        if (v >= V) break;
-        const int from = __builtin_amdgcn_readfirstlane(begin[r]), to = __builtin_amdgcn_readfirstlane(begin[r + 1]);
-        if (from == to && accumulate) continue;
-        const int c = (u - r * slices) * kSlice + lane * kVec;
-        const int left = K - c;
-        if (left <= 0) continue;
-        float sum[kVec];
+    auto add = [&](float (&sum)[kVec], int from, int to, int c) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+        if (c >= K) return;
         for (int i0 = from; i0 < to; i0 += kFewBatch) {
             Raw<TD, kVec> d[kFewBatch];
 #pragma unroll
             for (int i = 0; i < kFewBatch; ++i)
-                if (i0 + i < to) d[i].load(dy + static_cast<int64_t>(sorted_m[i0 + i]) * K + c, left);
+                if (i0 + i < to) d[i].load(dy + static_cast<int64_t>(sorted_m[i0 + i]) * K + c, K - c);
 #pragma unroll
             for (int i = 0; i < kFewBatch; ++i) {
                 if (i0 + i < to) {
@@ -569,7 +720,43 @@ __global__ __launch_bounds__(kSortThreads) void embedding_few_kernel(const I* __
                 }
             }
         }
-        write_row(dE + v * K + c, left, sum, scale, accumulate);
+    };
+    for (int u = wave; u < o.rows * slices; u += kSortWaves) {
+        const int r = u / slices;
+        const int64_t v = (static_cast<int64_t>(r) << o.log2_blocks) + blockIdx.x;
+        if (v >= V) break;
+        const int from = __builtin_amdgcn_readfirstlane(begin[r]), to = __builtin_amdgcn_readfirstlane(begin[r + 1]);
+        if (to - from > kFewShared) continue;
+        const int c0 = (u - r * slices) * kSlice, c = c0 + lane * kVec;
+        if (from == to) {
+            if (!accumulate) zero_row(dE + v * K, c0, min(c0 + kSlice, K), lane);
+            continue;
+        }
+        if (c >= K) continue;
+        float sum[kVec];
+        add(sum, from, to, c);
+        write_row(dE + v * K + c, K - c, sum, scale, accumulate);
+    }
+    const int shared = __builtin_amdgcn_readfirstlane(hot_count) * slices;
+    for (int u = 0; u < shared; ++u) {
+        const int r = __builtin_amdgcn_readfirstlane(hot[u / slices]);
+        const int from = __builtin_amdgcn_readfirstlane(begin[r]);
+        const int n = __builtin_amdgcn_readfirstlane(begin[r + 1]) - from;
+        const int c = u % slices * kSlice + lane * kVec;
+        float sum[kVec];
+        add(sum, from + n * wave / kSortWaves, from + n * (wave + 1) / kSortWaves, c);
+        if (u > 0) __syncthreads();  // the shares before are read
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) part[wave][j][lane] = sum[j];
+        __syncthreads();
+        if (wave == u % kSortWaves && c < K) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                sum[j] = part[0][j][lane];
+                for (int w = 1; w < kSortWaves; ++w) sum[j] += part[w][j][lane];
+            }
+            write_row(dE + ((static_cast<int64_t>(r) << o.log2_blocks) + blockIdx.x) * K + c, K - c, sum, scale, accumulate);
+        }
     }
 }
 
@@ -588,6 +775,24 @@ int32_t tile_tokens(int64_t M) {
     int64_t T = kTile;
     while ((M + T - 1) / T > kMaxTiles) T *= 2;
     return static_cast<int32_t>(T);
+}
+
+// Whether one launch does it all.
+constexpr int64_t kFewElements = int64_t(1) << 19, kFewTable = int64_t(1) << 27;
+bool few_tokens(int64_t M, int64_t V, int64_t K) {
+    return M <= kFewTokens && M * K <= kFewElements && V * K <= kFewTable;
+}
+
+// Chunks of the ids that are dealt out before the sort, 0 where they are not.
+constexpr int64_t kDealTokens = 16384;
+int64_t chunk_tokens(int64_t M) { return up_to((M + kChunks - 1) / kChunks, kSortThreads); }
+int32_t deal_chunks(int64_t M, const RowOrder& o) {
+    if (M < kDealTokens || (1 << o.log2_blocks) > kOwners) return 0;
+    return static_cast<int32_t>((M + chunk_tokens(M) - 1) / chunk_tokens(M));
+}
+size_t deal_bytes(int64_t M, const RowOrder& o) {
+    const int64_t chunks = deal_chunks(M, o), owners = int64_t(1) << o.log2_blocks;
+    return chunks == 0 ? 0 : static_cast<size_t>(M * 8 + up_to((owners + 1) * 4, 16) + chunks * owners * 4);
 }
 
 size_t start_bytes(const RowOrder& o) {
@@ -618,9 +823,10 @@ ss1_status backward_t(const EmbeddingArgs& a) {
     const TD* dy = static_cast<const TD*>(a.dy);
     TE* dE = static_cast<TE*>(a.dE);
     const unsigned blocks = 1u << o.log2_blocks;
-    if (a.M <= kSortThreads) {
-        hipLaunchKernelGGL((embedding_few_kernel<I, TD, TE>), dim3(blocks), dim3(kSortThreads), 0, stream, ids, dy, dE,
-                           static_cast<int>(a.M), a.V, a.K, o, a.scale, a.accumulate);
+    const int slices = (a.K + kSliceOf<TD> - 1) / kSliceOf<TD>;
+    if (few_tokens(a.M, a.V, a.K)) {
+        hipLaunchKernelGGL((embedding_few_kernel<I, TD, TE>), dim3(blocks), dim3(kSortThreads), 0, stream, ids,
+                           dy, dE, static_cast<int>(a.M), a.V, a.K, o, a.scale, a.accumulate);
         return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
     }
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -637,7 +843,7 @@ ss1_status backward_t(const EmbeddingArgs& a) {
     s.accumulate = a.accumulate;
     s.o = o;
     s.scale = a.scale;
-    s.slices = (a.K + kSliceOf<TD> - 1) / kSliceOf<TD>;
+    s.slices = slices;
     s.sum_blocks = (s.tiles * s.slices + kSumWaves - 1) / kSumWaves;
     // rows that the sort's launch clears: whole 16-byte vectors, but for the
     // rows at the table's end
@@ -648,14 +854,29 @@ ss1_status backward_t(const EmbeddingArgs& a) {
         zero_vecs = s.zeroed * row / 16;
         zero_blocks = (a.V - s.zeroed + kZeroRows * kSumWaves - 1) / (kZeroRows * kSumWaves);
     }
-    hipLaunchKernelGGL((embedding_sort_kernel<I>),
-                       dim3(blocks + static_cast<unsigned>((zero_vecs + kZeroVecs - 1) / kZeroVecs)),
-                       dim3(kSortThreads), 0, stream, ids, static_cast<int>(a.M), a.V, o, start, order,
-                       reinterpret_cast<u32x4*>(dE), zero_vecs);
+    const dim3 sort_grid(blocks + static_cast<unsigned>((zero_vecs + kZeroVecs - 1) / kZeroVecs));
+    const int M = static_cast<int>(a.M);
+    u32x4* zeros = reinterpret_cast<u32x4*>(dE);
+    if (const int chunks = deal_chunks(a.M, o)) {
+        const int chunk = static_cast<int>(chunk_tokens(a.M));
+        Token* tokens = reinterpret_cast<Token*>(s.partial + static_cast<int64_t>(s.tiles) * 2 * a.K);
+        int32_t* first = reinterpret_cast<int32_t*>(tokens + a.M);
+        int32_t* counts = first + up_to(static_cast<int64_t>(blocks) + 1, 4);
+        hipLaunchKernelGGL((embedding_count_kernel<I>), dim3(chunks), dim3(kSortThreads), 0, stream, ids, M, a.V, o,
+                           chunk, counts);
+        hipLaunchKernelGGL((embedding_deal_kernel<I>), dim3(chunks), dim3(kSortThreads), 0, stream, ids, M, a.V, o,
+                           chunk, chunks, counts, first, tokens);
+        hipLaunchKernelGGL((embedding_sort_kernel<Token>), sort_grid, dim3(kSortThreads), 0, stream, tokens, M, a.V, o,
+                           first, start, order, zeros, zero_vecs);
+    } else {
+        hipLaunchKernelGGL((embedding_sort_kernel<I>), sort_grid, dim3(kSortThreads), 0, stream, ids, M, a.V, o,
+                           static_cast<const int32_t*>(nullptr), start, order, zeros, zero_vecs);
+    }
     hipLaunchKernelGGL((embedding_sum_kernel<I, TD, TE>), dim3(static_cast<unsigned>(s.sum_blocks + zero_blocks)),
                        dim3(kSumThreads), 0, stream, ids, dy, dE, s);
-    hipLaunchKernelGGL((embedding_join_kernel<I, TD, TE>), dim3(static_cast<unsigned>(s.tiles * s.slices)),
-                       dim3(kSumThreads), 0, stream, ids, dE, s);
+    if (s.tiles > 0)
+        hipLaunchKernelGGL((embedding_join_kernel<I, TD, TE>), dim3(static_cast<unsigned>(s.tiles * s.slices)),
+                           dim3(kSumThreads), 0, stream, ids, dE, s);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
@@ -680,10 +901,11 @@ ss1_status launch_embedding_forward(const EmbeddingArgs& a) {
 }
 
 size_t embedding_backward_workspace(int64_t M, int64_t V, int32_t K) {
-    if (M <= kSortThreads) return 0;
+    if (few_tokens(M, V, K)) return 0;
     const RowOrder o = row_order(V);
     const int64_t T = tile_tokens(M), tiles = (M + T - 1) / T;
-    return start_bytes(o) + static_cast<size_t>(up_to(M * 4, 16)) + static_cast<size_t>(tiles) * 2 * K * 4;
+    return start_bytes(o) + static_cast<size_t>(up_to(M * 4, 16)) + static_cast<size_t>(tiles) * 2 * K * 4 +
+           deal_bytes(M, o);
 }
 
 ss1_status launch_embedding_backward(const EmbeddingArgs& a) {

@@ -16,6 +16,8 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 // a grid's threads are numbered in 32 bits: rows of a table over 64 rows a block
 constexpr int64_t kMaxTable = int64_t(1) << 29;
 constexpr int64_t kMaxWidth = int64_t(1) << 16;
+// tokens of an embedding's gradient: places rounded up to whole tiles stay under 2^31
+constexpr int64_t kMaxGradTokens = int64_t(1) << 30;
 // tiles of 128 x 128 of a matrix that is quantised, and of a product
 constexpr int64_t kMaxQuantTiles = int64_t(1) << 24;
 constexpr int64_t kMaxTiles = int64_t(1) << 22;
@@ -178,6 +180,7 @@ extern "C" ss1_status ss1_embedding_backward_query(const ss1_tokens* tokens, con
     if (!bytes) return SS1_ERR_NULL;
     SS1_TRY(check_tokens(tokens, false));
     SS1_TRY(check_table(dE, false));
+    if (tokens->count >= kMaxGradTokens) return SS1_ERR_SHAPE;
     if (tokens->count > 0 && dE->cols > (int64_t(1) << 40) / tokens->count) return SS1_ERR_SHAPE;
     *bytes = ss1::embedding_backward_workspace(tokens->count, dE->rows, static_cast<int32_t>(dE->cols));
     return SS1_OK;
@@ -191,6 +194,7 @@ extern "C" ss1_status ss1_embedding_backward(const ss1_tensor* dy, const ss1_tok
     SS1_TRY(check_table(dE, true));
     SS1_TRY(check_matrix(dy, true));
     SS1_TRY(check_sizes(dy, tokens->count, dE->cols));
+    if (tokens->count >= kMaxGradTokens) return SS1_ERR_SHAPE;
     if (!isfinite(scale) || (accumulate != 0 && accumulate != 1)) return SS1_ERR_SHAPE;
     SS1_TRY(check_workspace(workspace, workspace_bytes,
                             ss1::embedding_backward_workspace(tokens->count, dE->rows,

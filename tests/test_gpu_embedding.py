@@ -108,7 +108,11 @@ def check_backward(M, V, K, kind, dy_t, dE_t, id_t, accumulate, scale=0.75, seed
 
 SHAPES = [(1023, 300, 2056), (1024, 3000, 1283), (1100, 70, 33), (2000, 900, 1032), (1, 1, 1), (1, 1000, 512), (2, 5, 8), (15, 300, 72), (16, 300, 520), (17, 2003, 1283), (333, 2003, 1283),
           (1024, 700, 256), (1025, 31, 1000), (3000, 50000, 64), (8192, 1000, 136), (20000, 4000, 24), (0, 40, 64),
-          (40, 0, 64), (512, 140000, 8)]
+          (40, 0, 64), (512, 140000, 8),
+          # one launch: rows that a block's waves share; and the last sizes of it
+          (511, 700, 1000), (130, 5, 4032), (512, 50, 1024), (512, 50, 1025), (513, 50, 9), (8, 300, 65536),
+          # tokens dealt out before the sort: chunks of one step and of several, 256, 512 and (not dealt) 1024 owners
+          (16384, 3000, 40), (16383, 3000, 40), (40000, 200000, 8), (17000, 300000, 4), (150000, 900, 16)]
 
 
 @pytest.mark.parametrize("M,V,K", SHAPES)

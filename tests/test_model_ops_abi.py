@@ -117,6 +117,7 @@ def test_embedding_forward_checks(kw, status):
     (dict(dy=T(5000, 64, FP8)), DTYPE), (dict(dE=T(50, 64, 4)), DTYPE), (dict(tokens=K(5000, 1)), DTYPE),
     (dict(dy=T(5001, 64)), SHAPE), (dict(dE=T(50, 63)), SHAPE), (dict(accumulate=2), SHAPE), (dict(accumulate=-1), SHAPE),
     (dict(scale=NAN), SHAPE), (dict(nbytes=64), SHAPE), (dict(dE=T(1 << 29, 64)), SHAPE),
+    (dict(dy=T(1 << 30, 64), tokens=K(1 << 30), nbytes=1 << 40), SHAPE),
     (dict(ws=A + 4), ALIGN), (dict(dy=T(5000, 64, data=A + 4)), ALIGN), (dict(dE=T(50, 64, data=A + 4)), ALIGN),
     (dict(tokens=K(0, data=None), dy=T(0, 64, data=None), accumulate=1), OK),
     (dict(dE=T(0, 64, data=None)), OK),
@@ -131,11 +132,12 @@ def test_embedding_backward_checks(kw, status):
 def test_embedding_query():
     lib, n = _lib.load(), ctypes.c_size_t(0)
     q = lib.ss1_embedding_backward_query
-    for M, V, k in ((0, 50, 64), (1, 1, 1), (8192, 50000, 1280), ((1 << 31) - 1, (1 << 29) - 1, 512)):
+    for M, V, k in ((0, 50, 64), (1, 1, 1), (8192, 50000, 1280), ((1 << 30) - 1, (1 << 29) - 1, 512)):
         assert q(byref(K(M, data=None)), byref(T(V, k, data=None)), byref(n)) == OK
         assert n.value >= (4 * (V + 1 + M) if M > 1024 else 0)
     assert q(byref(K(8)), byref(T(50, 65537)), byref(n)) == SHAPE
-    assert q(byref(K((1 << 31) - 1)), byref(T(50, 1024)), byref(n)) == SHAPE
+    assert q(byref(K((1 << 30) - 1)), byref(T(50, 1025)), byref(n)) == SHAPE
+    assert q(byref(K(1 << 30)), byref(T(50, 1)), byref(n)) == SHAPE
     assert q(None, byref(T(50, 64)), byref(n)) == NULL
     assert q(byref(K(8)), None, byref(n)) == NULL
     assert q(byref(K(8)), byref(T(50, 64)), None) == NULL

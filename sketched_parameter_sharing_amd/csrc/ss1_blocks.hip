@@ -13,6 +13,10 @@
 // its codes leave as whole 128-byte lines.  For the transposed codes the values
 // also go to LDS, from where a thread takes two neighbouring columns and 32
 // rows.
+//
+// Bound by memory where x is large: 14336 x 4096 bf16, both ways in tiles (235
+// MB), 54 us, 4.4 TB/s (the transposed codes leave in pieces of 32 bytes).
+// 1111 x 1283 float32, both ways, is 8.3 us of kernel and 12.5 of the host's time.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>

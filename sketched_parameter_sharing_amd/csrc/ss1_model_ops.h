@@ -13,7 +13,9 @@ namespace ss1 {
 // ------------------------------------------------------------ gradient norm
 // Elements of one work item, and blocks (partial sums) of a call: an item each
 // for up to kNormMost of them, else kNormBlocks blocks (all on the card at once)
-// with a run of consecutive items each.
+// with a run of consecutive items each.  Measured against items of 8192 over at
+// most 2048 blocks: 20M bf16 12.8 us for 17.0, 5M float32 9.5 for 13.0, 118M
+// bf16 46.9 for 50.8 (tensors' last items read as vectors came later).
 constexpr int64_t kNormChunk = 4096;
 constexpr int64_t kNormMost = 2048, kNormBlocks = 1024;
 inline int gradnorm_blocks(int64_t chunks) {

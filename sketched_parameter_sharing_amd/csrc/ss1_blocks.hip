@@ -12,11 +12,12 @@
 // registers (8 elements a lane), so a row's maximum is four lane exchanges and
 // its codes leave as whole 128-byte lines.  For the transposed codes the values
 // also go to LDS, from where a thread takes two neighbouring columns and 32
-// rows.
+// rows; the codes go back there, so that they too leave as whole lines (44 us of
+// kernel for 51 with each thread's 32 bytes stored at once, at the size below).
 //
 // Bound by memory where x is large: 14336 x 4096 bf16, both ways in tiles (235
-// MB), 54 us, 4.4 TB/s (the transposed codes leave in pieces of 32 bytes).
-// 1111 x 1283 float32, both ways, is 8.3 us of kernel and 12.5 of the host's time.
+// MB), 50 us a call, 4.7 TB/s.  1111 x 1283 float32, both ways, is 8.3 us of
+// kernel and 12.4 of the host's time.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -103,6 +104,8 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     T* tile = reinterpret_cast<T*>(smem);  // [128][kPitch], only with qt
     constexpr int kPitch = kB + 16 / static_cast<int>(sizeof(T));
+    constexpr int kCodePitch = kB + 16;  // bytes; in the same place
+    static_assert(kCodePitch <= kPitch * sizeof(T), "the codes fit into the tile");
     __shared__ uint32_t s_top[4][kB];
     __shared__ uint32_t s_wave[kThreads / 64];
     const int tid = threadIdx.x, l16 = tid & 15;
@@ -172,14 +175,13 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     if (!qt.shift) {
         s_top[part][2 * pair] = tops[0];
         s_top[part][2 * pair + 1] = tops[1];
-        __syncthreads();
     }
+    __syncthreads();  // the tile is read: the transposed codes take its place
     const int64_t blocks = qt.code_cols / kB;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int col = 2 * pair + h;
         const int64_t c = c0 + col;
-        if (c >= C) continue;
         uint32_t m = all;
         if (!qt.shift) m = larger(larger(s_top[0][col], s_top[1][col]), larger(s_top[2][col], s_top[3][col]));
         const uint32_t byte = scale_byte(m);
@@ -192,14 +194,22 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
             for (int i = 0; i < 32; ++i)
                 if ((t.bits(i, h) & 0x7FFFFFFFu) >= kInf) w[i / 4] |= 0x7Fu << (8 * (i & 3));
         }
-        uint4* out = reinterpret_cast<uint4*>(qt.codes + c * qt.code_cols + r0 + part * 32);
+        uint4* out = reinterpret_cast<uint4*>(smem + col * kCodePitch + part * 32);
         out[0] = make_uint4(w[0], w[1], w[2], w[3]);
         out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        if (part == 0 && (qt.shift == 0 || col == 0)) {
+        if (c < C && part == 0 && (qt.shift == 0 || col == 0)) {
             uint8_t* srow = qt.scale + (c >> qt.shift) * qt.scale_cols;
             srow[br] = static_cast<uint8_t>(byte);
             pad_scales(srow, br, blocks, qt.scale_cols);
         }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kB * 8 / kThreads; ++i) {  // 8 lanes a column: whole lines
+        const int col = (i * kThreads + tid) >> 3, piece = tid & 7;
+        if (c0 + col < C)
+            *reinterpret_cast<uint4*>(qt.codes + (c0 + col) * qt.code_cols + r0 + piece * 16) =
+                *reinterpret_cast<const uint4*>(smem + col * kCodePitch + piece * 16);
     }
 }
 

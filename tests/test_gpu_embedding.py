@@ -203,6 +203,39 @@ def test_captured_calls_replay_on_new_tokens():
         assert torch.equal(y, want_y) and torch.equal(dE, want)
 
 
+@pytest.mark.parametrize("V,K,M", [(700, 128, 300), (900, 72, 20000)])
+@pytest.mark.parametrize("id_t", [torch.int32, torch.int64])
+def test_captured_gradients_of_few_and_of_many_tokens(V, K, M, id_t):
+    dy = torch.randn((M, K), generator=gen(8), device="cuda").to(H)
+    ids, shared = ids_of("text", M, V, id_t), torch.zeros((V, K), device="cuda")
+    ss1.embedding_backward(dy, ids, V)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dE = ss1.embedding_backward(dy, ids, V)
+        ss1.embedding_backward(dy, ids, V, dE=shared, accumulate=True)
+    for k, kind in enumerate(("any", "same", "text", "all", "none")):
+        ids.copy_(ids_of(kind, M, V, id_t, seed=20 + k))
+        dy.normal_()
+        shared.fill_(k)
+        graph.replay()
+        want = ss1.embedding_backward(dy, ids, V)
+        more = ss1.embedding_backward(dy, ids, V, dE=torch.full((V, K), float(k), device="cuda"), accumulate=True)
+        torch.cuda.synchronize()
+        assert torch.equal(dE, want) and torch.equal(shared, more)
+
+
+def test_gradient_rows_past_32_bits():
+    M, K, V = 300_007, 8192, 8  # 2.46e9 elements
+    dy, ids = torch.zeros((M, K), dtype=H, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda")
+    for m, v in ((0, 3), (262_145, 5), (262_146, 3), (M - 1, 7)):
+        dy[m], ids[m] = m % 7 + 1, v
+    dE = ss1.embedding_backward(dy, ids, V, dtype=F)
+    want = torch.zeros((V, K), device="cuda")
+    want[3], want[5], want[7] = 1 + 262_146 % 7 + 1, 262_145 % 7 + 1, (M - 1) % 7 + 1
+    assert torch.equal(dE, want)
+
+
 def test_another_stream():
     V, K, M = 700, 128, 900
     table, ids = torch.randn((V, K), generator=gen(), device="cuda"), ids_of("text", M, V, torch.int32)

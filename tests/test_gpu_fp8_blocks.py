@@ -103,6 +103,17 @@ def test_codes_and_scales(R, C, dtype, tile, which):
         assert torch.equal(q.codes[:, :C].view(torch.uint8).t(), qt.codes[:, :R].view(torch.uint8))
 
 
+@pytest.mark.parametrize("R,C", [(1, 1), (129, 257), (300, 72)])
+@pytest.mark.parametrize("dtype", [H, F])
+@pytest.mark.parametrize("of_q,of_qt", [(1, 128), (128, 1)])
+def test_a_scale_of_rows_and_one_of_tiles_in_one_call(R, C, dtype, of_q, of_qt):
+    x = values(R, C, dtype)
+    q, qt = ss1.Fp8Blocks.empty(R, C, of_q), ss1.Fp8Blocks.empty(C, R, of_qt)
+    ss1.quantize_fp8_blocks(x, q=q, qt=qt)
+    same(q, x, of_q)
+    same(qt, x.t().contiguous(), of_qt)
+
+
 @pytest.mark.parametrize("dtype", [H, F])
 def test_special_values(dtype):
     x = values(256, 256, dtype)

@@ -11,9 +11,11 @@
 // A block takes 128 x 128 elements.  Each 16 lanes hold a row of 128 in
 // registers (8 elements a lane), so a row's maximum is four lane exchanges and
 // its codes leave as whole 128-byte lines.  For the transposed codes the values
-// also go to LDS, from where a thread takes two neighbouring columns and 32
+// also go to LDS, from where a thread takes two neighbouring columns and 16
 // rows; the codes go back there, so that they too leave as whole lines (44 us of
-// kernel for 51 with each thread's 32 bytes stored at once, at the size below).
+// kernel for 51 with each thread's bytes stored at once, at the size below).
+// Eight waves a block: four took 43.4 us for 41.0 there, and 7.0 for 5.4 where
+// there are fewer blocks than compute units (333 x 768 float32); sixteen 45.5.
 //
 // Bound by memory where x is large: 14336 x 4096 bf16, both ways in tiles (235
 // MB), 50 us a call, 4.7 TB/s.  1111 x 1283 float32, both ways, is 8.3 us of
@@ -32,32 +34,35 @@ namespace {
 using namespace blocks;
 
 constexpr int kB = SS1_FP8_BLOCK;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kRowsAPass = kThreads / 16;
 constexpr int kPasses = kB / kRowsAPass;
+constexpr int kWaves = kThreads / 64;
+constexpr int kRows = kB / kWaves;  // of a wave's columns, for the transposed codes
+
 // The scale bytes of a row from its last block to the row's end are 127.
 __device__ __forceinline__ void pad_scales(uint8_t* row, int64_t block, int64_t blocks, int64_t cols) {
     if (block == blocks - 1)
         for (int64_t j = blocks; j < cols; ++j) row[j] = 127;
 }
 
-// A thread's columns 2p and 2p + 1 of the tile in LDS, 32 rows of them: row i as
+// A thread's columns 2p and 2p + 1 of the tile in LDS, kRows rows of them: row i as
 // the bits of the two values.
 template <typename T>
 struct Pairs;
 
 template <>
 struct Pairs<uint16_t> {
-    uint32_t w[32];
+    uint32_t w[kRows];
     __device__ __forceinline__ void load(const uint16_t* p, int pitch) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + i * pitch);
+        for (int i = 0; i < kRows; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + i * pitch);
     }
     __device__ __forceinline__ uint32_t bits(int i, int h) const { return h ? w[i] & 0xFFFF0000u : w[i] << 16; }
     __device__ __forceinline__ void tops(uint32_t (&t)[2]) const {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = max_halves(m, w[i]);
+        for (int i = 0; i < kRows; ++i) m = max_halves(m, w[i]);
         t[0] = m << 16;
         t[1] = m & 0xFFFF0000u;
     }
@@ -72,10 +77,10 @@ struct Pairs<uint16_t> {
 
 template <>
 struct Pairs<float> {
-    uint32_t w[2][32];
+    uint32_t w[2][kRows];
     __device__ __forceinline__ void load(const float* p, int pitch) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < kRows; ++i) {
             const uint2 v = *reinterpret_cast<const uint2*>(p + i * pitch);
             w[0][i] = v.x;
             w[1][i] = v.y;
@@ -87,7 +92,7 @@ struct Pairs<float> {
         for (int h = 0; h < 2; ++h) {
             t[h] = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) t[h] = larger(t[h], w[h][i] & 0x7FFFFFFFu);
+            for (int i = 0; i < kRows; ++i) t[h] = larger(t[h], w[h][i] & 0x7FFFFFFFu);
         }
     }
     __device__ __forceinline__ uint32_t codes(int j, int h, float scale) const {
@@ -106,8 +111,8 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     constexpr int kPitch = kB + 16 / static_cast<int>(sizeof(T));
     constexpr int kCodePitch = kB + 16;  // bytes; in the same place
     static_assert(kCodePitch <= kPitch * sizeof(T), "the codes fit into the tile");
-    __shared__ uint32_t s_top[4][kB];
-    __shared__ uint32_t s_wave[kThreads / 64];
+    __shared__ uint32_t s_top[kWaves][kB];
+    __shared__ uint32_t s_wave[kWaves];
     const int tid = threadIdx.x, l16 = tid & 15;
     const int64_t bc = blockIdx.x % col_blocks, br = blockIdx.x / col_blocks;
     const int64_t r0 = br * kB, c0 = bc * kB;
@@ -138,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     if (whole) {
         all = s_wave[0];
 #pragma unroll
-        for (int w = 1; w < kThreads / 64; ++w) all = larger(all, s_wave[w]);
+        for (int w = 1; w < kWaves; ++w) all = larger(all, s_wave[w]);
     }
     if (q.codes) {
         const int64_t blocks = q.code_cols / kB;
@@ -157,10 +162,10 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
         }
     }
     if (!qt.codes) return;
-    // columns 2 * pair and 2 * pair + 1, rows 32 * part ..
+    // columns 2 * pair and 2 * pair + 1, rows kRows * part ..
     const int pair = tid & 63, part = tid >> 6;
     Pairs<T> t;
-    t.load(tile + part * 32 * kPitch + 2 * pair, kPitch);
+    t.load(tile + part * kRows * kPitch + 2 * pair, kPitch);
     uint32_t tops[2];
     t.tops(tops);
     const bool odd = larger(tops[0], tops[1]) >= kInf;
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
         for (int h = 0; h < 2; ++h) {
             tops[h] = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tops[h] = larger(tops[h], finite_size(t.bits(i, h)));
+            for (int i = 0; i < kRows; ++i) tops[h] = larger(tops[h], finite_size(t.bits(i, h)));
         }
     }
     if (!qt.shift) {
@@ -183,20 +188,24 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
         const int col = 2 * pair + h;
         const int64_t c = c0 + col;
         uint32_t m = all;
-        if (!qt.shift) m = larger(larger(s_top[0][col], s_top[1][col]), larger(s_top[2][col], s_top[3][col]));
+        if (!qt.shift) {
+            m = s_top[0][col];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) m = larger(m, s_top[w][col]);
+        }
         const uint32_t byte = scale_byte(m);
         const float scale = scale_of(byte);
-        uint32_t w[8];
+        uint32_t w[kRows / 4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = t.codes(j, h, scale);
+        for (int j = 0; j < kRows / 4; ++j) w[j] = t.codes(j, h, scale);
         if (odd) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < kRows; ++i)
                 if ((t.bits(i, h) & 0x7FFFFFFFu) >= kInf) w[i / 4] |= 0x7Fu << (8 * (i & 3));
         }
-        uint4* out = reinterpret_cast<uint4*>(smem + col * kCodePitch + part * 32);
-        out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        uint4* out = reinterpret_cast<uint4*>(smem + col * kCodePitch + part * kRows);
+#pragma unroll
+        for (int i = 0; i < kRows / 16; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         if (c < C && part == 0 && (qt.shift == 0 || col == 0)) {
             uint8_t* srow = qt.scale + (c >> qt.shift) * qt.scale_cols;
             srow[br] = static_cast<uint8_t>(byte);

@@ -16,12 +16,12 @@
 // instruction for two, full rate) widens the operands exactly as they leave LDS
 // and the sums are float32's (8e-8).
 //
-// Rates: 4096 x 14336 x 4096 to bf16 230 us (2090 TFLOP/s; a library product of
-// plain E4M3 of this size 194 us), 8192 x 1280 x 5120 52 us (57), the float32
-// gradient 5120 x 1280 x 8192 about 105 us (a library product of bf16: 105).  The
-// large tile is bound by the way from L2 into LDS beside the matrix cores: these
-// are busy 42% of the time, the texture path 68%, no LDS conflicts; its loads
-// alone take 170 to 217 us, its MFMAs alone 178.
+// Rates: 4096 x 14336 x 4096 to bf16 231 us (2080 TFLOP/s; a library product of
+// plain E4M3 of this size 194 us), 8192^3 448 us (2450), 8192 x 1280 x 5120 52 us
+// (57), the float32 gradient 5120 x 1280 x 8192 about 105 us (a library product of
+// bf16: 105).  The large tiles are bound by the way from L2 into LDS beside the
+// matrix cores: of 192 x 256, these are busy 42% of the time, the texture path
+// 68%, no LDS conflicts; its loads alone take 170 to 217 us, its MFMAs alone 178.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -552,24 +552,34 @@ ss1_status launch_tile(const MatmulBlocksArgs& p, int splits = 1) {
 }
 
 // ------------------------------------------------------------------- choice
-// The tiles and what a stage of 128 takes them, in us: with at most one block a
-// compute unit, and with the two that fit (one for the largest).  Measured on
-// products of 17 to 8192 rows, 640 to 14336 columns and 1280 to 14336 deep; the
-// model below picks the fastest of them or one within 6%.
-//   M, N, K (bf16)        64x64  64x128  128x128  192x256   us a product
-//   64, 14336, 4096        11.9    16.6     23.0     36.0
-//   1024, 4096, 4096       31.2    25.7     29.7     44.9
-//   2048, 4096, 4096       55.1       -     34.7     42.1
-//   4096, 14336, 4096       396       -      264      230
-enum Tile { kTile64, kTile64x128, kTile128, kTile192, kTiles };
+// The tiles and what they take, in us: a round of blocks is stages of 128 deep
+// (first number each) and a prologue and epilogue (second), with at most one
+// block a compute unit, and with as many as fit.  Fitted to 27 products of 64 to
+// 16384 rows, 768 to 14336 columns and 768 to 14336 deep in each type of y; the
+// model below picks the fastest of them or one within 5%.  256 x 256 holds too
+// many registers for a float32 y's operands.
+//   M, N, K (bf16)        64x64  64x128  128x128  192x256  256x256   us a product
+//   64, 14336, 4096        12.5    16.6     23.6     36.4     47.1
+//   1024, 4096, 4096       30.0    25.0     27.4     39.6     50.5
+//   2048, 4096, 4096       55.9    45.2     35.7     43.0     52.3
+//   8192, 1280, 5120       93.3    73.1     68.2     51.5     64.0
+//   4096, 4096, 4096        107    84.2     66.6     81.1     58.4
+//   4096, 14336, 4096       429     338      264      231      231
+//   8192, 8192, 8192        889     702      548      510      448
+enum Tile { kTile64, kTile64x128, kTile128, kTile192, kTile256, kTiles };
+struct RoundUs {
+    double stage, ends;
+};
 struct TileRate {
     int bm, bn, fit;
-    double alone[2], full[2];  // bf16 y, float32 y
+    RoundUs alone[2], full[2];  // bf16 y, float32 y
 };
-constexpr TileRate kRates[kTiles] = {{64, 64, 2, {0.36, 0.50}, {0.52, 0.74}},
-                                     {64, 128, 2, {0.51, 0.79}, {0.80, 1.39}},
-                                     {128, 128, 2, {0.80, 1.20}, {1.20, 1.80}},
-                                     {192, 256, 1, {1.40, 2.50}, {1.44, 2.60}}};
+constexpr TileRate kRates[kTiles] = {
+    {64, 64, 2, {{0.26, 1.1}, {0.43, 1.1}}, {{0.41, 0.7}, {0.57, 1.6}}},
+    {64, 128, 2, {{0.39, 1.9}, {0.69, 3.5}}, {{0.64, 0.8}, {0.93, 3.8}}},
+    {128, 128, 2, {{0.62, 2.7}, {1.00, 5.3}}, {{1.10, 1.8}, {1.49, 7.1}}},
+    {192, 256, 1, {{1.02, 4.7}, {1.95, 10.1}}, {{1.33, 4.4}, {2.08, 13.8}}},
+    {256, 256, 1, {{1.38, 5.7}, {0, 0}}, {{1.66, 5.2}, {0, 0}}}};
 constexpr int64_t kCUs = 256;
 constexpr double kLaunchUs = 3.0;       // of the launch that joins splits
 constexpr double kJoinBytesUs = 4.0e6;  // bytes a us of partial sums, written and read
@@ -581,14 +591,15 @@ struct Choice {
 
 double tile_us(const TileRate& r, int64_t blocks, int64_t stages, bool f32) {
     const int64_t per = (blocks + kCUs - 1) / kCUs;
-    return static_cast<double>(stages) * (per <= 1 ? r.alone[f32] : r.full[f32] * ((per + r.fit - 1) / r.fit));
+    const RoundUs& u = per <= 1 ? r.alone[f32] : r.full[f32];
+    return static_cast<double>((per + r.fit - 1) / r.fit) * (static_cast<double>(stages) * u.stage + u.ends);
 }
 
 Choice choose(int64_t M, int64_t N, int64_t K, bool f32) {
     const int64_t stages = K / kKS;
     Choice best{kTile64, 1};
     double us = 1e30;
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < (f32 ? kTile256 : kTiles); ++t) {
         const TileRate& r = kRates[t];
         const int64_t tiles = ((M + r.bm - 1) / r.bm) * ((N + r.bn - 1) / r.bn);
         const double u = tile_us(r, tiles, stages, f32);
@@ -637,7 +648,10 @@ ss1_status launch_choice(const MatmulBlocksArgs& p) {
         case kTile64: return launch_tile<64, 64, 2, 2, 4, F32>(p);
         case kTile64x128: return launch_tile<64, 128, 2, 2, 3, F32>(p);
         case kTile128: return launch_tile<128, 128, 2, 2, 2, F32>(p);
-        default: return launch_tile<192, 256, 2, 4, 2, F32>(p);
+        case kTile192: return launch_tile<192, 256, 2, 4, 2, F32>(p);
+        default:
+            if constexpr (F32) return SS1_ERR_HIP;  // not chosen
+            else return launch_tile<256, 256, 2, 4, 2, false>(p);
     }
 }
 

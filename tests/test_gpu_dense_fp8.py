@@ -100,7 +100,8 @@ def test_products(M, dtype, tile):
 
 
 LARGE = [(4096, 1280, 768), (1111, 4096, 1283), (2048, 512, 5120), (300, 14336, 640), (16, 4096, 14336),
-         (1, 14336, 4096), (768, 500, 333), (5120, 1280, 8192), (129, 4097, 4096)]
+         (1, 14336, 4096), (768, 500, 333), (5120, 1280, 8192), (129, 4097, 4096),
+         (4000, 4001, 640), (8100, 1277, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)

@@ -13,7 +13,7 @@
 // rate of a large copy) and clipped in 73 more, read and written (6.5 TB/s); the
 // clipping pass finds nothing of the first one's reads in the last-level cache,
 // in either direction.  20M bf16 values take 10.4 us and the last sum 3.8; below
-// that the two launches are the time (700 tensors of 300 to 26,000 values: 11.9
+// that the two launches are the time (400 tensors of 1.5M values together: 11.9
 // us a call).
 #include <hip/hip_runtime.h>
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 // A block's work items, 64 at a time: lane l of every wave holds the l-th one's
 // address, elements left in its tensor and type, so that the chain of reads
 // (item, entry) is paid once for 64 items and not before each one's data (the
-// call over 700 small tensors: 13.6 -> 12.3 us).
+// call over 400 small tensors: 13.6 -> 12.3 us).
 struct Items {
     uint64_t at;
     int64_t left;  // 0: none

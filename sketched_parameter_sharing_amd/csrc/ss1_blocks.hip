@@ -39,6 +39,8 @@ constexpr int kRowsAPass = kThreads / 16;
 constexpr int kPasses = kB / kRowsAPass;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = kB / kWaves;  // of a wave's columns, for the transposed codes
+// blocks of a launch: a grid's threads are numbered in 32 bits
+constexpr int64_t kMostBlocks = ((int64_t(1) << 32) - 1) / kThreads;
 
 // The scale bytes of a row from its last block to the row's end are 127.
 __device__ __forceinline__ void pad_scales(uint8_t* row, int64_t block, int64_t blocks, int64_t cols) {
@@ -105,7 +107,8 @@ struct Pairs<float> {
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __restrict__ x, int64_t R, int64_t C,
-                                                                   uint32_t col_blocks, BlocksView q, BlocksView qt) {
+                                                                   uint32_t col_blocks, uint32_t first, BlocksView q,
+                                                                   BlocksView qt) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     T* tile = reinterpret_cast<T*>(smem);  // [128][kPitch], only with qt
     constexpr int kPitch = kB + 16 / static_cast<int>(sizeof(T));
@@ -114,7 +117,8 @@ __global__ __launch_bounds__(kThreads) void quantize_blocks_kernel(const T* __re
     __shared__ uint32_t s_top[kWaves][kB];
     __shared__ uint32_t s_wave[kWaves];
     const int tid = threadIdx.x, l16 = tid & 15;
-    const int64_t bc = blockIdx.x % col_blocks, br = blockIdx.x / col_blocks;
+    const uint32_t block = first + blockIdx.x;
+    const int64_t bc = block % col_blocks, br = block / col_blocks;
     const int64_t r0 = br * kB, c0 = bc * kB;
 
     Eight<T> v[kPasses];
@@ -233,9 +237,12 @@ ss1_status launch_t(const QuantizeBlocksArgs& a) {
         return SS1_ERR_HIP;
     const int64_t bc = (a.C + kB - 1) / kB;
     const int64_t br = (a.R + kB - 1) / kB;
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(bc * br)), dim3(kThreads), lds,
-                       static_cast<hipStream_t>(a.stream), static_cast<const T*>(a.x), a.R, a.C,
-                       static_cast<uint32_t>(bc), a.q, a.qt);
+    for (int64_t at = 0; at < bc * br; at += kMostBlocks) {
+        const int64_t n = bc * br - at < kMostBlocks ? bc * br - at : kMostBlocks;
+        hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(n)), dim3(kThreads), lds,
+                           static_cast<hipStream_t>(a.stream), static_cast<const T*>(a.x), a.R, a.C,
+                           static_cast<uint32_t>(bc), static_cast<uint32_t>(at), a.q, a.qt);
+    }
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 

@@ -1,0 +1,40 @@
+"""Sizes at which a launch's grid reaches its limit of 2^32 threads: quantisation
+of 2^23 tiles and more."""
+import pytest
+import torch
+
+import sketched_parameter_sharing_amd as ss1
+
+pytestmark = pytest.mark.gpu
+H = torch.bfloat16
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("along", ["q", "qt"])
+def test_quantising_more_tiles_than_one_launch_takes(along):
+    """A row, or a column, of 2^23 tiles and a bit: every part's codes are those of that part alone, to the last one."""
+    n = (1 << 30) + 300
+    x = torch.empty(n, dtype=H, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for i in range(0, n, 1 << 26):
+        part = x[i:i + (1 << 26)]
+        part.copy_(torch.randn(part.numel(), generator=g, device="cuda") * 2.0 ** (i >> 26))
+
+    def quantized(v):
+        if along == "q":
+            return ss1.quantize_fp8_blocks(v[None])[0]
+        return ss1.quantize_fp8_blocks(v[:, None], q=None, qt=True)[1]
+
+    b = quantized(x)
+    width = -(-n // 128) * 128
+    assert b.codes.shape == (1, width) and b.scale.shape == (1, -(-n // 512) * 4)
+    codes, scale = b.codes.view(torch.uint8).view(-1), b.scale.view(-1)
+    for i in range(0, n, 1 << 26):
+        end = min(n, i + (1 << 26))
+        part = quantized(x[i:end])
+        wide = part.codes.shape[1]
+        assert same(codes[i:i + wide], part.codes.view(-1)), i
+        assert same(scale[i // 128:i // 128 + part.scale.shape[1]], part.scale.view(-1)), i

@@ -478,15 +478,16 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
 // launch for it, one token 4096 -> 14336 11.7 and 26.5; 4 tokens 14336 -> 4096,
 // which a block would need 57 KB for, 23 and 16.
 constexpr int64_t kFewRows = 16;
+constexpr int kFewWaves = 4, kFewThreads = kFewWaves * 64;
 constexpr int64_t kInsideRows = 4;                 // rows for which a's reads do not count
 constexpr int64_t kInsideBytes = 32768;            // codes of x in a block's LDS
 constexpr int64_t kInsideAll = int64_t(20) << 20;  // elements that all blocks together quantise
 
 template <typename X, bool F32>
 ss1_status launch_few(const MatmulBlocksArgs& p) {
-    constexpr int NW = 4;
+    constexpr int NW = kFewWaves;
     const size_t lds = __is_same(X, void) ? 0 : static_cast<size_t>(up_to(p.M * (p.K + 16 + p.K / kKS), 16));
-    hipLaunchKernelGGL((few_rows_kernel<X, F32, NW>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(NW * 64), lds,
+    hipLaunchKernelGGL((few_rows_kernel<X, F32, NW>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(kFewThreads), lds,
                        static_cast<hipStream_t>(p.stream), p.a, p.b, static_cast<const X*>(p.x), p.xcols, p.y,
                        static_cast<int>(p.M), static_cast<int>(p.N), static_cast<int>(p.K));
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
@@ -624,8 +625,12 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool f32) {
 // Up to 16 rows go by the weight's rows where what all blocks read of a (M * K
 // bytes each) stays below 24 MB: 16 x 4096 against 14336 rows takes 17.5 us
 // that way and 12.0 in 64 x 64 tiles, 8 x 5120 against 1280 rows 7.8 and 13.8.
+// From 2^28 rows of the weight on the blocks of 16 would be too many: a grid's
+// threads are numbered in 32 bits.
 bool few_rows(int64_t M, int64_t N, int64_t K) {
-    return K > 0 && M <= kFewRows && (M <= kInsideRows || (N + 15) / 16 * M * K <= int64_t(24) << 20);
+    const int64_t blocks = (N + 15) / 16;
+    return K > 0 && M <= kFewRows && blocks * kFewThreads < int64_t(1) << 32 &&
+           (M <= kInsideRows || blocks * M * K <= int64_t(24) << 20);
 }
 
 template <bool F32P, bool F32Q>

@@ -1,5 +1,5 @@
 """Sizes at which a launch's grid reaches its limit of 2^32 threads: quantisation
-of 2^23 tiles and more."""
+of 2^23 tiles and more, a product of few rows with 2^28 and more."""
 import pytest
 import torch
 
@@ -38,3 +38,21 @@ def test_quantising_more_tiles_than_one_launch_takes(along):
         wide = part.codes.shape[1]
         assert same(codes[i:i + wide], part.codes.view(-1)), i
         assert same(scale[i // 128:i // 128 + part.scale.shape[1]], part.scale.view(-1)), i
+
+
+def test_few_rows_against_more_than_one_launch_takes():
+    """Sums that float32 holds exactly: codes of multiples of 2^-9 below 1/2, times 0, 1 or 2."""
+    M, N, K = 2, (1 << 28) + 77, 128
+    b = ss1.Fp8Blocks.empty(N, K, 128)
+    b.codes.view(torch.uint8).random_(0, 0x30, generator=torch.Generator(device="cuda").manual_seed(5))
+    b.scale.fill_(127)
+    a = ss1.Fp8Blocks.empty(M, K)
+    v = torch.randint(0, 3, (M, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).float()
+    a.codes.copy_(v.to(torch.float8_e4m3fn))
+    a.scale.fill_(127)
+    y = ss1.matmul_fp8_blocks(a, b, dtype=torch.float32)
+    h = ss1.matmul_fp8_blocks(a, b)
+    for i in range(0, N, 1 << 22):
+        want = v @ b.codes[i:i + (1 << 22)].float().t()
+        assert torch.equal(y[:, i:i + (1 << 22)], want), i
+        assert torch.equal(h[:, i:i + (1 << 22)], want.to(H)), i

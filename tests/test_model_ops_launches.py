@@ -85,6 +85,15 @@ def run(runtime):
             for add in (0, 1) if M < 1 << 30 else ():
                 call(f"backward {M} {V} {K} {dtype} {add}", "ss1_embedding_backward", T(M, K, dtype), tokens, 1.0, add,
                      T(V, K), A, ROOM, None)
+    for M, N, K in PRODUCTS:
+        for dtype in types:
+            call(f"matmul {M} {N} {K} {dtype}", "ss1_matmul_fp8_blocks", Q(M, K), Q(N, K, 128), T(M, N, dtype), A, ROOM,
+                 None)
+            call(f"dense {M} {N} {K} {dtype}", "ss1_dense_forward_fp8", T(M, K, dtype), Q(N, K, 128), T(M, N, dtype),
+                 Q(K, M), A, ROOM, None)
+            if max(M, N) < 1 << 23:  # the gradients' reductions
+                call(f"gradients {M} {N} {K} {dtype}", "ss1_dense_backward_fp8", T(M, N, dtype), Q(K, M), Q(K, N, 128),
+                     T(M, K, dtype), T(N, K), A, ROOM, None)
     for chunks in (1, 2048, 2049, (1 << 31) - 1):
         for name in ("ss1_gradnorm", "ss1_gradnorm_clip"):
             call(f"{name} {chunks}", name, A, 3, A, chunks, 1.0, A, A, A, ROOM, None)
@@ -98,6 +107,10 @@ QUANTIZE = [(1, 1), (1, 1 << 30), (1 << 30, 1), (1, (1 << 30) - 128), (1, (1 << 
 EMBEDDING = [(1, 1, 1), (MANY, 1000, 512), (MANY, (1 << 29) - 1, 1), (1 << 24, 1000, 1 << 16),
              ((1 << 30) - 1, (1 << 29) - 1, 1024), ((1 << 30) - 1, 262144, 1024), (1, (1 << 29) - 1, 2048), (512, 200000, 512),
              (16384, 262145, 8)]
+# [M][K] by [N][K]: up to 2^22 - 1 tiles of 128 x 128 in y, and either side of 2^28 columns for few rows
+PRODUCTS = [(1, 1, 1), (1, (1 << 28) - 16, 128), (1, 1 << 28, 128), (4, 1 << 28, 128), (4, (1 << 28) + 5, 512), (5, 1 << 28, 1),
+            (16, 1 << 28, 200), (1, (1 << 29) - 128, 128), ((1 << 29) - 128, 1, 128), (128, (1 << 29) - 128, 1),
+            (1 << 18, (1 << 18) - 128, 1024), (300, 300, (1 << 23) - 128), (1, 4096, (1 << 23) - 128)]
 
 
 @pytest.fixture(scope="module")

@@ -334,17 +334,30 @@ __device__ __forceinline__ void matmul_tile(const TileArgs& p, int block) {
 // loads return in order, and the weight's are in flight meanwhile.
 constexpr int kUnit = 4;  // blocks of 128 of a unit: the scales of one word
 
+constexpr int kFewWaves = 4, kFewThreads = kFewWaves * 64;
+
+struct FewArgs {
+    BlocksView a, b;
+    const void* x;
+    int64_t xcols;
+    void* y;
+    int M, N, K;
+};
+
+// smem: with X the codes and scales of x; part: the waves' sums.
 template <typename X, bool F32, int NW>
-__global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksView b, const X* __restrict__ x,
-                                                           int64_t xcols, void* __restrict__ y, int M, int N, int K) {
+__device__ __forceinline__ void few_rows_block(const FewArgs& p, int block, uint8_t* smem, f32x4 (*part)[64]) {
     constexpr bool INSIDE = !__is_same(X, void);
     constexpr int kAhead = 4;  // passes over x whose loads are issued before the weight's
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    __shared__ f32x4 part[NW][64];
+    const BlocksView &a = p.a, &b = p.b;
+    const X* __restrict__ x = static_cast<const X*>(p.x);
+    void* __restrict__ y = p.y;
+    const int64_t xcols = p.xcols;
+    const int M = p.M, N = p.N, K = p.K;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fr = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * 16;
+    const int n0 = block * 16;
     const int nkb = K / kKS;
     const int units = (nkb + kUnit - 1) / kUnit;
     const int u0 = units * wave / NW, u1 = units * (wave + 1) / NW;
@@ -473,23 +486,31 @@ __global__ __launch_bounds__(NW * 64) void few_rows_kernel(BlocksView a, BlocksV
     else store_run(static_cast<uint16_t*>(y) + at, out, N - c);
 }
 
+template <typename X, bool F32>
+__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(FewArgs p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    __shared__ f32x4 part[kFewWaves][64];
+    few_rows_block<X, F32, kFewWaves>(p, static_cast<int>(blockIdx.x), smem, part);
+}
+
 // Rows of a that the kernel above takes, and how much of x a block quantises:
 // 16 tokens 768 -> 768 take 8.3 us a call with x quantised inside and 12 with a
 // launch for it, one token 4096 -> 14336 11.7 and 26.5; 4 tokens 14336 -> 4096,
 // which a block would need 57 KB for, 23 and 16.
 constexpr int64_t kFewRows = 16;
-constexpr int kFewWaves = 4, kFewThreads = kFewWaves * 64;
 constexpr int64_t kInsideRows = 4;                 // rows for which a's reads do not count
 constexpr int64_t kInsideBytes = 32768;            // codes of x in a block's LDS
 constexpr int64_t kInsideAll = int64_t(20) << 20;  // elements that all blocks together quantise
 
+FewArgs few_args(const MatmulBlocksArgs& p) {
+    return {p.a, p.b, p.x, p.xcols, p.y, static_cast<int>(p.M), static_cast<int>(p.N), static_cast<int>(p.K)};
+}
+
 template <typename X, bool F32>
 ss1_status launch_few(const MatmulBlocksArgs& p) {
-    constexpr int NW = kFewWaves;
     const size_t lds = __is_same(X, void) ? 0 : static_cast<size_t>(up_to(p.M * (p.K + 16 + p.K / kKS), 16));
-    hipLaunchKernelGGL((few_rows_kernel<X, F32, NW>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(kFewThreads), lds,
-                       static_cast<hipStream_t>(p.stream), p.a, p.b, static_cast<const X*>(p.x), p.xcols, p.y,
-                       static_cast<int>(p.M), static_cast<int>(p.N), static_cast<int>(p.K));
+    hipLaunchKernelGGL((few_rows_kernel<X, F32>), dim3(static_cast<unsigned>((p.N + 15) / 16)), dim3(kFewThreads), lds,
+                       static_cast<hipStream_t>(p.stream), few_args(p));
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
@@ -498,12 +519,31 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_blocks_kernel(TileArgs p)
     matmul_tile<BM, BN, WM, WN, NSTG, F32, SPLIT>(p, blockIdx.x);
 }
 
-// Two small products side by side: the blocks of one, then of the other.
+// Two small products side by side: the blocks of one, then of the other.  Each
+// goes the way that it would go alone (by the weight's rows, or in 64 x 64 tiles),
+// so that its sums are the same bits with the other and without (4 tokens, 500 ->
+// 2048, float32: 8.5 us of kernels, 13.6 with few rows in tiles too).
+struct SideArgs {
+    TileArgs tile;
+    int blocks;
+    bool few;
+};
+
+template <bool F32>
+__device__ __forceinline__ void matmul_side(const SideArgs& s, int block) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const TileArgs& t = s.tile;
+    if (s.few)
+        few_rows_block<void, F32, kFewWaves>({t.a, t.b, nullptr, 0, t.y, t.M, t.N, t.K}, block, nullptr,
+                                             reinterpret_cast<f32x4(*)[64]>(smem));
+    else matmul_tile<64, 64, 2, 2, 4, F32, false>(t, block);
+}
+
 template <bool F32P, bool F32Q>
-__global__ __launch_bounds__(256) void matmul_pair_kernel(TileArgs p, TileArgs q, int blocks) {
+__global__ __launch_bounds__(kFewThreads) void matmul_pair_kernel(SideArgs p, SideArgs q) {
     const int block = static_cast<int>(blockIdx.x);
-    if (block < blocks) matmul_tile<64, 64, 2, 2, 4, F32P, false>(p, block);
-    else matmul_tile<64, 64, 2, 2, 4, F32Q, false>(q, block - blocks);
+    if (block < p.blocks) matmul_side<F32P>(p, block);
+    else matmul_side<F32Q>(q, block - p.blocks);
 }
 
 // y = the sum over the splits, in order.
@@ -633,15 +673,20 @@ bool few_rows(int64_t M, int64_t N, int64_t K) {
            (M <= kInsideRows || blocks * M * K <= int64_t(24) << 20);
 }
 
+SideArgs side_args(const MatmulBlocksArgs& p) {
+    const TileArgs t = tile_args<64, 64>(p, p.y, 1);
+    const bool few = few_rows(p.M, p.N, p.K);
+    return {t, few ? static_cast<int>((p.N + 15) / 16) : t.n_mt * t.n_nt, few};
+}
+
 template <bool F32P, bool F32Q>
 ss1_status launch_pair_t(const MatmulBlocksArgs& p, const MatmulBlocksArgs& q) {
     constexpr size_t lds = static_cast<size_t>(4) * 128 * (kKS + 4);
-    const TileArgs a = tile_args<64, 64>(p, p.y, 1), b = tile_args<64, 64>(q, q.y, 1);
+    const SideArgs a = side_args(p), b = side_args(q);
     auto kern = &matmul_pair_kernel<F32P, F32Q>;
     if (!allow_lds(kern, lds)) return SS1_ERR_HIP;
-    const int blocks = a.n_mt * a.n_nt;
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks + b.n_mt * b.n_nt)), dim3(256), lds,
-                       static_cast<hipStream_t>(p.stream), a, b, blocks);
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(a.blocks + b.blocks)), dim3(kFewThreads), lds,
+                       static_cast<hipStream_t>(p.stream), a, b);
     return hipGetLastError() == hipSuccess ? SS1_OK : SS1_ERR_HIP;
 }
 
@@ -660,13 +705,12 @@ ss1_status launch_choice(const MatmulBlocksArgs& p) {
     }
 }
 
-// Whether a product goes by 64 x 64 tiles in one round, with no splits: at most
-// kPairStages deep where it would go by the weight's rows otherwise.
-constexpr int64_t kPairStages = 16;
+// Whether a product goes by the weight's rows, or by 64 x 64 tiles in one round
+// with no splits.
 bool pairable(const MatmulBlocksArgs& p, bool f32) {
     const int64_t tiles = ((p.M + 63) / 64) * ((p.N + 63) / 64);
     if (p.K == 0 || tiles > kCUs) return false;
-    if (few_rows(p.M, p.N, p.K)) return p.K / kKS <= kPairStages;
+    if (few_rows(p.M, p.N, p.K)) return true;
     const Choice c = choose(p.M, p.N, p.K, f32);
     return c.tile == kTile64 && c.splits == 1;
 }

@@ -284,7 +284,10 @@ def quantize_fp8_blocks(x, tile: bool = False, q=True, qt=None, stream=None):
 def matmul_fp8_blocks(a: Fp8Blocks, b: Fp8Blocks, y=None, dtype=None, workspace=None, stream=None):
     """The product of two block-scaled matrices along their common columns
     (ss1_matmul_fp8_blocks): y [M][N] = a [M][K] times b [N][K] transposed.  A
-    new y is bfloat16 unless ``dtype`` says float32."""
+    new y is bfloat16 unless ``dtype`` says float32.  A bfloat16 y comes from the
+    8-bit matrix instructions, which keep 18 bits below the largest product of a
+    block of 128; a float32 y has float32 sums of exact products, over values up
+    to below 2^128 (a code times its scale beyond that counts as infinite)."""
     torch = _ops._torch or _ops._setup()
     dev = a.codes.get_device()
     if _elsewhere(stream, dev):
@@ -310,7 +313,8 @@ def dense_forward_fp8(x, w: Fp8Blocks, y=None, xt=None, save_xt: bool = False, w
     returns (y, xt) with y [M][N] = x W^T.  ``x`` [M][K] (bf16 or float32) is
     quantised in the call, ``w`` [N][K] by :func:`quantize_fp8_blocks`.  ``xt``, x
     quantised along its columns, is what :func:`dense_backward_fp8` takes: None
-    unless given or ``save_xt``."""
+    unless given or ``save_xt``.  y has x's dtype, and with it the arithmetic of
+    :func:`matmul_fp8_blocks` for that dtype."""
     _ops._torch or _ops._setup()
     dev = x.get_device()
     if _elsewhere(stream, dev):

@@ -402,7 +402,6 @@ extern "C" ss1_status ss1_dense_forward_fp8(const ss1_tensor* x, const ss1_fp8_b
     ss1::MatmulBlocksArgs p = product(q.q, view_of(w), y, static_cast<uint8_t*>(workspace) + at, stream);
     if (inside) {
         p.x = x->data;
-        p.x_dtype = x->dtype;
         p.xcols = K;
     }
     return ss1::launch_matmul_blocks(p);

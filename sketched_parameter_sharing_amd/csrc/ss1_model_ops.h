@@ -96,9 +96,8 @@ struct MatmulBlocksArgs {
     int32_t dtype;
     void* workspace;
     void* stream;
-    // instead of a's codes: x [M][xcols], quantised by the kernel itself
+    // instead of a's codes: x [M][xcols] of y's dtype, quantised by the kernel itself
     const void* x = nullptr;
-    int32_t x_dtype = 0;
     int64_t xcols = 0;
 };
 

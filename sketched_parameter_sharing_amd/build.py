@@ -25,10 +25,11 @@ COMMON = [
 ]
 
 
-# Per-source options.  The fold kernels keep 128 float32 accumulators per
-# lane, the largest tile of the block-scaled products 96; with MFMA results in ordinary VGPRs they fit beside the operands, while
-# the compiler's default (accumulators in AGPRs, other values spilled there)
-# copies about a hundred registers back and forth on every k-stage.
+# Per-source options.  The fold kernels and the largest tile of the
+# block-scaled products keep 128 float32 accumulators per lane; with MFMA
+# results in ordinary VGPRs they fit beside the operands, while the compiler's
+# default (accumulators in AGPRs, other values spilled there) copies about a
+# hundred registers back and forth on every k-stage.
 EXTRA = {
     "ss1_fold.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "ss1_group.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],

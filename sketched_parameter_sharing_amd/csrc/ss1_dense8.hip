@@ -17,11 +17,13 @@
 // and the sums are float32's (8e-8).
 //
 // Rates: 4096 x 14336 x 4096 to bf16 231 us (2080 TFLOP/s; a library product of
-// plain E4M3 of this size 194 us), 8192^3 448 us (2450), 8192 x 1280 x 5120 52 us
-// (57), the float32 gradient 5120 x 1280 x 8192 about 105 us (a library product of
-// bf16: 105).  The large tiles are bound by the way from L2 into LDS beside the
-// matrix cores: of 192 x 256, these are busy 42% of the time, the texture path
-// 68%, no LDS conflicts; its loads alone take 170 to 217 us, its MFMAs alone 178.
+// plain E4M3 of this size 194 us), 8192^3 448 us (2450), 8192 x 1280 x 5120 52
+// us (57; both over the same operands again and again, over six sets in turn
+// 63), the float32 gradient 5120 x 1280 x 8192 about 105 us (a library product
+// of bf16: 105).  The large tiles are bound by the way from L2 into LDS beside
+// the matrix cores: of 192 x 256, these are busy 42% of the time, the texture
+// path 68%, no LDS conflicts; its loads alone take 170 to 217 us, its MFMAs
+// alone 178.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>

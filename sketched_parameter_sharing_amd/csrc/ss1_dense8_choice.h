@@ -22,8 +22,16 @@ constexpr int64_t kInsideAll = int64_t(20) << 20;  // elements that all blocks t
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * 64;
 
 // Up to 16 rows go by the weight's rows where what all blocks read of a (M * K
-// bytes each) stays below 24 MB: 16 x 4096 against 14336 rows takes 17.5 us
-// that way and 12.0 in 64 x 64 tiles, 8 x 5120 against 1280 rows 7.8 and 13.8.
+// bytes each) stays below 24 MB.  us of kernels that way and in tiles, bf16 y:
+//   M, N, K               MB                       M, N, K               MB
+//   16,  1280,  5120       6    7.7    8.7         8,  8192,  4096      16   10.5   12.1
+//   16,  4096,  4096      16    6.7   10.0         8, 14336,  4096      28   16.3   15.9
+//   16,  6144,  4096      24   11.0   11.1         8,  8192,  8192      32   17.9   20.0
+//   16,  5120,  5120      25   12.9   13.0         8,  4096, 14336      28   16.5   18.3
+//   16,  8192,  4096      32   12.2   12.4         5, 14336,  4096      18   14.7   16.0
+//   16, 14336,  4096      56   19.4   15.8         5, 16384,  8192      40   29.0   35.2
+// The rule is out by at most 21% there (5 rows, 40 MB), and by 18% where the weight
+// has few rows and is deep (16, 1024, 8192: 10.5 and 8.9).
 // From 2^28 rows of the weight on the blocks of 16 would be too many: a grid's
 // threads are numbered in 32 bits.
 inline bool few_rows(int64_t M, int64_t N, int64_t K) {

@@ -13,7 +13,8 @@
 // ids and has counters of its own, and lanes of one row take their rank from a
 // ballot for each bit of the row number, so the order is stable, nothing is
 // atomic in global memory, and one launch sorts.  From kDealTokens on the ids
-// are dealt to their blocks first, and few tokens go in one launch altogether.
+// are dealt to their blocks first (in tables of up to 262144 rows), and few tokens
+// go in one launch altogether.
 //
 // Sum.  A wave takes T consecutive places of the sorted order and 64 lanes'
 // worth of columns, so a row with many tokens is shared by many waves.  A row
@@ -23,11 +24,11 @@
 // sum's launch.
 //
 // Bound by memory where the table or the batch is large: 8192 x 1280 bf16 into
-// 50000 rows of bf16 (149 MB) 41 us a call, of which sort and the first zeros 16,
-// sum and the other zeros 20, join 5; 2048 tokens into 128256 x 4096 float32
+// 50000 rows of bf16 (149 MB) 35 to 41 us a call, of which sort and the first zeros
+// 16, sum and the other zeros 15, join 4; 2048 tokens into 128256 x 4096 float32
 // (2.1 GB) 392 us, 5.4 TB/s.  333 tokens of 1283 into 2003 rows: 8.9 us, one
-// launch.  One row with all the tokens is the worst: 131072 of them 255 us for
-// 108, since one block sorts and joins them.
+// launch.  One row with all the tokens is the worst: 131072 of them, 768 wide, 238
+// us for 109, since one block sorts and joins them.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -256,7 +257,9 @@ __device__ __forceinline__ int scan_before(int mine, int32_t* sums) {
 // ------------------------------------------------------------- many tokens
 // With many tokens, every block's reading of all ids is the time (256 blocks x
 // 131072 ids: 91 us of the sort), so they are first handed out to the blocks
-// that own them: chunk c of the ids counts them by owner, and then puts them,
+// that own them (up to kOwners of them, which 262144 rows have; a larger table's
+// blocks still read all ids: 131072 tokens, 64 wide, into 262144 rows 89 us and into
+// 262145 317, 768 wide 176 and 418; 8192 tokens, 64 wide, 31 and 40): chunk c of the ids counts them by owner, and then puts them,
 // in order, behind those of the chunks before it.  Every chunk adds up the
 // counts for itself.
 constexpr int kOwners = 512;   // owners at most
@@ -788,20 +791,28 @@ int32_t tile_tokens(int64_t M) {
     return static_cast<int32_t>(T);
 }
 
-// Whether one launch does it all: 333 tokens of 1283 take 8.9 us that way and
-// 19.8 by sort, sum and join.  A frequent row's tokens all go through one compute
-// unit there, so M * K is bounded: 1024 tokens of one row, 1280 wide, took 192 us
-// that way and 52 by the other, 511 of them 768 wide 47 and 35 (31 and 33 in
-// different rows).  Tables beyond 2^27 elements took 20% longer with rows zeroed
-// 256 apart.
+// Whether one launch does it all.  A frequent row's tokens all go through one
+// compute unit there, so M * K is bounded: the bound weighs what tokens of text gain
+// against what tokens of one row lose.  us that way and by sort, sum and join, into
+// 2003 rows:
+//   tokens x width     text           all apart      all one row
+//   512 x  256          8.0   14.8     4.4   14.2    16.6   12.4
+//   333 x 1283          9.1   16.7     7.7   15.9    39.8   14.1
+//   512 x 1024          9.3   16.4     6.5   15.3    36.4   13.5   the bound
+//   512 x 2048         12.2   17.9     9.3   16.8    61.4   15.3
+//   128 x 8192         18.8   23.8    19.3   23.0    79.2   23.6
+// Into 50000 rows, where the zeros are the time, 511 x 768 takes 29.5 and 30.6, all
+// one row 52.5 and 29.9.  Tables beyond 2^27 elements took 20% longer with rows
+// zeroed 256 apart.
 constexpr int64_t kFewElements = int64_t(1) << 19, kFewTable = int64_t(1) << 27;
 bool few_tokens(int64_t M, int64_t V, int64_t K) {
     return M <= kFewTokens && M * K <= kFewElements && V * K <= kFewTable;
 }
 
 // Chunks of the ids that are dealt out before the sort, 0 where they are not: two
-// more launches.  Tokens into 50000 x 768 without and with: 12000 42.4 and 44.3
-// us, 16384 47.9 and 47.4, 32768 71.3 and 55.8, 131072 235 and 137.
+// more launches.  Tokens into 50000 x 768 without and with: 8192 31.0 and 34.1 us,
+// 12000 36.0 and 38.5, 16384 39.6 and 39.9, 24000 55.6 and 48.1, 131072 215 and 112;
+// into 2003 x 1280: 12000 27.9 and 29.7, 16384 32.3 and 31.6, 24000 41.4 and 35.6.
 constexpr int64_t kDealTokens = 16384;
 int64_t chunk_tokens(int64_t M) { return up_to((M + kChunks - 1) / kChunks, kSortThreads); }
 int32_t deal_chunks(int64_t M, const RowOrder& o) {

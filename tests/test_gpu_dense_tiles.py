@@ -47,6 +47,7 @@ def test_products_of_every_tile(product):
     assert (home[:16] == 7).all() and (home[16 + M * N:] == 7).all()
     assert torch.equal(ss1.matmul_fp8_blocks(a, b, dtype=dtype), y)
     # every row, column, scale and block of the reduction in its place
-    a, b = whole_numbers(M, K, 1, 7 + stages), whole_numbers(N, K, 128 if stages % 2 else 1, 8 + stages)
-    y = ss1.matmul_fp8_blocks(a, b, dtype=dtype)
-    assert torch.equal(y.double(), (value(a) @ value(b).t()).to(dtype).double())
+    for of_a, of_b in ((1, 128), (128, 1), (1, 1), (128, 128)):
+        a, b = whole_numbers(M, K, of_a, 7 + stages), whole_numbers(N, K, of_b, 8 + stages)
+        y = ss1.matmul_fp8_blocks(a, b, dtype=dtype)
+        assert torch.equal(y.double(), (value(a) @ value(b).t()).to(dtype).double()), (of_a, of_b)

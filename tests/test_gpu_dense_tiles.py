@@ -16,7 +16,7 @@ TILES = {
     ((64, 64), 1): {H: [(61, 61, s) for s in range(1, 10)] + [(700, 900, 6)],
                     F: [(61, 61, s) for s in range(1, 10)] + [(700, 900, 6)]},
     ((64, 64), 2): {H: [(500, 700, 35), (500, 700, 36), (500, 641, 37), (500, 641, 38)],
-                    F: [(333, 641, 21), (333, 641, 22), (500, 641, 23), (500, 641, 24)]},
+                    F: [(333, 641, 21), (333, 641, 22), (500, 641, 23), (641, 641, 28)]},
     ((64, 64), 4): {H: [(61, 61, s) for s in range(16, 21)], F: [(61, 61, s) for s in range(16, 21)]},
     ((64, 64), 8): {H: [(61, 61, s) for s in range(32, 38)], F: [(61, 61, s) for s in range(32, 38)]},
     ((64, 128), 1): {H: [(129, 12001, s) for s in range(1, 8)], F: [(129, 12001, s) for s in range(3, 10)]},

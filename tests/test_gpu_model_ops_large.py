@@ -1,5 +1,6 @@
 """Sizes at which a launch's grid reaches its limit of 2^32 threads: quantisation
-of 2^23 tiles and more, a product of few rows with 2^28 and more."""
+of 2^23 tiles and more, a product of few rows with 2^28 and more; and gradients of
+millions of tokens."""
 import pytest
 import torch
 
@@ -56,3 +57,21 @@ def test_few_rows_against_more_than_one_launch_takes():
         want = v @ b.codes[i:i + (1 << 22)].float().t()
         assert torch.equal(y[:, i:i + (1 << 22)], want), i
         assert torch.equal(h[:, i:i + (1 << 22)], want.to(H)), i
+
+
+@pytest.mark.parametrize("M,V", [(20_000_003, 3000), (3_000_001, 300_000)], ids=["dealt", "not dealt"])
+@pytest.mark.parametrize("kind", ["some", "same"])
+def test_gradients_of_millions_of_tokens(M, V, kind):
+    """Whole numbers: every partial sum is one that float32 holds."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dy = torch.randint(-1, 2, (M, 4), generator=g, device="cuda").to(H)
+    ids = torch.randint(-1, V, (M,), generator=g, device="cuda", dtype=torch.int32)
+    if kind == "same":
+        ids[ids % 8 > 0] = 7
+    dE = ss1.embedding_backward(dy, ids, V, dtype=torch.float32)
+    real = (ids >= 0).cpu()
+    want = torch.zeros((V, 4), dtype=torch.float64)
+    want.index_add_(0, ids.cpu()[real].long(), dy.double().cpu()[real])
+    assert torch.equal(dE.double().cpu(), want)
+    more = ss1.embedding_backward(dy, ids, V, dE=dE.clone(), accumulate=True)
+    assert torch.equal(more, dE * 2)
